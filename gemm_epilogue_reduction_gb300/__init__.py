@@ -20,6 +20,8 @@ SB_W_PACKED = 0x100  # layout flag OR'ed into `surface`: W is the packed copy (s
 SURFACES = {"token": SB_TOKEN, "token_logprob": SB_TOKEN_LOGPROB,
             "full_logits": SB_FULL_LOGITS, "gumbel_token": SB_GUMBEL_TOKEN,
             "topk_logprob": SB_TOPK_LOGPROB}
+SB_REDUCE_NONE, SB_REDUCE_SUM, SB_REDUCE_MEAN = 0, 1, 2
+REDUCTIONS = {"none": SB_REDUCE_NONE, "sum": SB_REDUCE_SUM, "mean": SB_REDUCE_MEAN}
 SB_OK = 0
 SB_ERR_INVALID_ARG = 1
 SB_ERR_UNSUPPORTED = 2
@@ -108,6 +110,16 @@ def lib():
         L.sb_partial_completion.argtypes = [P, P, i64, i64, i64, i32, P, i32, P,
                                             ctypes.c_size_t, P]
         L.sb_partial_completion.restype = i32
+        L.sb_cross_entropy_workspace_bytes.argtypes = [i64] * 3
+        L.sb_cross_entropy_workspace_bytes.restype = ctypes.c_size_t
+        L.sb_cross_entropy_forward.argtypes = [P, P, P, i64, i64, i64, i32, i32, ctypes.c_float,
+                                               P, P, P, ctypes.c_size_t, P]
+        L.sb_cross_entropy_forward.restype = i32
+        L.sb_cross_entropy_backward_workspace_bytes.argtypes = [i64] * 4 + [i32] * 2
+        L.sb_cross_entropy_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.sb_cross_entropy_backward.argtypes = [P, P, P, P, P, i64, i64, i64, i32, i32,
+                                                ctypes.c_float, i64, P, P, P, ctypes.c_size_t, P]
+        L.sb_cross_entropy_backward.restype = i32
         L.sb_select_source_projection.argtypes = [ctypes.c_double] * 8 + [
             ctypes.POINTER(ctypes.c_double)]
         L.sb_select_source_projection.restype = i32
@@ -304,6 +316,33 @@ def partial_completion(X, W, lanes: int, *, out_bf16: bool = True, stream=None, 
     return Y, workspace
 
 
+def sb_cross_entropy_workspace_bytes(M: int, d: int, V: int) -> int:
+    return int(lib().sb_cross_entropy_workspace_bytes(M, d, V))
+
+
+def sb_cross_entropy_forward(H, W, targets, M, d, V, ignore_index, reduction, z_loss, loss, lse,
+                             workspace, workspace_bytes, stream=None) -> int:
+    return int(lib().sb_cross_entropy_forward(_ptr(H), _ptr(W), _ptr(targets), M, d, V,
+                                              ignore_index, reduction, float(z_loss), _ptr(loss),
+                                              _ptr(lse), _ptr(workspace), int(workspace_bytes),
+                                              _stream(stream)))
+
+
+def sb_cross_entropy_backward_workspace_bytes(M: int, d: int, V: int, piece: int, with_dH: bool,
+                                              with_dW: bool) -> int:
+    return int(lib().sb_cross_entropy_backward_workspace_bytes(M, d, V, piece, int(with_dH),
+                                                               int(with_dW)))
+
+
+def sb_cross_entropy_backward(H, W, targets, lse, grad, M, d, V, ignore_index, reduction, z_loss,
+                              piece, dH, dW, workspace, workspace_bytes, stream=None) -> int:
+    return int(lib().sb_cross_entropy_backward(_ptr(H), _ptr(W), _ptr(targets), _ptr(lse),
+                                               _ptr(grad), M, d, V, ignore_index, reduction,
+                                               float(z_loss), piece, _ptr(dH), _ptr(dW),
+                                               _ptr(workspace), int(workspace_bytes),
+                                               _stream(stream)))
+
+
 def sb_select_source_projection(bytes_ref, bytes_proj, frames_ref, frames_proj,
                                 link_bytes_per_s, frame_startup_s, local_proj_s, local_ref_s):
     """Equation (7) plan choice: returns (decision, margin_s); 1 = project at the source."""
@@ -425,3 +464,132 @@ def project(H, W, k: int, surface: int = SB_TOKEN_LOGPROB, *, temperature: float
         raise SbError(st, "sb_lmhead_project")
     bufs["_outputs"] = out
     return bufs
+
+
+# ------------------------------------------------------------------ training the head
+def _tensor(name, t, shape, dtypes, device, where):
+    """Refuses a tensor the kernels would misread: another shape or type, one that is not
+    contiguous, or one that is not on the current CUDA device."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{where}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{where}: {name} is on {t.device}, not {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} is not contiguous")
+    return t
+
+
+def _device(where):
+    import torch
+    if not torch.cuda.is_available():
+        raise RuntimeError(f"{where}: no CUDA device")
+    return torch.device("cuda", torch.cuda.current_device())
+
+
+class _on_stream:
+    """Makes `stream` (None, a torch stream or a raw handle) torch's current one, so that what a
+    call allocates belongs to the stream its kernels run on."""
+
+    def __init__(self, stream):
+        import torch
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        self._ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _reduction(reduction, where):
+    try:
+        return REDUCTIONS[reduction]
+    except KeyError:
+        raise ValueError(f"{where}: reduction is one of {sorted(REDUCTIONS)}, "
+                         f"not {reduction!r}") from None
+
+
+def _loss_problem(H, W, targets, where):
+    import torch
+    dev = _device(where)
+    if H.dim() != 2 or W.dim() != 2:
+        raise ValueError(f"{where}: H is [M, d] and W [V, d]")
+    M, d = H.shape
+    V = W.shape[0]
+    _tensor("H", H, (M, d), (torch.bfloat16,), dev, where)
+    _tensor("W", W, (V, d), (torch.bfloat16,), dev, where)
+    _tensor("targets", targets, (M,), (torch.int32,), dev, where)
+    return M, d, V, dev
+
+
+def _workspace(nbytes, workspace, device, where):
+    import torch
+    if nbytes == 0:
+        raise SbError(SB_ERR_INVALID_ARG, where)
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return workspace
+
+
+def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.0,
+                  reduction: str = "mean", stream=None, workspace=None):
+    """The cross entropy of the rows' targets under logits H Wᵀ, without keeping the logits:
+    lse - z_target + z_loss lse² per row, 0 for rows whose target is ``ignore_index``.
+
+    H [M, d] and W [V, d] bf16, targets [M] int32, contiguous CUDA tensors. Returns a dict:
+    loss (float32, [M] for reduction "none", [1] for "sum" and "mean"), lse [M] and workspace.
+    Asynchronous on ``stream``; raises SbError on a bad status. A target outside [0, V) that is
+    not ``ignore_index`` gives a NaN loss, and ``device_status`` of the workspace reports it."""
+    import torch
+    where = "cross_entropy"
+    red = _reduction(reduction, where)
+    M, d, V, dev = _loss_problem(H, W, targets, where)
+    with _on_stream(stream):
+        workspace = _workspace(sb_cross_entropy_workspace_bytes(M, d, V), workspace, dev, where)
+        loss = torch.empty(M if red == SB_REDUCE_NONE else 1, dtype=torch.float32, device=dev)
+        lse = torch.empty(M, dtype=torch.float32, device=dev)
+        st = sb_cross_entropy_forward(H, W, targets, M, d, V, ignore_index, red, z_loss, loss,
+                                      lse, workspace, workspace.numel(), stream)
+    if st != SB_OK:
+        raise SbError(st, "sb_cross_entropy_forward")
+    return {"loss": loss, "lse": lse, "workspace": workspace}
+
+
+def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int = -100,
+                           z_loss: float = 0.0, reduction: str = "mean", need_dH: bool = True,
+                           need_dW: bool = True, piece: int = 0, stream=None, workspace=None):
+    """The gradients of ``cross_entropy`` in H and W, bf16, from its ``lse`` and the same
+    arguments; ``grad`` is the incoming gradient (float32, [M] for "none", else [1]; None stands
+    for ones). The vocabulary is worked off in pieces of ``piece`` columns (0: the library's
+    choice). Returns a dict: dH, dW (None where not needed) and workspace."""
+    import torch
+    where = "cross_entropy_backward"
+    red = _reduction(reduction, where)
+    M, d, V, dev = _loss_problem(H, W, targets, where)
+    _tensor("lse", lse, (M,), (torch.float32,), dev, where)
+    if grad is not None:
+        _tensor("grad", grad, (M if red == SB_REDUCE_NONE else 1,), (torch.float32,), dev, where)
+    with _on_stream(stream):
+        workspace = _workspace(
+            sb_cross_entropy_backward_workspace_bytes(M, d, V, piece, need_dH, need_dW),
+            workspace, dev, where)
+        dH = torch.empty_like(H) if need_dH else None
+        dW = torch.empty_like(W) if need_dW else None
+        st = sb_cross_entropy_backward(H, W, targets, lse, grad, M, d, V, ignore_index, red,
+                                       z_loss, piece, dH, dW, workspace, workspace.numel(),
+                                       stream)
+    if st != SB_OK:
+        raise SbError(st, "sb_cross_entropy_backward")
+    return {"dH": dH, "dW": dW, "workspace": workspace}
+
+
+def device_status(workspace) -> int:
+    """``sb_last_device_status`` of a workspace tensor (synchronises)."""
+    return sb_last_device_status(sb_outputs(workspace=_ptr(workspace),
+                                            workspace_bytes=workspace.numel()))

@@ -953,7 +953,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.ws.epoch = p.epoch;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.ws.epoch[0] = p.epoch;
+        p.ws.epoch[1] = 0;
+    }
     if (VOCAB && (p.flags & kFlagTargets))
         for (int i = threadIdx.x; i < p.M; i += blockDim.x) tgt_s[i] = p.targets[i];
     // Scoring targets outside [0, V) would leave their log-prob undefined: CTA 0 checks them
@@ -962,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool bad = false;
         for (int i = threadIdx.x; i < p.M; i += blockDim.x) {
             const int t = p.targets[i];
-            bad |= (t < 0 || t >= p.V);
+            bad |= (t < 0 || t >= p.V) && !(p.has_ignore && t == p.ignore_index);
         }
         if (bad) record_status(p.ws.status, p.epoch, 1u);  // SB_ERR_INVALID_ARG
     }
@@ -1177,7 +1180,7 @@ cudaError_t launch_t1(const CUtensorMap &tmA, const CUtensorMap &tmB, const Gemm
     // a programmatic dependent of the previous kernel in the stream: its CTAs may start
     // their setup early and wait (griddepcontrol.wait) before touching global memory
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].val.programmaticStreamSerializationAllowed = p.early ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     // persistent grid: as many clusters as can be resident at once (one CTA per SM)

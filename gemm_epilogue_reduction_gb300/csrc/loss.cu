@@ -1,0 +1,362 @@
+// loss.cu -- the cross entropy of the output head: the rows' losses from the projection
+// records, and the host side of both directions.
+//
+// Forward is the record GEMM of lmhead.cu (with the targets' logits) followed by one kernel:
+//   lse_r  = m + log sum_t s_rt·exp(m_rt - m),  m = max_t m_rt   (records t of 128 columns)
+//   loss_r = lse_r - z_r,target + z_loss·lse_r²,  0 where the target is the ignored index,
+// one block per row, and the last block to finish adds the rows' losses up (SUM, MEAN) in a
+// fixed order, so the bits do not depend on which block that is.  The rows kernel reads
+// 8 bytes for each 128 columns of a row: next to the GEMM's time it is small (M = 4096,
+// V = 200,064: 51 MB).  Backward is loss_grad.cu; its host side here cuts the vocabulary into
+// pieces and chooses the split of the dH reduction.
+#include <cmath>
+
+#include "sb.h"
+#include "sb_combine_math.cuh"
+#include "sb_internal.h"
+#include "sb_ptx.cuh"
+
+namespace sb {
+namespace {
+
+constexpr int kRowThreads = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct MaxSum {
+    float m, s;
+};
+// Sums of exp relative to the larger maximum; -inf maxima (nothing seen) carry s = 0.
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
+    const float m = fmaxf(a.m, b.m);
+    if (m == -INFINITY) return MaxSum{m, 0.f};
+    return MaxSum{m, a.s * ex2_approx((a.m - m) * kLog2e) + b.s * ex2_approx((b.m - m) * kLog2e)};
+}
+
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const LossParams p) {
+    __shared__ float sm[kRowThreads / 32], ss[kRowThreads / 32];
+    __shared__ int is_last;
+    const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // all the records' writes first, then let the next kernel set up
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const float *rm = p.ws.m + static_cast<size_t>(row) * p.T;
+    const float *rs = p.ws.s + static_cast<size_t>(row) * p.T;
+    MaxSum a{-INFINITY, 0.f};
+    for (int t = threadIdx.x; t < p.T; t += 4 * kRowThreads) {
+        MaxSum x[4];  // four records in flight
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = t + u * kRowThreads;
+            x[u] = i < p.T ? MaxSum{rm[i], rs[i]} : MaxSum{-INFINITY, 0.f};
+        }
+        a = join(a, join(join(x[0], x[1]), join(x[2], x[3])));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        a = join(a, MaxSum{__shfl_xor_sync(0xFFFFFFFFu, a.m, o),
+                           __shfl_xor_sync(0xFFFFFFFFu, a.s, o)});
+    if (lane == 0) {
+        sm[warp] = a.m;
+        ss[warp] = a.s;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < kRowThreads / 32; ++w) a = join(a, MaxSum{sm[w], ss[w]});
+        const float lse = a.m + logf(a.s);
+        const int t = p.targets[row];
+        float loss = 0.f;
+        if (t != p.ignore_index)
+            // a target outside the vocabulary has no logit: the status word reports it
+            loss = t >= 0 && t < p.V
+                       ? (lse - p.ws.tz[row]) + p.z_loss * lse * lse
+                       : __uint_as_float(0x7FC00000u);
+        p.lse[row] = lse;
+        p.rows[row] = loss;
+        is_last = 0;
+        if (p.reduction != SB_REDUCE_NONE) {
+            __threadfence();  // this row's loss before its count
+            is_last = atomicAdd(p.ws.epoch + 1, 1u) == static_cast<uint32_t>(p.M) - 1u;
+        }
+    }
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    // 64-bit partial sums: M terms of one size
+    double sum = 0.0;
+    int count = 0;
+    for (int r = threadIdx.x; r < p.M; r += kRowThreads)
+        if (p.targets[r] != p.ignore_index) {
+            sum += static_cast<double>(__ldcg(p.rows + r));
+            ++count;
+        }
+    __shared__ double sd[kRowThreads];
+    __shared__ int sc[kRowThreads];
+    sd[threadIdx.x] = sum;
+    sc[threadIdx.x] = count;
+    __syncthreads();
+    for (int w = kRowThreads / 2; w > 0; w >>= 1) {
+        if (threadIdx.x < w) {
+            sd[threadIdx.x] += sd[threadIdx.x + w];
+            sc[threadIdx.x] += sc[threadIdx.x + w];
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        *p.loss = static_cast<float>(
+            p.reduction == SB_REDUCE_MEAN ? sd[0] / (sc[0] > 0 ? sc[0] : 1) : sd[0]);
+}
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// M = 0 (a batch without tokens) is a valid problem of its own.
+bool loss_shape_ok(int64_t M, int64_t d, int64_t V) {
+    return M >= 0 && M <= (int64_t(1) << 30) && V >= 1 && V < (int64_t(1) << 31) - 512 && d >= 8 &&
+           d <= (int64_t(1) << 24);
+}
+
+int32_t check_loss(const void *H, const void *W, const int32_t *targets, int64_t M, int64_t d,
+                   int64_t V, int32_t reduction, float z_loss) {
+    if (!W || (M > 0 && (!H || !targets)) || !loss_shape_ok(M, d, V) ||
+        reduction < SB_REDUCE_NONE || reduction > SB_REDUCE_MEAN || !std::isfinite(z_loss))
+        return SB_ERR_INVALID_ARG;
+    if (d % 8 != 0 || !on(H, 16) || !on(W, 16) || !on(targets, 4)) return SB_ERR_ALIGNMENT;
+    return SB_OK;
+}
+
+// How a backward call runs: the piece of the vocabulary, the split of the dH reduction, and the
+// workspace.
+struct Plan {
+    int64_t piece, ldg;
+    int splits;
+    size_t g_off, h_off, part_off, total;
+};
+
+constexpr int64_t kPieceBytes = int64_t(256) << 20;  // of G, where the caller leaves the choice
+
+// A block of work is one 256 x 256 tile over ATOMS * 64 of the reduction (0.34 us per 64 on one
+// CTA pair); a dW tile costs at least its 128 KB of output, about six 64-blocks' time.
+struct Work {
+    int64_t kb, long_blocks, short_blocks, longs, shorts;
+};
+Work work_of(int64_t M, int64_t d, int64_t cols, bool with_dH, bool with_dW) {
+    Work w;
+    const int64_t rt = (M + 255) / 256, dt = (d + 255) / 256, ct = (cols + 255) / 256;
+    const int atoms = rt < 2 ? 1 : 2;
+    w.kb = 64 * atoms;
+    w.long_blocks = (cols + w.kb - 1) / w.kb;
+    w.short_blocks = (M + w.kb - 1) / w.kb;
+    if (w.short_blocks < 6 / atoms) w.short_blocks = 6 / atoms;
+    w.longs = with_dH ? rt * dt : 0;
+    w.shorts = with_dW ? ct * dt : 0;
+    return w;
+}
+
+// Splits of the dH reduction: the smallest estimated time over both products.  Unsplit, few
+// dH tiles of a long reduction leave most CTA pairs idle (16 rows, d = 5120: 20 tiles of 2374
+// blocks for 76 pairs); every split adds its fp32 partial sums' traffic.
+int choose_splits(int64_t M, int64_t d, int64_t piece, bool with_dH, bool with_dW, int pairs) {
+    if (!with_dH) return 1;
+    const Work w = work_of(M, d, piece, with_dH, with_dW);
+    int best = 1;
+    double best_t = 0;
+    for (int s = 1; s <= 64 && s <= w.long_blocks; ++s) {
+        const int64_t blocks = (w.long_blocks + s - 1) / s;
+        const int64_t rounds = (w.longs * s + pairs - 1) / pairs;
+        const double even = (static_cast<double>(w.longs) * s * blocks +
+                             static_cast<double>(w.shorts) * w.short_blocks) / pairs;
+        double t = static_cast<double>(rounds * blocks);
+        if (even > t) t = even;
+        t *= 0.34 * static_cast<double>(w.kb) / 64;                     // us
+        if (s > 1) t += static_cast<double>(s) * M * d * 8 / 6.8e6;     // written and read again
+        if (s == 1 || t < best_t) {
+            best = s;
+            best_t = t;
+        }
+    }
+    return best;
+}
+
+Plan plan_of(int64_t M, int64_t d, int64_t V, int64_t piece, bool with_dH, bool with_dW,
+             int pairs) {
+    Plan pl{};
+    if (piece == 0) {
+        const int64_t n = (2 * M * V + kPieceBytes - 1) / kPieceBytes;
+        piece = (V + n - 1) / n;
+    }
+    piece = (piece + 255) / 256 * 256;
+    pl.piece = piece < V ? piece : V;
+    pl.ldg = (pl.piece + 63) / 64 * 64;
+    pl.splits = choose_splits(M, d, pl.piece, with_dH, with_dW, pairs);
+    pl.g_off = 256;
+    pl.h_off = pl.g_off + up256(static_cast<size_t>(M) * pl.ldg * 2);
+    pl.part_off = pl.h_off + (with_dW ? up256(static_cast<size_t>(M) * d * 2) : 0);
+    pl.total = pl.part_off;
+    if (with_dH && (pl.splits > 1 || pl.piece < V))
+        pl.total += up256(static_cast<size_t>(pl.splits) * M * d * 4);
+    return pl;
+}
+
+}  // namespace
+
+cudaError_t launch_loss_rows(const LossParams &p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.M);
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rows_kernel, p);
+}
+
+}  // namespace sb
+
+using namespace sb;
+
+extern "C" {
+
+size_t sb_cross_entropy_workspace_bytes(int64_t M, int64_t d, int64_t V) {
+    if (!loss_shape_ok(M, d, V) || d % 8 != 0) return 0;
+    if (M == 0) return 256;
+    const size_t records = sb_workspace_bytes(M, V, 1, SB_TOKEN);
+    return records ? records + up256(static_cast<size_t>(M) * 4) : 0;
+}
+
+int32_t sb_cross_entropy_forward(const void *H, const void *W, const int32_t *targets, int64_t M,
+                                 int64_t d, int64_t V, int32_t ignore_index, int32_t reduction,
+                                 float z_loss, float *loss, float *lse, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+    if (int32_t e = check_loss(H, W, targets, M, d, V, reduction, z_loss)) return e;
+    const bool scalar = reduction != SB_REDUCE_NONE;
+    if (((M > 0 || scalar) && !loss) || (M > 0 && !lse) || !workspace) return SB_ERR_INVALID_ARG;
+    if (!on(loss, 4) || !on(lse, 4) || !on(workspace, 256)) return SB_ERR_ALIGNMENT;
+    if (workspace_bytes < sb_cross_entropy_workspace_bytes(M, d, V))
+        return SB_ERR_WORKSPACE_TOO_SMALL;
+    if (int32_t e = device_sms_cc(nullptr, nullptr)) return e;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (M == 0) {  // no rows: the sum (and the mean) of nothing is 0
+        if (cudaMemsetAsync(workspace, 0, 256, st) != cudaSuccess ||
+            (scalar && cudaMemsetAsync(loss, 0, 4, st) != cudaSuccess))
+            return SB_ERR_CUDA;
+        return SB_OK;
+    }
+    const size_t records = sb_workspace_bytes(M, V, 1, SB_TOKEN);
+    LossParams p{};
+    if (int32_t e = enqueue_target_records(H, W, targets, M, d, V, ignore_index, workspace,
+                                           records, &p.ws, st))
+        return e;
+    p.M = static_cast<int>(M);
+    p.V = static_cast<int>(V);
+    p.T = sb_tiles_per_shard(M, V, 1);
+    p.reduction = reduction;
+    p.ignore_index = ignore_index;
+    p.z_loss = z_loss;
+    p.targets = targets;
+    p.lse = lse;
+    p.loss = loss;
+    p.rows = scalar ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + records)
+                    : loss;
+    return launch_loss_rows(p, st) == cudaSuccess ? SB_OK : SB_ERR_CUDA;
+}
+
+size_t sb_cross_entropy_backward_workspace_bytes(int64_t M, int64_t d, int64_t V, int64_t piece,
+                                                 int32_t with_dH, int32_t with_dW) {
+    if (!loss_shape_ok(M, d, V) || d % 8 != 0 || piece < 0 || !(with_dH || with_dW)) return 0;
+    if (M == 0) return 256;
+    int sms = 0;
+    if (device_sms_cc(&sms, nullptr) != SB_OK) return 0;
+    return plan_of(M, d, V, piece, with_dH != 0, with_dW != 0, sms / 2).total;
+}
+
+int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *targets,
+                                  const float *lse, const float *grad, int64_t M, int64_t d,
+                                  int64_t V, int32_t ignore_index, int32_t reduction,
+                                  float z_loss, int64_t piece, void *dH, void *dW,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    if (int32_t e = check_loss(H, W, targets, M, d, V, reduction, z_loss)) return e;
+    if ((!dH && !dW) || (M > 0 && !lse) || !workspace || piece < 0) return SB_ERR_INVALID_ARG;
+    if (!on(lse, 4) || !on(grad, 4) || !on(dH, 16) || !on(dW, 16) || !on(workspace, 256))
+        return SB_ERR_ALIGNMENT;
+    int sms = 0;
+    if (int32_t e = device_sms_cc(&sms, nullptr)) return e;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (M == 0) {  // no rows: dW is the empty sum
+        if (workspace_bytes < 256) return SB_ERR_WORKSPACE_TOO_SMALL;
+        if (cudaMemsetAsync(workspace, 0, 256, st) != cudaSuccess ||
+            (dW && cudaMemsetAsync(dW, 0, static_cast<size_t>(V) * d * 2, st) != cudaSuccess))
+            return SB_ERR_CUDA;
+        return SB_OK;
+    }
+    const int pairs = sms / 2;
+    const Plan pl = plan_of(M, d, V, piece, dH != nullptr, dW != nullptr, pairs);
+    if (workspace_bytes < pl.total) return SB_ERR_WORKSPACE_TOO_SMALL;
+
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    LossGradParams p{};
+    p.M = static_cast<int>(M);
+    p.d = static_cast<int>(d);
+    p.V = static_cast<int>(V);
+    p.ldg = static_cast<int>(pl.ldg);
+    p.row_tiles = static_cast<int>((M + 255) / 256);
+    p.d_tiles = static_cast<int>((d + 255) / 256);
+    p.splits = pl.splits;
+    p.reduction = reduction;
+    p.ignore_index = ignore_index;
+    p.z_loss = z_loss;
+    p.targets = targets;
+    p.lse = lse;
+    p.grad = grad;
+    p.G = reinterpret_cast<uint16_t *>(ws + pl.g_off);
+    p.H = static_cast<const uint16_t *>(H);
+    p.part = reinterpret_cast<float *>(ws + pl.part_off);
+    p.scale = reinterpret_cast<float *>(ws + 16);
+    p.dH = static_cast<uint16_t *>(dH);
+    p.dW = static_cast<uint16_t *>(dW);
+    p.epoch_word = reinterpret_cast<uint32_t *>(ws);
+    p.status = reinterpret_cast<unsigned long long *>(ws + 8);
+    p.epoch = next_epoch();
+    p.timeout_ns = wait_limit_ns();
+    p.debug_stall = debug_stall();
+    const int64_t most = (pl.piece + 255) / 256 * p.d_tiles +
+                         static_cast<int64_t>(p.row_tiles) * p.d_tiles * p.splits;
+    if (most >= (int64_t(1) << 31) ||
+        (pl.piece + 255) / 256 * p.row_tiles >= (int64_t(1) << 31))
+        return SB_ERR_INVALID_ARG;
+
+    uint16_t *copy = dW ? reinterpret_cast<uint16_t *>(ws + pl.h_off) : nullptr;
+    CUtensorMap tmH, tmC, tmW, tmG;
+    if (!encode_bf16_map(&tmH, H, M, d, 64) || !encode_bf16_map(&tmW, W, V, d, 64) ||
+        !encode_bf16_map(&tmC, copy ? copy : H, M, d, 64))
+        return SB_ERR_CUDA;
+    int64_t mapped = 0;
+    for (int64_t c0 = 0; c0 < V; c0 += pl.piece) {
+        const int64_t cols = V - c0 < pl.piece ? V - c0 : pl.piece;
+        // the map ends at the piece's last column: what lies past it reads as zero
+        if (mapped != cols && !encode_bf16_map(&tmG, p.G, M, cols, 64, pl.ldg)) return SB_ERR_CUDA;
+        mapped = cols;
+        p.c0 = static_cast<int>(c0);
+        p.cols = static_cast<int>(cols);
+        p.first = c0 == 0;
+        p.Hc = p.first ? copy : nullptr;
+        p.last = c0 + cols == V;
+        p.col_tiles = static_cast<int>((cols + 255) / 256);
+        const Work w = work_of(M, d, cols, dH != nullptr, dW != nullptr);
+        p.dh_units = static_cast<int>(w.longs * pl.splits);
+        p.dw_units = static_cast<int>(w.shorts);
+        p.fill = static_cast<int>(((w.long_blocks + pl.splits - 1) / pl.splits) / w.short_blocks);
+        if (launch_loss_logits(tmH, tmW, p, sms, st) != cudaSuccess ||
+            launch_loss_operands(tmG, tmW, tmC, p, sms, st) != cudaSuccess)
+            return SB_ERR_CUDA;
+    }
+    if (dH && pl.splits > 1 &&
+        launch_loss_sum(p.part, dH, static_cast<size_t>(M) * d, pl.splits, p.scale, st) !=
+            cudaSuccess)
+        return SB_ERR_CUDA;
+    return SB_OK;
+}
+
+}  // extern "C"

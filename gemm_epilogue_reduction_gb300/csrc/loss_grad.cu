@@ -1,0 +1,642 @@
+// loss_grad.cu -- the gradient of the output head's cross entropy, in pieces of the
+// vocabulary, without keeping logits.
+//
+// With z = H·Wᵀ, lse_r = log sum_j exp(z_rj), t_r the target of row r, g_r the gradient of the
+// loss in row r's loss and l = z_loss weight, row r's loss is lse_r - z_rt + l·lse_r², so
+//   G_rj = dL/dz_rj = g_r·((1 + 2·l·lse_r)·exp(z_rj - lse_r) - [j = t_r]),
+//   dH = G·W,   dW = Gᵀ·H,
+// three products of 2·M·d·V operations (the logits are formed again from H and W).  Rows whose
+// target is the ignored index have G = 0.  For each piece of `cols` vocabulary columns:
+//   logits_kernel    z tile by tile as in the forward pass, and G in bf16 straight out of TMEM
+//                    into the piece buffer [M][cols];
+//                    the piece buffer [M][cols]; with the first piece also a copy of H whose
+//                    ignored rows are zero, so that what those rows hold (an infinity, a NaN)
+//                    does not meet the zeros of G in dW;
+//   operands_kernel  one launch for both products that read G: the dH tiles (reduction over
+//                    the piece's columns) and the dW tiles (reduction over the rows);
+// and, when the dH reduction was split, sum_kernel adds the splits in ascending order.
+//
+// G is held in bf16, the type of the tensor cores' operands here: a relative error of 2^-8 at
+// most per entry (rms 2^-9), independent from entry to entry, so that a sum over many of them loses less
+// than the rounding of dH and dW to bf16 does.  For that the scale that all rows share (the
+// incoming gradient, 1/count, or the largest |g|) stays out of G and is applied in fp32 in the
+// epilogue: rounding it into G would shift every entry the same way.  Accumulation is fp32 in
+// TMEM and, over the pieces, fp32 in memory.
+//
+// Both kernels: persistent CTA pairs, one cta_group::2 MMA of 256 x 256 per 16-wide K step
+// (tcgen05, bf16 x bf16 -> fp32), joint TMA stages, two TMEM accumulators, eight epilogue
+// warps; bounded waits as in sb_pipe.cuh.  Operands whose reduction index is the outer one in
+// memory (W in dH = G·W; G and H in dW = Gᵀ·H) are staged in boxes of 64 contiguous elements x
+// 64 reduction rows and read by the MMA "MN-major", so that nothing is transposed.
+#include <atomic>
+#include <cuda_bf16.h>
+
+#include "sb_internal.h"
+#include "sb_pipe.cuh"
+#include "sb_ptx.cuh"
+
+namespace sb {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTile = 256;                       // rows and columns of a pair's tile
+constexpr int kBox = 64;                         // rows of a TMA box (64 elements = 128 bytes)
+constexpr uint32_t kBoxBytes = kBox * 128;       // 8 KB
+constexpr uint32_t kAtomBytes = 2 * kBoxBytes;   // one operand, one CTA, 64 of the reduction
+constexpr uint32_t kRingBytes = 192 * 1024;
+constexpr uint32_t kGradSmem = kRingBytes + 1024 /* barriers and scalars */ + 1024 /* align */;
+
+// ATOMS 64-wide slices of the reduction per stage: 2 halves the waits and commits per
+// operation, 1 gives six stages instead of three.
+template <int ATOMS>
+struct Ring {
+    static constexpr uint32_t kOperand = ATOMS * kAtomBytes;
+    static constexpr uint32_t kStage = 2 * kOperand;  // A, then B
+    static constexpr int kStages = kRingBytes / kStage;
+};
+
+// Shared-memory matrix descriptor of an MN-major bf16 operand: blocks of 64 contiguous M (or
+// N) elements (128 bytes, 128-byte swizzle) x 64 reduction rows, as a 64 x 64 TMA box leaves
+// them.  Leading byte offset: from one block of 64 elements to the next (8 KB); stride byte
+// offset: from 8 reduction rows to the next 8 (1024 bytes).  A 16-wide K step adds 2048 bytes.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(kBoxBytes >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+constexpr uint32_t kIdescAMajorMN = 1u << 15, kIdescBMajorMN = 1u << 16;
+
+// One 256 x 256 tile of work.  a_x, a_y (b_x, b_y): box coordinates of this CTA's half of the
+// operand at reduction index 0; a_mn: the operand is MN-major, i.e. x is the tile's row and y
+// the reduction index (otherwise the other way round).
+struct Unit {
+    bool dw;             // operands_kernel: a tile of dW (otherwise of dH)
+    int row0, col0;      // of the output, this CTA's rows
+    int split;
+    int k0, kblocks;     // first reduction index and blocks of ATOMS * 64
+};
+
+template <bool LOGITS, int ATOMS>
+__device__ __forceinline__ bool unit_at(const LossGradParams &p, int pair, int pairs, int rank,
+                                        int i, Unit &u) {
+    constexpr int KB = ATOMS * kBlockK;
+    u.split = 0;
+    u.k0 = 0;
+    if (LOGITS) {
+        const int tile = pair + i * pairs;
+        if (tile >= p.row_tiles * p.col_tiles) return false;
+        u.dw = false;
+        // neighbouring pairs share a tile of W
+        u.col0 = (tile / p.row_tiles) * kTile;
+        u.row0 = (tile % p.row_tiles) * kTile + rank * kTileA;
+        u.kblocks = (p.d + KB - 1) / KB;
+        return true;
+    }
+    // The dH tiles, which are long (the piece's columns), come first, dealt out in turn; the
+    // short dW tiles then even out the pairs: those that are one dH tile behind the others
+    // take `fill` dW tiles each before the rest is dealt out in turn.
+    const int longs = p.dh_units, rem = longs % pairs, own = longs / pairs + (pair < rem ? 1 : 0);
+    if (i < own) {
+        const int t = pair + i * pairs;
+        const int per = p.row_tiles * p.d_tiles;
+        u.dw = false;
+        u.split = t / per;
+        const int q = t - u.split * per;
+        u.row0 = (q / p.d_tiles) * kTile + rank * kTileA;
+        u.col0 = (q % p.d_tiles) * kTile;
+        const int blocks = (p.cols + KB - 1) / KB;
+        const int b0 = static_cast<int>(static_cast<long long>(blocks) * u.split / p.splits);
+        const int b1 = static_cast<int>(static_cast<long long>(blocks) * (u.split + 1) / p.splits);
+        u.k0 = b0 * KB;
+        u.kblocks = b1 - b0;
+        return true;
+    }
+    int j = i - own;
+    const int shorts = p.dw_units;
+    int t;
+    if (rem == 0) {
+        t = j * pairs + pair;
+    } else {
+        const int behind = pairs - rem;
+        if (pair >= rem) {
+            if (j < p.fill) {
+                t = j * behind + (pair - rem);
+                if (t >= shorts) return false;
+            } else {
+                j -= p.fill;
+                t = behind * p.fill + j * pairs + (pair - rem);
+            }
+        } else {
+            t = behind * p.fill + j * pairs + behind + pair;
+        }
+    }
+    if (t >= shorts) return false;
+    u.dw = true;
+    u.row0 = (t / p.d_tiles) * kTile + rank * kTileA;
+    u.col0 = (t % p.d_tiles) * kTile;
+    u.kblocks = (p.M + KB - 1) / KB;
+    return true;
+}
+
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool epi_any(bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(pred))
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Stores 32 consecutive bf16 values, of which the first n (a multiple of 8, at most 32) count.
+__device__ __forceinline__ void store_bf16_row(uint16_t *dst, const float (&v)[32], int n) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+    if (n == 32 && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+        st_global_v8(dst, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
+        st_global_v8(dst + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
+    } else {
+        uint4 *d4 = reinterpret_cast<uint4 *>(dst);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (8 * j < n)
+                d4[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+    }
+}
+
+// The scale that all rows share, by all 256 epilogue threads (e = 0..255); red: 16 words of
+// shared memory.  SUM: the incoming gradient; MEAN: that over the count of rows that are not
+// ignored (at least 1); NONE: the largest |g_r| of those rows.
+__device__ __forceinline__ float shared_scale(const LossGradParams &p, int e, float *red) {
+    const float up = (p.reduction != 0 && p.grad) ? __ldg(p.grad) : 1.f;
+    if (p.reduction == 1 || (p.reduction == 0 && !p.grad)) return up;
+    float best = 0.f;
+    int count = 0;
+    for (int r = e; r < p.M; r += 256)
+        if (__ldg(p.targets + r) != p.ignore_index) {
+            ++count;
+            if (p.reduction == 0) best = fmaxf(best, fabsf(__ldg(p.grad + r)));
+        }
+    count = __reduce_add_sync(0xFFFFFFFFu, count);
+    // |g| >= 0: its bits order like the values
+    best = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(best)));
+    if ((e & 31) == 0) {
+        red[e >> 5] = best;
+        reinterpret_cast<int *>(red)[8 + (e >> 5)] = count;
+    }
+    epi_sync();
+    count = 0;
+    best = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        best = fmaxf(best, red[w]);
+        count += reinterpret_cast<int *>(red)[8 + w];
+    }
+    return p.reduction == 2 ? up / static_cast<float>(count > 0 ? count : 1) : best;
+}
+
+// ------------------------------------------------------------------ epilogues
+// Thread (quadrant q, half h, lane) owns output row row0 + 32q + lane and 128 of the tile's
+// 256 columns, in chunks of 32; the accumulator is released once its last chunk is read.
+template <typename F>
+__device__ __forceinline__ void for_chunks(uint32_t taddr, int h, int lane, uint64_t *tempty,
+                                           uint32_t tempty_remote, F f) {
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+        uint32_t raw[32];
+        tmem_ld32x32b_x32(taddr + 128 * h + 32 * ch, raw);
+        if (ch == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (tempty_remote)
+                    mbar_arrive_remote(tempty_remote);
+                else
+                    mbar_arrive(tempty);
+            }
+        }
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+        f(128 * h + 32 * ch, v);
+    }
+}
+
+__device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const Unit &u,
+                                                uint32_t taddr, uint64_t *tempty,
+                                                uint32_t tempty_remote, int q, int h, int lane,
+                                                float scale) {
+    const int row = u.row0 + 32 * q + lane;
+    const bool rv = row < p.M;
+    float a = 0.f, b = 0.f, l2 = 0.f;
+    int tgt = -1;
+    if (rv) {
+        const int t = __ldg(p.targets + row);
+        if (t != p.ignore_index) {
+            const float lse = __ldg(p.lse + row);
+            // NONE: the row's own weight relative to the shared scale
+            b = (p.reduction == 0 && p.grad) ? (scale > 0.f ? __ldg(p.grad + row) / scale : 0.f)
+                                             : 1.f;
+            a = b * (1.f + 2.f * p.z_loss * lse);
+            l2 = lse * kLog2e;
+            // the target's column in this tile (a target outside the vocabulary has none)
+            if (t >= 0 && t < p.V) tgt = t - p.c0 - u.col0;
+        }
+    }
+    for_chunks(taddr, h, lane, tempty, tempty_remote, [&](int c, float (&v)[32]) {
+        if (!rv || u.col0 + c >= p.cols) return;
+        if (b == 0.f && a == 0.f) {  // ignored (a finite logit times 0 would do as well)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float e = a * ex2_approx(fmaf(v[j], kLog2e, -l2));
+                v[j] = c + j == tgt ? e - b : e;
+            }
+        }
+        // the piece buffer's rows are padded to 64 columns, so a whole chunk always fits;
+        // columns past the piece's last one are never read
+        store_bf16_row(p.G + static_cast<size_t>(row) * p.ldg + u.col0 + c, v, 32);
+    });
+}
+
+__device__ __forceinline__ void epilogue_operands(const LossGradParams &p, const Unit &u,
+                                                  uint32_t taddr, uint64_t *tempty,
+                                                  uint32_t tempty_remote, int q, int h, int lane,
+                                                  float scale) {
+    const int row = u.row0 + 32 * q + lane;
+    const bool rv = row < (u.dw ? p.cols : p.M);
+    // dH: fp32 partial sums in memory unless this piece is the only one and not split
+    const bool through = !u.dw && (p.splits > 1 || !(p.first && p.last));
+    const bool out = u.dw || (p.splits == 1 && p.last);
+    uint16_t *dst = u.dw ? p.dW + (static_cast<size_t>(p.c0) + row) * p.d
+                         : p.dH + static_cast<size_t>(row) * p.d;
+    float *part = p.part + (static_cast<size_t>(u.split) * p.M + row) * p.d;
+    for_chunks(taddr, h, lane, tempty, tempty_remote, [&](int c, float (&v)[32]) {
+        const int col = u.col0 + c;
+        const int n = min(32, p.d - col);
+        if (!rv || n <= 0) return;
+        if (u.kblocks == 0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        }
+        if (through && !p.first) {
+            const float4 *src = reinterpret_cast<const float4 *>(part + col);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (4 * j < n) {
+                    const float4 x = src[j];
+                    v[4 * j] += x.x;
+                    v[4 * j + 1] += x.y;
+                    v[4 * j + 2] += x.z;
+                    v[4 * j + 3] += x.w;
+                }
+        }
+        if (out) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= scale;
+            store_bf16_row(dst + col, v, n);
+        } else {
+            float4 *to = reinterpret_cast<float4 *>(part + col);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (4 * j < n) to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+    });
+}
+
+// ------------------------------------------------------------------ the kernel
+// LOGITS: tmX = H, tmY = W (both K-major: x is the reduction index).  Otherwise tmX = the piece
+// of G, tmY = W, tmZ = the copy of H.
+template <bool LOGITS, int ATOMS>
+__global__ void __launch_bounds__(kThreads, 1)
+    grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY,
+                const __grid_constant__ CUtensorMap tmZ, const LossGradParams p) {
+    using R = Ring<ATOMS>;
+    constexpr int KB = ATOMS * kBlockK;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRingBytes);
+    uint64_t *empty = full + R::kStages;
+    uint64_t *tfull = empty + R::kStages;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *drain = tempty + 2;
+    uint64_t *stall = drain + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kRingBytes + 512);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kRingBytes + 516);
+    float *red = reinterpret_cast<float *>(smem + kRingBytes + 528);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const WaitCtx wc{p.status, p.epoch, p.timeout_ns, abort_flag};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < R::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 2 * kEpiWarps);  // the epilogue warps of both CTAs
+        }
+        mbar_init(drain, 1);
+        mbar_init(stall, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmY);
+        if (!LOGITS) tma_prefetch_desc(&tmZ);
+    }
+    if (warp == 1) {
+        tmem_alloc2(tmem_slot, 512);
+        tmem_relinquish2();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer's barriers are initialised before any copy lands
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    // Everything read from here on may have been written by the kernel before (G, the partial
+    // sums, and W by an optimizer step), so all of it waits; the next kernel may then set up.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (LOGITS && blockIdx.x == 0 && threadIdx.x == 0) *p.epoch_word = p.epoch;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer.  The leader's full
+        // barrier counts every copy of the pair; its one commit per stage frees the stage in
+        // both CTAs.
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_normal();
+            int st = 0;
+            uint32_t ph = 0, issued = 0;
+            bool ok = true;
+            Unit u;
+            for (int i = 0; ok && unit_at<LOGITS, ATOMS>(p, pair, pairs, rank, i, u); ++i) {
+                const int bn = u.col0 + rank * kTileA;  // this CTA's half of the B operand
+                for (int kb = 0; kb < u.kblocks; ++kb) {
+                    if (!bwait_cluster(&empty[st], ph ^ 1u, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * R::kStage);
+                    uint8_t *sa = smem + st * R::kStage, *sbuf = sa + R::kOperand;
+                    // the leader's barrier at its cluster address, for both CTAs
+                    const uint32_t bar = mapa_rank(&full[st], 0);
+#pragma unroll
+                    for (int at = 0; at < ATOMS; ++at) {
+                        const int k = u.k0 + kb * KB + at * kBlockK;  // past the end: zeros
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            uint8_t *da = sa + at * kAtomBytes + b * kBoxBytes;
+                            uint8_t *db = sbuf + at * kAtomBytes + b * kBoxBytes;
+                            const int o = b * kBox;
+                            if (LOGITS) {
+                                tma_load_2d_pair(da, &tmX, bar, k, u.row0 + o, pol);
+                                tma_load_2d_pair(db, &tmY, bar, k, p.c0 + bn + o, pol);
+                            } else if (u.dw) {
+                                tma_load_2d_pair(da, &tmX, bar, u.row0 + o, k, pol);
+                                tma_load_2d_pair(db, &tmZ, bar, bn + o, k, pol);
+                            } else {
+                                tma_load_2d_pair(da, &tmX, bar, k, u.row0 + o, pol);
+                                tma_load_2d_pair(db, &tmY, bar, bn + o, p.c0 + k, pol);
+                            }
+                        }
+                    }
+                    ++issued;
+                    if (++st == R::kStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (rank == 0) {
+                // every copy that the barriers count has landed before this CTA exits
+                const uint32_t n = issued < R::kStages ? issued : R::kStages;
+                for (uint32_t i = issued - n; i < issued; ++i)
+                    if (!bwait_drain(&full[i % R::kStages], (i / R::kStages) & 1u, wc)) break;
+            } else if (!ok) {
+                // the peer's copies complete on the leader's barriers: after an abort it gives
+                // the last ones (issued at least one wait limit ago) a bounded time to land
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 50000u) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (the pair's leader)
+        if (rank == 0 && lane == 0) {
+            constexpr uint16_t kBoth = 3;
+            const uint32_t s0 = smem_u32(smem);
+            const uint64_t k_desc = sw128_kmajor_desc(s0), mn_desc = sw128_mnmajor_desc(s0);
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true, any = false;
+            Unit u;
+            for (int i = 0; ok && unit_at<LOGITS, ATOMS>(p, pair, pairs, rank, i, u); ++i) {
+                const int b = i & 1;
+                const uint32_t tph = (i >> 1) & 1;
+                if (!bwait_cluster(&tempty[b], tph ^ 1u, wc)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kTile);
+                const bool a_mn = !LOGITS && u.dw, b_mn = !LOGITS;
+                const uint32_t idesc = idesc_bf16_f32(2 * kTileA, kTile) |
+                                       (a_mn ? kIdescAMajorMN : 0u) | (b_mn ? kIdescBMajorMN : 0u);
+                const uint64_t ad0 = a_mn ? mn_desc : k_desc;
+                const uint64_t bd0 = (b_mn ? mn_desc : k_desc) + (R::kOperand >> 4);
+                const uint32_t a_step = a_mn ? 2048u >> 4 : 32u >> 4;
+                const uint32_t b_step = b_mn ? 2048u >> 4 : 32u >> 4;
+                for (int kb = 0; kb < u.kblocks; ++kb) {
+                    if (!bwait_cluster(&full[st], ph, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t so = (static_cast<uint32_t>(st) * R::kStage) >> 4;
+#pragma unroll
+                    for (int at = 0; at < ATOMS; ++at)
+#pragma unroll
+                        for (int ks = 0; ks < kBlockK / 16; ++ks)
+                            umma_bf16_pair(d_tmem, ad0 + so + at * (kAtomBytes >> 4) + ks * a_step,
+                                           bd0 + so + at * (kAtomBytes >> 4) + ks * b_step, idesc,
+                                           (kb | at | ks) != 0 ? 1u : 0u);
+                    umma_commit_pair(&empty[st], kBoth);
+                    any = true;
+                    if (++st == R::kStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (ok) umma_commit_pair(&tfull[b], kBoth);
+                any = true;
+            }
+            if (any) {  // until every MMA this thread issued has completed
+                umma_commit_pair(drain, 1);
+                bwait_drain(drain, 0, wc);
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------ the copy of H for dW (first piece)
+        if (LOGITS && p.Hc) {
+            const int n16 = p.d / 8;
+            for (int r = blockIdx.x; r < p.M; r += gridDim.x) {
+                const bool keep = __ldg(p.targets + r) != p.ignore_index;
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.H + static_cast<size_t>(r) * p.d);
+                uint4 *dst = reinterpret_cast<uint4 *>(p.Hc + static_cast<size_t>(r) * p.d);
+#pragma unroll 4
+                for (int i = lane; i < n16; i += 32)
+                    dst[i] = keep ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue warps
+        const int q = warp & 3;                     // TMEM lane quadrant this warp may read
+        const int h = (warp - kFirstEpiWarp) >> 2;  // which half of the columns
+        float scale;
+        if (LOGITS) {
+            scale = shared_scale(p, threadIdx.x - 32 * kFirstEpiWarp, red);
+            if (blockIdx.x == 0 && threadIdx.x == 32 * kFirstEpiWarp) *p.scale = scale;
+        } else {
+            scale = *p.scale;
+        }
+        Unit u;
+        for (int i = 0; unit_at<LOGITS, ATOMS>(p, pair, pairs, rank, i, u); ++i) {
+            const int b = i & 1;
+            const uint32_t tph = (i >> 1) & 1;
+            const bool ok = p.debug_stall ? bwait(stall, 0, wc) : bwait_cluster(&tfull[b], tph, wc);
+            if (epi_any(!ok)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                   static_cast<uint32_t>(b * kTile);
+            const uint32_t remote = rank == 1 ? mapa_rank(&tempty[b], 0) : 0u;
+            if (LOGITS)
+                epilogue_logits(p, u, taddr, &tempty[b], remote, q, h, lane, scale);
+            else
+                epilogue_operands(p, u, taddr, &tempty[b], remote, q, h, lane, scale);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // nothing of the peer's lands here after this CTA has left
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc2(tmem_base, 512);
+    }
+}
+
+// dH = scale * (split 0 + split 1 + ...), four values per thread.
+__global__ void __launch_bounds__(256) sum_kernel(const float4 *part, uint2 *dH, size_t n4,
+                                                  int splits, const float *scale) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= n4) return;
+    const float f = *scale;
+    float4 a = part[i];
+    for (int s = 1; s < splits; ++s) {
+        const float4 x = part[s * n4 + i];
+        a.x += x.x;
+        a.y += x.y;
+        a.z += x.z;
+        a.w += x.w;
+    }
+    dH[i] = make_uint2(pack_bf16(f * a.x, f * a.y), pack_bf16(f * a.z, f * a.w));
+}
+
+template <bool LOGITS, int ATOMS>
+cudaError_t launch_grad(const CUtensorMap &x, const CUtensorMap &y, const CUtensorMap &z,
+                        const LossGradParams &p, int units, int num_sms, cudaStream_t stream) {
+    auto kern = grad_kernel<LOGITS, ATOMS>;
+    static std::atomic<uint64_t> opted_in{0};
+    static std::atomic<int> pairs_by_dev[64];  // co-resident pairs (GPCs may not pair every SM)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+    if (!bit || !(opted_in.load() & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+        if (e != cudaSuccess) return e;
+        opted_in.fetch_or(bit);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kGradSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    int pairs = dev < 64 ? pairs_by_dev[dev].load() : 0;
+    if (pairs <= 0) {
+        cfg.gridDim = dim3(num_sms / 2 * 2);
+        if (cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg) != cudaSuccess || pairs <= 0 ||
+            pairs > num_sms / 2)
+            pairs = num_sms / 2;
+        if (dev < 64) pairs_by_dev[dev].store(pairs);
+    }
+    if (pairs > units) pairs = units;
+    if (pairs < 1) pairs = 1;
+    cfg.gridDim = dim3(2 * pairs);
+    return cudaLaunchKernelEx(&cfg, kern, x, y, z, p);
+}
+
+}  // namespace
+
+cudaError_t launch_loss_logits(const CUtensorMap &h, const CUtensorMap &w, const LossGradParams &p,
+                               int num_sms, cudaStream_t stream) {
+    const int units = p.row_tiles * p.col_tiles;
+    // one 64-wide slice per stage when a single pair of row tiles reads each W tile (the W
+    // stream sets the pace and wants more stages), two otherwise
+    return p.row_tiles < 2 ? launch_grad<true, 1>(h, w, w, p, units, num_sms, stream)
+                           : launch_grad<true, 2>(h, w, w, p, units, num_sms, stream);
+}
+
+cudaError_t launch_loss_operands(const CUtensorMap &g, const CUtensorMap &w, const CUtensorMap &h,
+                                 const LossGradParams &p, int num_sms, cudaStream_t stream) {
+    const int units = p.dh_units + p.dw_units;
+    return p.row_tiles < 2 ? launch_grad<false, 1>(g, w, h, p, units, num_sms, stream)
+                           : launch_grad<false, 2>(g, w, h, p, units, num_sms, stream);
+}
+
+cudaError_t launch_loss_sum(const float *part, void *dH, size_t n, int splits, const float *scale,
+                            cudaStream_t stream) {
+    const size_t n4 = n / 4;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((n4 + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sum_kernel, reinterpret_cast<const float4 *>(part),
+                              static_cast<uint2 *>(dH), n4, splits, scale);
+}
+
+}  // namespace sb

@@ -110,7 +110,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 // device state, so reusing one for the same pointer and shape is exact).
 struct MapCacheEntry {
     const void *base;
-    int64_t rows, d;
+    int64_t rows, d, ld;
     int box_rows;
     int packed_k;  // 0: a 2-D map over a row-major matrix; k: the 4-D map of a packed W
     CUtensorMap map;
@@ -121,13 +121,15 @@ std::mutex g_map_mu;
 MapCacheEntry g_map_cache[kMapCache];
 int g_map_next = 0;
 
-// 2-D map over a row-major bf16 matrix [rows, d]: boxes of 64 x box_rows, 128-byte swizzle,
-// out-of-range elements read as zero.
-bool make_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t d, int box_rows) {
+// 2-D map over a row-major bf16 matrix [rows, d], its rows ld elements apart (0: d): boxes of
+// 64 x box_rows, 128-byte swizzle, out-of-range elements read as zero.
+bool make_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t d, int box_rows,
+              int64_t ld = 0) {
+    if (ld == 0) ld = d;
     {
         std::lock_guard<std::mutex> lock(g_map_mu);
         for (const auto &e : g_map_cache)
-            if (e.used && e.base == base && e.rows == rows && e.d == d &&
+            if (e.used && e.base == base && e.rows == rows && e.d == d && e.ld == ld &&
                 e.box_rows == box_rows && e.packed_k == 0) {
                 *tm = e.map;
                 return true;
@@ -136,7 +138,7 @@ bool make_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t d, int bo
     auto enc = encoder();
     if (!enc) return false;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(d) * 2};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(kBlockK), static_cast<cuuint32_t>(box_rows)};
     cuuint32_t es[2] = {1, 1};
     if (enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
@@ -144,7 +146,7 @@ bool make_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t d, int bo
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;
     std::lock_guard<std::mutex> lock(g_map_mu);
-    g_map_cache[g_map_next] = MapCacheEntry{base, rows, d, box_rows, 0, *tm, true};
+    g_map_cache[g_map_next] = MapCacheEntry{base, rows, d, ld, box_rows, 0, *tm, true};
     g_map_next = (g_map_next + 1) % kMapCache;
     return true;
 }
@@ -184,7 +186,7 @@ bool make_packed_map(CUtensorMap *tm, const void *base, int64_t V, int64_t d, in
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;
     std::lock_guard<std::mutex> lock(g_map_mu);
-    g_map_cache[g_map_next] = MapCacheEntry{base, V, d, kTileA, k, *tm, true};
+    g_map_cache[g_map_next] = MapCacheEntry{base, V, d, d, kTileA, k, *tm, true};
     g_map_next = (g_map_next + 1) % kMapCache;
     return true;
 }
@@ -277,8 +279,8 @@ CombineParams combine_params(const sb_outputs *out, const Workspace &w, int64_t 
 
 namespace sb {
 bool encode_bf16_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t cols,
-                     int box_rows) {
-    return make_map(tm, base, rows, cols, box_rows);
+                     int box_rows, int64_t ld) {
+    return make_map(tm, base, rows, cols, box_rows, ld);
 }
 int32_t device_sms_cc(int *sms, int *cc) {
     DevInfo dev;
@@ -289,6 +291,7 @@ int32_t device_sms_cc(int *sms, int *cc) {
 }
 uint32_t next_epoch() { return g_epoch.fetch_add(1) + 1; }
 unsigned long long wait_limit_ns() { return g_timeout_ns.load(); }
+int32_t debug_stall() { return g_debug_stall.load(); }
 }  // namespace sb
 
 extern "C" {
@@ -414,6 +417,7 @@ int32_t prepare(const void *H, const void *W, int64_t M, int64_t d, int64_t V, i
     p.ws = ws_views(out->workspace, L, gumbel, K);
     p.timeout_ns = g_timeout_ns.load();
     p.debug_stall = g_debug_stall.load();
+    p.early = 1;
 
     // rows mode: each CTA of a cluster loads 256 / cluster rows of the shared W tile; with a
     // packed W every W box (128 rows, 64 columns) is one 16 KB block of the packed layout
@@ -453,6 +457,27 @@ int32_t enqueue(const void *H, const void *W, int64_t M, int64_t d, int64_t V, i
 }
 
 }  // namespace
+
+namespace sb {
+int32_t enqueue_target_records(const void *H, const void *W, const int32_t *targets, int64_t M,
+                               int64_t d, int64_t V, int32_t ignore_index, void *workspace,
+                               size_t workspace_bytes, Workspace *ws, cudaStream_t stream) {
+    sb_outputs out{};
+    // the records call writes neither of these two; they only have to be there
+    out.token = static_cast<int32_t *>(workspace);
+    out.target_logprob = static_cast<float *>(workspace);
+    out.target_ids = targets;
+    out.workspace = workspace;
+    out.workspace_bytes = workspace_bytes;
+    Prepared pr;
+    if (int32_t e = prepare(H, W, M, d, V, 1, SB_TOKEN, 1.f, 0, &out, &pr)) return e;
+    pr.p.has_ignore = 1;
+    pr.p.ignore_index = ignore_index;
+    pr.p.early = 0;
+    *ws = pr.p.ws;
+    return launch(pr, stream, false);
+}
+}  // namespace sb
 
 extern "C" {
 

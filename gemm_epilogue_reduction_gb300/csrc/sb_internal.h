@@ -50,7 +50,7 @@ enum : int { kEpiPlain = 0, kEpiFull = 1, kEpiGumbel = 2, kEpiTopk = 3, kEpiTopk
              kEpiTopk4 = 5 };
 
 struct Workspace {       // device views into the caller's workspace
-    uint32_t *epoch;     // header word 0
+    uint32_t *epoch;     // header word 0; word 1, zeroed by the GEMM, counts finished rows (loss.cu)
     unsigned long long *status;  // header word 1: (epoch << 32) | code
     float *m;
     int32_t *idx;
@@ -89,6 +89,50 @@ struct GemmParams {
     uint32_t epoch;
     unsigned long long timeout_ns;
     int debug_stall;
+    int has_ignore;        // targets equal to `ignore_index` are no error (their tz is unwritten)
+    int ignore_index;
+    int early;             // host: launch as a programmatic dependent (W loads start early)
+};
+
+// One piece of the cross-entropy gradient (loss_grad.cu).
+struct LossGradParams {
+    int M, d, V;
+    int c0, cols;          // the piece: columns [c0, c0 + cols) of the vocabulary
+    int ldg;               // row pitch of the piece buffer G, in elements
+    int first, last;       // of the pieces
+    int row_tiles, col_tiles, d_tiles;  // 256-wide tiles of M, cols and d
+    int splits;            // of the reduction over the piece's columns in dH
+    int dh_units, dw_units, fill;       // operands_kernel's tiles and how they are dealt out
+    int reduction;         // sb_reduction
+    int ignore_index;
+    float z_loss;
+    const int32_t *targets;
+    const float *lse;
+    const float *grad;     // [M] (NONE) or [1]; null: 1
+    uint16_t *G;           // [M][ldg] bf16
+    const uint16_t *H;
+    uint16_t *Hc;          // [M][d]: H with its ignored rows zero; null: not to be written
+    float *scale;          // written by the logits kernel, read by the others
+    float *part;           // [splits][M][d] fp32 partial sums of dH
+    uint16_t *dH, *dW;
+    uint32_t *epoch_word;
+    unsigned long long *status;
+    uint32_t epoch;
+    unsigned long long timeout_ns;
+    int debug_stall;
+};
+
+// The rows' losses from the projection records (loss.cu).
+struct LossParams {
+    int M, T, V;
+    int reduction;
+    int ignore_index;
+    float z_loss;
+    Workspace ws;
+    const int32_t *targets;
+    float *rows;           // [M] losses (the output for NONE, scratch otherwise)
+    float *loss;           // [1] (SUM, MEAN)
+    float *lse;            // [M]
 };
 
 struct CombineParams {
@@ -125,12 +169,29 @@ cudaError_t launch_merge_payload(const CombineParams &c, const void *payload,
 cudaError_t launch_copy16(void *dst, const void *src, size_t n16, int num_sms,
                           cudaStream_t stream);
 
+cudaError_t launch_loss_rows(const LossParams &p, cudaStream_t stream);
+cudaError_t launch_loss_logits(const CUtensorMap &h, const CUtensorMap &w, const LossGradParams &p,
+                               int num_sms, cudaStream_t stream);
+cudaError_t launch_loss_operands(const CUtensorMap &g, const CUtensorMap &w, const CUtensorMap &h,
+                                 const LossGradParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_loss_sum(const float *part, void *dH, size_t n, int splits, const float *scale,
+                            cudaStream_t stream);
+
 size_t lmhead_smem_bytes(int nb, int stages_a, int stages_b, bool vocab_mode, int flags,
                          int topk, int atoms);
 
 // Host helpers shared by the entry points (sb_api.cu).
+// (ld: elements from row to row, 0: cols)
 bool encode_bf16_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t cols,
-                     int box_rows);
+                     int box_rows, int64_t ld = 0);
+// The records of sb_lmhead_records (SB_TOKEN, k = 1) and the targets' logits; a target equal to
+// ignore_index is no error and leaves its logit unwritten.  Enqueued without loading W early:
+// the kernel before may write it.  The workspace is that of sb_workspace_bytes(M, V, 1,
+// SB_TOKEN); *ws receives its views.
+int32_t enqueue_target_records(const void *H, const void *W, const int32_t *targets, int64_t M,
+                               int64_t d, int64_t V, int32_t ignore_index, void *workspace,
+                               size_t workspace_bytes, Workspace *ws, cudaStream_t stream);
+int32_t debug_stall();
 int32_t device_sms_cc(int *sms, int *cc);  // SB_OK, SB_ERR_CUDA or SB_ERR_UNSUPPORTED
 uint32_t next_epoch();
 unsigned long long wait_limit_ns();

@@ -121,7 +121,7 @@ typedef struct sb_outputs {
 /*
  * Workspace layout (byte offsets from `workspace`; n = M * k * T with T =
  * sb_tiles_per_shard(M, V, k); each array starts on a 256-byte boundary, in this order):
- *   [0, 256)      header: uint32 epoch of the last launch, uint32 reserved,
+ *   [0, 256)      header: uint32 epoch of the last launch, uint32 (internal use),
  *                 uint64 status word = (epoch << 32) | sb_status of that launch
  *   float   m[n]     per-tile record: max of y over the tile's columns
  *   int32   idx[n]   lowest global column attaining m
@@ -411,6 +411,74 @@ int32_t sb_select_source_projection(double bytes_ref, double bytes_proj, double 
                                     double frames_proj, double link_bytes_per_s,
                                     double frame_startup_s, double local_proj_s,
                                     double local_ref_s, double *margin_s);
+
+/*
+ * Training the head: the cross entropy of the rows' targets and its gradients (no paper
+ * counterpart; the logits are those of sb_lmhead_project, and like there no logits are kept).
+ *   lse_r  = log sum_j exp(z_rj),   z = H·Wᵀ
+ *   loss_r = lse_r - z_r,target(r) + z_loss * lse_r^2
+ * and 0, without a gradient, for rows whose target equals ignore_index (their row of dH is 0,
+ * and they add nothing to dW, whatever their row of H holds).
+ */
+typedef enum sb_reduction {
+    SB_REDUCE_NONE = 0, /* every row's own loss, [M]                                     */
+    SB_REDUCE_SUM = 1,  /* their sum, [1]                                                */
+    SB_REDUCE_MEAN = 2  /* the sum over the count of rows not ignored (0 where none is)  */
+} sb_reduction;
+
+/* Bytes of workspace of the forward call; 0 if the arguments are invalid. */
+size_t sb_cross_entropy_workspace_bytes(int64_t M, int64_t d, int64_t V);
+
+/*
+ * The losses: the record GEMM of sb_lmhead_records, then one kernel over the records.
+ *   H, W, M, d, V   as for sb_lmhead_project (row-major W); M = 0 is allowed (a batch without
+ *               tokens: the sum and the mean are 0), and H, targets and lse may then be NULL.
+ *   targets     device int32 [M]: in [0, V), or ignore_index (any value, also one inside the
+ *               vocabulary, which then never counts as a target).  Another value gives the
+ *               row's loss as NaN, and sb_last_device_status reports SB_ERR_INVALID_ARG.
+ *   reduction   an sb_reduction;  z_loss: finite.
+ *   loss        device float [M] (SB_REDUCE_NONE) or [1].
+ *   lse         device float [M]: every row's logsumexp, also the ignored ones'; the backward
+ *               call reads it.
+ *   workspace   device, 256-byte aligned, >= sb_cross_entropy_workspace_bytes(M, d, V); no
+ *               initialisation.  Its header is read by sb_last_device_status.
+ * Two kernels on `stream`.  W may be written by the kernel before (an optimizer step): unlike
+ * sb_lmhead_project, this call loads nothing before that kernel has finished.
+ */
+int32_t sb_cross_entropy_forward(const void *H, const void *W, const int32_t *targets, int64_t M,
+                                 int64_t d, int64_t V, int32_t ignore_index, int32_t reduction,
+                                 float z_loss, float *loss, float *lse, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of the backward call, which depend on the SM count of the current device
+ * (the dH reduction may be split over the SMs): 0 for invalid arguments or without a device.
+ * with_dH, with_dW: whether that gradient is asked for (at least one). */
+size_t sb_cross_entropy_backward_workspace_bytes(int64_t M, int64_t d, int64_t V, int64_t piece,
+                                                 int32_t with_dH, int32_t with_dW);
+
+/*
+ * The gradients, in pieces of the vocabulary: for each piece the logits are formed again and
+ * G = dL/dz of the piece is written in bf16 to the workspace, then dH += G·W and dW = Gᵀ·H in
+ * one launch.  Accumulation is fp32; dH and dW are rounded to bf16 once.  Every sum has a
+ * fixed order, so equal calls give equal bits.
+ *   H, W, targets, M, d, V, ignore_index, reduction, z_loss   as in the forward call.
+ *   lse         device float [M], from the forward call.
+ *   grad        device float: the incoming gradient, [M] for SB_REDUCE_NONE, else [1]; NULL
+ *               stands for ones.  Read on the device when the kernels run.
+ *   piece       vocabulary columns per piece, rounded up to a multiple of 256; 0 leaves the
+ *               choice to the library (at most 256 MB for the piece of G).
+ *   dH, dW      device bf16 [M, d] and [V, d], 16-byte aligned, overwritten; either may be NULL
+ *               (a frozen head, or a first layer), and its product is then not formed.
+ *   workspace   device, 256-byte aligned, of at least
+ *               sb_cross_entropy_backward_workspace_bytes(M, d, V, piece, dH, dW) bytes.
+ * A target outside [0, V) that is not ignore_index contributes no "- 1" term; the forward call
+ * reports it.  M = 0 writes dW = 0.
+ */
+int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *targets,
+                                  const float *lse, const float *grad, int64_t M, int64_t d,
+                                  int64_t V, int32_t ignore_index, int32_t reduction,
+                                  float z_loss, int64_t piece, void *dH, void *dW,
+                                  void *workspace, size_t workspace_bytes, void *stream);
 
 /* Device status of the last call that used out->workspace: SB_OK, SB_ERR_DEVICE_TIMEOUT
  * (a bounded wait gave up) or SB_ERR_INVALID_ARG (a scoring target outside [0, V); when
