@@ -21,6 +21,8 @@ SURFACES = {"token": SB_TOKEN, "token_logprob": SB_TOKEN_LOGPROB,
             "full_logits": SB_FULL_LOGITS, "gumbel_token": SB_GUMBEL_TOKEN,
             "topk_logprob": SB_TOPK_LOGPROB}
 SB_REDUCE_NONE, SB_REDUCE_SUM, SB_REDUCE_MEAN = 0, 1, 2
+SB_BF16, SB_F32 = 0, 1
+SB_GATE_NONE, SB_GATE_CHANNEL, SB_GATE_TOKEN = 0, 1, 2
 REDUCTIONS = {"none": SB_REDUCE_NONE, "sum": SB_REDUCE_SUM, "mean": SB_REDUCE_MEAN}
 SB_OK = 0
 SB_ERR_INVALID_ARG = 1
@@ -49,6 +51,15 @@ class sb_outputs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
                 ("topk_ids", ctypes.c_void_p), ("topk_logprob", ctypes.c_void_p),
                 ("topk", ctypes.c_int32)]
+
+
+class sb_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("scale_sq", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_double), ("param_type", ctypes.c_int32),
+                ("grad_type", ctypes.c_int32)]
 
 
 def lib():
@@ -120,6 +131,16 @@ def lib():
         L.sb_cross_entropy_backward.argtypes = [P, P, P, P, P, i64, i64, i64, i32, i32,
                                                 ctypes.c_float, i64, P, P, P, ctypes.c_size_t, P]
         L.sb_cross_entropy_backward.restype = i32
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        L.sb_residual_norm_forward.argtypes = [P] * 5 + [i32, i64, i64, i32, i32, f32, f32, P, P, P]
+        L.sb_residual_norm_forward.restype = i32
+        L.sb_residual_norm_workspace_bytes.argtypes = [i64] * 2
+        L.sb_residual_norm_workspace_bytes.restype = ctypes.c_size_t
+        L.sb_residual_norm_backward.argtypes = ([P] * 7 + [i32, i64, i64, i32, i32, f32, f32] +
+                                                [P] * 6 + [ctypes.c_size_t, P])
+        L.sb_residual_norm_backward.restype = i32
+        L.sb_adamw_step.argtypes = [P, i64, f64, f64, f64, f64, i64, i32, P, P]
+        L.sb_adamw_step.restype = i32
         L.sb_select_source_projection.argtypes = [ctypes.c_double] * 8 + [
             ctypes.POINTER(ctypes.c_double)]
         L.sb_select_source_projection.restype = i32
@@ -341,6 +362,34 @@ def sb_cross_entropy_backward(H, W, targets, lse, grad, M, d, V, ignore_index, r
                                                float(z_loss), piece, _ptr(dH), _ptr(dW),
                                                _ptr(workspace), int(workspace_bytes),
                                                _stream(stream)))
+
+
+def sb_residual_norm_forward(h, y, pre, post, gate, gate_kind, M, d, stream_type, weight_type,
+                             scale, eps, h_out, x, stream=None) -> int:
+    return int(lib().sb_residual_norm_forward(_ptr(h), _ptr(y), _ptr(pre), _ptr(post), _ptr(gate),
+                                              gate_kind, M, d, stream_type, weight_type,
+                                              float(scale), float(eps), _ptr(h_out), _ptr(x),
+                                              _stream(stream)))
+
+
+def sb_residual_norm_workspace_bytes(M: int, d: int) -> int:
+    return int(lib().sb_residual_norm_workspace_bytes(M, d))
+
+
+def sb_residual_norm_backward(dx, dh, h, y, pre, post, gate, gate_kind, M, d, stream_type,
+                              weight_type, scale, eps, dh_out, dy, dpre, dpost, dgate, workspace,
+                              workspace_bytes, stream=None) -> int:
+    return int(lib().sb_residual_norm_backward(
+        _ptr(dx), _ptr(dh), _ptr(h), _ptr(y), _ptr(pre), _ptr(post), _ptr(gate), gate_kind, M, d,
+        stream_type, weight_type, float(scale), float(eps), _ptr(dh_out), _ptr(dy), _ptr(dpre),
+        _ptr(dpost), _ptr(dgate), _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def sb_adamw_step(tensors, count, lr, beta1, beta2, eps, step, state_bits, grad_scale=None,
+                  stream=None) -> int:
+    """tensors: a ctypes array of sb_adamw_tensor (or None for count 0)."""
+    return int(lib().sb_adamw_step(tensors, count, lr, beta1, beta2, eps, step, state_bits,
+                                   _ptr(grad_scale), _stream(stream)))
 
 
 def sb_select_source_projection(bytes_ref, bytes_proj, frames_ref, frames_proj,
@@ -593,3 +642,166 @@ def device_status(workspace) -> int:
     """``sb_last_device_status`` of a workspace tensor (synchronises)."""
     return sb_last_device_status(sb_outputs(workspace=_ptr(workspace),
                                             workspace_bytes=workspace.numel()))
+
+
+def _norm_problem(h, y, pre, post, gate, where):
+    """Checks the arguments both directions share; returns (M, d, gate kind, types, device)."""
+    import torch
+    dev = _device(where)
+    if h.dim() != 2:
+        raise ValueError(f"{where}: h is [M, d]")
+    both = (torch.bfloat16, torch.float32)
+    M, d = h.shape
+    _tensor("h", h, (M, d), both, dev, where)
+    _tensor("y", y, (M, d), (torch.bfloat16,), dev, where)
+    _tensor("pre", pre, (d,), both, dev, where)
+    if post is not None:
+        _tensor("post", post, (d,), (pre.dtype,), dev, where)
+    kind = SB_GATE_NONE
+    if gate is not None:
+        kind = SB_GATE_CHANNEL if gate.dim() == 1 else SB_GATE_TOKEN
+        if kind == SB_GATE_CHANNEL:
+            _tensor("gate", gate, (d,), (pre.dtype,), dev, where)
+        else:
+            _tensor("gate", gate, (M, d), (torch.bfloat16,), dev, where)
+    types = [SB_F32 if t.dtype == torch.float32 else SB_BF16 for t in (h, pre)]
+    return M, d, kind, types, dev
+
+
+def residual_norm(h, y, pre, *, post=None, gate=None, scale: float = 1.0, eps: float = 1e-6,
+                  stream=None):
+    """The end of a block: h' = scale h + gate n(y; post) and x = n(h'; pre), with
+    n(x; w) = w x / sqrt(mean(x²) + eps) over the last axis.
+
+    h [M, d] bf16 or float32 (the residual stream), y [M, d] bf16 (the block's output), pre and
+    post [d] of one type, bf16 or float32 (post None: no norm of y), gate [d] of that type,
+    [M, d] bf16, or None. Returns a dict: h (h', of h's type) and x (bf16: what the next block,
+    or ``project`` and ``cross_entropy``, read). Asynchronous on ``stream``."""
+    import torch
+    M, d, kind, types, dev = _norm_problem(h, y, pre, post, gate, "residual_norm")
+    with _on_stream(stream):
+        h_out, x = torch.empty_like(h), torch.empty_like(y)
+        st = sb_residual_norm_forward(h, y, pre, post, gate, kind, M, d, *types, scale, eps, h_out,
+                                      x, stream)
+    if st != SB_OK:
+        raise SbError(st, "sb_residual_norm_forward")
+    return {"h": h_out, "x": x}
+
+
+def residual_norm_backward(dx, dh, h, y, pre, *, post=None, gate=None, scale: float = 1.0,
+                           eps: float = 1e-6, stream=None, workspace=None):
+    """The gradients of ``residual_norm``: dx [M, d] bf16 is the gradient of its x, dh that of
+    its h' (None: nothing else reads h'), ``h`` the h' that it returned; the rest as there.
+    Returns a dict: dh (the gradient of the incoming stream), dy, dpre, dpost, dgate (None where
+    there is no such input) and workspace. The weights' gradients have the weights' type."""
+    import torch
+    where = "residual_norm_backward"
+    M, d, kind, types, dev = _norm_problem(h, y, pre, post, gate, where)
+    _tensor("dx", dx, (M, d), (torch.bfloat16,), dev, where)
+    if dh is not None:
+        _tensor("dh", dh, (M, d), (h.dtype,), dev, where)
+    with _on_stream(stream):
+        workspace = _workspace(sb_residual_norm_workspace_bytes(M, d), workspace, dev, where)
+        out = {"dh": torch.empty_like(h), "dy": torch.empty_like(y), "dpre": torch.empty_like(pre),
+               "dpost": None if post is None else torch.empty_like(post),
+               "dgate": None if gate is None else torch.empty_like(gate)}
+        st = sb_residual_norm_backward(dx, dh, h, y, pre, post, gate, kind, M, d, *types, scale,
+                                       eps, out["dh"], out["dy"], out["dpre"], out["dpost"],
+                                       out["dgate"], workspace, workspace.numel(), stream)
+    if st != SB_OK:
+        raise SbError(st, "sb_residual_norm_backward")
+    out["workspace"] = workspace
+    return out
+
+
+class AdamW:
+    """AdamW over a list of tensors, updated in place by one kernel launch per step
+    (``sb_adamw_step``; its formulas and formats are described in sb.h).
+
+    params: contiguous CUDA tensors, bf16 or float32, of any shape. grads: one for each, of the
+    same shape, bf16 or float32; they are read by every ``step`` (give new ones to ``step`` when
+    they move). masters: float32 copies of bf16 parameters (a list with None where a parameter
+    has none, or None for none at all). state_bits: 32, or 8 for E4M3 codes in blocks of 256
+    values. states: existing moments, a tuple for each parameter, ``(m, v)`` float32 or
+    ``(m, root, m_scale, root_scale)`` with float8_e4m3fn codes; None starts from zeros.
+    weight_decay: one number, or one for each parameter. step: steps already taken."""
+
+    def __init__(self, params, grads=None, *, lr: float = 1e-3, betas=(0.9, 0.999),
+                 eps: float = 1e-8, weight_decay=0.01, state_bits: int = 32, masters=None,
+                 states=None, step: int = 0):
+        import torch
+        where = "AdamW"
+        if state_bits not in (8, 32):
+            raise ValueError(f"{where}: state_bits is 8 or 32, not {state_bits!r}")
+        self.params = list(params)
+        n = len(self.params)
+        self.lr, self.betas, self.eps = lr, tuple(betas), eps
+        self.state_bits, self.step_count = state_bits, step
+        self.masters = [None] * n if masters is None else list(masters)
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        self.states = [None] * n if states is None else [tuple(s) for s in states]
+        for name, x in (("masters", self.masters), ("weight_decay", decay), ("states", self.states)):
+            if len(x) != n:
+                raise ValueError(f"{where}: {len(x)} {name} for {n} parameters")
+        self._device = _device(where)
+        both, f32 = (torch.bfloat16, torch.float32), (torch.float32,)
+        self._list = (sb_adamw_tensor * n)()
+        for i, p in enumerate(self.params):
+            _tensor(f"params[{i}]", p, p.shape, both, self._device, where)
+            w = self.masters[i]
+            if w is not None:
+                if p.dtype != torch.bfloat16:
+                    raise TypeError(f"{where}: params[{i}] is float32 and has no master")
+                _tensor(f"masters[{i}]", w, p.shape, f32, self._device, where)
+            k = p.numel()
+            blocks = (k + 255) // 256
+            kinds = ([(k, torch.float8_e4m3fn)] * 2 + [(blocks, torch.float32)] * 2
+                     if state_bits == 8 else [(k, torch.float32)] * 2)
+            if self.states[i] is None:
+                self.states[i] = tuple(torch.zeros(c, dtype=t, device=self._device)
+                                       for c, t in kinds)
+            if len(self.states[i]) != len(kinds):
+                raise ValueError(f"{where}: states[{i}] has {len(self.states[i])} tensors, "
+                                 f"not {len(kinds)}")
+            for j, (s, (c, t)) in enumerate(zip(self.states[i], kinds)):
+                if s.numel() != c:
+                    raise ValueError(f"{where}: states[{i}][{j}] has {s.numel()} values, not {c}")
+                _tensor(f"states[{i}][{j}]", s, s.shape, (t,), self._device, where)
+            scales = self.states[i][2:] or (None, None)
+            self._list[i] = sb_adamw_tensor(
+                _ptr(p), None, _ptr(w), _ptr(self.states[i][0]), _ptr(self.states[i][1]),
+                _ptr(scales[0]), _ptr(scales[1]), k, float(decay[i]),
+                SB_F32 if p.dtype == torch.float32 else SB_BF16, SB_BF16)
+        self.grads = None
+        if grads is not None:
+            self._bind(grads)
+
+    def _bind(self, grads):
+        import torch
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"AdamW: {len(grads)} gradients for {len(self.params)} parameters")
+        for i, (g, p, t) in enumerate(zip(grads, self.params, self._list)):
+            _tensor(f"grads[{i}]", g, p.shape, (torch.bfloat16, torch.float32), self._device,
+                    "AdamW")
+            t.grad = g.data_ptr()
+            t.grad_type = SB_F32 if g.dtype == torch.float32 else SB_BF16
+        self.grads = grads
+
+    def step(self, grads=None, *, grad_scale=None, lr=None, stream=None) -> None:
+        """One step, asynchronous on ``stream``: ``grads`` replaces the gradients bound so far,
+        ``grad_scale`` (float32 [1] on the device) multiplies them, ``lr`` replaces the rate."""
+        if grads is not None:
+            self._bind(grads)
+        if self.grads is None and self.params:
+            raise ValueError("AdamW: no gradients have been given")
+        if grad_scale is not None:
+            import torch
+            _tensor("grad_scale", grad_scale, (1,), (torch.float32,), self._device, "AdamW")
+        if lr is not None:
+            self.lr = lr
+        st = sb_adamw_step(self._list, len(self.params), self.lr, self.betas[0], self.betas[1],
+                           self.eps, self.step_count + 1, self.state_bits, grad_scale, stream)
+        if st != SB_OK:
+            raise SbError(st, "sb_adamw_step")
+        self.step_count += 1

@@ -480,6 +480,107 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
                                   float z_loss, int64_t piece, void *dH, void *dW,
                                   void *workspace, size_t workspace_bytes, void *stream);
 
+/* Storage type of an array that may be bf16 or fp32. */
+typedef enum sb_type { SB_BF16 = 0, SB_F32 = 1 } sb_type;
+
+/* The gate of sb_residual_norm_*. */
+typedef enum sb_gate {
+    SB_GATE_NONE = 0,    /* factor 1                                                     */
+    SB_GATE_CHANNEL = 1, /* one vector [d] for all rows, of the weights' type            */
+    SB_GATE_TOKEN = 2    /* bf16 [M, d], one value per row and channel                   */
+} sb_gate;
+
+/*
+ * The end of a transformer block, and what the output head reads after the last one (no paper
+ * counterpart).  With n(x; w) = w * x / sqrt(mean(x^2) + eps) over a row:
+ *   h_out = scale * h + gate * n(y; post),     x = n(h_out; pre).
+ *   h           device [M, d] of stream_type (an sb_type): the residual stream.
+ *   y           device bf16 [M, d]: the block's output.
+ *   pre         device [d] of weight_type (an sb_type): the next block's (or the head's) norm.
+ *   post        device [d] of weight_type, or NULL: no norm after the block, n(y; post) is y.
+ *   gate        as gate_kind (an sb_gate) says; ignored for SB_GATE_NONE.
+ *   M, d        M >= 0 rows; 1 <= d <= 16384.  Every array is contiguous; 16-byte aligned
+ *               arrays with d a multiple of 8 (or 4) are read in wide loads, others value by
+ *               value.
+ *   scale, eps  finite; eps >= 0 (a row of zeros with eps = 0 gives NaN).
+ *   h_out       device [M, d] of stream_type; may be h itself.
+ *   x           device bf16 [M, d]; may be y itself.  Formed from h_out before its rounding.
+ * One kernel on `stream`; no workspace.
+ */
+int32_t sb_residual_norm_forward(const void *h, const void *y, const void *pre, const void *post,
+                                 const void *gate, int32_t gate_kind, int64_t M, int64_t d,
+                                 int32_t stream_type, int32_t weight_type, float scale, float eps,
+                                 void *h_out, void *x, void *stream);
+
+/* Bytes of workspace of the backward call, which depend on the SM count of the current device;
+ * 0 for invalid arguments or without a device. */
+size_t sb_residual_norm_workspace_bytes(int64_t M, int64_t d);
+
+/*
+ * Its gradients.  h is here the forward call's h_out as it was stored; y, pre, post, gate,
+ * gate_kind, the types, scale and eps as there.
+ *   dx          device bf16 [M, d]: the gradient of x.
+ *   dh          device [M, d] of stream_type: the gradient of h_out from its other readers, or
+ *               NULL where there is none (the last block).
+ *   dh_out      device [M, d] of stream_type: the gradient of the forward call's h; may be dh.
+ *   dy          device bf16 [M, d]; may be dx.
+ *   dpre, dpost device [d] of weight_type (dpost only with post), summed over the rows in fp32
+ *               in a fixed order: equal calls give equal bits.
+ *   dgate       like gate (NULL for SB_GATE_NONE); summed over the rows for SB_GATE_CHANNEL.
+ *   workspace   device, 16-byte aligned, >= sb_residual_norm_workspace_bytes(M, d); no
+ *               initialisation.
+ * Two kernels on `stream`.  M = 0 writes zeros to dpre, dpost and the gate vector's gradient.
+ */
+int32_t sb_residual_norm_backward(const void *dx, const void *dh, const void *h, const void *y,
+                                  const void *pre, const void *post, const void *gate,
+                                  int32_t gate_kind, int64_t M, int64_t d, int32_t stream_type,
+                                  int32_t weight_type, float scale, float eps, void *dh_out,
+                                  void *dy, void *dpre, void *dpost, void *dgate, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/*
+ * An AdamW step over many tensors at once (no paper counterpart).  Per value, with g the
+ * gradient times *grad_scale and t the step:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   w = (1 - lr weight_decay) w - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps),
+ * all in fp32, each operation rounded by itself.  w is `master` where there is one (then param
+ * receives its rounding to bf16), else param.  The moments are held
+ *   state_bits = 32: in fp32;
+ *   state_bits = 8: as E4M3 codes (the 8-bit floating-point type with 4 exponent and 3 mantissa
+ *     bits, largest value 448) in blocks of 256 consecutive values with one fp32 scale each (the
+ *     largest magnitude / 448; a block whose largest is below 2^-100 is stored as zeros).
+ *     exp_avg_sq then holds sqrt(v), whose range of exponents is half of v's, and a root that is
+ *     not zero is never stored as zero, so that no small v turns into a division by eps alone.
+ *     The step itself uses m and v before they are stored.
+ */
+typedef struct sb_adamw_tensor {
+    void *param;        /* device [n] of param_type                                          */
+    const void *grad;   /* device [n] of grad_type                                           */
+    float *master;      /* device fp32 [n], for a bf16 param; NULL: param is the weight      */
+    void *exp_avg;      /* device [n]: fp32, or E4M3 codes (one byte each)                   */
+    void *exp_avg_sq;   /* device [n]: fp32, or E4M3 codes of the root                       */
+    float *scale;       /* state_bits = 8: device fp32 [ceil(n / 256)], of exp_avg           */
+    float *scale_sq;    /* state_bits = 8: device fp32 [ceil(n / 256)], of exp_avg_sq        */
+    int64_t n;          /* values; 0 is allowed (the tensor is skipped)                      */
+    double weight_decay;
+    int32_t param_type, grad_type; /* sb_type                                                */
+} sb_adamw_tensor;
+
+/*
+ *   tensors     host array of `count` (>= 0) descriptors, read during the call.  Arrays of
+ *               different tensors must not overlap.  Tensors whose arrays are all 16-byte
+ *               aligned are read in wide loads, others value by value.
+ *   lr          >= 0; 0 <= beta1, beta2 < 1; eps >= 0; weight_decay >= 0; all finite.
+ *   step        t, >= 1.
+ *   grad_scale  device float [1] (an inverse loss scale, a clipping factor), read when the
+ *               kernels run; NULL: 1.
+ * One kernel per 384 tensors on `stream`; no workspace.  The kernel does not let its successor
+ * start early, so a projection that follows may load the new weight at once.
+ */
+int32_t sb_adamw_step(const sb_adamw_tensor *tensors, int64_t count, double lr, double beta1,
+                      double beta2, double eps, int64_t step, int32_t state_bits,
+                      const float *grad_scale, void *stream);
+
 /* Device status of the last call that used out->workspace: SB_OK, SB_ERR_DEVICE_TIMEOUT
  * (a bounded wait gave up) or SB_ERR_INVALID_ARG (a scoring target outside [0, V); when
  * both happen the timeout is reported).  Synchronous: copies the header to the host (call

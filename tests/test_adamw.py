@@ -1,0 +1,310 @@
+"""The AdamW step over many tensors.
+
+The kernel rounds every fp32 operation by itself, in the order of the formulas, so the same
+formulas in elementary torch operations on the same device give the same bits: values and codes
+are compared for equality. Against the 64-bit definition: ten fp32 roundings between input and
+output, so |m|, |v| and the update are within 16·2^-24 of the magnitudes they are sums of, a
+rounding to bf16 adds 2^-8 and one to E4M3 2^-4 of the value plus the spacing of its smallest
+numbers (2^-10 of a code), relative to the block's scale.
+"""
+import math
+
+import pytest
+import torch
+
+import gemm_epilogue_reduction_gb300 as sb
+
+gpu = pytest.mark.gpu
+BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+E = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gemm_epilogue_reduction_gb300 import build as sbbuild
+    sbbuild.build()
+
+
+def _pad(x):
+    out = torch.zeros(-(-x.numel() // 256) * 256, dtype=x.dtype, device=x.device)
+    out[:x.numel()] = x.reshape(-1)
+    return out
+
+
+def _codes(x, root):
+    """E4M3 codes and scales of a block format tensor, as sb.h describes them."""
+    b = _pad(x).view(-1, 256)
+    top = b.abs().amax(1)
+    small = top < 2.0 ** -100
+    mul = torch.where(small, 0.0, 448.0 / torch.where(small, 1.0, top))
+    q = b * mul[:, None]
+    if root:
+        q = torch.where((q > 0) & (q < 2.0 ** -9), 2.0 ** -9, q)
+    return q.to(F8).view(-1)[:x.numel()], torch.where(small, 0.0, top * (1 / 448.0))
+
+
+def _values(codes, scale):
+    return (_pad(codes.float()).view(-1, 256) * scale[:, None]).view(-1)[:codes.numel()]
+
+
+def _make(sizes, *, param=BF, master=True, grad=BF, bits=32, seed=0, offset=0):
+    """Parameters, gradients, masters and states (offset: values into an allocation)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def place(v):
+        room = torch.zeros(v.numel() + offset, dtype=v.dtype, device="cuda")
+        room[offset:].view(torch.uint8 if v.dtype == F8 else v.dtype).copy_(
+            v.view(torch.uint8) if v.dtype == F8 else v)
+        return room[offset:]
+
+    p, gr, ma, st = [], [], [], []
+    for k in sizes:
+        w = 0.02 * torch.randn(k, generator=g, device="cuda")
+        p.append(place(w.to(param)))
+        ma.append(place(w) if master and param == BF else None)
+        gr.append(place((1e-3 * torch.randn(k, generator=g, device="cuda")).to(grad)))
+        m = 1e-3 * torch.randn(k, generator=g, device="cuda")
+        r = 1e-3 * torch.randn(k, generator=g, device="cuda").abs()
+        if bits == 8:
+            (a, sa), (b, sb_) = _codes(m, False), _codes(r, True)
+            st.append((place(a), place(b), sa, sb_))
+        else:
+            st.append((place(m), place(r * r)))
+    return p, gr, ma, st
+
+
+def _step(p, g, w, state, *, lr, b1, b2, eps, wd, t, gs, bits):
+    """One tensor's step in elementary operations; returns (param, master or None, state)."""
+    x = (p if w is None else w).float()
+    g = g.float() if gs is None else g.float() * gs
+    m, v = (state if bits == 32 else (_values(state[0], state[2]), _values(state[1], state[3])))
+    if bits == 8:
+        v = v * v
+    m = m * b1 + g * (1 - b1)
+    v = v * b2 + g * g * (1 - b2)
+    root = v.sqrt()
+    upd = m / (root * (1 / math.sqrt(1 - b2 ** t)) + eps)
+    x = x * (1 - lr * wd) - upd * (lr / (1 - b1 ** t))
+    if bits == 32:
+        state = (m, v)
+    else:
+        (a, sa), (b, sb_) = _codes(m, False), _codes(root, True)
+        state = (a, b, sa, sb_)
+    return x.to(p.dtype), (None if w is None else x), state
+
+
+def _equal(a, b, name):
+    if a.dtype == F8:
+        a, b = a.view(torch.uint8), b.view(torch.uint8)
+    assert torch.equal(a, b), (name, int((a != b).sum()), a.numel())
+
+
+HYPER = {"lr": 1e-2, "b1": 0.9, "b2": 0.95, "eps": 1e-8}
+
+
+def _compare(sizes, *, bits, steps=3, gs=None, wd=0.1, start=0, offset=0, **kw):
+    p, g, w, st = _make(sizes, bits=bits, offset=offset, **kw)
+    q = [(a.clone(), None if b is None else b.clone(), tuple(x.clone() for x in s))
+         for a, b, s in zip(p, w, st)]
+    opt = sb.AdamW(p, g, lr=HYPER["lr"], betas=(HYPER["b1"], HYPER["b2"]), eps=HYPER["eps"],
+                   weight_decay=wd, state_bits=bits, masters=w, states=st, step=start)
+    decay = wd if isinstance(wd, list) else [wd] * len(sizes)
+    for t in range(start + 1, start + steps + 1):
+        opt.step(grad_scale=gs)
+        q = [_step(a, gr, b, s, t=t, wd=d, gs=gs, bits=bits, **HYPER)
+             for (a, b, s), gr, d in zip(q, g, decay)]
+    torch.cuda.synchronize()
+    assert opt.step_count == start + steps
+    for i, (a, b, s) in enumerate(q):
+        _equal(p[i], a, f"param {i}")
+        if b is not None:
+            _equal(w[i], b, f"master {i}")
+        for j, (x, y) in enumerate(zip(st[i], s)):
+            _equal(x, y, f"state {i}.{j}")
+
+
+SIZES = [1, 255, 256, 257, 0, 7, 2048, 2049, 5120, 4096 * 33 + 5]
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("param,master,grad", [(BF, True, BF), (BF, False, BF), (F32, False, F32),
+                                               (BF, True, F32), (F32, False, BF)])
+def test_steps_give_the_formulas_bits(bits, param, master, grad):
+    _compare(SIZES, bits=bits, param=param, master=master, grad=grad)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_grad_scale_late_steps_and_a_decay_for_each(bits):
+    gs = torch.tensor([0.37], device="cuda")
+    _compare([300, 512, 1000], bits=bits, gs=gs, wd=[0.0, 0.5, 0.01], start=12345)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_arrays_off_the_wide_alignment(bits):
+    _compare([300, 512, 4097], bits=bits, offset=1)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_more_tensors_than_one_launch_takes(bits):
+    _compare([(37 * i) % 700 for i in range(800)], bits=bits, steps=2)
+
+
+@gpu
+def test_mixed_types_in_one_list():
+    a = _make([500], param=BF, grad=F32, seed=1)
+    b = _make([600], param=F32, grad=BF, seed=2)
+    p, g, w, st = (x + y for x, y in zip(a, b))
+    want = [_step(p[i].clone(), g[i], None if w[i] is None else w[i].clone(), st[i], t=1, wd=0.1,
+                  gs=None, bits=32, **HYPER) for i in range(2)]
+    sb.AdamW(p, g, lr=HYPER["lr"], betas=(HYPER["b1"], HYPER["b2"]), eps=HYPER["eps"],
+             weight_decay=0.1, masters=w, states=st).step()
+    for i in range(2):
+        _equal(p[i], want[i][0], f"param {i}")
+
+
+@gpu
+def test_against_the_definition_in_64_bits():
+    n, t = 70000, 5
+    for bits in (32, 8):
+        p, g, w, st = _make([n], bits=bits, seed=3)
+        w0, g0 = w[0].double(), g[0].double()
+        if bits == 8:
+            m, v = _values(st[0][0], st[0][2]).double(), _values(st[0][1], st[0][3]).double() ** 2
+        else:
+            m, v = st[0][0].double(), st[0][1].double()
+        sb.AdamW(p, g, lr=1e-2, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, state_bits=bits,
+                 masters=w, states=st, step=t - 1).step()
+        m, mm = 0.9 * m + 0.1 * g0, 0.9 * m.abs() + 0.1 * g0.abs()
+        v = 0.95 * v + 0.05 * g0 ** 2
+        den = (v / (1 - 0.95 ** t)).sqrt() + 1e-8
+        rate = 1e-2 / (1 - 0.9 ** t)
+        x = w0 * (1 - 1e-3) - rate * m / den
+        off = (w[0].double() - x).abs()
+        assert (off <= 16 * E * (w0.abs() + rate * mm / den)).all()
+        assert ((p[0].double() - x).abs() <= off + 2.0 ** -8 * x.abs()).all()
+        if bits == 32:
+            assert ((st[0][0].double() - m).abs() <= 16 * E * mm).all()
+            assert ((st[0][1].double() - v).abs() <= 16 * E * v).all()
+        else:
+            for code, scale, value in ((st[0][0], st[0][2], m), (st[0][1], st[0][3], v.sqrt())):
+                s = scale.double().repeat_interleave(256)[:n]
+                held = _values(code, scale).double()
+                assert ((held - value).abs() <= 2.0 ** -4 * value.abs() + 2.0 ** -9 * s).all()
+
+
+@gpu
+def test_blocks_of_zeros_tiny_and_huge_values():
+    """8 bits: an all-zero block, one whose magnitudes span the whole format, one below 2^-100
+    and one with a single large gradient; roots that are there stay above zero."""
+    n = 256 * 5
+    p, g, w, st = _make([n], bits=8, param=F32, grad=F32, seed=4)
+    m, r = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    g[0][:256] = 0
+    m[256:512] = torch.logspace(-12, 3, 256, device="cuda")
+    r[256:512] = torch.logspace(-9, 2, 256, device="cuda")
+    g[0][512:768] = 1e-32
+    g[0][768:1024] = 0
+    g[0][800] = 1e4
+    (a, sa), (b, sb_) = _codes(m, False), _codes(r, True)
+    st = [(a, b, sa, sb_)]
+    q = _step(p[0].clone(), g[0], None, st[0], t=1, wd=0.1, gs=None, bits=8, **HYPER)
+    sb.AdamW(p, g, lr=HYPER["lr"], betas=(HYPER["b1"], HYPER["b2"]), eps=HYPER["eps"],
+             weight_decay=0.1, state_bits=8, states=st).step()
+    _equal(p[0], q[0], "param")
+    for x, y in zip(st[0], q[2]):
+        _equal(x, y, "state")
+    assert torch.isfinite(p[0]).all()
+    assert (_values(st[0][1], st[0][3])[256:512] > 0).all()
+
+
+@gpu
+def test_a_nan_gradient_stays_where_it_is():
+    for bits in (32, 8):
+        p, g, w, st = _make([1024], bits=bits, seed=5)
+        g[0][700] = float("nan")
+        sb.AdamW(p, g, masters=w, states=st, state_bits=bits).step()
+        bad = torch.isnan(p[0])
+        assert bad[700] and int(bad.sum()) == 1
+
+
+@gpu
+def test_new_gradients_streams_and_graphs():
+    for bits in (32, 8):
+        p, g, w, st = _make([3000, 77], bits=bits, seed=6)
+        p2, _, w2, st2 = _make([3000, 77], bits=bits, seed=6)
+        opt = sb.AdamW(p, masters=w, states=st, state_bits=bits)
+        with pytest.raises(ValueError):
+            opt.step()
+        opt.step(g)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        opt.step([2 * x for x in g], lr=0.5, stream=side)  # made and used on two streams:
+        torch.cuda.synchronize()                           # kept alive by the handle until here
+        ref = sb.AdamW(p2, [x.clone() for x in g], masters=w2, states=st2, state_bits=bits)
+        ref.step()
+        ref.step([2 * x for x in g], lr=0.5)
+        for a, b in zip(p + w, p2 + w2):
+            _equal(a, b, "after two steps")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):  # the step number is the captured one
+            opt.step(g)
+        graph.replay()
+        ref.step(g)
+        torch.cuda.synchronize()
+        for a, b in zip(p + w, p2 + w2):
+            _equal(a, b, "after a replay")
+
+
+@gpu
+def test_python_refusals():
+    p, g, w, st = _make([64, 65])
+    with pytest.raises(ValueError):
+        sb.AdamW(p, g, state_bits=16)
+    with pytest.raises(ValueError):
+        sb.AdamW(p, g[:1])
+    with pytest.raises(ValueError):
+        sb.AdamW(p, [g[0], g[0]])
+    with pytest.raises(TypeError):
+        sb.AdamW([x.half() for x in p], g)
+    with pytest.raises(TypeError):
+        sb.AdamW([x.float() for x in p], g, masters=w)
+    with pytest.raises(ValueError):
+        sb.AdamW([torch.zeros(8, 8, device="cuda").t()[1:]], None)
+    with pytest.raises(ValueError):
+        sb.AdamW(p, g, states=[s[:1] for s in st])
+    with pytest.raises(ValueError):
+        sb.AdamW(p, g, weight_decay=[0.1])
+    opt = sb.AdamW(p, g, lr=-1.0)
+    with pytest.raises(sb.SbError):
+        opt.step()
+    with pytest.raises(TypeError):
+        sb.AdamW(p, g).step(grad_scale=torch.ones(1, device="cuda", dtype=torch.float64))
+    with pytest.raises(ValueError):
+        sb.AdamW([x.cpu() for x in p], g)
+
+
+def test_c_refusals():
+    P = 1 << 20
+
+    def call(count=1, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, step=1, bits=32, gs=None, lst=True, **kw):
+        f = {"param": P, "grad": P, "master": None, "exp_avg": P, "exp_avg_sq": P, "scale": P,
+             "scale_sq": P, "n": 4, "weight_decay": 0.0, "param_type": 0, "grad_type": 0, **kw}
+        arr = (sb.sb_adamw_tensor * 1)(sb.sb_adamw_tensor(**f))
+        return sb.sb_adamw_step(arr if lst else None, count, lr, b1, b2, eps, step, bits, gs, 0)
+
+    bad, off, nan = sb.SB_ERR_INVALID_ARG, sb.SB_ERR_ALIGNMENT, float("nan")
+    for kw in ({"count": -1}, {"lst": False}, {"lr": -1.0}, {"lr": nan}, {"lr": float("inf")},
+               {"b1": 1.0}, {"b1": -0.1}, {"b2": nan}, {"eps": -1e-8}, {"eps": nan}, {"step": 0},
+               {"bits": 16}, {"param": None}, {"grad": None}, {"exp_avg": None},
+               {"exp_avg_sq": None}, {"bits": 8, "scale": None}, {"bits": 8, "scale_sq": None},
+               {"n": -1}, {"param_type": 2}, {"grad_type": -1}, {"weight_decay": -0.5},
+               {"weight_decay": nan}, {"param_type": 1, "master": P}):
+        assert call(**kw) == bad, kw
+    for kw in ({"param": P + 1}, {"param": P + 2, "param_type": 1}, {"grad": P + 1},
+               {"master": P + 2}, {"exp_avg": P + 2}, {"exp_avg_sq": P + 1},
+               {"bits": 8, "scale": P + 2}, {"gs": P + 2}):
+        assert call(**kw) == off, kw
