@@ -171,6 +171,8 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         import torch
+        if torch.cuda.is_initialized():  # the raw handle: a tenth of current_stream()'s time
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -518,23 +520,23 @@ def project(H, W, k: int, surface: int = SB_TOKEN_LOGPROB, *, temperature: float
 # ------------------------------------------------------------------ training the head
 def _tensor(name, t, shape, dtypes, device, where):
     """Refuses a tensor the kernels would misread: another shape or type, one that is not
-    contiguous, or one that is not on the current CUDA device."""
+    contiguous, or one that is not on the current CUDA device (its index: `device`)."""
+    if (t.shape == shape and t.dtype in dtypes and t.get_device() == device and
+            t.is_contiguous()):
+        return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{where}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{where}: {name} is on {t.device}, not {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{where}: {name} is not contiguous")
-    return t
+    if t.get_device() != device:
+        raise ValueError(f"{where}: {name} is on {t.device}, not cuda:{device}")
+    raise ValueError(f"{where}: {name} is not contiguous")
 
 
-def _device(where):
+def _device():
+    """Index of the current CUDA device."""
     import torch
-    if not torch.cuda.is_available():
-        raise RuntimeError(f"{where}: no CUDA device")
-    return torch.device("cuda", torch.cuda.current_device())
+    return torch.cuda.current_device()
 
 
 class _on_stream:
@@ -542,10 +544,12 @@ class _on_stream:
     call allocates belongs to the stream its kernels run on."""
 
     def __init__(self, stream):
-        import torch
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        self._ctx = None if stream is None else torch.cuda.stream(stream)
+        self._ctx = None
+        if stream is not None:
+            import torch
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream)
+            self._ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
         if self._ctx is not None:
@@ -566,7 +570,7 @@ def _reduction(reduction, where):
 
 def _loss_problem(H, W, targets, where):
     import torch
-    dev = _device(where)
+    dev = _device()
     if H.dim() != 2 or W.dim() != 2:
         raise ValueError(f"{where}: H is [M, d] and W [V, d]")
     M, d = H.shape
@@ -577,13 +581,13 @@ def _loss_problem(H, W, targets, where):
     return M, d, V, dev
 
 
-def _workspace(nbytes, workspace, device, where):
+def _workspace(nbytes, like, where):
+    """A workspace of `nbytes()` bytes on the device of the tensor `like`."""
     import torch
-    if nbytes == 0:
+    n = nbytes()
+    if n == 0:
         raise SbError(SB_ERR_INVALID_ARG, where)
-    if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return workspace
+    return like.new_empty(n, dtype=torch.uint8)
 
 
 def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.0,
@@ -600,9 +604,10 @@ def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.
     red = _reduction(reduction, where)
     M, d, V, dev = _loss_problem(H, W, targets, where)
     with _on_stream(stream):
-        workspace = _workspace(sb_cross_entropy_workspace_bytes(M, d, V), workspace, dev, where)
-        loss = torch.empty(M if red == SB_REDUCE_NONE else 1, dtype=torch.float32, device=dev)
-        lse = torch.empty(M, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = _workspace(lambda: sb_cross_entropy_workspace_bytes(M, d, V), H, where)
+        loss = H.new_empty(M if red == SB_REDUCE_NONE else 1, dtype=torch.float32)
+        lse = H.new_empty(M, dtype=torch.float32)
         st = sb_cross_entropy_forward(H, W, targets, M, d, V, ignore_index, red, z_loss, loss,
                                       lse, workspace, workspace.numel(), stream)
     if st != SB_OK:
@@ -625,9 +630,10 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
     if grad is not None:
         _tensor("grad", grad, (M if red == SB_REDUCE_NONE else 1,), (torch.float32,), dev, where)
     with _on_stream(stream):
-        workspace = _workspace(
-            sb_cross_entropy_backward_workspace_bytes(M, d, V, piece, need_dH, need_dW),
-            workspace, dev, where)
+        if workspace is None:
+            workspace = _workspace(
+                lambda: sb_cross_entropy_backward_workspace_bytes(M, d, V, piece, need_dH, need_dW),
+                H, where)
         dH = torch.empty_like(H) if need_dH else None
         dW = torch.empty_like(W) if need_dW else None
         st = sb_cross_entropy_backward(H, W, targets, lse, grad, M, d, V, ignore_index, red,
@@ -647,7 +653,7 @@ def device_status(workspace) -> int:
 def _norm_problem(h, y, pre, post, gate, where):
     """Checks the arguments both directions share; returns (M, d, gate kind, types, device)."""
     import torch
-    dev = _device(where)
+    dev = _device()
     if h.dim() != 2:
         raise ValueError(f"{where}: h is [M, d]")
     both = (torch.bfloat16, torch.float32)
@@ -701,7 +707,8 @@ def residual_norm_backward(dx, dh, h, y, pre, *, post=None, gate=None, scale: fl
     if dh is not None:
         _tensor("dh", dh, (M, d), (h.dtype,), dev, where)
     with _on_stream(stream):
-        workspace = _workspace(sb_residual_norm_workspace_bytes(M, d), workspace, dev, where)
+        if workspace is None:
+            workspace = _workspace(lambda: sb_residual_norm_workspace_bytes(M, d), h, where)
         out = {"dh": torch.empty_like(h), "dy": torch.empty_like(y), "dpre": torch.empty_like(pre),
                "dpost": None if post is None else torch.empty_like(post),
                "dgate": None if gate is None else torch.empty_like(gate)}
@@ -743,7 +750,7 @@ class AdamW:
         for name, x in (("masters", self.masters), ("weight_decay", decay), ("states", self.states)):
             if len(x) != n:
                 raise ValueError(f"{where}: {len(x)} {name} for {n} parameters")
-        self._device = _device(where)
+        self._device = _device()
         both, f32 = (torch.bfloat16, torch.float32), (torch.float32,)
         self._list = (sb_adamw_tensor * n)()
         for i, p in enumerate(self.params):
@@ -758,8 +765,7 @@ class AdamW:
             kinds = ([(k, torch.float8_e4m3fn)] * 2 + [(blocks, torch.float32)] * 2
                      if state_bits == 8 else [(k, torch.float32)] * 2)
             if self.states[i] is None:
-                self.states[i] = tuple(torch.zeros(c, dtype=t, device=self._device)
-                                       for c, t in kinds)
+                self.states[i] = tuple(p.new_zeros(c, dtype=t) for c, t in kinds)
             if len(self.states[i]) != len(kinds):
                 raise ValueError(f"{where}: states[{i}] has {len(self.states[i])} tensors, "
                                  f"not {len(kinds)}")

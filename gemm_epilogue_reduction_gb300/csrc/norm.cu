@@ -3,7 +3,7 @@
 // gradients.  With n(x; w) = w·x / sqrt(mean(x²) + eps) over a row of d values:
 //   forward    h' = scale·h + gate·n(y; post),   x = n(h'; pre)
 //   backward   given h' and y and the gradients dx of x and dh of h':
-//     rh = 1 / sqrt(mean(h'²) + eps),  t = dh + rh·(dx·pre - h'·rh²·mean(dx·pre·h'))
+//     a = dx·pre,  rh = 1 / sqrt(mean(h'²) + eps),  t = dh + rh·(a - h'·rh²·mean(a·h'))
 //     dpre = sum over rows of dx·h'·rh,   gradient of h = scale·t
 //     u = n(y; post),  dgate = t·u (summed over the rows when the gate is one vector)
 //     f = t·gate·post,  dpost = sum over rows of t·gate·y·ry,
@@ -11,322 +11,50 @@
 // (post and gate are optional: u = y without the one, factor 1 without the other).
 //
 // Both kernels are bound by memory: forward reads h and y and writes h' and x, backward reads
-// dx, dh, h' and y and writes two gradients, each once.  A row belongs to one group of threads
-// that keeps its values in registers between the row reductions; the second reduction needs the
-// first one's result, so a row costs two barriers.  All sums are fp32; x comes from the
-// unrounded h' (one rounding per output), backward differentiates at the h' that was stored.
-// Backward's column sums: every block adds up its rows in registers and leaves one partial
-// vector each, and columns_kernel adds the partials in ascending order, so equal calls give
-// equal bits.
+// dx, dh, h' and y and writes two gradients, each once.  A row belongs to a group of threads,
+// and its values stay in registers, as do the weights, over all rows of the group.  Row reductions would stall the loads behind
+// them, so the next rows are on their way meanwhile: every thread copies its own values of the
+// rows ahead to shared memory with cp.async, and as it alone reads them no barrier is needed
+// (a ring of up to kMaxDepth rows per group; without it backward reached 38 % of the memory
+// rate at 8192 x 6144).  Arrays that are not 16-byte aligned, or have d not a multiple of 4, or
+// rows too long for two of them to fit, are read directly.
+//
+// All sums are fp32.  Forward needs two row reductions in turn, and x comes from the unrounded
+// h' (one rounding per output).  Backward differentiates at the h' that was stored and needs
+// one: with b = gate·post·y, sum(f·y) = sum(b·dh) + rh·(sum(b·a) - rh²·mean(a·h')·sum(b·h')),
+// so all six sums are known at once, with the rounding of t's own terms.  Its column sums stay
+// in registers over all rows of a group; the groups of a block add up in shared memory, every
+// block leaves one partial vector each, and columns_kernel adds the partials in ascending
+// order: equal calls give equal bits.
 #include <cmath>
-#include <cuda_bf16.h>
 
+#include "norm_common.cuh"
 #include "sb.h"
-#include "sb_internal.h"
 
 namespace sb {
 namespace {
 
-constexpr int kMaxRowThreads = 1024;
-constexpr int kMaxWarpsN = kMaxRowThreads / 32;
-constexpr int kMaxNormD = 16384;
-
-struct NormParams {
-    int M, d;
-    int row_threads;  // threads of a row's group, a multiple of 32
-    int gate_kind;    // 0: none, 1: one vector, 2: one per row
-    float scale, eps, inv_d;
-    const void *h, *y, *pre, *post, *gate;
-    void *h_out, *x;            // forward
-    const void *dx, *dh;        // backward
-    void *dh_out, *dy, *dgate;  // dgate: of a gate per row
-    float *part;                // [blocks][sums][d]
-    int sums;                   // vectors of column sums: dpre, dpost, dgate (those there are)
-};
-
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f(float v) { return v; }
-
-// VEC consecutive values; the address is VEC * sizeof(T) aligned (up to 16 bytes).
-template <int VEC, typename T>
-__device__ __forceinline__ void load(const T *p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = to_f(*p);
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) {
-            const float4 x = reinterpret_cast<const float4 *>(p)[i];
-            v[4 * i] = x.x;
-            v[4 * i + 1] = x.y;
-            v[4 * i + 2] = x.z;
-            v[4 * i + 3] = x.w;
-        }
-    } else {
-        uint32_t w[VEC / 2];
-        if constexpr (VEC == 8) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(p);
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-        } else {
-            const uint2 x = *reinterpret_cast<const uint2 *>(p);
-            w[0] = x.x, w[1] = x.y;
-        }
-#pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-}
-
-template <int VEC, typename T>
-__device__ __forceinline__ void store(T *p, const float (&v)[VEC]) {
-    if constexpr (sizeof(T) == 4) {
-        if constexpr (VEC == 1) {
-            *p = v[0];
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC / 4; ++i)
-                reinterpret_cast<float4 *>(p)[i] =
-                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        }
-    } else if constexpr (VEC == 1) {
-        *p = __float2bfloat16_rn(v[0]);
-    } else {
-        uint32_t w[VEC / 2];
-#pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&b);
-        }
-        if constexpr (VEC == 8)
-            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        else
-            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-    }
-}
-
-// Sums of N values over the row's group; every thread gets them.  `red` is the group's own
-// space of kMaxWarpsN * N words (not reused before another barrier has passed).  All groups of
-// the block call it together.
-template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int warps, int warp, float *red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], o);
-    if (warps == 1) return;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int n = 0; n < N; ++n) red[warp * N + n] = v[n];
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] = 0.f;
-    for (int w = 0; w < warps; ++w)
-#pragma unroll
-        for (int n = 0; n < N; ++n) v[n] += red[w * N + n];
-}
-
-// A thread's values: EPT = VEC * steps, step i at (i * row_threads + thread) * VEC.
-template <typename HT, typename WT, int VEC, int EPT>
-__global__ void __launch_bounds__(kMaxRowThreads) forward_kernel(const NormParams p) {
-    constexpr int S = EPT / VEC;
-    __shared__ float red[2][kMaxWarpsN];
-    const int group = threadIdx.x / p.row_threads, t = threadIdx.x - group * p.row_threads;
-    const int warps = p.row_threads / 32, warp = t >> 5;
-    const int row = blockIdx.x * (blockDim.x / p.row_threads) + group;
-    const bool rv = row < p.M;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const size_t base = static_cast<size_t>(rv ? row : 0) * p.d;
-    const HT *h = static_cast<const HT *>(p.h) + base;
-    const __nv_bfloat16 *y = static_cast<const __nv_bfloat16 *>(p.y) + base;
-    const WT *pre = static_cast<const WT *>(p.pre), *post = static_cast<const WT *>(p.post);
-    float a[S][VEC], b[S][VEC];
-    float yy[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        const int e = (i * p.row_threads + t) * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) a[i][j] = b[i][j] = 0.f;
-        if (rv && e < p.d) {
-            load<VEC>(h + e, a[i]);
-            load<VEC>(y + e, b[i]);
-        }
-    }
-    if (post) {
-#pragma unroll
-        for (int i = 0; i < S; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) yy[0] = fmaf(b[i][j], b[i][j], yy[0]);
-        row_sum<1>(yy, warps, warp, red[0] + group * warps);
-    }
-    const float ry = post ? rsqrtf(yy[0] * p.inv_d + p.eps) : 1.f;
-    float hh[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        const int e = (i * p.row_threads + t) * VEC;
-        if (e >= p.d) continue;
-        if (post) {
-            float w[VEC];
-            load<VEC>(post + e, w);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) b[i][j] = b[i][j] * ry * w[j];
-        }
-        if (p.gate_kind == 1) {
-            float g[VEC];
-            load<VEC>(static_cast<const WT *>(p.gate) + e, g);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) b[i][j] *= g[j];
-        } else if (p.gate_kind == 2 && rv) {
-            float g[VEC];
-            load<VEC>(static_cast<const __nv_bfloat16 *>(p.gate) + base + e, g);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) b[i][j] *= g[j];
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            a[i][j] = fmaf(a[i][j], p.scale, b[i][j]);
-            hh[0] = fmaf(a[i][j], a[i][j], hh[0]);
-        }
-        if (rv) store<VEC>(static_cast<HT *>(p.h_out) + base + e, a[i]);
-    }
-    row_sum<1>(hh, warps, warp, red[1] + group * warps);
-    if (!rv) return;
-    const float rh = rsqrtf(hh[0] * p.inv_d + p.eps);
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        const int e = (i * p.row_threads + t) * VEC;
-        if (e >= p.d) continue;
-        float w[VEC];
-        load<VEC>(pre + e, w);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) w[j] *= a[i][j] * rh;
-        store<VEC>(static_cast<__nv_bfloat16 *>(p.x) + base + e, w);
-    }
-}
-
-// One row at a time per block, rows dealt out in turn.
-template <typename HT, typename WT, int VEC, int EPT>
-__global__ void __launch_bounds__(kMaxRowThreads) backward_kernel(const NormParams p) {
-    constexpr int S = EPT / VEC;
-    __shared__ float red1[2][kMaxWarpsN * 3], red2[2][kMaxWarpsN];
-    const int t = threadIdx.x;
-    const int warps = p.row_threads / 32, warp = t >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const WT *pre = static_cast<const WT *>(p.pre), *post = static_cast<const WT *>(p.post);
-    float s_pre[S][VEC], s_post[S][VEC], s_gate[S][VEC];
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) s_pre[i][j] = s_post[i][j] = s_gate[i][j] = 0.f;
-    int turn = 0;
-    for (int row = blockIdx.x; row < p.M; row += gridDim.x, turn ^= 1) {
-        const size_t base = static_cast<size_t>(row) * p.d;
-        float dx[S][VEC], tt[S][VEC], h[S][VEC], y[S][VEC];
-        float sum[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const int e = (i * p.row_threads + t) * VEC;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) dx[i][j] = tt[i][j] = h[i][j] = y[i][j] = 0.f;
-            if (e < p.d) {
-                load<VEC>(static_cast<const __nv_bfloat16 *>(p.dx) + base + e, dx[i]);
-                if (p.dh) load<VEC>(static_cast<const HT *>(p.dh) + base + e, tt[i]);
-                load<VEC>(static_cast<const HT *>(p.h) + base + e, h[i]);
-                load<VEC>(static_cast<const __nv_bfloat16 *>(p.y) + base + e, y[i]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const int e = (i * p.row_threads + t) * VEC;
-            if (e >= p.d) continue;
-            float w[VEC];
-            load<VEC>(pre + e, w);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                sum[0] = fmaf(h[i][j], h[i][j], sum[0]);
-                sum[1] = fmaf(dx[i][j] * w[j], h[i][j], sum[1]);
-                sum[2] = fmaf(y[i][j], y[i][j], sum[2]);
-            }
-        }
-        row_sum<3>(sum, warps, warp, red1[turn]);
-        const float rh = rsqrtf(sum[0] * p.inv_d + p.eps);
-        const float c = rh * rh * (sum[1] * p.inv_d);
-        const float ry = post ? rsqrtf(sum[2] * p.inv_d + p.eps) : 1.f;
-        float fy[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const int e = (i * p.row_threads + t) * VEC;
-            if (e >= p.d) continue;
-            float w[VEC], g[VEC], o[VEC];
-            load<VEC>(pre + e, w);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                s_pre[i][j] = fmaf(dx[i][j], h[i][j] * rh, s_pre[i][j]);
-                tt[i][j] += rh * (dx[i][j] * w[j] - h[i][j] * c);
-                o[j] = p.scale * tt[i][j];
-            }
-            store<VEC>(static_cast<HT *>(p.dh_out) + base + e, o);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) w[j] = 1.f;
-            if (post) load<VEC>(post + e, w);
-            if (p.gate_kind) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) o[j] = tt[i][j] * (y[i][j] * ry * w[j]);
-                if (p.gate_kind == 1) {
-                    load<VEC>(static_cast<const WT *>(p.gate) + e, g);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) s_gate[i][j] += o[j];
-                } else {
-                    load<VEC>(static_cast<const __nv_bfloat16 *>(p.gate) + base + e, g);
-                    store<VEC>(static_cast<__nv_bfloat16 *>(p.dgate) + base + e, o);
-                }
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) tt[i][j] *= g[j];
-            }
-            if (post) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    s_post[i][j] = fmaf(tt[i][j], y[i][j] * ry, s_post[i][j]);
-                    tt[i][j] *= w[j];
-                    fy[0] = fmaf(tt[i][j], y[i][j], fy[0]);
-                }
-            }
-        }
-        if (post) row_sum<1>(fy, warps, warp, red2[turn]);
-        const float c2 = post ? ry * ry * (fy[0] * p.inv_d) : 0.f;
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const int e = (i * p.row_threads + t) * VEC;
-            if (e >= p.d) continue;
-            float o[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) o[j] = ry * (tt[i][j] - y[i][j] * c2);
-            store<VEC>(static_cast<__nv_bfloat16 *>(p.dy) + base + e, o);
-        }
-    }
-    float *part = p.part + static_cast<size_t>(blockIdx.x) * p.sums * p.d;
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        const int e = (i * p.row_threads + t) * VEC;
-        if (e >= p.d) continue;
-        float *to = part + e;
-        store<VEC>(to, s_pre[i]);
-        if (post) store<VEC>(to += p.d, s_post[i]);
-        if (p.gate_kind == 1) store<VEC>(to + p.d, s_gate[i]);
-    }
-}
-
 // Column sums of the blocks' partial vectors, in ascending order: 32 columns x 8 slices of the
-// partials per block; out[k]: where vector k of p.sums goes.
+// partials per block.  Vector 0 is dpre; vector 1, v = sum of t·(gate of the row)·y·ry, gives
+// dpost = gate·v and, where the gate is one vector, dgate = post·v.
 struct ColumnParams {
     const float *part;
-    int blocks, sums, d;
-    void *out[3];
-    int f32;
+    int blocks, sums, d, f32;
+    const void *post, *gate;
+    void *dpre, *dpost, *dgate;
 };
 constexpr int kSlices = 8;
+__device__ __forceinline__ float weight_at(const void *w, int f32, int i) {
+    if (!w) return 1.f;
+    return f32 ? one(static_cast<const float *>(w) + i)
+               : one(static_cast<const __nv_bfloat16 *>(w) + i);
+}
+__device__ __forceinline__ void put_at(void *w, int f32, int i, float v) {
+    if (f32)
+        put_one(static_cast<float *>(w) + i, v);
+    else
+        put_one(static_cast<__nv_bfloat16 *>(w) + i, v);
+}
 __global__ void __launch_bounds__(32 * kSlices) columns_kernel(const ColumnParams p) {
     __shared__ float sh[kSlices][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -346,50 +74,12 @@ __global__ void __launch_bounds__(32 * kSlices) columns_kernel(const ColumnParam
     if (slice != 0 || col >= p.d) return;
 #pragma unroll
     for (int s = 1; s < kSlices; ++s) a += sh[s][lane];
-    if (p.f32)
-        static_cast<float *>(p.out[k])[col] = a;
-    else
-        static_cast<__nv_bfloat16 *>(p.out[k])[col] = __float2bfloat16_rn(a);
-}
-
-template <typename P, typename K>
-cudaError_t launch_pdl(K kern, dim3 grid, int threads, const P &p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
-template <bool BACK, typename HT, typename WT>
-cudaError_t launch_types(const NormParams &p, int vec, int ept, dim3 grid, int threads,
-                         cudaStream_t st) {
-    if (vec == 8 && ept == 8)
-        return launch_pdl(BACK ? backward_kernel<HT, WT, 8, 8> : forward_kernel<HT, WT, 8, 8>, grid,
-                          threads, p, st);
-    if (vec == 8)
-        return launch_pdl(BACK ? backward_kernel<HT, WT, 8, 16> : forward_kernel<HT, WT, 8, 16>,
-                          grid, threads, p, st);
-    if (vec == 4)
-        return launch_pdl(BACK ? backward_kernel<HT, WT, 4, 16> : forward_kernel<HT, WT, 4, 16>,
-                          grid, threads, p, st);
-    return launch_pdl(BACK ? backward_kernel<HT, WT, 1, 16> : forward_kernel<HT, WT, 1, 16>, grid,
-                      threads, p, st);
-}
-
-template <bool BACK>
-cudaError_t launch_norm(const NormParams &p, bool h32, bool w32, int vec, int ept, dim3 grid,
-                        int threads, cudaStream_t st) {
-    if (h32)
-        return w32 ? launch_types<BACK, float, float>(p, vec, ept, grid, threads, st)
-                   : launch_types<BACK, float, __nv_bfloat16>(p, vec, ept, grid, threads, st);
-    return w32 ? launch_types<BACK, __nv_bfloat16, float>(p, vec, ept, grid, threads, st)
-               : launch_types<BACK, __nv_bfloat16, __nv_bfloat16>(p, vec, ept, grid, threads, st);
+    if (k == 0) {
+        put_at(p.dpre, p.f32, col, a);
+    } else {
+        if (p.dpost) put_at(p.dpost, p.f32, col, a * weight_at(p.gate, p.f32, col));
+        if (p.dgate) put_at(p.dgate, p.f32, col, a * weight_at(p.post, p.f32, col));
+    }
 }
 
 bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -425,10 +115,37 @@ int vector_width(int64_t d, Ptr... ptrs) {
 
 int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
 
-// Blocks of the backward kernel: what is resident on the device at once, at most one row each.
-int backward_blocks(int64_t M, int sms) {
-    const int64_t b = 2 * static_cast<int64_t>(sms);
-    return static_cast<int>(M < b ? M : b);
+// Sixteen values a thread: 384 threads hold a row of up to 6144 with 168 registers each, which
+// backward's weights, column sums and row take.  (Eight values on 768 threads: 73 and 192 us at
+// 8192 x 6144 against 71 and 119; a warp's fixed work per row then counts twice.)
+NormShape shape_of(int64_t d, int vec) {
+    return NormShape{vec, 16, d <= 16 * 384 ? 384 : (d <= 16 * 512 && vec == 8 ? 512 : 1024)};
+}
+
+// One block per SM, filled with groups; no more groups than a block has rows.
+struct NormLayout {
+    NormShape shape;
+    int row_threads, groups, blocks, depth;
+    size_t smem;
+};
+// row_bytes: of a row in the ring; sum_bytes: what the groups' column sums take.
+NormLayout layout_of(int64_t M, int64_t d, int vec, int value_bytes, size_t sum_bytes, int sms) {
+    NormLayout l{};
+    l.shape = shape_of(d, vec);
+    l.row_threads = round32((d + l.shape.ept - 1) / l.shape.ept);
+    const int64_t rows = (M + sms - 1) / sms;
+    l.groups = l.shape.max_threads / l.row_threads;
+    if (l.groups > kMaxGroups) l.groups = kMaxGroups;
+    if (l.groups > rows) l.groups = static_cast<int>(rows);
+    const int64_t blocks = (M + l.groups - 1) / l.groups;
+    l.blocks = static_cast<int>(blocks < sms ? blocks : sms);
+    const size_t row_bytes = static_cast<size_t>(l.row_threads) * l.shape.ept * value_bytes;
+    // a ring of two rows at least: one is on its way while another one is worked on
+    const size_t fit = vec == 1 ? 0 : kNormRingBytes / l.groups / row_bytes;
+    l.depth = fit < 2 ? 0 : (fit > kMaxDepth ? kMaxDepth : static_cast<int>(fit));
+    l.smem = static_cast<size_t>(l.depth) * l.groups * row_bytes;
+    if (l.groups > 1 && l.smem < sum_bytes) l.smem = sum_bytes;
+    return l;
 }
 
 }  // namespace
@@ -453,7 +170,6 @@ int32_t sb_residual_norm_forward(const void *h, const void *y, const void *pre, 
     NormParams p{};
     p.M = static_cast<int>(M);
     p.d = static_cast<int>(d);
-    p.gate_kind = gate_kind;
     p.scale = scale;
     p.eps = eps;
     p.inv_d = 1.f / static_cast<float>(d);
@@ -461,17 +177,20 @@ int32_t sb_residual_norm_forward(const void *h, const void *y, const void *pre, 
     p.y = y;
     p.pre = pre;
     p.post = post;
-    p.gate = gate_kind ? gate : nullptr;
+    p.gate = gate_kind == SB_GATE_CHANNEL ? gate : nullptr;
+    p.gate_rows = gate_kind == SB_GATE_TOKEN ? gate : nullptr;
+    p.w32 = weight_type == SB_F32;
     p.h_out = h_out;
     p.x = x;
-    const int vec = vector_width(d, h, y, pre, post, p.gate, h_out, x);
-    const int ept = vec == 8 && d <= 8 * kMaxRowThreads && M <= 2 * sms ? 8 : 16;
-    p.row_threads = round32((d + ept - 1) / ept);
-    const int groups = p.row_threads >= 128 ? 1 : 128 / p.row_threads;
-    const dim3 grid(static_cast<unsigned>((M + groups - 1) / groups));
-    return launch_norm<false>(p, stream_type == SB_F32, weight_type == SB_F32, vec, ept, grid,
-                              groups * p.row_threads,
-                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+    const bool h32 = stream_type == SB_F32;
+    const int vec = vector_width(d, h, y, pre, post, gate_kind ? gate : nullptr, h_out, x);
+    const int value_bytes = (h32 ? 4 : 2) + 2 + (p.gate_rows ? 2 : 0);
+    const NormLayout l = layout_of(M, d, vec, value_bytes, 0, sms);
+    p.row_threads = l.row_threads;
+    p.groups = l.groups;
+    p.depth = l.depth;
+    return launch_norm_forward(p, l.shape, h32, l.blocks, l.smem,
+                               static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? SB_OK
                : SB_ERR_CUDA;
 }
@@ -480,8 +199,8 @@ size_t sb_residual_norm_workspace_bytes(int64_t M, int64_t d) {
     if (M < 0 || M >= (int64_t(1) << 31) - 65536 || d < 1 || d > kMaxNormD) return 0;
     int sms = 0;
     if (device_sms_cc(&sms, nullptr) != SB_OK) return 0;
-    const size_t n = up256(static_cast<size_t>(backward_blocks(M, sms)) * 3 * d * 4);
-    return n ? n : 256;
+    const int64_t blocks = M < sms ? (M < 1 ? 1 : M) : sms;
+    return up256(static_cast<size_t>(blocks) * 2 * d * 4);
 }
 
 int32_t sb_residual_norm_backward(const void *dx, const void *dh, const void *h, const void *y,
@@ -508,19 +227,19 @@ int32_t sb_residual_norm_backward(const void *dx, const void *dh, const void *h,
     ColumnParams c{};
     c.d = static_cast<int>(d);
     c.f32 = weight_type == SB_F32;
-    c.out[c.sums++] = dpre;
-    if (post) c.out[c.sums++] = dpost;
-    if (gate_kind == SB_GATE_CHANNEL) c.out[c.sums++] = dgate;
+    c.dpre = dpre;
+    c.dpost = post ? dpost : nullptr;
+    c.dgate = gate_kind == SB_GATE_CHANNEL ? dgate : nullptr;
+    c.sums = c.dpost || c.dgate ? 2 : 1;
     if (M == 0) {  // the empty sums
-        for (int k = 0; k < c.sums; ++k)
-            if (cudaMemsetAsync(c.out[k], 0, static_cast<size_t>(d) * wa, st) != cudaSuccess)
+        for (void *v : {c.dpre, c.dpost, c.dgate})
+            if (v && cudaMemsetAsync(v, 0, static_cast<size_t>(d) * wa, st) != cudaSuccess)
                 return SB_ERR_CUDA;
         return SB_OK;
     }
     NormParams p{};
     p.M = static_cast<int>(M);
     p.d = static_cast<int>(d);
-    p.gate_kind = gate_kind;
     p.scale = scale;
     p.eps = eps;
     p.inv_d = 1.f / static_cast<float>(d);
@@ -528,25 +247,32 @@ int32_t sb_residual_norm_backward(const void *dx, const void *dh, const void *h,
     p.y = y;
     p.pre = pre;
     p.post = post;
-    p.gate = gate_kind ? gate : nullptr;
+    p.gate = gate_kind == SB_GATE_CHANNEL ? gate : nullptr;
+    p.gate_rows = gate_kind == SB_GATE_TOKEN ? gate : nullptr;
+    p.w32 = weight_type == SB_F32;
     p.dx = dx;
     p.dh = dh;
     p.dh_out = dh_out;
     p.dy = dy;
-    p.dgate = gate_kind == SB_GATE_TOKEN ? dgate : nullptr;
+    p.dgate_rows = gate_kind == SB_GATE_TOKEN ? dgate : nullptr;
     p.part = static_cast<float *>(workspace);
     p.sums = c.sums;
-    const int vec =
-        vector_width(d, dx, dh, h, y, pre, post, p.gate, dh_out, dy, p.dgate, workspace);
-    const int ept = vec == 8 && d <= 8 * kMaxRowThreads ? 8 : 16;
-    p.row_threads = round32((d + ept - 1) / ept);
-    const int blocks = backward_blocks(M, sms);
+    const bool h32 = stream_type == SB_F32;
+    const int vec = vector_width(d, dx, dh, h, y, pre, post, gate_kind ? gate : nullptr, dh_out, dy,
+                                 p.dgate_rows, workspace);
+    const int value_bytes = (h32 ? 8 : 4) + 4 + (p.gate_rows ? 2 : 0);
+    const NormLayout l =
+        layout_of(M, d, vec, value_bytes, static_cast<size_t>(c.sums) * d * 4, sms);
+    p.row_threads = l.row_threads;
+    p.groups = l.groups;
+    p.depth = l.depth;
     c.part = p.part;
-    c.blocks = blocks;
-    if (launch_norm<true>(p, stream_type == SB_F32, weight_type == SB_F32, vec, ept, dim3(blocks),
-                          p.row_threads, st) != cudaSuccess ||
-        launch_pdl(columns_kernel, dim3(static_cast<unsigned>((d + 31) / 32), c.sums), 32 * kSlices,
-                   c, st) != cudaSuccess)
+    c.blocks = l.blocks;
+    c.post = p.post;
+    c.gate = p.gate;
+    if (launch_norm_backward(p, l.shape, h32, l.blocks, l.smem, st) != cudaSuccess ||
+        launch_dependent(columns_kernel, dim3(static_cast<unsigned>((d + 31) / 32), c.sums),
+                         32 * kSlices, 0, c, st) != cudaSuccess)
         return SB_ERR_CUDA;
     return SB_OK;
 }
