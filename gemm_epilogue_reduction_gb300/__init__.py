@@ -521,43 +521,31 @@ def project(H, W, k: int, surface: int = SB_TOKEN_LOGPROB, *, temperature: float
 def _tensor(name, t, shape, dtypes, device, where):
     """Refuses a tensor the kernels would misread: another shape or type, one that is not
     contiguous, or one that is not on the current CUDA device (its index: `device`)."""
-    if (t.shape == shape and t.dtype in dtypes and t.get_device() == device and
-            t.is_contiguous()):
-        return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{where}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
     if t.get_device() != device:
         raise ValueError(f"{where}: {name} is on {t.device}, not cuda:{device}")
-    raise ValueError(f"{where}: {name} is not contiguous")
-
-
-def _device():
-    """Index of the current CUDA device."""
-    import torch
-    return torch.cuda.current_device()
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} is not contiguous")
 
 
 class _on_stream:
-    """Makes `stream` (None, a torch stream or a raw handle) torch's current one, so that what a
-    call allocates belongs to the stream its kernels run on."""
+    """Makes `stream` (a torch stream or a raw handle) torch's current one, so that what a call
+    allocates belongs to the stream its kernels run on."""
 
     def __init__(self, stream):
-        self._ctx = None
-        if stream is not None:
-            import torch
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream)
-            self._ctx = torch.cuda.stream(stream)
+        import torch
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        self._ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
+        self._ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+        self._ctx.__exit__(*exc)
 
 
 def _reduction(reduction, where):
@@ -569,25 +557,28 @@ def _reduction(reduction, where):
 
 
 def _loss_problem(H, W, targets, where):
+    """Checks the arguments both directions share; returns (M, d, V, device index)."""
     import torch
-    dev = _device()
+    dev = torch.cuda.current_device()
     if H.dim() != 2 or W.dim() != 2:
         raise ValueError(f"{where}: H is [M, d] and W [V, d]")
     M, d = H.shape
-    V = W.shape[0]
-    _tensor("H", H, (M, d), (torch.bfloat16,), dev, where)
-    _tensor("W", W, (V, d), (torch.bfloat16,), dev, where)
-    _tensor("targets", targets, (M,), (torch.int32,), dev, where)
+    V, dw = W.shape
+    bf16 = torch.bfloat16
+    if not (dw == d and H.dtype is bf16 and W.dtype is bf16 and targets.dtype is torch.int32 and
+            targets.shape == (M,) and H.get_device() == dev and W.get_device() == dev and
+            targets.get_device() == dev and H.is_contiguous() and W.is_contiguous() and
+            targets.is_contiguous()):
+        _tensor("H", H, (M, d), (bf16,), dev, where)
+        _tensor("W", W, (V, d), (bf16,), dev, where)
+        _tensor("targets", targets, (M,), (torch.int32,), dev, where)
     return M, d, V, dev
 
 
-def _workspace(nbytes, like, where):
-    """A workspace of `nbytes()` bytes on the device of the tensor `like`."""
-    import torch
-    n = nbytes()
-    if n == 0:
+def _nonzero(nbytes, where):
+    if nbytes == 0:
         raise SbError(SB_ERR_INVALID_ARG, where)
-    return like.new_empty(n, dtype=torch.uint8)
+    return nbytes
 
 
 def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.0,
@@ -599,17 +590,22 @@ def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.
     loss (float32, [M] for reduction "none", [1] for "sum" and "mean"), lse [M] and workspace.
     Asynchronous on ``stream``; raises SbError on a bad status. A target outside [0, V) that is
     not ``ignore_index`` gives a NaN loss, and ``device_status`` of the workspace reports it."""
+    if stream is not None:
+        with _on_stream(stream):
+            return cross_entropy(H, W, targets, ignore_index=ignore_index, z_loss=z_loss,
+                                 reduction=reduction, workspace=workspace)
     import torch
-    where = "cross_entropy"
-    red = _reduction(reduction, where)
-    M, d, V, dev = _loss_problem(H, W, targets, where)
-    with _on_stream(stream):
-        if workspace is None:
-            workspace = _workspace(lambda: sb_cross_entropy_workspace_bytes(M, d, V), H, where)
-        loss = H.new_empty(M if red == SB_REDUCE_NONE else 1, dtype=torch.float32)
-        lse = H.new_empty(M, dtype=torch.float32)
-        st = sb_cross_entropy_forward(H, W, targets, M, d, V, ignore_index, red, z_loss, loss,
-                                      lse, workspace, workspace.numel(), stream)
+    red = _reduction(reduction, "cross_entropy")
+    M, d, V, dev = _loss_problem(H, W, targets, "cross_entropy")
+    L = lib()
+    if workspace is None:
+        n = _nonzero(L.sb_cross_entropy_workspace_bytes(M, d, V), "cross_entropy")
+        workspace = torch.empty(n, dtype=torch.uint8, device=H.device)
+    loss = torch.empty(M if red == SB_REDUCE_NONE else 1, dtype=torch.float32, device=H.device)
+    lse = torch.empty(M, dtype=torch.float32, device=H.device)
+    st = L.sb_cross_entropy_forward(H.data_ptr(), W.data_ptr(), targets.data_ptr(), M, d, V,
+                                    ignore_index, red, z_loss, loss.data_ptr(), lse.data_ptr(),
+                                    workspace.data_ptr(), workspace.numel(), _stream(None))
     if st != SB_OK:
         raise SbError(st, "sb_cross_entropy_forward")
     return {"loss": loss, "lse": lse, "workspace": workspace}
@@ -622,6 +618,12 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
     arguments; ``grad`` is the incoming gradient (float32, [M] for "none", else [1]; None stands
     for ones). The vocabulary is worked off in pieces of ``piece`` columns (0: the library's
     choice). Returns a dict: dH, dW (None where not needed) and workspace."""
+    if stream is not None:
+        with _on_stream(stream):
+            return cross_entropy_backward(H, W, targets, lse, grad=grad,
+                                          ignore_index=ignore_index, z_loss=z_loss,
+                                          reduction=reduction, need_dH=need_dH, need_dW=need_dW,
+                                          piece=piece, workspace=workspace)
     import torch
     where = "cross_entropy_backward"
     red = _reduction(reduction, where)
@@ -629,16 +631,17 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
     _tensor("lse", lse, (M,), (torch.float32,), dev, where)
     if grad is not None:
         _tensor("grad", grad, (M if red == SB_REDUCE_NONE else 1,), (torch.float32,), dev, where)
-    with _on_stream(stream):
-        if workspace is None:
-            workspace = _workspace(
-                lambda: sb_cross_entropy_backward_workspace_bytes(M, d, V, piece, need_dH, need_dW),
-                H, where)
-        dH = torch.empty_like(H) if need_dH else None
-        dW = torch.empty_like(W) if need_dW else None
-        st = sb_cross_entropy_backward(H, W, targets, lse, grad, M, d, V, ignore_index, red,
-                                       z_loss, piece, dH, dW, workspace, workspace.numel(),
-                                       stream)
+    L = lib()
+    if workspace is None:
+        n = _nonzero(L.sb_cross_entropy_backward_workspace_bytes(M, d, V, piece, need_dH, need_dW),
+                     where)
+        workspace = torch.empty(n, dtype=torch.uint8, device=H.device)
+    dH = torch.empty_like(H) if need_dH else None
+    dW = torch.empty_like(W) if need_dW else None
+    st = L.sb_cross_entropy_backward(H.data_ptr(), W.data_ptr(), targets.data_ptr(),
+                                     lse.data_ptr(), _ptr(grad), M, d, V, ignore_index, red,
+                                     z_loss, piece, _ptr(dH), _ptr(dW), workspace.data_ptr(),
+                                     workspace.numel(), _stream(None))
     if st != SB_OK:
         raise SbError(st, "sb_cross_entropy_backward")
     return {"dH": dH, "dW": dW, "workspace": workspace}
@@ -651,27 +654,31 @@ def device_status(workspace) -> int:
 
 
 def _norm_problem(h, y, pre, post, gate, where):
-    """Checks the arguments both directions share; returns (M, d, gate kind, types, device)."""
+    """Checks the arguments both directions share; returns (M, d, gate kind, the types of the
+    stream and of the weights, device index)."""
     import torch
-    dev = _device()
+    dev = torch.cuda.current_device()
     if h.dim() != 2:
         raise ValueError(f"{where}: h is [M, d]")
-    both = (torch.bfloat16, torch.float32)
     M, d = h.shape
-    _tensor("h", h, (M, d), both, dev, where)
-    _tensor("y", y, (M, d), (torch.bfloat16,), dev, where)
-    _tensor("pre", pre, (d,), both, dev, where)
-    if post is not None:
-        _tensor("post", post, (d,), (pre.dtype,), dev, where)
+    f32, bf16 = torch.float32, torch.bfloat16
+    ht, wt = h.dtype, pre.dtype
     kind = SB_GATE_NONE
     if gate is not None:
         kind = SB_GATE_CHANNEL if gate.dim() == 1 else SB_GATE_TOKEN
-        if kind == SB_GATE_CHANNEL:
-            _tensor("gate", gate, (d,), (pre.dtype,), dev, where)
-        else:
-            _tensor("gate", gate, (M, d), (torch.bfloat16,), dev, where)
-    types = [SB_F32 if t.dtype == torch.float32 else SB_BF16 for t in (h, pre)]
-    return M, d, kind, types, dev
+    gs, gt = ((d,), wt) if kind == SB_GATE_CHANNEL else ((M, d), bf16)
+    if not ((ht is bf16 or ht is f32) and (wt is bf16 or wt is f32) and y.dtype is bf16 and
+            y.shape == (M, d) and pre.shape == (d,) and h.get_device() == dev and
+            y.get_device() == dev and pre.get_device() == dev and h.is_contiguous() and
+            y.is_contiguous() and pre.is_contiguous()):
+        _tensor("h", h, (M, d), (bf16, f32), dev, where)
+        _tensor("y", y, (M, d), (bf16,), dev, where)
+        _tensor("pre", pre, (d,), (bf16, f32), dev, where)
+    if post is not None:
+        _tensor("post", post, (d,), (wt,), dev, where)
+    if gate is not None:
+        _tensor("gate", gate, gs, (gt,), dev, where)
+    return (M, d, kind, SB_F32 if ht is f32 else SB_BF16, SB_F32 if wt is f32 else SB_BF16, dev)
 
 
 def residual_norm(h, y, pre, *, post=None, gate=None, scale: float = 1.0, eps: float = 1e-6,
@@ -683,12 +690,15 @@ def residual_norm(h, y, pre, *, post=None, gate=None, scale: float = 1.0, eps: f
     post [d] of one type, bf16 or float32 (post None: no norm of y), gate [d] of that type,
     [M, d] bf16, or None. Returns a dict: h (h', of h's type) and x (bf16: what the next block,
     or ``project`` and ``cross_entropy``, read). Asynchronous on ``stream``."""
+    if stream is not None:
+        with _on_stream(stream):
+            return residual_norm(h, y, pre, post=post, gate=gate, scale=scale, eps=eps)
     import torch
-    M, d, kind, types, dev = _norm_problem(h, y, pre, post, gate, "residual_norm")
-    with _on_stream(stream):
-        h_out, x = torch.empty_like(h), torch.empty_like(y)
-        st = sb_residual_norm_forward(h, y, pre, post, gate, kind, M, d, *types, scale, eps, h_out,
-                                      x, stream)
+    M, d, kind, ht, wt, _ = _norm_problem(h, y, pre, post, gate, "residual_norm")
+    h_out, x = torch.empty_like(h), torch.empty_like(y)
+    st = lib().sb_residual_norm_forward(h.data_ptr(), y.data_ptr(), pre.data_ptr(), _ptr(post),
+                                        _ptr(gate), kind, M, d, ht, wt, scale, eps,
+                                        h_out.data_ptr(), x.data_ptr(), _stream(None))
     if st != SB_OK:
         raise SbError(st, "sb_residual_norm_forward")
     return {"h": h_out, "x": x}
@@ -700,25 +710,32 @@ def residual_norm_backward(dx, dh, h, y, pre, *, post=None, gate=None, scale: fl
     its h' (None: nothing else reads h'), ``h`` the h' that it returned; the rest as there.
     Returns a dict: dh (the gradient of the incoming stream), dy, dpre, dpost, dgate (None where
     there is no such input) and workspace. The weights' gradients have the weights' type."""
+    if stream is not None:
+        with _on_stream(stream):
+            return residual_norm_backward(dx, dh, h, y, pre, post=post, gate=gate, scale=scale,
+                                          eps=eps, workspace=workspace)
     import torch
     where = "residual_norm_backward"
-    M, d, kind, types, dev = _norm_problem(h, y, pre, post, gate, where)
+    M, d, kind, ht, wt, dev = _norm_problem(h, y, pre, post, gate, where)
     _tensor("dx", dx, (M, d), (torch.bfloat16,), dev, where)
     if dh is not None:
         _tensor("dh", dh, (M, d), (h.dtype,), dev, where)
-    with _on_stream(stream):
-        if workspace is None:
-            workspace = _workspace(lambda: sb_residual_norm_workspace_bytes(M, d), h, where)
-        out = {"dh": torch.empty_like(h), "dy": torch.empty_like(y), "dpre": torch.empty_like(pre),
-               "dpost": None if post is None else torch.empty_like(post),
-               "dgate": None if gate is None else torch.empty_like(gate)}
-        st = sb_residual_norm_backward(dx, dh, h, y, pre, post, gate, kind, M, d, *types, scale,
-                                       eps, out["dh"], out["dy"], out["dpre"], out["dpost"],
-                                       out["dgate"], workspace, workspace.numel(), stream)
+    L = lib()
+    if workspace is None:
+        n = _nonzero(L.sb_residual_norm_workspace_bytes(M, d), where)
+        workspace = torch.empty(n, dtype=torch.uint8, device=h.device)
+    dh_out, dy, dpre = torch.empty_like(h), torch.empty_like(y), torch.empty_like(pre)
+    dpost = None if post is None else torch.empty_like(post)
+    dgate = None if gate is None else torch.empty_like(gate)
+    st = L.sb_residual_norm_backward(dx.data_ptr(), _ptr(dh), h.data_ptr(), y.data_ptr(),
+                                     pre.data_ptr(), _ptr(post), _ptr(gate), kind, M, d, ht, wt,
+                                     scale, eps, dh_out.data_ptr(), dy.data_ptr(),
+                                     dpre.data_ptr(), _ptr(dpost), _ptr(dgate),
+                                     workspace.data_ptr(), workspace.numel(), _stream(None))
     if st != SB_OK:
         raise SbError(st, "sb_residual_norm_backward")
-    out["workspace"] = workspace
-    return out
+    return {"dh": dh_out, "dy": dy, "dpre": dpre, "dpost": dpost, "dgate": dgate,
+            "workspace": workspace}
 
 
 class AdamW:
@@ -750,7 +767,7 @@ class AdamW:
         for name, x in (("masters", self.masters), ("weight_decay", decay), ("states", self.states)):
             if len(x) != n:
                 raise ValueError(f"{where}: {len(x)} {name} for {n} parameters")
-        self._device = _device()
+        self._device = torch.cuda.current_device()
         both, f32 = (torch.bfloat16, torch.float32), (torch.float32,)
         self._list = (sb_adamw_tensor * n)()
         for i, p in enumerate(self.params):

@@ -143,7 +143,7 @@ struct Work {
 Work work_of(int64_t M, int64_t d, int64_t cols, bool with_dH, bool with_dW) {
     Work w;
     const int64_t rt = (M + 255) / 256, dt = (d + 255) / 256, ct = (cols + 255) / 256;
-    const int atoms = rt < 2 ? 1 : 2;
+    const int atoms = loss_box_rows(static_cast<int>(rt)) / 64;
     w.kb = 64 * atoms;
     w.long_blocks = (cols + w.kb - 1) / w.kb;
     w.short_blocks = (M + w.kb - 1) / w.kb;
@@ -329,14 +329,16 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
 
     uint16_t *copy = dW ? reinterpret_cast<uint16_t *>(ws + pl.h_off) : nullptr;
     CUtensorMap tmH, tmC, tmW, tmG;
-    if (!encode_bf16_map(&tmH, H, M, d, 64) || !encode_bf16_map(&tmW, W, V, d, 64) ||
-        !encode_bf16_map(&tmC, copy ? copy : H, M, d, 64))
+    const int rows = loss_box_rows(p.row_tiles);
+    if (!encode_bf16_map(&tmH, H, M, d, rows) || !encode_bf16_map(&tmW, W, V, d, rows) ||
+        !encode_bf16_map(&tmC, copy ? copy : H, M, d, rows))
         return SB_ERR_CUDA;
     int64_t mapped = 0;
     for (int64_t c0 = 0; c0 < V; c0 += pl.piece) {
         const int64_t cols = V - c0 < pl.piece ? V - c0 : pl.piece;
         // the map ends at the piece's last column: what lies past it reads as zero
-        if (mapped != cols && !encode_bf16_map(&tmG, p.G, M, cols, 64, pl.ldg)) return SB_ERR_CUDA;
+        if (mapped != cols && !encode_bf16_map(&tmG, p.G, M, cols, rows, pl.ldg))
+            return SB_ERR_CUDA;
         mapped = cols;
         p.c0 = static_cast<int>(c0);
         p.cols = static_cast<int>(cols);

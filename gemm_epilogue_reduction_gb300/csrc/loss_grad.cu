@@ -30,6 +30,7 @@
 // 64 reduction rows and read by the MMA "MN-major", so that nothing is transposed.
 #include <atomic>
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "sb_internal.h"
 #include "sb_pipe.cuh"
@@ -40,33 +41,54 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 256;                       // rows and columns of a pair's tile
-constexpr int kBox = 64;                         // rows of a TMA box (64 elements = 128 bytes)
-constexpr uint32_t kBoxBytes = kBox * 128;       // 8 KB
-constexpr uint32_t kAtomBytes = 2 * kBoxBytes;   // one operand, one CTA, 64 of the reduction
+constexpr uint32_t kAtomBytes = kTileA * 128;    // one operand, one CTA, 64 of the reduction
 constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr uint32_t kGradSmem = kRingBytes + 1024 /* barriers and scalars */ + 1024 /* align */;
 
 // ATOMS 64-wide slices of the reduction per stage: 2 halves the waits and commits per
-// operation, 1 gives six stages instead of three.
+// operation, 1 gives six stages instead of three.  Every TMA box is 64 elements (128 bytes)
+// wide and 64 * ATOMS rows high, two boxes to an operand.
 template <int ATOMS>
 struct Ring {
+    static constexpr int kBoxRows = 64 * ATOMS;
+    static constexpr uint32_t kBoxBytes = kBoxRows * 128;
     static constexpr uint32_t kOperand = ATOMS * kAtomBytes;
+    static_assert(kOperand == 2 * kBoxBytes);
     static constexpr uint32_t kStage = 2 * kOperand;  // A, then B
     static constexpr int kStages = kRingBytes / kStage;
 };
 
-// Shared-memory matrix descriptor of an MN-major bf16 operand: blocks of 64 contiguous M (or
-// N) elements (128 bytes, 128-byte swizzle) x 64 reduction rows, as a 64 x 64 TMA box leaves
-// them.  Leading byte offset: from one block of 64 elements to the next (8 KB); stride byte
-// offset: from 8 reduction rows to the next 8 (1024 bytes).  A 16-wide K step adds 2048 bytes.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
+// Shared-memory matrix descriptor of an MN-major bf16 operand: two blocks of 64 contiguous M (or
+// N) elements (128 bytes, 128-byte swizzle) x the stage's reduction rows, as a TMA box leaves
+// them.  Leading byte offset: from one block of 64 elements to the next; stride byte offset:
+// from 8 reduction rows to the next 8 (1024 bytes).  A 16-wide K step adds 2048 bytes.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t block_bytes) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(kBoxBytes >> 4) << 16;
+    d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
     d |= static_cast<uint64_t>(1024u >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
     return d;
+}
+
+// This CTA's 128 rows (columns of the output, for B) of an operand from `mn`, reduction indexes
+// from `k`.  MN: the map's x is the operand's row and y the reduction index; else the other way
+// round.
+template <bool MN, int ATOMS>
+__device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *tm, uint32_t bar,
+                                             int mn, int k, uint64_t pol) {
+    using R = Ring<ATOMS>;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        uint8_t *to = dst + b * R::kBoxBytes;
+        if (MN)
+            tma_load_2d_pair(to, tm, bar, mn + 64 * b, k, pol);
+        else if (ATOMS == 2)
+            tma_load_2d_pair(to, tm, bar, k + 64 * b, mn, pol);
+        else
+            tma_load_2d_pair(to, tm, bar, k, mn + 64 * b, pol);
+    }
 }
 constexpr uint32_t kIdescAMajorMN = 1u << 15, kIdescBMajorMN = 1u << 16;
 
@@ -385,48 +407,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         // barrier counts every copy of the pair; its one commit per stage frees the stage in
         // both CTAs.
         if (lane == 0) {
-            const uint64_t pol = policy_evict_normal();
+            // every operand is read by many pairs, and again for other tiles soon: kept in L2
+            const uint64_t pol = policy_evict_last();
             int st = 0;
             uint32_t ph = 0, issued = 0;
             bool ok = true;
-            Unit u;
-            for (int i = 0; ok && unit_at<LOGITS, ATOMS>(p, pair, pairs, rank, i, u); ++i) {
-                const int bn = u.col0 + rank * kTileA;  // this CTA's half of the B operand
+            // One thread issues all copies, and its own instructions per stage bound how fast
+            // they go out: the layouts are compile-time constants of the loop (with a branch at
+            // every copy and boxes of 64 rows the operands kernel had 71 % of the tensor
+            // pipe's cycles).
+            auto tile = [&](const Unit &u, auto a_mn, auto b_mn, const CUtensorMap *ta,
+                            const CUtensorMap *tb, int b_row, int b_k) {
                 for (int kb = 0; kb < u.kblocks; ++kb) {
-                    if (!bwait_cluster(&empty[st], ph ^ 1u, wc)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!bwait_cluster(&empty[st], ph ^ 1u, wc)) return false;
                     if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * R::kStage);
-                    uint8_t *sa = smem + st * R::kStage, *sbuf = sa + R::kOperand;
+                    uint8_t *sa = smem + st * R::kStage;
                     // the leader's barrier at its cluster address, for both CTAs
                     const uint32_t bar = mapa_rank(&full[st], 0);
-#pragma unroll
-                    for (int at = 0; at < ATOMS; ++at) {
-                        const int k = u.k0 + kb * KB + at * kBlockK;  // past the end: zeros
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            uint8_t *da = sa + at * kAtomBytes + b * kBoxBytes;
-                            uint8_t *db = sbuf + at * kAtomBytes + b * kBoxBytes;
-                            const int o = b * kBox;
-                            if (LOGITS) {
-                                tma_load_2d_pair(da, &tmX, bar, k, u.row0 + o, pol);
-                                tma_load_2d_pair(db, &tmY, bar, k, p.c0 + bn + o, pol);
-                            } else if (u.dw) {
-                                tma_load_2d_pair(da, &tmX, bar, u.row0 + o, k, pol);
-                                tma_load_2d_pair(db, &tmZ, bar, bn + o, k, pol);
-                            } else {
-                                tma_load_2d_pair(da, &tmX, bar, k, u.row0 + o, pol);
-                                tma_load_2d_pair(db, &tmY, bar, bn + o, p.c0 + k, pol);
-                            }
-                        }
-                    }
+                    const int k = u.k0 + kb * KB;  // past the end: zeros
+                    load_operand<decltype(a_mn)::value, ATOMS>(sa, ta, bar, u.row0, k, pol);
+                    load_operand<decltype(b_mn)::value, ATOMS>(sa + R::kOperand, tb, bar, b_row,
+                                                               b_k + k, pol);
                     ++issued;
                     if (++st == R::kStages) {
                         st = 0;
                         ph ^= 1u;
                     }
                 }
+                return true;
+            };
+            Unit u;
+            for (int i = 0; ok && unit_at<LOGITS, ATOMS>(p, pair, pairs, rank, i, u); ++i) {
+                const int bn = u.col0 + rank * kTileA;  // this CTA's half of the B operand
+                const std::true_type mn;
+                const std::false_type km;
+                if (LOGITS)
+                    ok = tile(u, km, km, &tmX, &tmY, p.c0 + bn, 0);
+                else if (u.dw)
+                    ok = tile(u, mn, mn, &tmX, &tmZ, bn, 0);
+                else
+                    ok = tile(u, km, mn, &tmX, &tmY, bn, p.c0);
             }
             if (rank == 0) {
                 // every copy that the barriers count has landed before this CTA exits
@@ -446,7 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rank == 0 && lane == 0) {
             constexpr uint16_t kBoth = 3;
             const uint32_t s0 = smem_u32(smem);
-            const uint64_t k_desc = sw128_kmajor_desc(s0), mn_desc = sw128_mnmajor_desc(s0);
+            const uint64_t k_desc = sw128_kmajor_desc(s0);
+            const uint64_t mn_desc = sw128_mnmajor_desc(s0, R::kBoxBytes);
             int st = 0;
             uint32_t ph = 0;
             bool ok = true, any = false;
@@ -462,8 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        (a_mn ? kIdescAMajorMN : 0u) | (b_mn ? kIdescBMajorMN : 0u);
                 const uint64_t ad0 = a_mn ? mn_desc : k_desc;
                 const uint64_t bd0 = (b_mn ? mn_desc : k_desc) + (R::kOperand >> 4);
+                // a 16-wide K step: 32 bytes along a K-major row (the next 64-wide slice is the
+                // next atom), 16 rows of an MN-major one
                 const uint32_t a_step = a_mn ? 2048u >> 4 : 32u >> 4;
                 const uint32_t b_step = b_mn ? 2048u >> 4 : 32u >> 4;
+                const uint32_t a_atom = a_mn ? 4 * (2048u >> 4) : kAtomBytes >> 4;
+                const uint32_t b_atom = b_mn ? 4 * (2048u >> 4) : kAtomBytes >> 4;
                 for (int kb = 0; kb < u.kblocks; ++kb) {
                     if (!bwait_cluster(&full[st], ph, wc)) {
                         ok = false;
@@ -475,8 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int at = 0; at < ATOMS; ++at)
 #pragma unroll
                         for (int ks = 0; ks < kBlockK / 16; ++ks)
-                            umma_bf16_pair(d_tmem, ad0 + so + at * (kAtomBytes >> 4) + ks * a_step,
-                                           bd0 + so + at * (kAtomBytes >> 4) + ks * b_step, idesc,
+                            umma_bf16_pair(d_tmem, ad0 + so + at * a_atom + ks * a_step,
+                                           bd0 + so + at * b_atom + ks * b_step, idesc,
                                            (kb | at | ks) != 0 ? 1u : 0u);
                     umma_commit_pair(&empty[st], kBoth);
                     any = true;
@@ -607,20 +632,24 @@ cudaError_t launch_grad(const CUtensorMap &x, const CUtensorMap &y, const CUtens
 
 }  // namespace
 
+// One 64-wide slice per stage when a single pair of row tiles reads each W tile (the W stream
+// sets the pace and wants more stages), two otherwise.
+int loss_box_rows(int row_tiles) { return row_tiles < 2 ? Ring<1>::kBoxRows : Ring<2>::kBoxRows; }
+
 cudaError_t launch_loss_logits(const CUtensorMap &h, const CUtensorMap &w, const LossGradParams &p,
                                int num_sms, cudaStream_t stream) {
     const int units = p.row_tiles * p.col_tiles;
-    // one 64-wide slice per stage when a single pair of row tiles reads each W tile (the W
-    // stream sets the pace and wants more stages), two otherwise
-    return p.row_tiles < 2 ? launch_grad<true, 1>(h, w, w, p, units, num_sms, stream)
-                           : launch_grad<true, 2>(h, w, w, p, units, num_sms, stream);
+    return loss_box_rows(p.row_tiles) == Ring<1>::kBoxRows
+               ? launch_grad<true, 1>(h, w, w, p, units, num_sms, stream)
+               : launch_grad<true, 2>(h, w, w, p, units, num_sms, stream);
 }
 
 cudaError_t launch_loss_operands(const CUtensorMap &g, const CUtensorMap &w, const CUtensorMap &h,
                                  const LossGradParams &p, int num_sms, cudaStream_t stream) {
     const int units = p.dh_units + p.dw_units;
-    return p.row_tiles < 2 ? launch_grad<false, 1>(g, w, h, p, units, num_sms, stream)
-                           : launch_grad<false, 2>(g, w, h, p, units, num_sms, stream);
+    return loss_box_rows(p.row_tiles) == Ring<1>::kBoxRows
+               ? launch_grad<false, 1>(g, w, h, p, units, num_sms, stream)
+               : launch_grad<false, 2>(g, w, h, p, units, num_sms, stream);
 }
 
 cudaError_t launch_loss_sum(const float *part, void *dH, size_t n, int splits, const float *scale,

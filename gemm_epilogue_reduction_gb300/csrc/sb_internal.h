@@ -170,6 +170,8 @@ cudaError_t launch_copy16(void *dst, const void *src, size_t n16, int num_sms,
                           cudaStream_t stream);
 
 cudaError_t launch_loss_rows(const LossParams &p, cudaStream_t stream);
+// Rows of the TMA boxes (64 elements wide) that the gradient kernels use for this many row tiles.
+int loss_box_rows(int row_tiles);
 cudaError_t launch_loss_logits(const CUtensorMap &h, const CUtensorMap &w, const LossGradParams &p,
                                int num_sms, cudaStream_t stream);
 cudaError_t launch_loss_operands(const CUtensorMap &g, const CUtensorMap &w, const CUtensorMap &h,
