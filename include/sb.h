@@ -543,7 +543,8 @@ int32_t sb_residual_norm_backward(const void *dx, const void *dh, const void *h,
  * gradient times *grad_scale and t the step:
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
  *   w = (1 - lr weight_decay) w - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps),
- * all in fp32, each operation rounded by itself.  w is `master` where there is one (then param
+ * all in fp32, the moments' operations rounded each by itself, the square root and the
+ * quotient within 2^-20.  w is `master` where there is one (then param
  * receives its rounding to bf16), else param.  The moments are held
  *   state_bits = 32: in fp32;
  *   state_bits = 8: as E4M3 codes (the 8-bit floating-point type with 4 exponent and 3 mantissa

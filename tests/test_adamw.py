@@ -1,11 +1,17 @@
 """The AdamW step over many tensors.
 
-The kernel rounds every fp32 operation by itself, in the order of the formulas, so the same
-formulas in elementary torch operations on the same device give the same bits: values and codes
-are compared for equality. Against the 64-bit definition: ten fp32 roundings between input and
-output, so |m|, |v| and the update are within 16·2^-24 of the magnitudes they are sums of, a
-rounding to bf16 adds 2^-8 and one to E4M3 2^-4 of the value plus the spacing of its smallest
-numbers (2^-10 of a code), relative to the block's scale.
+Against the formulas in elementary fp32 operations on the same device, which the kernel follows
+operation by operation: the moments' bits are equal (values, codes and scales of the first
+moment). The kernel's square root and reciprocal are approximations within 2^-22, so the update is
+within 2^-20 of the formulas' and a weight within that plus one rounding (2^-23 of the weight);
+a root's scale is within 2^-21, and a root's code differs by one step at most, which happens to a
+value within 2^-21 of a tie: one in 2^16 or fewer of the values, as the codes are 2^-4 apart.
+Every step is compared from the state that the kernel had before it.
+
+Against the 64-bit definition: ten fp32 roundings between input and output, so |m|, |v| and the
+update are within 16·2^-24 (the update: and 2^-20) of the magnitudes they are sums of, a rounding
+to bf16 adds 2^-8 and one to E4M3 2^-4 of the value plus the spacing of its smallest numbers
+(2^-10 of a code), relative to the block's scale.
 """
 import math
 
@@ -74,7 +80,7 @@ def _make(sizes, *, param=BF, master=True, grad=BF, bits=32, seed=0, offset=0):
 
 
 def _step(p, g, w, state, *, lr, b1, b2, eps, wd, t, gs, bits):
-    """One tensor's step in elementary operations; returns (param, master or None, state)."""
+    """One tensor's step in elementary operations; returns (fp32 weight, state)."""
     x = (p if w is None else w).float()
     g = g.float() if gs is None else g.float() * gs
     m, v = (state if bits == 32 else (_values(state[0], state[2]), _values(state[1], state[3])))
@@ -90,7 +96,7 @@ def _step(p, g, w, state, *, lr, b1, b2, eps, wd, t, gs, bits):
     else:
         (a, sa), (b, sb_) = _codes(m, False), _codes(root, True)
         state = (a, b, sa, sb_)
-    return x.to(p.dtype), (None if w is None else x), state
+    return x, state
 
 
 def _equal(a, b, name):
@@ -102,25 +108,47 @@ def _equal(a, b, name):
 HYPER = {"lr": 1e-2, "b1": 0.9, "b2": 0.95, "eps": 1e-8}
 
 
+def _near(got, want, old, name):
+    """A weight (or its bf16 rounding) against the formulas' fp32 one, from the old weight."""
+    off = (got.double() - want.double()).abs()
+    bound = 2.0 ** -20 * (want.double() - old.double()).abs() + 2.0 ** -22 * want.double().abs()
+    if got.dtype == BF:
+        bound = bound + 2.0 ** -8 * want.double().abs()
+    assert (off <= bound + 1e-45).all(), (name, float((off - bound).max()))
+
+
+def _check_state(got, want, bits, name):
+    _equal(got[0], want[0], name + " m")
+    if bits == 32:
+        _equal(got[1], want[1], name + " v")
+        return
+    _equal(got[2], want[2], name + " scale of m")
+    off = (got[3].double() - want[3].double()).abs()
+    assert (off <= 2.0 ** -21 * want[3].double()).all(), name + " scale of the root"
+    d = (got[1].view(torch.uint8).int() - want[1].view(torch.uint8).int()).abs()
+    n = max(d.numel(), 1)
+    assert d.numel() == 0 or (int(d.max()) <= 1 and int((d > 0).sum()) <= 2 + n / 2 ** 15), name
+
+
 def _compare(sizes, *, bits, steps=3, gs=None, wd=0.1, start=0, offset=0, **kw):
     p, g, w, st = _make(sizes, bits=bits, offset=offset, **kw)
-    q = [(a.clone(), None if b is None else b.clone(), tuple(x.clone() for x in s))
-         for a, b, s in zip(p, w, st)]
     opt = sb.AdamW(p, g, lr=HYPER["lr"], betas=(HYPER["b1"], HYPER["b2"]), eps=HYPER["eps"],
                    weight_decay=wd, state_bits=bits, masters=w, states=st, step=start)
     decay = wd if isinstance(wd, list) else [wd] * len(sizes)
     for t in range(start + 1, start + steps + 1):
+        old = [(a if b is None else b).clone() for a, b in zip(p, w)]
+        want = [_step(a, gr, b, s, t=t, wd=d, gs=gs, bits=bits, **HYPER)
+                for a, gr, b, s, d in zip(p, g, w, st, decay)]
         opt.step(grad_scale=gs)
-        q = [_step(a, gr, b, s, t=t, wd=d, gs=gs, bits=bits, **HYPER)
-             for (a, b, s), gr, d in zip(q, g, decay)]
+        for i, (x, state) in enumerate(want):
+            if w[i] is not None:
+                _near(w[i], x, old[i], f"master {i}")
+                _equal(p[i], w[i].to(BF), f"param {i}")
+            else:
+                _near(p[i], x, old[i], f"param {i}")
+            _check_state(st[i], state, bits, f"state {i}")
     torch.cuda.synchronize()
     assert opt.step_count == start + steps
-    for i, (a, b, s) in enumerate(q):
-        _equal(p[i], a, f"param {i}")
-        if b is not None:
-            _equal(w[i], b, f"master {i}")
-        for j, (x, y) in enumerate(zip(st[i], s)):
-            _equal(x, y, f"state {i}.{j}")
 
 
 SIZES = [1, 255, 256, 257, 0, 7, 2048, 2049, 5120, 4096 * 33 + 5]
@@ -130,7 +158,7 @@ SIZES = [1, 255, 256, 257, 0, 7, 2048, 2049, 5120, 4096 * 33 + 5]
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("param,master,grad", [(BF, True, BF), (BF, False, BF), (F32, False, F32),
                                                (BF, True, F32), (F32, False, BF)])
-def test_steps_give_the_formulas_bits(bits, param, master, grad):
+def test_steps_follow_the_formulas(bits, param, master, grad):
     _compare(SIZES, bits=bits, param=param, master=master, grad=grad)
 
 
@@ -158,12 +186,15 @@ def test_mixed_types_in_one_list():
     a = _make([500], param=BF, grad=F32, seed=1)
     b = _make([600], param=F32, grad=BF, seed=2)
     p, g, w, st = (x + y for x, y in zip(a, b))
-    want = [_step(p[i].clone(), g[i], None if w[i] is None else w[i].clone(), st[i], t=1, wd=0.1,
-                  gs=None, bits=32, **HYPER) for i in range(2)]
+    old = [w[0].clone(), p[1].clone()]
+    want = [_step(p[i], g[i], w[i], st[i], t=1, wd=0.1, gs=None, bits=32, **HYPER)
+            for i in range(2)]
     sb.AdamW(p, g, lr=HYPER["lr"], betas=(HYPER["b1"], HYPER["b2"]), eps=HYPER["eps"],
              weight_decay=0.1, masters=w, states=st).step()
-    for i in range(2):
-        _equal(p[i], want[i][0], f"param {i}")
+    for got, (x, state), o, s in zip((w[0], p[1]), want, old, st):
+        _near(got, x, o, "weight")
+        _check_state(s, state, 32, "state")
+    _equal(p[0], w[0].to(BF), "param")
 
 
 @gpu
@@ -184,7 +215,7 @@ def test_against_the_definition_in_64_bits():
         rate = 1e-2 / (1 - 0.9 ** t)
         x = w0 * (1 - 1e-3) - rate * m / den
         off = (w[0].double() - x).abs()
-        assert (off <= 16 * E * (w0.abs() + rate * mm / den)).all()
+        assert (off <= 16 * E * (w0.abs() + rate * mm / den) + 2.0 ** -20 * rate * mm / den).all()
         assert ((p[0].double() - x).abs() <= off + 2.0 ** -8 * x.abs()).all()
         if bits == 32:
             assert ((st[0][0].double() - m).abs() <= 16 * E * mm).all()
@@ -211,12 +242,12 @@ def test_blocks_of_zeros_tiny_and_huge_values():
     g[0][800] = 1e4
     (a, sa), (b, sb_) = _codes(m, False), _codes(r, True)
     st = [(a, b, sa, sb_)]
-    q = _step(p[0].clone(), g[0], None, st[0], t=1, wd=0.1, gs=None, bits=8, **HYPER)
+    old = p[0].clone()
+    want, state = _step(p[0], g[0], None, st[0], t=1, wd=0.1, gs=None, bits=8, **HYPER)
     sb.AdamW(p, g, lr=HYPER["lr"], betas=(HYPER["b1"], HYPER["b2"]), eps=HYPER["eps"],
              weight_decay=0.1, state_bits=8, states=st).step()
-    _equal(p[0], q[0], "param")
-    for x, y in zip(st[0], q[2]):
-        _equal(x, y, "state")
+    _near(p[0], want, old, "param")
+    _check_state(st[0], state, 8, "state")
     assert torch.isfinite(p[0]).all()
     assert (_values(st[0][1], st[0][3])[256:512] > 0).all()
 
