@@ -328,16 +328,20 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
         return SB_ERR_INVALID_ARG;
 
     uint16_t *copy = dW ? reinterpret_cast<uint16_t *>(ws + pl.h_off) : nullptr;
-    CUtensorMap tmH, tmC, tmW, tmG;
     const int rows = loss_box_rows(p.row_tiles);
-    if (!encode_bf16_map(&tmH, H, M, d, rows) || !encode_bf16_map(&tmW, W, V, d, rows) ||
-        !encode_bf16_map(&tmC, copy ? copy : H, M, d, rows))
+    LossGradMaps logits{}, operands{};  // maps of gradients not asked for are not used
+    if (!encode_bf16_map(&logits.x, H, M, d, rows) || !encode_bf16_map(&logits.y, W, V, d, rows) ||
+        !encode_bf16_map(&operands.z, copy ? copy : H, M, d, rows) ||
+        !encode_bf16_map(&operands.dw, dW ? dW : W, V, d, 32) ||
+        !encode_bf16_map(&operands.dh, dH ? dH : H, M, d, 32))
         return SB_ERR_CUDA;
+    operands.y = logits.y;
     int64_t mapped = 0;
     for (int64_t c0 = 0; c0 < V; c0 += pl.piece) {
         const int64_t cols = V - c0 < pl.piece ? V - c0 : pl.piece;
         // the map ends at the piece's last column: what lies past it reads as zero
-        if (mapped != cols && !encode_bf16_map(&tmG, p.G, M, cols, rows, pl.ldg))
+        if (mapped != cols && (!encode_bf16_map(&operands.x, p.G, M, cols, rows, pl.ldg) ||
+                               !encode_bf16_map(&logits.g, p.G, M, cols, 32, pl.ldg)))
             return SB_ERR_CUDA;
         mapped = cols;
         p.c0 = static_cast<int>(c0);
@@ -350,8 +354,8 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
         p.dh_units = static_cast<int>(w.longs * pl.splits);
         p.dw_units = static_cast<int>(w.shorts);
         p.fill = static_cast<int>(((w.long_blocks + pl.splits - 1) / pl.splits) / w.short_blocks);
-        if (launch_loss_logits(tmH, tmW, p, sms, st) != cudaSuccess ||
-            launch_loss_operands(tmG, tmW, tmC, p, sms, st) != cudaSuccess)
+        if (launch_loss_logits(logits, p, sms, st) != cudaSuccess ||
+            launch_loss_operands(operands, p, sms, st) != cudaSuccess)
             return SB_ERR_CUDA;
     }
     if (dH && pl.splits > 1 &&

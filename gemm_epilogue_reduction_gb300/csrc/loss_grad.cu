@@ -43,7 +43,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 256;                       // rows and columns of a pair's tile
 constexpr uint32_t kAtomBytes = kTileA * 128;    // one operand, one CTA, 64 of the reduction
 constexpr uint32_t kRingBytes = 192 * 1024;
-constexpr uint32_t kGradSmem = kRingBytes + 1024 /* barriers and scalars */ + 1024 /* align */;
+constexpr uint32_t kOutBytes = 32 * 128;         // an epilogue warp's output box: 32 rows x 64 bf16
+constexpr uint32_t kOutAt = kRingBytes + 1024 /* barriers and scalars */;
+constexpr uint32_t kGradSmem = kOutAt + kEpiWarps * kOutBytes + 1024 /* align */;
+static_assert(kGradSmem <= kSmemLimit);
 
 // ATOMS 64-wide slices of the reduction per stage: 2 halves the waits and commits per
 // operation, 1 gives six stages instead of three.  Every TMA box is 64 elements (128 bytes)
@@ -183,23 +186,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Stores 32 consecutive bf16 values, of which the first n (a multiple of 8, at most 32) count.
-__device__ __forceinline__ void store_bf16_row(uint16_t *dst, const float (&v)[32], int n) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-    if (n == 32 && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
-        st_global_v8(dst, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
-        st_global_v8(dst + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
-    } else {
-        uint4 *d4 = reinterpret_cast<uint4 *>(dst);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (8 * j < n)
-                d4[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-    }
-}
-
 // The scale that all rows share, by all 256 epilogue threads (e = 0..255); red: 16 words of
 // shared memory.  SUM: the incoming gradient; MEAN: that over the count of rows that are not
 // ignored (at least 1); NONE: the largest |g_r| of those rows.
@@ -232,41 +218,68 @@ __device__ __forceinline__ float shared_scale(const LossGradParams &p, int e, fl
 }
 
 // ------------------------------------------------------------------ epilogues
-// Thread (quadrant q, half h, lane) owns output row row0 + 32q + lane and 128 of the tile's
-// 256 columns, in chunks of 32; the accumulator is released once its last chunk is read.
+// Warp (quadrant q, half h) owns 32 rows of the tile (thread: one row) and 128 of its 256
+// columns, in two parts of 64.  bf16 output leaves through shared memory: the warp's 32 x 64 box
+// in the 128-byte swizzle, then one TMA store (32 rows of whole 128-byte lines; stored row by
+// row from the threads, the short dW tiles of few tokens were bound by the stores).
+struct Out {
+    uint8_t *box;        // this warp's, 1024-byte aligned
+    uint64_t *tempty;    // the accumulator's release: local, or
+    uint32_t tempty_remote;  // the pair leader's, if not 0
+    int q, h, lane;
+};
+
+// f(column in the tile, values): what becomes of 64 columns of the thread's row.
 template <typename F>
-__device__ __forceinline__ void for_chunks(uint32_t taddr, int h, int lane, uint64_t *tempty,
-                                           uint32_t tempty_remote, F f) {
+__device__ __forceinline__ void for_parts(uint32_t taddr, const Out &o, F f) {
 #pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-        uint32_t raw[32];
-        tmem_ld32x32b_x32(taddr + 128 * h + 32 * ch, raw);
-        if (ch == 3) {
+    for (int part = 0; part < 2; ++part) {
+        uint32_t raw[64];
+        tmem_ld32x32b_x64(taddr + 128 * o.h + 64 * part, raw);
+        if (part == 1) {  // the accumulator is read
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                if (tempty_remote)
-                    mbar_arrive_remote(tempty_remote);
+            if (o.lane == 0) {
+                if (o.tempty_remote)
+                    mbar_arrive_remote(o.tempty_remote);
                 else
-                    mbar_arrive(tempty);
+                    mbar_arrive(o.tempty);
             }
         }
-        float v[32];
+        float v[64];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
-        f(128 * h + 32 * ch, v);
+        for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(raw[j]);
+        f(128 * o.h + 64 * part, v);
     }
 }
 
-__device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const Unit &u,
-                                                uint32_t taddr, uint64_t *tempty,
-                                                uint32_t tempty_remote, int q, int h, int lane,
-                                                float scale) {
-    const int row = u.row0 + 32 * q + lane;
-    const bool rv = row < p.M;
+// The warp's 32 x 64 box to column x, row y of the map.
+__device__ __forceinline__ void store_box(const CUtensorMap *tm, const Out &o, const float (&v)[64],
+                                          int x, int y, uint64_t pol) {
+    if (o.lane == 0) bulk_wait_read();  // the box before has been read
+    __syncwarp();
+    const uint32_t row = smem_u32(o.box) + o.lane * 128;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ (o.lane & 7)) << 4)),
+                     "r"(pack_bf16(v[8 * c], v[8 * c + 1])), "r"(pack_bf16(v[8 * c + 2], v[8 * c + 3])),
+                     "r"(pack_bf16(v[8 * c + 4], v[8 * c + 5])), "r"(pack_bf16(v[8 * c + 6], v[8 * c + 7]))
+                     : "memory");
+    fence_async_smem();
+    __syncwarp();
+    if (o.lane == 0) {
+        tma_store_2d(tm, o.box, x, y, pol);
+        bulk_commit();
+    }
+}
+
+__device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const CUtensorMap *tmG,
+                                                const Unit &u, uint32_t taddr, const Out &o,
+                                                float scale, uint64_t pol) {
+    const int row0 = u.row0 + 32 * o.q, row = row0 + o.lane;
     float a = 0.f, b = 0.f, l2 = 0.f;
     int tgt = -1;
-    if (rv) {
+    if (row < p.M) {
         const int t = __ldg(p.targets + row);
         if (t != p.ignore_index) {
             const float lse = __ldg(p.lse + row);
@@ -279,48 +292,40 @@ __device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const U
             if (t >= 0 && t < p.V) tgt = t - p.c0 - u.col0;
         }
     }
-    for_chunks(taddr, h, lane, tempty, tempty_remote, [&](int c, float (&v)[32]) {
-        if (!rv || u.col0 + c >= p.cols) return;
-        if (b == 0.f && a == 0.f) {  // ignored (a finite logit times 0 would do as well)
+    const bool dead = a == 0.f && b == 0.f;  // an ignored row, whatever its logits are
+    for_parts(taddr, o, [&](int c, float (&v)[64]) {
+        if (row0 >= p.M || u.col0 + c >= p.cols) return;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.f;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float e = a * ex2_approx(fmaf(v[j], kLog2e, -l2));
-                v[j] = c + j == tgt ? e - b : e;
-            }
+        for (int j = 0; j < 64; ++j) {
+            const float e = a * ex2_approx(fmaf(v[j], kLog2e, -l2));
+            v[j] = dead ? 0.f : (c + j == tgt ? e - b : e);
         }
-        // the piece buffer's rows are padded to 64 columns, so a whole chunk always fits;
-        // columns past the piece's last one are never read
-        store_bf16_row(p.G + static_cast<size_t>(row) * p.ldg + u.col0 + c, v, 32);
+        store_box(tmG, o, v, u.col0 + c, row0, pol);
     });
 }
 
-__device__ __forceinline__ void epilogue_operands(const LossGradParams &p, const Unit &u,
-                                                  uint32_t taddr, uint64_t *tempty,
-                                                  uint32_t tempty_remote, int q, int h, int lane,
-                                                  float scale) {
-    const int row = u.row0 + 32 * q + lane;
-    const bool rv = row < (u.dw ? p.cols : p.M);
+__device__ __forceinline__ void epilogue_operands(const LossGradParams &p, const CUtensorMap *tmDW,
+                                                  const CUtensorMap *tmDH, const Unit &u,
+                                                  uint32_t taddr, const Out &o, float scale,
+                                                  uint64_t pol) {
+    const int row0 = u.row0 + 32 * o.q, row = row0 + o.lane;
+    const int rows = u.dw ? p.cols : p.M;
     // dH: fp32 partial sums in memory unless this piece is the only one and not split
     const bool through = !u.dw && (p.splits > 1 || !(p.first && p.last));
     const bool out = u.dw || (p.splits == 1 && p.last);
-    uint16_t *dst = u.dw ? p.dW + (static_cast<size_t>(p.c0) + row) * p.d
-                         : p.dH + static_cast<size_t>(row) * p.d;
     float *part = p.part + (static_cast<size_t>(u.split) * p.M + row) * p.d;
-    for_chunks(taddr, h, lane, tempty, tempty_remote, [&](int c, float (&v)[32]) {
+    for_parts(taddr, o, [&](int c, float (&v)[64]) {
         const int col = u.col0 + c;
-        const int n = min(32, p.d - col);
-        if (!rv || n <= 0) return;
+        const int n = min(64, p.d - col);
+        if (row0 >= rows || n <= 0) return;
         if (u.kblocks == 0) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            for (int j = 0; j < 64; ++j) v[j] = 0.f;
         }
-        if (through && !p.first) {
+        if (through && !p.first && row < rows) {
             const float4 *src = reinterpret_cast<const float4 *>(part + col);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 16; ++j)
                 if (4 * j < n) {
                     const float4 x = src[j];
                     v[4 * j] += x.x;
@@ -331,24 +336,23 @@ __device__ __forceinline__ void epilogue_operands(const LossGradParams &p, const
         }
         if (out) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= scale;
-            store_bf16_row(dst + col, v, n);
-        } else {
+            for (int j = 0; j < 64; ++j) v[j] *= scale;
+            store_box(u.dw ? tmDW : tmDH, o, v, col, (u.dw ? p.c0 : 0) + row0, pol);
+        } else if (row < rows) {
             float4 *to = reinterpret_cast<float4 *>(part + col);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 16; ++j)
                 if (4 * j < n) to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
     });
 }
 
 // ------------------------------------------------------------------ the kernel
-// LOGITS: tmX = H, tmY = W (both K-major: x is the reduction index).  Otherwise tmX = the piece
-// of G, tmY = W, tmZ = the copy of H.
+// LOGITS: m.x = H, m.y = W (both K-major: x is the reduction index), output m.g.  Otherwise m.x =
+// the piece of G, m.y = W, m.z = the copy of H, outputs m.dw and m.dh.
 template <bool LOGITS, int ATOMS>
 __global__ void __launch_bounds__(kThreads, 1)
-    grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY,
-                const __grid_constant__ CUtensorMap tmZ, const LossGradParams p) {
+    grad_kernel(const __grid_constant__ LossGradMaps m, const LossGradParams p) {
     using R = Ring<ATOMS>;
     constexpr int KB = ATOMS * kBlockK;
     extern __shared__ uint8_t smem_raw[];
@@ -383,9 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(stall, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&tmX);
-        tma_prefetch_desc(&tmY);
-        if (!LOGITS) tma_prefetch_desc(&tmZ);
+        tma_prefetch_desc(&m.x);
+        tma_prefetch_desc(&m.y);
+        if (!LOGITS) tma_prefetch_desc(&m.z);
     }
     if (warp == 1) {
         tmem_alloc2(tmem_slot, 512);
@@ -442,11 +446,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const std::true_type mn;
                 const std::false_type km;
                 if (LOGITS)
-                    ok = tile(u, km, km, &tmX, &tmY, p.c0 + bn, 0);
+                    ok = tile(u, km, km, &m.x, &m.y, p.c0 + bn, 0);
                 else if (u.dw)
-                    ok = tile(u, mn, mn, &tmX, &tmZ, bn, 0);
+                    ok = tile(u, mn, mn, &m.x, &m.z, bn, 0);
                 else
-                    ok = tile(u, km, mn, &tmX, &tmY, bn, p.c0);
+                    ok = tile(u, km, mn, &m.x, &m.y, bn, p.c0);
             }
             if (rank == 0) {
                 // every copy that the barriers count has landed before this CTA exits
@@ -533,8 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------ epilogue warps
-        const int q = warp & 3;                     // TMEM lane quadrant this warp may read
-        const int h = (warp - kFirstEpiWarp) >> 2;  // which half of the columns
+        Out o;
+        o.q = warp & 3;                     // TMEM lane quadrant this warp may read
+        o.h = (warp - kFirstEpiWarp) >> 2;  // which half of the columns
+        o.lane = lane;
+        o.box = smem + kOutAt + (warp - kFirstEpiWarp) * kOutBytes;
+        // G is read next (by the operands kernel); dW and dH are not read here again
+        const uint64_t pol = LOGITS ? policy_evict_normal() : policy_evict_first();
         float scale;
         if (LOGITS) {
             scale = shared_scale(p, threadIdx.x - 32 * kFirstEpiWarp, red);
@@ -549,14 +558,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool ok = p.debug_stall ? bwait(stall, 0, wc) : bwait_cluster(&tfull[b], tph, wc);
             if (epi_any(!ok)) break;
             tc_fence_after();
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * o.q) << 16) +
                                    static_cast<uint32_t>(b * kTile);
-            const uint32_t remote = rank == 1 ? mapa_rank(&tempty[b], 0) : 0u;
+            o.tempty = &tempty[b];
+            o.tempty_remote = rank == 1 ? mapa_rank(&tempty[b], 0) : 0u;
             if (LOGITS)
-                epilogue_logits(p, u, taddr, &tempty[b], remote, q, h, lane, scale);
+                epilogue_logits(p, &m.g, u, taddr, o, scale, pol);
             else
-                epilogue_operands(p, u, taddr, &tempty[b], remote, q, h, lane, scale);
+                epilogue_operands(p, &m.dw, &m.dh, u, taddr, o, scale, pol);
         }
+        if (lane == 0) bulk_wait();
     }
 
     tc_fence_before();
@@ -589,8 +600,8 @@ __global__ void __launch_bounds__(256) sum_kernel(const float4 *part, uint2 *dH,
 }
 
 template <bool LOGITS, int ATOMS>
-cudaError_t launch_grad(const CUtensorMap &x, const CUtensorMap &y, const CUtensorMap &z,
-                        const LossGradParams &p, int units, int num_sms, cudaStream_t stream) {
+cudaError_t launch_grad(const LossGradMaps &m, const LossGradParams &p, int units, int num_sms,
+                        cudaStream_t stream) {
     auto kern = grad_kernel<LOGITS, ATOMS>;
     static std::atomic<uint64_t> opted_in{0};
     static std::atomic<int> pairs_by_dev[64];  // co-resident pairs (GPCs may not pair every SM)
@@ -627,7 +638,7 @@ cudaError_t launch_grad(const CUtensorMap &x, const CUtensorMap &y, const CUtens
     if (pairs > units) pairs = units;
     if (pairs < 1) pairs = 1;
     cfg.gridDim = dim3(2 * pairs);
-    return cudaLaunchKernelEx(&cfg, kern, x, y, z, p);
+    return cudaLaunchKernelEx(&cfg, kern, m, p);
 }
 
 }  // namespace
@@ -636,20 +647,20 @@ cudaError_t launch_grad(const CUtensorMap &x, const CUtensorMap &y, const CUtens
 // sets the pace and wants more stages), two otherwise.
 int loss_box_rows(int row_tiles) { return row_tiles < 2 ? Ring<1>::kBoxRows : Ring<2>::kBoxRows; }
 
-cudaError_t launch_loss_logits(const CUtensorMap &h, const CUtensorMap &w, const LossGradParams &p,
-                               int num_sms, cudaStream_t stream) {
+cudaError_t launch_loss_logits(const LossGradMaps &m, const LossGradParams &p, int num_sms,
+                               cudaStream_t stream) {
     const int units = p.row_tiles * p.col_tiles;
     return loss_box_rows(p.row_tiles) == Ring<1>::kBoxRows
-               ? launch_grad<true, 1>(h, w, w, p, units, num_sms, stream)
-               : launch_grad<true, 2>(h, w, w, p, units, num_sms, stream);
+               ? launch_grad<true, 1>(m, p, units, num_sms, stream)
+               : launch_grad<true, 2>(m, p, units, num_sms, stream);
 }
 
-cudaError_t launch_loss_operands(const CUtensorMap &g, const CUtensorMap &w, const CUtensorMap &h,
-                                 const LossGradParams &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_loss_operands(const LossGradMaps &m, const LossGradParams &p, int num_sms,
+                                 cudaStream_t stream) {
     const int units = p.dh_units + p.dw_units;
     return loss_box_rows(p.row_tiles) == Ring<1>::kBoxRows
-               ? launch_grad<false, 1>(g, w, h, p, units, num_sms, stream)
-               : launch_grad<false, 2>(g, w, h, p, units, num_sms, stream);
+               ? launch_grad<false, 1>(m, p, units, num_sms, stream)
+               : launch_grad<false, 2>(m, p, units, num_sms, stream);
 }
 
 cudaError_t launch_loss_sum(const float *part, void *dH, size_t n, int splits, const float *scale,

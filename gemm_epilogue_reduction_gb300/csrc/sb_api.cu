@@ -110,7 +110,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 // device state, so reusing one for the same pointer and shape is exact).
 struct MapCacheEntry {
     const void *base;
-    int64_t rows, d, ld;
+    int64_t rows, d;
     int box_rows;
     int packed_k;  // 0: a 2-D map over a row-major matrix; k: the 4-D map of a packed W
     CUtensorMap map;
@@ -121,32 +121,36 @@ std::mutex g_map_mu;
 MapCacheEntry g_map_cache[kMapCache];
 int g_map_next = 0;
 
-// 2-D map over a row-major bf16 matrix [rows, d], its rows ld elements apart (0: d): boxes of
-// 64 x box_rows, 128-byte swizzle, out-of-range elements read as zero.
-bool make_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t d, int box_rows,
-              int64_t ld = 0) {
-    if (ld == 0) ld = d;
-    {
-        std::lock_guard<std::mutex> lock(g_map_mu);
-        for (const auto &e : g_map_cache)
-            if (e.used && e.base == base && e.rows == rows && e.d == d && e.ld == ld &&
-                e.box_rows == box_rows && e.packed_k == 0) {
-                *tm = e.map;
-                return true;
-            }
-    }
+// 2-D map over a row-major bf16 matrix [rows, d], its rows ld elements apart: boxes of 64 x
+// box_rows, 128-byte swizzle, out-of-range elements read as zero.
+bool encode_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t d, int64_t ld,
+                int box_rows) {
     auto enc = encoder();
     if (!enc) return false;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(kBlockK), static_cast<cuuint32_t>(box_rows)};
     cuuint32_t es[2] = {1, 1};
-    if (enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
-            box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
+               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same over contiguous rows, through the cache.
+bool make_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t d, int box_rows) {
+    {
+        std::lock_guard<std::mutex> lock(g_map_mu);
+        for (const auto &e : g_map_cache)
+            if (e.used && e.base == base && e.rows == rows && e.d == d &&
+                e.box_rows == box_rows && e.packed_k == 0) {
+                *tm = e.map;
+                return true;
+            }
+    }
+    if (!encode_map(tm, base, rows, d, d, box_rows)) return false;
     std::lock_guard<std::mutex> lock(g_map_mu);
-    g_map_cache[g_map_next] = MapCacheEntry{base, rows, d, ld, box_rows, 0, *tm, true};
+    g_map_cache[g_map_next] = MapCacheEntry{base, rows, d, box_rows, 0, *tm, true};
     g_map_next = (g_map_next + 1) % kMapCache;
     return true;
 }
@@ -186,7 +190,7 @@ bool make_packed_map(CUtensorMap *tm, const void *base, int64_t V, int64_t d, in
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;
     std::lock_guard<std::mutex> lock(g_map_mu);
-    g_map_cache[g_map_next] = MapCacheEntry{base, V, d, d, kTileA, k, *tm, true};
+    g_map_cache[g_map_next] = MapCacheEntry{base, V, d, kTileA, k, *tm, true};
     g_map_next = (g_map_next + 1) % kMapCache;
     return true;
 }
@@ -280,7 +284,7 @@ CombineParams combine_params(const sb_outputs *out, const Workspace &w, int64_t 
 namespace sb {
 bool encode_bf16_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t cols,
                      int box_rows, int64_t ld) {
-    return make_map(tm, base, rows, cols, box_rows, ld);
+    return encode_map(tm, base, rows, cols, ld ? ld : cols, box_rows);
 }
 int32_t device_sms_cc(int *sms, int *cc) {
     DevInfo dev;

@@ -122,6 +122,12 @@ struct LossGradParams {
     int debug_stall;
 };
 
+// Tensor maps of one launch: operands x, y, z as the kernel says; outputs in boxes of 32 rows x 64
+// columns.
+struct LossGradMaps {
+    CUtensorMap x, y, z, g, dw, dh;
+};
+
 // The rows' losses from the projection records (loss.cu).
 struct LossParams {
     int M, T, V;
@@ -172,10 +178,10 @@ cudaError_t launch_copy16(void *dst, const void *src, size_t n16, int num_sms,
 cudaError_t launch_loss_rows(const LossParams &p, cudaStream_t stream);
 // Rows of the TMA boxes (64 elements wide) that the gradient kernels use for this many row tiles.
 int loss_box_rows(int row_tiles);
-cudaError_t launch_loss_logits(const CUtensorMap &h, const CUtensorMap &w, const LossGradParams &p,
-                               int num_sms, cudaStream_t stream);
-cudaError_t launch_loss_operands(const CUtensorMap &g, const CUtensorMap &w, const CUtensorMap &h,
-                                 const LossGradParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_loss_logits(const LossGradMaps &m, const LossGradParams &p, int num_sms,
+                               cudaStream_t stream);
+cudaError_t launch_loss_operands(const LossGradMaps &m, const LossGradParams &p, int num_sms,
+                                 cudaStream_t stream);
 cudaError_t launch_loss_sum(const float *part, void *dH, size_t n, int splits, const float *scale,
                             cudaStream_t stream);
 
