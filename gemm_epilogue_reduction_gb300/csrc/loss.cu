@@ -110,6 +110,11 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LossParams p) {
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// min(floor(2^32 / n), 2^32 - 1)
+uint32_t inverse(int n) {
+    return n == 1 ? 0xFFFFFFFFu : static_cast<uint32_t>((uint64_t(1) << 32) / n);
+}
+
 // M = 0 (a batch without tokens) is a valid problem of its own.
 bool loss_shape_ok(int64_t M, int64_t d, int64_t V) {
     return M >= 0 && M <= (int64_t(1) << 30) && V >= 1 && V < (int64_t(1) << 31) - 512 && d >= 8 &&
@@ -155,7 +160,11 @@ Work work_of(int64_t M, int64_t d, int64_t cols, bool with_dH, bool with_dW) {
 
 // Splits of the dH reduction: the smallest estimated time over both products.  Unsplit, few
 // dH tiles of a long reduction leave most CTA pairs idle (16 rows, d = 5120: 20 tiles of 2374
-// blocks for 76 pairs); every split adds its fp32 partial sums' traffic.
+// blocks for 76 pairs); every split adds its fp32 partial sums' traffic.  Of several row tiles
+// the pairs without a dH unit can make it up with dW tiles, as both are bound by the tensor
+// cores; of one row tile dH is bound by reading W, which wants all SMs, so its rounds count in
+// full (64 rows, d = 4096, V = 151,936: two splits on 32 pairs took 541 us, 19 on all of them
+// take 505 us).
 int choose_splits(int64_t M, int64_t d, int64_t piece, bool with_dH, bool with_dW, int pairs) {
     if (!with_dH) return 1;
     const Work w = work_of(M, d, piece, with_dH, with_dW);
@@ -164,12 +173,13 @@ int choose_splits(int64_t M, int64_t d, int64_t piece, bool with_dH, bool with_d
     for (int s = 1; s <= 64 && s <= w.long_blocks; ++s) {
         const int64_t blocks = (w.long_blocks + s - 1) / s;
         const int64_t rounds = (w.longs * s + pairs - 1) / pairs;
-        const double even = (static_cast<double>(w.longs) * s * blocks +
-                             static_cast<double>(w.shorts) * w.short_blocks) / pairs;
-        double t = static_cast<double>(rounds * blocks);
-        if (even > t) t = even;
+        const double dh = static_cast<double>(rounds * blocks);
+        const double dw = static_cast<double>(w.shorts) * w.short_blocks / pairs;
+        const double even = static_cast<double>(w.longs) * s * blocks / pairs + dw;
+        double t = w.kb == 64 ? dh + dw : (dh > even ? dh : even);
         t *= 0.34 * static_cast<double>(w.kb) / 64;                     // us
-        if (s > 1) t += static_cast<double>(s) * M * d * 8 / 6.8e6;     // written and read again
+        // the partial sums are written and read again, by a kernel of its own
+        if (s > 1) t += 3 + 0.05 * s + static_cast<double>(s) * M * d * 8 / 6.8e6;
         if (s == 1 || t < best_t) {
             best = s;
             best_t = t;
@@ -303,6 +313,8 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
     p.ldg = static_cast<int>(pl.ldg);
     p.row_tiles = static_cast<int>((M + 255) / 256);
     p.d_tiles = static_cast<int>((d + 255) / 256);
+    p.row_tiles_inv = inverse(p.row_tiles);
+    p.d_tiles_inv = inverse(p.d_tiles);
     p.splits = pl.splits;
     p.reduction = reduction;
     p.ignore_index = ignore_index;

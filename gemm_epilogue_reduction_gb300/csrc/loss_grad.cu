@@ -42,15 +42,12 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 256;                       // rows and columns of a pair's tile
 constexpr uint32_t kAtomBytes = kTileA * 128;    // one operand, one CTA, 64 of the reduction
-constexpr uint32_t kRingBytes = 192 * 1024;
-constexpr uint32_t kOutBytes = 32 * 128;         // an epilogue warp's output box: 32 rows x 64 bf16
-constexpr uint32_t kOutAt = kRingBytes + 1024 /* barriers and scalars */;
-constexpr uint32_t kGradSmem = kOutAt + kEpiWarps * kOutBytes + 1024 /* align */;
-static_assert(kGradSmem <= kSmemLimit);
+constexpr uint32_t kOutBytes = 32 * 128;         // an output box: 32 rows x 64 bf16
 
-// ATOMS 64-wide slices of the reduction per stage: 2 halves the waits and commits per
-// operation, 1 gives six stages instead of three.  Every TMA box is 64 elements (128 bytes)
-// wide and 64 * ATOMS rows high, two boxes to an operand.
+// ATOMS 64-wide slices of the reduction per stage: 2 halves the waits and commits per operation;
+// 1, for few rows, gives more stages and a second output box per epilogue warp (of few rows a dW
+// tile is written nearly as fast as it is computed).  Every operand box is 64 elements (128
+// bytes) wide and 64 * ATOMS rows high, two boxes to an operand.
 template <int ATOMS>
 struct Ring {
     static constexpr int kBoxRows = 64 * ATOMS;
@@ -58,7 +55,13 @@ struct Ring {
     static constexpr uint32_t kOperand = ATOMS * kAtomBytes;
     static_assert(kOperand == 2 * kBoxBytes);
     static constexpr uint32_t kStage = 2 * kOperand;  // A, then B
-    static constexpr int kStages = kRingBytes / kStage;
+    static constexpr int kStages = ATOMS == 1 ? 5 : 3;
+    static constexpr int kOutBoxes = ATOMS == 1 ? 2 : 1;
+    // shared memory: stages, output boxes, barriers and scalars
+    static constexpr uint32_t kOutAt = kStages * kStage;
+    static constexpr uint32_t kBarAt = kOutAt + kEpiWarps * kOutBoxes * kOutBytes;
+    static constexpr uint32_t kSmem = kBarAt + 1024 + 1024 /* align */;
+    static_assert(kSmem <= kSmemLimit);
 };
 
 // Shared-memory matrix descriptor of an MN-major bf16 operand: two blocks of 64 contiguous M (or
@@ -95,9 +98,7 @@ __device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *tm
 }
 constexpr uint32_t kIdescAMajorMN = 1u << 15, kIdescBMajorMN = 1u << 16;
 
-// One 256 x 256 tile of work.  a_x, a_y (b_x, b_y): box coordinates of this CTA's half of the
-// operand at reduction index 0; a_mn: the operand is MN-major, i.e. x is the tile's row and y
-// the reduction index (otherwise the other way round).
+// One 256 x 256 tile of work.
 struct Unit {
     bool dw;             // operands_kernel: a tile of dW (otherwise of dH)
     int row0, col0;      // of the output, this CTA's rows
@@ -105,67 +106,97 @@ struct Unit {
     int k0, kblocks;     // first reduction index and blocks of ATOMS * 64
 };
 
-template <bool LOGITS, int ATOMS>
-__device__ __forceinline__ bool unit_at(const LossGradParams &p, int pair, int pairs, int rank,
-                                        int i, Unit &u) {
-    constexpr int KB = ATOMS * kBlockK;
-    u.split = 0;
-    u.k0 = 0;
-    if (LOGITS) {
-        const int tile = pair + i * pairs;
-        if (tile >= p.row_tiles * p.col_tiles) return false;
-        u.dw = false;
-        // neighbouring pairs share a tile of W
-        u.col0 = (tile / p.row_tiles) * kTile;
-        u.row0 = (tile % p.row_tiles) * kTile + rank * kTileA;
-        u.kblocks = (p.d + KB - 1) / KB;
-        return true;
+__device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
+// t / d and t % d with inv = min(floor(2^32 / d), 2^32 - 1): the product is one too low at most.
+// (Every role walks through the units; with integer divisions that took longer than the MMAs of
+// a dW tile of 64 tokens.)
+__device__ __forceinline__ void div_mod(int t, int d, uint32_t inv, int &q, int &r) {
+    q = static_cast<int>(__umulhi(static_cast<uint32_t>(t), inv));
+    r = t - q * d;
+    if (r >= d) {
+        ++q;
+        r -= d;
     }
-    // The dH tiles, which are long (the piece's columns), come first, dealt out in turn; the
-    // short dW tiles then even out the pairs: those that are one dH tile behind the others
-    // take `fill` dW tiles each before the rest is dealt out in turn.
-    const int longs = p.dh_units, rem = longs % pairs, own = longs / pairs + (pair < rem ? 1 : 0);
-    if (i < own) {
-        const int t = pair + i * pairs;
-        const int per = p.row_tiles * p.d_tiles;
-        u.dw = false;
-        u.split = t / per;
-        const int q = t - u.split * per;
-        u.row0 = (q / p.d_tiles) * kTile + rank * kTileA;
-        u.col0 = (q % p.d_tiles) * kTile;
-        const int blocks = (p.cols + KB - 1) / KB;
-        const int b0 = static_cast<int>(static_cast<long long>(blocks) * u.split / p.splits);
-        const int b1 = static_cast<int>(static_cast<long long>(blocks) * (u.split + 1) / p.splits);
-        u.k0 = b0 * KB;
-        u.kblocks = b1 - b0;
-        return true;
-    }
-    int j = i - own;
-    const int shorts = p.dw_units;
-    int t;
-    if (rem == 0) {
-        t = j * pairs + pair;
-    } else {
-        const int behind = pairs - rem;
-        if (pair >= rem) {
-            if (j < p.fill) {
-                t = j * behind + (pair - rem);
-                if (t >= shorts) return false;
-            } else {
-                j -= p.fill;
-                t = behind * p.fill + j * pairs + (pair - rem);
-            }
-        } else {
-            t = behind * p.fill + j * pairs + behind + pair;
-        }
-    }
-    if (t >= shorts) return false;
-    u.dw = true;
-    u.row0 = (t / p.d_tiles) * kTile + rank * kTileA;
-    u.col0 = (t % p.d_tiles) * kTile;
-    u.kblocks = (p.M + KB - 1) / KB;
-    return true;
 }
+
+// The units of one pair, in order.  Logits: the tiles dealt out in turn, neighbouring pairs on
+// the same tile of W.  Operands: the dH units, which are long (the piece's columns), are dealt
+// out in turn; the short dW tiles then even out the pairs: those that are one dH unit behind
+// the others take `fill` dW tiles each before the rest is dealt out in turn.
+//
+// (With few rows dH reads W and dW writes its gradient, both at the memory's pace.  Half of the
+// pairs going through their units from the end, so that reads and writes overlap, was slower: 545
+// against 505 us at 64 x 4096 x 151,936.)
+template <bool LOGITS, int ATOMS>
+struct Walk {
+    static constexpr int KB = ATOMS * kBlockK;
+    const LossGradParams &p;
+    int pair, pairs, rank, own, rem, n;
+
+    __device__ __forceinline__ Walk(const LossGradParams &p, int pair, int pairs, int rank)
+        : p(p), pair(pair), pairs(pairs), rank(rank), own(0), rem(0) {
+        if (LOGITS) {
+            n = div_up(max(p.row_tiles * p.col_tiles - pair, 0), pairs);
+            return;
+        }
+        rem = p.dh_units % pairs;
+        own = p.dh_units / pairs + (pair < rem ? 1 : 0);
+        const int late = pairs - rem;  // pairs that are behind (all of them if rem == 0)
+        n = own;
+        int taken = 0, turn = pair;    // dW tiles of the first dealing; this pair's place after it
+        if (rem != 0) {
+            taken = min(late * p.fill, p.dw_units);
+            turn = pair >= rem ? pair - rem : late + pair;
+            if (pair >= rem) n += div_up(max(taken - turn, 0), late);
+        }
+        n += div_up(max(p.dw_units - taken - turn, 0), pairs);
+    }
+
+    __device__ __forceinline__ Unit at(int i) const {
+        Unit u;
+        u.split = 0;
+        u.k0 = 0;
+        u.dw = false;
+        int q, r;
+        if (LOGITS) {
+            div_mod(pair + i * pairs, p.row_tiles, p.row_tiles_inv, q, r);
+            u.col0 = q * kTile;
+            u.row0 = r * kTile + rank * kTileA;
+            u.kblocks = div_up(p.d, KB);
+            return u;
+        }
+        if (i < own) {
+            div_mod(pair + i * pairs, p.d_tiles, p.d_tiles_inv, q, r);
+            u.split = q / p.row_tiles;
+            u.row0 = (q - u.split * p.row_tiles) * kTile + rank * kTileA;
+            u.col0 = r * kTile;
+            const int blocks = div_up(p.cols, KB);
+            const int b0 = static_cast<int>(static_cast<long long>(blocks) * u.split / p.splits);
+            const int b1 = static_cast<int>(static_cast<long long>(blocks) * (u.split + 1) / p.splits);
+            u.k0 = b0 * KB;
+            u.kblocks = b1 - b0;
+            return u;
+        }
+        int j = i - own, t;
+        if (rem == 0) {
+            t = j * pairs + pair;
+        } else {
+            const int late = pairs - rem, first = min(late * p.fill, p.dw_units);
+            if (pair >= rem) {
+                const int mine = div_up(max(first - (pair - rem), 0), late);
+                t = j < mine ? j * late + (pair - rem) : first + (j - mine) * pairs + (pair - rem);
+            } else {
+                t = first + j * pairs + late + pair;
+            }
+        }
+        div_mod(t, p.d_tiles, p.d_tiles_inv, q, r);
+        u.dw = true;
+        u.row0 = q * kTile + rank * kTileA;
+        u.col0 = r * kTile;
+        u.kblocks = div_up(p.M, KB);
+        return u;
+    }
+};
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool epi_any(bool pred) {
@@ -223,7 +254,8 @@ __device__ __forceinline__ float shared_scale(const LossGradParams &p, int e, fl
 // in the 128-byte swizzle, then one TMA store (32 rows of whole 128-byte lines; stored row by
 // row from the threads, the short dW tiles of few tokens were bound by the stores).
 struct Out {
-    uint8_t *box;        // this warp's, 1024-byte aligned
+    uint8_t *box;        // this warp's boxes, 1024-byte aligned
+    int next;            // the box that is written next
     uint64_t *tempty;    // the accumulator's release: local, or
     uint32_t tempty_remote;  // the pair leader's, if not 0
     int q, h, lane;
@@ -231,7 +263,7 @@ struct Out {
 
 // f(column in the tile, values): what becomes of 64 columns of the thread's row.
 template <typename F>
-__device__ __forceinline__ void for_parts(uint32_t taddr, const Out &o, F f) {
+__device__ __forceinline__ void for_parts(uint32_t taddr, Out &o, F f) {
 #pragma unroll 1
     for (int part = 0; part < 2; ++part) {
         uint32_t raw[64];
@@ -254,11 +286,15 @@ __device__ __forceinline__ void for_parts(uint32_t taddr, const Out &o, F f) {
 }
 
 // The warp's 32 x 64 box to column x, row y of the map.
-__device__ __forceinline__ void store_box(const CUtensorMap *tm, const Out &o, const float (&v)[64],
+template <int ATOMS>
+__device__ __forceinline__ void store_box(const CUtensorMap *tm, Out &o, const float (&v)[64],
                                           int x, int y, uint64_t pol) {
-    if (o.lane == 0) bulk_wait_read();  // the box before has been read
+    constexpr int N = Ring<ATOMS>::kOutBoxes;
+    if (o.lane == 0) bulk_wait_read<N - 1>();  // what this box held before has been read
     __syncwarp();
-    const uint32_t row = smem_u32(o.box) + o.lane * 128;
+    uint8_t *box = o.box + o.next * kOutBytes;
+    o.next = o.next + 1 == N ? 0 : o.next + 1;
+    const uint32_t row = smem_u32(box) + o.lane * 128;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ (o.lane & 7)) << 4)),
@@ -268,13 +304,14 @@ __device__ __forceinline__ void store_box(const CUtensorMap *tm, const Out &o, c
     fence_async_smem();
     __syncwarp();
     if (o.lane == 0) {
-        tma_store_2d(tm, o.box, x, y, pol);
+        tma_store_2d(tm, box, x, y, pol);
         bulk_commit();
     }
 }
 
+template <int ATOMS>
 __device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const CUtensorMap *tmG,
-                                                const Unit &u, uint32_t taddr, const Out &o,
+                                                const Unit &u, uint32_t taddr, Out &o,
                                                 float scale, uint64_t pol) {
     const int row0 = u.row0 + 32 * o.q, row = row0 + o.lane;
     float a = 0.f, b = 0.f, l2 = 0.f;
@@ -300,13 +337,14 @@ __device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const C
             const float e = a * ex2_approx(fmaf(v[j], kLog2e, -l2));
             v[j] = dead ? 0.f : (c + j == tgt ? e - b : e);
         }
-        store_box(tmG, o, v, u.col0 + c, row0, pol);
+        store_box<ATOMS>(tmG, o, v, u.col0 + c, row0, pol);
     });
 }
 
+template <int ATOMS>
 __device__ __forceinline__ void epilogue_operands(const LossGradParams &p, const CUtensorMap *tmDW,
                                                   const CUtensorMap *tmDH, const Unit &u,
-                                                  uint32_t taddr, const Out &o, float scale,
+                                                  uint32_t taddr, Out &o, float scale,
                                                   uint64_t pol) {
     const int row0 = u.row0 + 32 * o.q, row = row0 + o.lane;
     const int rows = u.dw ? p.cols : p.M;
@@ -337,7 +375,7 @@ __device__ __forceinline__ void epilogue_operands(const LossGradParams &p, const
         if (out) {
 #pragma unroll
             for (int j = 0; j < 64; ++j) v[j] *= scale;
-            store_box(u.dw ? tmDW : tmDH, o, v, col, (u.dw ? p.c0 : 0) + row0, pol);
+            store_box<ATOMS>(u.dw ? tmDW : tmDH, o, v, col, (u.dw ? p.c0 : 0) + row0, pol);
         } else if (row < rows) {
             float4 *to = reinterpret_cast<float4 *>(part + col);
 #pragma unroll
@@ -358,20 +396,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRingBytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + R::kBarAt);
     uint64_t *empty = full + R::kStages;
     uint64_t *tfull = empty + R::kStages;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
     uint64_t *stall = drain + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kRingBytes + 512);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kRingBytes + 516);
-    float *red = reinterpret_cast<float *>(smem + kRingBytes + 528);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + R::kBarAt + 512);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + R::kBarAt + 516);
+    float *red = reinterpret_cast<float *>(smem + R::kBarAt + 528);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
-    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const Walk<LOGITS, ATOMS> walk(p, blockIdx.x / 2, gridDim.x / 2, rank);
     const WaitCtx wc{p.status, p.epoch, p.timeout_ns, abort_flag};
 
     if (threadIdx.x == 0) {
@@ -411,8 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // barrier counts every copy of the pair; its one commit per stage frees the stage in
         // both CTAs.
         if (lane == 0) {
-            // every operand is read by many pairs, and again for other tiles soon: kept in L2
+            // H and G are read by many pairs and again soon: kept in L2.  W is too where several
+            // row tiles read it; few read it once, and it then leaves room for the others.
             const uint64_t pol = policy_evict_last();
+            const uint64_t pol_w = p.row_tiles <= kWEvictFirstGroups ? policy_evict_first() : pol;
             int st = 0;
             uint32_t ph = 0, issued = 0;
             bool ok = true;
@@ -421,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every copy and boxes of 64 rows the operands kernel had 71 % of the tensor
             // pipe's cycles).
             auto tile = [&](const Unit &u, auto a_mn, auto b_mn, const CUtensorMap *ta,
-                            const CUtensorMap *tb, int b_row, int b_k) {
+                            const CUtensorMap *tb, int b_row, int b_k, uint64_t pol_b) {
                 for (int kb = 0; kb < u.kblocks; ++kb) {
                     if (!bwait_cluster(&empty[st], ph ^ 1u, wc)) return false;
                     if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * R::kStage);
@@ -431,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int k = u.k0 + kb * KB;  // past the end: zeros
                     load_operand<decltype(a_mn)::value, ATOMS>(sa, ta, bar, u.row0, k, pol);
                     load_operand<decltype(b_mn)::value, ATOMS>(sa + R::kOperand, tb, bar, b_row,
-                                                               b_k + k, pol);
+                                                               b_k + k, pol_b);
                     ++issued;
                     if (++st == R::kStages) {
                         st = 0;
@@ -440,17 +480,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            Unit u;
-            for (int i = 0; ok && unit_at<LOGITS, ATOMS>(p, pair, pairs, rank, i, u); ++i) {
+            for (int i = 0; ok && i < walk.n; ++i) {
+                const Unit u = walk.at(i);
                 const int bn = u.col0 + rank * kTileA;  // this CTA's half of the B operand
                 const std::true_type mn;
                 const std::false_type km;
                 if (LOGITS)
-                    ok = tile(u, km, km, &m.x, &m.y, p.c0 + bn, 0);
+                    ok = tile(u, km, km, &m.x, &m.y, p.c0 + bn, 0, pol_w);
                 else if (u.dw)
-                    ok = tile(u, mn, mn, &m.x, &m.z, bn, 0);
+                    ok = tile(u, mn, mn, &m.x, &m.z, bn, 0, pol);
                 else
-                    ok = tile(u, km, mn, &m.x, &m.y, bn, p.c0);
+                    ok = tile(u, km, mn, &m.x, &m.y, bn, p.c0, pol_w);
             }
             if (rank == 0) {
                 // every copy that the barriers count has landed before this CTA exits
@@ -475,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int st = 0;
             uint32_t ph = 0;
             bool ok = true, any = false;
-            Unit u;
-            for (int i = 0; ok && unit_at<LOGITS, ATOMS>(p, pair, pairs, rank, i, u); ++i) {
+            for (int i = 0; ok && i < walk.n; ++i) {
+                const Unit u = walk.at(i);
                 const int b = i & 1;
                 const uint32_t tph = (i >> 1) & 1;
                 if (!bwait_cluster(&tempty[b], tph ^ 1u, wc)) break;
@@ -541,7 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         o.q = warp & 3;                     // TMEM lane quadrant this warp may read
         o.h = (warp - kFirstEpiWarp) >> 2;  // which half of the columns
         o.lane = lane;
-        o.box = smem + kOutAt + (warp - kFirstEpiWarp) * kOutBytes;
+        o.box = smem + R::kOutAt + (warp - kFirstEpiWarp) * R::kOutBoxes * kOutBytes;
+        o.next = 0;
         // G is read next (by the operands kernel); dW and dH are not read here again
         const uint64_t pol = LOGITS ? policy_evict_normal() : policy_evict_first();
         float scale;
@@ -551,8 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
             scale = *p.scale;
         }
-        Unit u;
-        for (int i = 0; unit_at<LOGITS, ATOMS>(p, pair, pairs, rank, i, u); ++i) {
+        for (int i = 0; i < walk.n; ++i) {
+            const Unit u = walk.at(i);
             const int b = i & 1;
             const uint32_t tph = (i >> 1) & 1;
             const bool ok = p.debug_stall ? bwait(stall, 0, wc) : bwait_cluster(&tfull[b], tph, wc);
@@ -563,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             o.tempty = &tempty[b];
             o.tempty_remote = rank == 1 ? mapa_rank(&tempty[b], 0) : 0u;
             if (LOGITS)
-                epilogue_logits(p, &m.g, u, taddr, o, scale, pol);
+                epilogue_logits<ATOMS>(p, &m.g, u, taddr, o, scale, pol);
             else
-                epilogue_operands(p, &m.dw, &m.dh, u, taddr, o, scale, pol);
+                epilogue_operands<ATOMS>(p, &m.dw, &m.dh, u, taddr, o, scale, pol);
         }
         if (lane == 0) bulk_wait();
     }
@@ -589,6 +630,7 @@ __global__ void __launch_bounds__(256) sum_kernel(const float4 *part, uint2 *dH,
     if (i >= n4) return;
     const float f = *scale;
     float4 a = part[i];
+#pragma unroll 4
     for (int s = 1; s < splits; ++s) {
         const float4 x = part[s * n4 + i];
         a.x += x.x;
@@ -610,13 +652,14 @@ cudaError_t launch_grad(const LossGradMaps &m, const LossGradParams &p, int unit
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
     if (!bit || !(opted_in.load() & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Ring<ATOMS>::kSmem);
         if (e != cudaSuccess) return e;
         opted_in.fetch_or(bit);
     }
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kGradSmem;
+    cfg.dynamicSmemBytes = Ring<ATOMS>::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -107,9 +107,11 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *tm, const void *
 __device__ __forceinline__ void bulk_commit() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// Until the sources of this thread's bulk stores have been read / until they are complete.
+// Until the sources of all but this thread's last PENDING bulk stores have been read / until all
+// its stores are complete.
+template <int PENDING>
 __device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
 }
 __device__ __forceinline__ void bulk_wait() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
