@@ -9,13 +9,14 @@
 // consecutive ones to a lane: in 8 bits a group is one block of the format, and its largest
 // magnitude is one warp reduction.
 //
-// The moments' operations are rounded each by itself (no contraction into FMAs), so that an 8-bit
-// code of the first moment never differs from the one that the formulas give.  The square root
-// and the reciprocal are the hardware's approximations (relative errors below 2^-22): they meet
-// the weight only through its update, where they stay below the rounding of the weight unless
-// the update is larger than the weight, and with IEEE ones the 8-bit kernel was bound by
-// instructions instead of memory (2.98 ms for 778 M values against 1.93 ms, 95 % of the memory
-// rate).
+// What the states keep is rounded operation by operation (no contraction into FMAs; IEEE square
+// roots in 8 bits), so that an 8-bit code or scale never differs from the one that the formulas
+// give: one differing code changes the next step's update by its spacing.  What meets the weight
+// only (the reciprocal, and the root in 32 bits) is the hardware's approximation, with relative
+// errors below 2^-22: below the rounding of the weight unless the update is larger than the
+// weight.  (With IEEE division as well, the 8-bit kernel was bound by instructions instead of
+// memory: 2.98 ms for 778 M values against 2.00.  Approximate roots with IEEE ones only where a
+// code was in doubt took 2.14 ms.)
 #include <cmath>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -59,7 +60,9 @@ struct AdamParams {
 };
 
 __device__ __forceinline__ float2 both(float f) { return make_float2(f, f); }
+template <bool EXACT>
 __device__ __forceinline__ float root_of(float v) {
+    if (EXACT) return __fsqrt_rn(v);
     float r;
     asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
@@ -76,13 +79,15 @@ __device__ __forceinline__ float mixed(float x, float a, float y, float b) {
     return __fadd_rn(__fmul_rn(x, a), __fmul_rn(y, b));
 }
 
-// One step of two values: m, v and w are replaced; returns the roots of the new v.
+// One step of two values: m, v and w are replaced; returns the roots of the new v.  EXACT: the
+// roots are kept (as 8-bit codes).
+template <bool EXACT>
 __device__ __forceinline__ float2 advance(const AdamScalars &s, float decay, float2 g, float2 &m,
                                           float2 &v, float2 &w) {
     m = make_float2(mixed(m.x, s.b1, g.x, s.c1), mixed(m.y, s.b1, g.y, s.c1));
     v = make_float2(mixed(v.x, s.b2, __fmul_rn(g.x, g.x), s.c2),
                     mixed(v.y, s.b2, __fmul_rn(g.y, g.y), s.c2));
-    const float2 root = make_float2(root_of(v.x), root_of(v.y));
+    const float2 root = make_float2(root_of<EXACT>(v.x), root_of<EXACT>(v.y));
     const float2 den = __ffma2_rn(root, both(s.root), both(s.eps));
     const float2 step = __fmul2_rn(m, make_float2(inverse(den.x), inverse(den.y)));
     w = __ffma2_rn(step, both(-s.rate), __fmul2_rn(w, both(decay)));
@@ -177,35 +182,43 @@ __device__ __forceinline__ void load_codes(const uint8_t *p, float scale, bool w
     v[2] = __fmul2_rn(codes_f(c.y & 0xFFFFu), both(scale));
     v[3] = __fmul2_rn(codes_f(c.y >> 16), both(scale));
 }
+// The largest magnitude of the warp's 256 values.
+__device__ __forceinline__ float warp_top(const float2 (&v)[4]) {
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
+    // magnitudes order like their bits
+    return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
+}
+// What the values are multiplied by to become codes; lane 0 leaves the block's scale.
+__device__ __forceinline__ float scale_of(float top, float *scale, int lane) {
+    const bool small = top < 7.888609052210118e-31f;  // 2^-100
+    if (lane == 0) *scale = small ? 0.f : __fmul_rn(top, static_cast<float>(1.0 / 448.0));
+    return small ? 0.f : __fmul_rn(__frcp_rn(top), kTop);
+}
 // The codes of the warp's 256 values and their scale.  ROOT: values >= 0 whose codes are zero
 // only where the value is.
 template <bool ROOT>
 __device__ __forceinline__ void store_codes(uint8_t *p, float *scale, bool wide, int n, int lane,
                                             const float2 (&v)[4]) {
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
-    // magnitudes order like their bits
-    top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
-    const bool small = top < 7.888609052210118e-31f;  // 2^-100
-    const float mul = small ? 0.f : __fdiv_rn(kTop, top);
-    if (lane == 0) *scale = small ? 0.f : __fmul_rn(top, static_cast<float>(1.0 / 448.0));
+    const float2 mul = both(scale_of(warp_top(v), scale, lane));
     uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        float2 q = __fmul2_rn(v[j], both(mul));
+        float2 q = __fmul2_rn(v[j], mul);
         if (ROOT) {
             if (q.x > 0.f) q.x = fmaxf(q.x, kLeast);
             if (q.y > 0.f) q.y = fmaxf(q.y, kLeast);
         }
         c[j] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
     }
+    const uint2 all = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     if (wide) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+        *reinterpret_cast<uint2 *>(p) = all;
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < n) p[j] = static_cast<uint8_t>(c[j / 2] >> (8 * (j & 1)));
+            if (j < n) p[j] = static_cast<uint8_t>((j < 4 ? all.x : all.y) >> (8 * (j & 3)));
     }
 }
 
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(kThreadsAdam)
     float2 root[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        root[j] = advance(p.s, t.decay, __fmul2_rn(g[j], both(gs)), m[j], v[j], w[j]);
+        root[j] = advance<BITS8>(p.s, t.decay, __fmul2_rn(g[j], both(gs)), m[j], v[j], w[j]);
     if (t.w) store_f32(t.w + i, wide, n, w);
     if (!(t.flags & kParamF32)) store_bf16(static_cast<uint16_t *>(t.p) + i, wide, n, w);
     if (BITS8) {

@@ -4,7 +4,10 @@
 // Forward is the record GEMM of lmhead.cu (with the targets' logits) followed by one kernel:
 //   lse_r  = m + log sum_t s_rt·exp(m_rt - m),  m = max_t m_rt   (records t of 128 columns)
 //   loss_r = lse_r - z_r,target + z_loss·lse_r²,  0 where the target is the ignored index,
-// one block per row, and the last block to finish adds the rows' losses up (SUM, MEAN) in a
+// one block per row.  The tensor cores truncate as they accumulate, which leaves a logit of d =
+// 5120 products some 1e-5 short; the target's logit stands alone in the loss (every other one is
+// averaged in lse), so its block forms it again in fp32 FMAs and lse follows by the target's share
+// p of the sum:  lse += log(1 + p·(exp(z - z_tc) - 1)).  The last block to finish adds the rows' losses up (SUM, MEAN) in a
 // fixed order, so the bits do not depend on which block that is.  The rows kernel reads
 // 8 bytes for each 128 columns of a row: next to the GEMM's time it is small (M = 4096,
 // V = 200,064: 51 MB).  Backward is loss_grad.cu; its host side here cuts the vocabulary into
@@ -33,44 +36,73 @@ __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
 }
 
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LossParams p) {
-    __shared__ float sm[kRowThreads / 32], ss[kRowThreads / 32];
+    __shared__ float sm[kRowThreads / 32], ss[kRowThreads / 32], sz[kRowThreads / 32];
     __shared__ int is_last;
     const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // all the records' writes first, then let the next kernel set up
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int t = p.targets[row];
+    const bool inside = t >= 0 && t < p.V && t != p.ignore_index;
+    // the target's logit
+    float dot = 0.f;
+    if (inside) {
+        const uint4 *h = reinterpret_cast<const uint4 *>(p.H + static_cast<size_t>(row) * p.d);
+        const uint4 *w = reinterpret_cast<const uint4 *>(p.W + static_cast<size_t>(t) * p.d);
+        float d0 = 0.f, d1 = 0.f;
+#pragma unroll 2
+        for (int i = threadIdx.x; i < p.d / 8; i += kRowThreads) {
+            const uint4 x = h[i], y = w[i];
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                d0 = fmaf(__uint_as_float(xs[j] << 16), __uint_as_float(ys[j] << 16), d0);
+                d1 = fmaf(__uint_as_float(xs[j] & 0xFFFF0000u),
+                          __uint_as_float(ys[j] & 0xFFFF0000u), d1);
+            }
+        }
+        dot = d0 + d1;
+    }
     const float *rm = p.ws.m + static_cast<size_t>(row) * p.T;
     const float *rs = p.ws.s + static_cast<size_t>(row) * p.T;
     MaxSum a{-INFINITY, 0.f};
-    for (int t = threadIdx.x; t < p.T; t += 4 * kRowThreads) {
+    for (int k = threadIdx.x; k < p.T; k += 4 * kRowThreads) {
         MaxSum x[4];  // four records in flight
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int i = t + u * kRowThreads;
+            const int i = k + u * kRowThreads;
             x[u] = i < p.T ? MaxSum{rm[i], rs[i]} : MaxSum{-INFINITY, 0.f};
         }
         a = join(a, join(join(x[0], x[1]), join(x[2], x[3])));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 16; o > 0; o >>= 1) {
         a = join(a, MaxSum{__shfl_xor_sync(0xFFFFFFFFu, a.m, o),
                            __shfl_xor_sync(0xFFFFFFFFu, a.s, o)});
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+    }
     if (lane == 0) {
         sm[warp] = a.m;
         ss[warp] = a.s;
+        sz[warp] = dot;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
 #pragma unroll
-        for (int w = 1; w < kRowThreads / 32; ++w) a = join(a, MaxSum{sm[w], ss[w]});
-        const float lse = a.m + logf(a.s);
-        const int t = p.targets[row];
+        for (int w = 1; w < kRowThreads / 32; ++w) {
+            a = join(a, MaxSum{sm[w], ss[w]});
+            dot += sz[w];
+        }
+        float lse = a.m + logf(a.s);
         float loss = 0.f;
-        if (t != p.ignore_index)
+        if (inside) {
+            const float tz = p.ws.tz[row];
+            lse += log1pf(__expf(tz - lse) * expm1f(dot - tz));
+            loss = (lse - dot) + p.z_loss * lse * lse;
+        } else if (t != p.ignore_index) {
             // a target outside the vocabulary has no logit: the status word reports it
-            loss = t >= 0 && t < p.V
-                       ? (lse - p.ws.tz[row]) + p.z_loss * lse * lse
-                       : __uint_as_float(0x7FC00000u);
+            loss = __uint_as_float(0x7FC00000u);
+        }
         p.lse[row] = lse;
         p.rows[row] = loss;
         is_last = 0;
@@ -130,6 +162,14 @@ int32_t check_loss(const void *H, const void *W, const int32_t *targets, int64_t
     return SB_OK;
 }
 
+// Rows of G: up to kTwoPartRows rows are held in two bf16 parts (loss_grad.cu), the second ones
+// from row `lo` on, which is the next multiple of an output box's 32 rows.  Up to 32 rows they
+// cost nothing (both parts are one 64-wide reduction block of dW); at 64 rows they would cost 7 %
+// (4096 x 151,936: 993 against 932 us a step), and the roundings of that many targets average out.
+constexpr int64_t kTwoPartRows = 32;
+int64_t lo_row(int64_t M) { return M <= kTwoPartRows ? (M + 31) / 32 * 32 : 0; }
+int64_t g_rows(int64_t M) { return M <= kTwoPartRows ? 2 * lo_row(M) : M; }
+
 // How a backward call runs: the piece of the vocabulary, the split of the dH reduction, and the
 // workspace.
 struct Plan {
@@ -151,7 +191,7 @@ Work work_of(int64_t M, int64_t d, int64_t cols, bool with_dH, bool with_dW) {
     const int atoms = loss_box_rows(static_cast<int>(rt)) / 64;
     w.kb = 64 * atoms;
     w.long_blocks = (cols + w.kb - 1) / w.kb;
-    w.short_blocks = (M + w.kb - 1) / w.kb;
+    w.short_blocks = (g_rows(M) + w.kb - 1) / w.kb;
     if (w.short_blocks < 6 / atoms) w.short_blocks = 6 / atoms;
     w.longs = with_dH ? rt * dt : 0;
     w.shorts = with_dW ? ct * dt : 0;
@@ -179,7 +219,7 @@ int choose_splits(int64_t M, int64_t d, int64_t piece, bool with_dH, bool with_d
         double t = w.kb == 64 ? dh + dw : (dh > even ? dh : even);
         t *= 0.34 * static_cast<double>(w.kb) / 64;                     // us
         // the partial sums are written and read again, by a kernel of its own
-        if (s > 1) t += 3 + 0.05 * s + static_cast<double>(s) * M * d * 8 / 6.8e6;
+        if (s > 1) t += 3 + 0.05 * s + static_cast<double>(s) * g_rows(M) * d * 8 / 6.8e6;
         if (s == 1 || t < best_t) {
             best = s;
             best_t = t;
@@ -192,7 +232,7 @@ Plan plan_of(int64_t M, int64_t d, int64_t V, int64_t piece, bool with_dH, bool 
              int pairs) {
     Plan pl{};
     if (piece == 0) {
-        const int64_t n = (2 * M * V + kPieceBytes - 1) / kPieceBytes;
+        const int64_t n = (2 * g_rows(M) * V + kPieceBytes - 1) / kPieceBytes;
         piece = (V + n - 1) / n;
     }
     piece = (piece + 255) / 256 * 256;
@@ -200,11 +240,12 @@ Plan plan_of(int64_t M, int64_t d, int64_t V, int64_t piece, bool with_dH, bool 
     pl.ldg = (pl.piece + 63) / 64 * 64;
     pl.splits = choose_splits(M, d, pl.piece, with_dH, with_dW, pairs);
     pl.g_off = 256;
-    pl.h_off = pl.g_off + up256(static_cast<size_t>(M) * pl.ldg * 2);
-    pl.part_off = pl.h_off + (with_dW ? up256(static_cast<size_t>(M) * d * 2) : 0);
+    const size_t rows = static_cast<size_t>(g_rows(M));
+    pl.h_off = pl.g_off + up256(rows * pl.ldg * 2);
+    pl.part_off = pl.h_off + (with_dW ? up256(rows * d * 2) : 0);
     pl.total = pl.part_off;
-    if (with_dH && (pl.splits > 1 || pl.piece < V))
-        pl.total += up256(static_cast<size_t>(pl.splits) * M * d * 4);
+    if (with_dH && (pl.splits > 1 || pl.piece < V || lo_row(M)))
+        pl.total += up256(pl.splits * rows * d * 4);
     return pl;
 }
 
@@ -265,6 +306,9 @@ int32_t sb_cross_entropy_forward(const void *H, const void *W, const int32_t *ta
     p.reduction = reduction;
     p.ignore_index = ignore_index;
     p.z_loss = z_loss;
+    p.H = static_cast<const uint16_t *>(H);
+    p.W = static_cast<const uint16_t *>(W);
+    p.d = static_cast<int>(d);
     p.targets = targets;
     p.lse = lse;
     p.loss = loss;
@@ -311,6 +355,8 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
     p.d = static_cast<int>(d);
     p.V = static_cast<int>(V);
     p.ldg = static_cast<int>(pl.ldg);
+    p.lo = static_cast<int>(lo_row(M));
+    p.g_rows = static_cast<int>(g_rows(M));
     p.row_tiles = static_cast<int>((M + 255) / 256);
     p.d_tiles = static_cast<int>((d + 255) / 256);
     p.row_tiles_inv = inverse(p.row_tiles);
@@ -343,7 +389,7 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
     const int rows = loss_box_rows(p.row_tiles);
     LossGradMaps logits{}, operands{};  // maps of gradients not asked for are not used
     if (!encode_bf16_map(&logits.x, H, M, d, rows) || !encode_bf16_map(&logits.y, W, V, d, rows) ||
-        !encode_bf16_map(&operands.z, copy ? copy : H, M, d, rows) ||
+        !encode_bf16_map(&operands.z, copy ? copy : H, copy ? p.g_rows : M, d, rows) ||
         !encode_bf16_map(&operands.dw, dW ? dW : W, V, d, 32) ||
         !encode_bf16_map(&operands.dh, dH ? dH : H, M, d, 32))
         return SB_ERR_CUDA;
@@ -352,8 +398,8 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
     for (int64_t c0 = 0; c0 < V; c0 += pl.piece) {
         const int64_t cols = V - c0 < pl.piece ? V - c0 : pl.piece;
         // the map ends at the piece's last column: what lies past it reads as zero
-        if (mapped != cols && (!encode_bf16_map(&operands.x, p.G, M, cols, rows, pl.ldg) ||
-                               !encode_bf16_map(&logits.g, p.G, M, cols, 32, pl.ldg)))
+        if (mapped != cols && (!encode_bf16_map(&operands.x, p.G, p.g_rows, cols, rows, pl.ldg) ||
+                               !encode_bf16_map(&logits.g, p.G, p.g_rows, cols, 32, pl.ldg)))
             return SB_ERR_CUDA;
         mapped = cols;
         p.c0 = static_cast<int>(c0);
@@ -370,10 +416,7 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
             launch_loss_operands(operands, p, sms, st) != cudaSuccess)
             return SB_ERR_CUDA;
     }
-    if (dH && pl.splits > 1 &&
-        launch_loss_sum(p.part, dH, static_cast<size_t>(M) * d, pl.splits, p.scale, st) !=
-            cudaSuccess)
-        return SB_ERR_CUDA;
+    if (dH && (pl.splits > 1 || p.lo) && launch_loss_sum(p, st) != cudaSuccess) return SB_ERR_CUDA;
     return SB_OK;
 }
 

@@ -17,11 +17,14 @@
 // and, when the dH reduction was split, sum_kernel adds the splits in ascending order.
 //
 // G is held in bf16, the type of the tensor cores' operands here: a relative error of 2^-8 at
-// most per entry (rms 2^-9), independent from entry to entry, so that a sum over many of them loses less
-// than the rounding of dH and dW to bf16 does.  For that the scale that all rows share (the
-// incoming gradient, 1/count, or the largest |g|) stays out of G and is applied in fp32 in the
-// epilogue: rounding it into G would shift every entry the same way.  Accumulation is fp32 in
-// TMEM and, over the pieces, fp32 in memory.
+// most per entry (rms 2^-9), independent from entry to entry, so that a sum over many of them
+// loses less than the rounding of dH and dW to bf16 does.  For that the scale that all rows share
+// (the incoming gradient, 1/count, or the largest |g|) stays out of G and is applied in fp32 in
+// the epilogue: rounding it into G would shift every entry the same way.  A few rows have few
+// large entries (their targets'), whose roundings do not average out, so up to 32 rows G is held as
+// two bf16 numbers, the value and what its rounding left (2^-16 together): the second ones are
+// further rows of G, which fill the row tile and the 64-wide reduction block that few rows leave
+// empty.  Accumulation is fp32 in TMEM and, over the pieces, fp32 in memory.
 //
 // Both kernels: persistent CTA pairs, one cta_group::2 MMA of 256 x 256 per 16-wide K step
 // (tcgen05, bf16 x bf16 -> fp32), joint TMA stages, two TMEM accumulators, eight epilogue
@@ -193,7 +196,7 @@ struct Walk {
         u.dw = true;
         u.row0 = q * kTile + rank * kTileA;
         u.col0 = r * kTile;
-        u.kblocks = div_up(p.M, KB);
+        u.kblocks = div_up(p.g_rows, KB);
         return u;
     }
 };
@@ -338,6 +341,11 @@ __device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const C
             v[j] = dead ? 0.f : (c + j == tgt ? e - b : e);
         }
         store_box<ATOMS>(tmG, o, v, u.col0 + c, row0, pol);
+        if (p.lo) {  // (rows past M, up to the next 32, are zero in both)
+#pragma unroll
+            for (int j = 0; j < 64; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+            store_box<ATOMS>(tmG, o, v, u.col0 + c, p.lo + row0, pol);
+        }
     });
 }
 
@@ -347,11 +355,12 @@ __device__ __forceinline__ void epilogue_operands(const LossGradParams &p, const
                                                   uint32_t taddr, Out &o, float scale,
                                                   uint64_t pol) {
     const int row0 = u.row0 + 32 * o.q, row = row0 + o.lane;
-    const int rows = u.dw ? p.cols : p.M;
-    // dH: fp32 partial sums in memory unless this piece is the only one and not split
-    const bool through = !u.dw && (p.splits > 1 || !(p.first && p.last));
-    const bool out = u.dw || (p.splits == 1 && p.last);
-    float *part = p.part + (static_cast<size_t>(u.split) * p.M + row) * p.d;
+    const int rows = u.dw ? p.cols : p.g_rows;
+    // dH: fp32 partial sums in memory unless this piece is the only one, not split and G one number
+    const bool sums = p.splits > 1 || p.lo;
+    const bool through = !u.dw && (sums || !(p.first && p.last));
+    const bool out = u.dw || (!sums && p.last);
+    float *part = p.part + (static_cast<size_t>(u.split) * p.g_rows + row) * p.d;
     for_parts(taddr, o, [&](int c, float (&v)[64]) {
         const int col = u.col0 + c;
         const int n = min(64, p.d - col);
@@ -566,9 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ the copy of H for dW (first piece)
         if (LOGITS && p.Hc) {
             const int n16 = p.d / 8;
-            for (int r = blockIdx.x; r < p.M; r += gridDim.x) {
-                const bool keep = __ldg(p.targets + r) != p.ignore_index;
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.H + static_cast<size_t>(r) * p.d);
+            for (int r = blockIdx.x; r < p.g_rows; r += gridDim.x) {
+                const int from = p.lo && r >= p.lo ? r - p.lo : r;  // once for each part of G
+                const bool keep = from < p.M && __ldg(p.targets + from) != p.ignore_index;
+                const uint4 *src =
+                    reinterpret_cast<const uint4 *>(p.H + static_cast<size_t>(keep ? from : 0) * p.d);
                 uint4 *dst = reinterpret_cast<uint4 *>(p.Hc + static_cast<size_t>(r) * p.d);
 #pragma unroll 4
                 for (int i = lane; i < n16; i += 32)
@@ -621,22 +632,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// dH = scale * (split 0 + split 1 + ...), four values per thread.
+// dH = scale * (split 0 + split 1 + ...), of both parts of G, four values per thread: n4 of them,
+// stride4 from split to split, the second part's rows lo4 after the first's (0: one part).
 __global__ void __launch_bounds__(256) sum_kernel(const float4 *part, uint2 *dH, size_t n4,
-                                                  int splits, const float *scale) {
+                                                  size_t stride4, size_t lo4, int splits,
+                                                  const float *scale) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= n4) return;
     const float f = *scale;
-    float4 a = part[i];
-#pragma unroll 4
-    for (int s = 1; s < splits; ++s) {
-        const float4 x = part[s * n4 + i];
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4 x) {
         a.x += x.x;
         a.y += x.y;
         a.z += x.z;
         a.w += x.w;
+    };
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+        add(part[s * stride4 + i]);
+        if (lo4) add(part[s * stride4 + lo4 + i]);
     }
     dH[i] = make_uint2(pack_bf16(f * a.x, f * a.y), pack_bf16(f * a.z, f * a.w));
 }
@@ -706,9 +722,8 @@ cudaError_t launch_loss_operands(const LossGradMaps &m, const LossGradParams &p,
                : launch_grad<false, 2>(m, p, units, num_sms, stream);
 }
 
-cudaError_t launch_loss_sum(const float *part, void *dH, size_t n, int splits, const float *scale,
-                            cudaStream_t stream) {
-    const size_t n4 = n / 4;
+cudaError_t launch_loss_sum(const LossGradParams &p, cudaStream_t stream) {
+    const size_t n4 = static_cast<size_t>(p.M) * p.d / 4;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>((n4 + 255) / 256));
     cfg.blockDim = dim3(256);
@@ -718,8 +733,10 @@ cudaError_t launch_loss_sum(const float *part, void *dH, size_t n, int splits, c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sum_kernel, reinterpret_cast<const float4 *>(part),
-                              static_cast<uint2 *>(dH), n4, splits, scale);
+    return cudaLaunchKernelEx(&cfg, sum_kernel, reinterpret_cast<const float4 *>(p.part),
+                              reinterpret_cast<uint2 *>(p.dH), n4,
+                              static_cast<size_t>(p.g_rows) * p.d / 4,
+                              static_cast<size_t>(p.lo) * p.d / 4, p.splits, p.scale);
 }
 
 }  // namespace sb

@@ -99,6 +99,8 @@ struct LossGradParams {
     int M, d, V;
     int c0, cols;          // the piece: columns [c0, c0 + cols) of the vocabulary
     int ldg;               // row pitch of the piece buffer G, in elements
+    int lo;                // first row of G's second parts (0: G has one part)
+    int g_rows;            // of G and of the copy of H: M, or 2 * lo
     int first, last;       // of the pieces
     int row_tiles, col_tiles, d_tiles;  // 256-wide tiles of M, cols and d
     uint32_t row_tiles_inv, d_tiles_inv;  // min(floor(2^32 / tiles), 2^32 - 1)
@@ -110,11 +112,11 @@ struct LossGradParams {
     const int32_t *targets;
     const float *lse;
     const float *grad;     // [M] (NONE) or [1]; null: 1
-    uint16_t *G;           // [M][ldg] bf16
+    uint16_t *G;           // [g_rows][ldg] bf16
     const uint16_t *H;
-    uint16_t *Hc;          // [M][d]: H with its ignored rows zero; null: not to be written
+    uint16_t *Hc;          // [g_rows][d]: H with its ignored rows zero; null: not to be written
     float *scale;          // written by the logits kernel, read by the others
-    float *part;           // [splits][M][d] fp32 partial sums of dH
+    float *part;           // [splits][g_rows][d] fp32 partial sums of dH
     uint16_t *dH, *dW;
     uint32_t *epoch_word;
     unsigned long long *status;
@@ -131,11 +133,12 @@ struct LossGradMaps {
 
 // The rows' losses from the projection records (loss.cu).
 struct LossParams {
-    int M, T, V;
+    int M, T, V, d;
     int reduction;
     int ignore_index;
     float z_loss;
     Workspace ws;
+    const uint16_t *H, *W;
     const int32_t *targets;
     float *rows;           // [M] losses (the output for NONE, scratch otherwise)
     float *loss;           // [1] (SUM, MEAN)
@@ -183,8 +186,7 @@ cudaError_t launch_loss_logits(const LossGradMaps &m, const LossGradParams &p, i
                                cudaStream_t stream);
 cudaError_t launch_loss_operands(const LossGradMaps &m, const LossGradParams &p, int num_sms,
                                  cudaStream_t stream);
-cudaError_t launch_loss_sum(const float *part, void *dH, size_t n, int splits, const float *scale,
-                            cudaStream_t stream);
+cudaError_t launch_loss_sum(const LossGradParams &p, cudaStream_t stream);
 
 size_t lmhead_smem_bytes(int nb, int stages_a, int stages_b, bool vocab_mode, int flags,
                          int topk, int atoms);
