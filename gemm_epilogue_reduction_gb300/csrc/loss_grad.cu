@@ -82,14 +82,15 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint3
 }
 
 // This CTA's 128 rows (columns of the output, for B) of an operand from `mn`, reduction indexes
-// from `k`.  MN: the map's x is the operand's row and y the reduction index; else the other way
-// round.
+// from `k`.  MN: the map's x is the operand's row and y the reduction index, and `boxes` = 1 loads
+// the first 64 rows only; else the other way round.
 template <bool MN, int ATOMS>
 __device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *tm, uint32_t bar,
-                                             int mn, int k, uint64_t pol) {
+                                             int mn, int k, uint64_t pol, int boxes) {
     using R = Ring<ATOMS>;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
+        if (MN && b == 1 && boxes == 1) break;
         uint8_t *to = dst + b * R::kBoxBytes;
         if (MN)
             tma_load_2d_pair(to, tm, bar, mn + 64 * b, k, pol);
@@ -107,6 +108,9 @@ struct Unit {
     int row0, col0;      // of the output, this CTA's rows
     int split;
     int k0, kblocks;     // first reduction index and blocks of ATOMS * 64
+    int slices;          // 64-wide slices of the last block that hold anything
+    int n;               // columns of the tile that the MMA forms: 256, less (a multiple of 32) in
+                         // the last tile of dH and dW
 };
 
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
@@ -155,6 +159,17 @@ struct Walk {
         n += div_up(max(p.dw_units - taken - turn, 0), pairs);
     }
 
+    // the blocks of `len` reduction indexes
+    static __device__ __forceinline__ void reduce_over(Unit &u, int len) {
+        u.kblocks = div_up(len, KB);
+        u.slices = ATOMS - (u.kblocks * KB - len) / kBlockK;
+    }
+    // the columns of a tile of dH or dW
+    __device__ __forceinline__ void columns(Unit &u, int tile) const {
+        u.col0 = tile * kTile;
+        u.n = min(kTile, (p.d - u.col0 + 31) & ~31);
+    }
+
     __device__ __forceinline__ Unit at(int i) const {
         Unit u;
         u.split = 0;
@@ -165,19 +180,20 @@ struct Walk {
             div_mod(pair + i * pairs, p.row_tiles, p.row_tiles_inv, q, r);
             u.col0 = q * kTile;
             u.row0 = r * kTile + rank * kTileA;
-            u.kblocks = div_up(p.d, KB);
+            u.n = kTile;
+            reduce_over(u, p.d);
             return u;
         }
         if (i < own) {
             div_mod(pair + i * pairs, p.d_tiles, p.d_tiles_inv, q, r);
             u.split = q / p.row_tiles;
             u.row0 = (q - u.split * p.row_tiles) * kTile + rank * kTileA;
-            u.col0 = r * kTile;
+            columns(u, r);
             const int blocks = div_up(p.cols, KB);
             const int b0 = static_cast<int>(static_cast<long long>(blocks) * u.split / p.splits);
             const int b1 = static_cast<int>(static_cast<long long>(blocks) * (u.split + 1) / p.splits);
             u.k0 = b0 * KB;
-            u.kblocks = b1 - b0;
+            reduce_over(u, min(b1 * KB, p.cols) - u.k0);
             return u;
         }
         int j = i - own, t;
@@ -195,8 +211,8 @@ struct Walk {
         div_mod(t, p.d_tiles, p.d_tiles_inv, q, r);
         u.dw = true;
         u.row0 = q * kTile + rank * kTileA;
-        u.col0 = r * kTile;
-        u.kblocks = div_up(p.g_rows, KB);
+        columns(u, r);
+        reduce_over(u, p.g_rows);
         return u;
     }
 };
@@ -471,16 +487,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             // pipe's cycles).
             auto tile = [&](const Unit &u, auto a_mn, auto b_mn, const CUtensorMap *ta,
                             const CUtensorMap *tb, int b_row, int b_k, uint64_t pol_b) {
+                // 64 or 128 of the B operand's rows per CTA
+                const int boxes = decltype(b_mn)::value && u.n <= 128 ? 1 : 2;
+                const uint32_t bytes = 2 * (R::kOperand + boxes * R::kBoxBytes);
                 for (int kb = 0; kb < u.kblocks; ++kb) {
                     if (!bwait_cluster(&empty[st], ph ^ 1u, wc)) return false;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * R::kStage);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
                     uint8_t *sa = smem + st * R::kStage;
                     // the leader's barrier at its cluster address, for both CTAs
                     const uint32_t bar = mapa_rank(&full[st], 0);
                     const int k = u.k0 + kb * KB;  // past the end: zeros
-                    load_operand<decltype(a_mn)::value, ATOMS>(sa, ta, bar, u.row0, k, pol);
+                    load_operand<decltype(a_mn)::value, ATOMS>(sa, ta, bar, u.row0, k, pol, 2);
                     load_operand<decltype(b_mn)::value, ATOMS>(sa + R::kOperand, tb, bar, b_row,
-                                                               b_k + k, pol_b);
+                                                               b_k + k, pol_b, boxes);
                     ++issued;
                     if (++st == R::kStages) {
                         st = 0;
@@ -491,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int i = 0; ok && i < walk.n; ++i) {
                 const Unit u = walk.at(i);
-                const int bn = u.col0 + rank * kTileA;  // this CTA's half of the B operand
+                const int bn = u.col0 + rank * (u.n / 2);  // this CTA's half of the B operand
                 const std::true_type mn;
                 const std::false_type km;
                 if (LOGITS)
@@ -532,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kTile);
                 const bool a_mn = !LOGITS && u.dw, b_mn = !LOGITS;
-                const uint32_t idesc = idesc_bf16_f32(2 * kTileA, kTile) |
+                const uint32_t idesc = idesc_bf16_f32(2 * kTileA, u.n) |
                                        (a_mn ? kIdescAMajorMN : 0u) | (b_mn ? kIdescBMajorMN : 0u);
                 const uint64_t ad0 = a_mn ? mn_desc : k_desc;
                 const uint64_t bd0 = (b_mn ? mn_desc : k_desc) + (R::kOperand >> 4);
@@ -549,13 +568,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t so = (static_cast<uint32_t>(st) * R::kStage) >> 4;
+                    const int slices = kb + 1 < u.kblocks ? ATOMS : u.slices;
 #pragma unroll
-                    for (int at = 0; at < ATOMS; ++at)
+                    for (int at = 0; at < ATOMS; ++at) {
+                        if (at >= slices) break;  // nothing but zeros
 #pragma unroll
                         for (int ks = 0; ks < kBlockK / 16; ++ks)
                             umma_bf16_pair(d_tmem, ad0 + so + at * a_atom + ks * a_step,
                                            bd0 + so + at * b_atom + ks * b_step, idesc,
                                            (kb | at | ks) != 0 ? 1u : 0u);
+                    }
                     umma_commit_pair(&empty[st], kBoth);
                     any = true;
                     if (++st == R::kStages) {
