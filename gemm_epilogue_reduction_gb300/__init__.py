@@ -521,14 +521,16 @@ def project(H, W, k: int, surface: int = SB_TOKEN_LOGPROB, *, temperature: float
 def _tensor(name, t, shape, dtypes, device, where):
     """Refuses a tensor the kernels would misread: another shape or type, one that is not
     contiguous, or one that is not on the current CUDA device (its index: `device`)."""
+    if (t.shape == shape and t.dtype in dtypes and t.get_device() == device and
+            t.is_contiguous()):
+        return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{where}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
     if t.get_device() != device:
         raise ValueError(f"{where}: {name} is on {t.device}, not cuda:{device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{where}: {name} is not contiguous")
+    raise ValueError(f"{where}: {name} is not contiguous")
 
 
 class _on_stream:
@@ -605,7 +607,7 @@ def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.
     lse = torch.empty(M, dtype=torch.float32, device=H.device)
     st = L.sb_cross_entropy_forward(H.data_ptr(), W.data_ptr(), targets.data_ptr(), M, d, V,
                                     ignore_index, red, z_loss, loss.data_ptr(), lse.data_ptr(),
-                                    workspace.data_ptr(), workspace.numel(), _stream(None))
+                                    workspace.data_ptr(), workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
     if st != SB_OK:
         raise SbError(st, "sb_cross_entropy_forward")
     return {"loss": loss, "lse": lse, "workspace": workspace}
@@ -641,7 +643,7 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
     st = L.sb_cross_entropy_backward(H.data_ptr(), W.data_ptr(), targets.data_ptr(),
                                      lse.data_ptr(), _ptr(grad), M, d, V, ignore_index, red,
                                      z_loss, piece, _ptr(dH), _ptr(dW), workspace.data_ptr(),
-                                     workspace.numel(), _stream(None))
+                                     workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
     if st != SB_OK:
         raise SbError(st, "sb_cross_entropy_backward")
     return {"dH": dH, "dW": dW, "workspace": workspace}
@@ -694,11 +696,11 @@ def residual_norm(h, y, pre, *, post=None, gate=None, scale: float = 1.0, eps: f
         with _on_stream(stream):
             return residual_norm(h, y, pre, post=post, gate=gate, scale=scale, eps=eps)
     import torch
-    M, d, kind, ht, wt, _ = _norm_problem(h, y, pre, post, gate, "residual_norm")
+    M, d, kind, ht, wt, dev = _norm_problem(h, y, pre, post, gate, "residual_norm")
     h_out, x = torch.empty_like(h), torch.empty_like(y)
     st = lib().sb_residual_norm_forward(h.data_ptr(), y.data_ptr(), pre.data_ptr(), _ptr(post),
                                         _ptr(gate), kind, M, d, ht, wt, scale, eps,
-                                        h_out.data_ptr(), x.data_ptr(), _stream(None))
+                                        h_out.data_ptr(), x.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
     if st != SB_OK:
         raise SbError(st, "sb_residual_norm_forward")
     return {"h": h_out, "x": x}
@@ -731,7 +733,7 @@ def residual_norm_backward(dx, dh, h, y, pre, *, post=None, gate=None, scale: fl
                                      pre.data_ptr(), _ptr(post), _ptr(gate), kind, M, d, ht, wt,
                                      scale, eps, dh_out.data_ptr(), dy.data_ptr(),
                                      dpre.data_ptr(), _ptr(dpost), _ptr(dgate),
-                                     workspace.data_ptr(), workspace.numel(), _stream(None))
+                                     workspace.data_ptr(), workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
     if st != SB_OK:
         raise SbError(st, "sb_residual_norm_backward")
     return {"dh": dh_out, "dy": dy, "dpre": dpre, "dpost": dpost, "dgate": dgate,
@@ -768,33 +770,34 @@ class AdamW:
             if len(x) != n:
                 raise ValueError(f"{where}: {len(x)} {name} for {n} parameters")
         self._device = torch.cuda.current_device()
-        both, f32 = (torch.bfloat16, torch.float32), (torch.float32,)
+        dev, bf16, f32 = self._device, torch.bfloat16, torch.float32
+        code = torch.float8_e4m3fn if state_bits == 8 else f32
         self._list = (sb_adamw_tensor * n)()
-        for i, p in enumerate(self.params):
-            _tensor(f"params[{i}]", p, p.shape, both, self._device, where)
-            w = self.masters[i]
-            if w is not None:
-                if p.dtype != torch.bfloat16:
-                    raise TypeError(f"{where}: params[{i}] is float32 and has no master")
-                _tensor(f"masters[{i}]", w, p.shape, f32, self._device, where)
+        for i, (p, w, t) in enumerate(zip(self.params, self.masters, self._list)):
+            _tensor(f"params[{i}]", p, p.shape, (bf16, f32), dev, where)
             k = p.numel()
-            blocks = (k + 255) // 256
-            kinds = ([(k, torch.float8_e4m3fn)] * 2 + [(blocks, torch.float32)] * 2
-                     if state_bits == 8 else [(k, torch.float32)] * 2)
-            if self.states[i] is None:
-                self.states[i] = tuple(p.new_zeros(c, dtype=t) for c, t in kinds)
-            if len(self.states[i]) != len(kinds):
-                raise ValueError(f"{where}: states[{i}] has {len(self.states[i])} tensors, "
-                                 f"not {len(kinds)}")
-            for j, (s, (c, t)) in enumerate(zip(self.states[i], kinds)):
-                if s.numel() != c:
-                    raise ValueError(f"{where}: states[{i}][{j}] has {s.numel()} values, not {c}")
-                _tensor(f"states[{i}][{j}]", s, s.shape, (t,), self._device, where)
-            scales = self.states[i][2:] or (None, None)
-            self._list[i] = sb_adamw_tensor(
-                _ptr(p), None, _ptr(w), _ptr(self.states[i][0]), _ptr(self.states[i][1]),
-                _ptr(scales[0]), _ptr(scales[1]), k, float(decay[i]),
-                SB_F32 if p.dtype == torch.float32 else SB_BF16, SB_BF16)
+            if w is not None:
+                if p.dtype is not bf16:
+                    raise TypeError(f"{where}: params[{i}] is float32 and has no master")
+                _tensor(f"masters[{i}]", w, p.shape, (f32,), dev, where)
+                t.master = w.data_ptr()
+            shapes = ((k, code), (k, code))
+            if state_bits == 8:
+                shapes += (((k + 255) // 256, f32),) * 2
+            s = self.states[i]
+            if s is None:
+                s = self.states[i] = tuple(p.new_zeros(c, dtype=d) for c, d in shapes)
+            if len(s) != len(shapes):
+                raise ValueError(f"{where}: states[{i}] has {len(s)} tensors, not {len(shapes)}")
+            for j, (x, (c, d)) in enumerate(zip(s, shapes)):
+                if x.numel() != c:
+                    raise ValueError(f"{where}: states[{i}][{j}] has {x.numel()} values, not {c}")
+                _tensor(f"states[{i}][{j}]", x, x.shape, (d,), dev, where)
+            t.param, t.exp_avg, t.exp_avg_sq = p.data_ptr(), s[0].data_ptr(), s[1].data_ptr()
+            if state_bits == 8:
+                t.scale, t.scale_sq = s[2].data_ptr(), s[3].data_ptr()
+            t.n, t.weight_decay = k, decay[i]
+            t.param_type = SB_F32 if p.dtype is f32 else SB_BF16
         self.grads = None
         if grads is not None:
             self._bind(grads)

@@ -235,8 +235,8 @@ Plan plan_of(int64_t M, int64_t d, int64_t V, int64_t piece, bool with_dH, bool 
         const int64_t n = (2 * g_rows(M) * V + kPieceBytes - 1) / kPieceBytes;
         piece = (V + n - 1) / n;
     }
-    piece = (piece + 255) / 256 * 256;
-    pl.piece = piece < V ? piece : V;
+    pl.piece = piece < V ? (piece + 255) / 256 * 256 : V;
+    if (pl.piece > V) pl.piece = V;
     pl.ldg = (pl.piece + 63) / 64 * 64;
     pl.splits = choose_splits(M, d, pl.piece, with_dH, with_dW, pairs);
     pl.g_off = 256;

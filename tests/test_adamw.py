@@ -281,6 +281,29 @@ def test_new_gradients_streams_and_graphs():
 
 
 @gpu
+def test_offsets_past_32_bits():
+    """A tensor of more than 2^31 values: its ends and its middle step as short tensors do."""
+    n, k = 2 ** 31 + 1000, 512
+    p, g = (torch.zeros(n, dtype=BF, device="cuda") for _ in range(2))
+    st = [(torch.zeros(n, dtype=torch.uint8, device="cuda").view(F8),
+           torch.zeros(n, dtype=torch.uint8, device="cuda").view(F8),
+           torch.zeros((n + 255) // 256, device="cuda"), torch.zeros((n + 255) // 256, device="cuda"))]
+    at = [0, 2 ** 30, 2 ** 31 - 256, n // 256 * 256 - 256]  # the last one ends inside a block
+    sp, sg, _, sst = _make([min(k, n - a) for a in at], bits=8, master=False, seed=7)
+    for a, x, y, s in zip(at, sp, sg, sst):
+        p[a:a + x.numel()], g[a:a + x.numel()] = x, y
+        for j, per in ((0, 1), (1, 1), (2, 256), (3, 256)):
+            to = st[0][j].view(torch.uint8) if j < 2 else st[0][j]
+            to[a // per:a // per + s[j].numel()] = s[j].view(torch.uint8) if j < 2 else s[j]
+    sb.AdamW([p], [g], states=st, state_bits=8).step()
+    sb.AdamW(sp, sg, states=sst, state_bits=8).step()
+    for a, x, s in zip(at, sp, sst):
+        _equal(p[a:a + x.numel()], x, a)
+        for j, per in ((0, 1), (1, 1), (2, 256), (3, 256)):
+            _equal(st[0][j][a // per:a // per + s[j].numel()], s[j], (a, j))
+
+
+@gpu
 def test_python_refusals():
     p, g, w, st = _make([64, 65])
     with pytest.raises(ValueError):

@@ -348,6 +348,38 @@ def test_watchdog_of_the_backward_call():
 
 
 @gpu
+def test_offsets_past_32_bits():
+    """A head of more than 2^31 weights: the rows at its end, which 32-bit offsets would miss."""
+    M, d, V = 40, 4096, 530_000
+    W = torch.zeros(V, d, dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1, 255, 262_143, 262_144, 524_288, 524_289, V - 257, V - 256, V - 1]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    W[rows] = (torch.randn(len(rows), d, generator=g, device="cuda") * d ** -0.5).bfloat16()
+    H = torch.randn(M, d, generator=g, device="cuda").bfloat16()
+    t = torch.tensor([rows[i % len(rows)] for i in range(M)], dtype=torch.int32, device="cuda")
+    got = _run(H, W, t, reduction="sum", piece=0)
+    # all other logits are 0: the definition over the rows that are not, the rest counted
+    few = W[rows]
+    z = H.double() @ few.double().T
+    lse = torch.log(torch.exp(z).sum(1) + (V - len(rows)))
+    at = torch.arange(M, device="cuda") % len(rows)
+    loss = (lse - z[torch.arange(M, device="cuda"), at]).sum()
+    assert abs(float(got["loss"]) - float(loss)) <= 1e-5 * float(loss)
+    p = torch.exp(z - lse[:, None])
+    p[torch.arange(M, device="cuda"), at] -= 1
+    want = p.T @ H.double()
+    off = (got["dW"][rows].double() - want).norm() / want.norm()
+    assert off <= 2.0 ** -7, float(off)
+    off = (got["dH"].double() - p @ few.double()).norm() / (p @ few.double()).norm()
+    assert off <= 2.0 ** -7, float(off)
+    # a row of no target and weight 0: the same small share of H's sum everywhere
+    rest = (torch.exp(-lse)[None, :] @ H.double())[0]
+    for r in (2, 524_290, V - 2):
+        off = (got["dW"][r].double() - rest).norm() / rest.norm()
+        assert off <= 2.0 ** -7, (r, float(off))
+
+
+@gpu
 def test_python_refusals():
     H, W, t = _inputs(8, 64, 100, 2)
     lse = torch.zeros(8, device="cuda")
@@ -373,6 +405,7 @@ def test_python_refusals():
         sb.cross_entropy_backward(H, W, t, lse, need_dH=False, need_dW=False)
     with pytest.raises(sb.SbError):
         sb.cross_entropy_backward(H, W, t, lse, piece=-1)
+    sb.cross_entropy_backward(H, W, t, lse, piece=2 ** 63 - 1)  # one piece
     with pytest.raises(ValueError):
         sb.cross_entropy_backward(H, W, t, lse, grad=torch.ones(8, device="cuda"))
     with pytest.raises(ValueError):

@@ -255,6 +255,28 @@ def test_repeats_streams_and_graphs_give_the_same_bits():
 
 
 @gpu
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last rows, which 32-bit offsets would miss, are as alone."""
+    M, d, n = 350_003, 6144, 40
+    s = {k: torch.zeros(M, d, dtype=torch.bfloat16, device="cuda") for k in ("h", "y", "dx", "dh")}
+    small = _make(n, d, weights=torch.bfloat16, seed=10)
+    for k in s:
+        s[k][M - n:] = small[k]
+    kw = _kw(small)
+    f = sb.residual_norm(s["h"], s["y"], small["pre"], **kw)
+    g = sb.residual_norm(small["h"], small["y"], small["pre"], **kw)
+    for k in ("h", "x"):
+        assert torch.equal(f[k][M - n:], g[k]) and not f[k][:M - n].any(), k
+    b = sb.residual_norm_backward(s["dx"], s["dh"], s["h"], s["y"], small["pre"], **kw)
+    c = sb.residual_norm_backward(*(small[k] for k in ("dx", "dh", "h", "y", "pre")), **kw)
+    for k in ("dh", "dy"):
+        assert torch.equal(b[k][M - n:], c[k]) and not b[k][:M - n].any(), k
+    want = _backward_exact(small, 1.0, 1e-6)
+    for k in ("dpre", "dpost", "dgate"):
+        _within(b[k], want[k], k)
+
+
+@gpu
 def test_python_refusals():
     s = _make(8, 64)
     with pytest.raises(TypeError):
