@@ -171,8 +171,8 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         import torch
-        if torch.cuda.is_initialized():  # the raw handle: a tenth of current_stream()'s time
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if torch.cuda.is_initialized():
+            return _current(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -533,6 +533,12 @@ def _tensor(name, t, shape, dtypes, device, where):
     raise ValueError(f"{where}: {name} is not contiguous")
 
 
+def _current(device):
+    """The raw handle of torch's current stream (a tenth of current_stream()'s time)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 class _on_stream:
     """Makes `stream` (a torch stream or a raw handle) torch's current one, so that what a call
     allocates belongs to the stream its kernels run on."""
@@ -607,7 +613,7 @@ def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.
     lse = torch.empty(M, dtype=torch.float32, device=H.device)
     st = L.sb_cross_entropy_forward(H.data_ptr(), W.data_ptr(), targets.data_ptr(), M, d, V,
                                     ignore_index, red, z_loss, loss.data_ptr(), lse.data_ptr(),
-                                    workspace.data_ptr(), workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
+                                    workspace.data_ptr(), workspace.numel(), _current(dev))
     if st != SB_OK:
         raise SbError(st, "sb_cross_entropy_forward")
     return {"loss": loss, "lse": lse, "workspace": workspace}
@@ -643,7 +649,7 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
     st = L.sb_cross_entropy_backward(H.data_ptr(), W.data_ptr(), targets.data_ptr(),
                                      lse.data_ptr(), _ptr(grad), M, d, V, ignore_index, red,
                                      z_loss, piece, _ptr(dH), _ptr(dW), workspace.data_ptr(),
-                                     workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
+                                     workspace.numel(), _current(dev))
     if st != SB_OK:
         raise SbError(st, "sb_cross_entropy_backward")
     return {"dH": dH, "dW": dW, "workspace": workspace}
@@ -700,7 +706,7 @@ def residual_norm(h, y, pre, *, post=None, gate=None, scale: float = 1.0, eps: f
     h_out, x = torch.empty_like(h), torch.empty_like(y)
     st = lib().sb_residual_norm_forward(h.data_ptr(), y.data_ptr(), pre.data_ptr(), _ptr(post),
                                         _ptr(gate), kind, M, d, ht, wt, scale, eps,
-                                        h_out.data_ptr(), x.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+                                        h_out.data_ptr(), x.data_ptr(), _current(dev))
     if st != SB_OK:
         raise SbError(st, "sb_residual_norm_forward")
     return {"h": h_out, "x": x}
@@ -733,7 +739,7 @@ def residual_norm_backward(dx, dh, h, y, pre, *, post=None, gate=None, scale: fl
                                      pre.data_ptr(), _ptr(post), _ptr(gate), kind, M, d, ht, wt,
                                      scale, eps, dh_out.data_ptr(), dy.data_ptr(),
                                      dpre.data_ptr(), _ptr(dpost), _ptr(dgate),
-                                     workspace.data_ptr(), workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
+                                     workspace.data_ptr(), workspace.numel(), _current(dev))
     if st != SB_OK:
         raise SbError(st, "sb_residual_norm_backward")
     return {"dh": dh_out, "dy": dy, "dpre": dpre, "dpost": dpost, "dgate": dgate,

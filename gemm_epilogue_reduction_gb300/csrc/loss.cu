@@ -387,8 +387,11 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
 
     uint16_t *copy = dW ? reinterpret_cast<uint16_t *>(ws + pl.h_off) : nullptr;
     const int rows = loss_box_rows(p.row_tiles);
+    // fewer rows of H than a box has: a box of as many (a multiple of the swizzle's eight)
+    const int h_rows = M < rows ? static_cast<int>((M + 7) / 8 * 8) : rows;
+    p.h_box_bytes = static_cast<uint32_t>(h_rows) * 128;
     LossGradMaps logits{}, operands{};  // maps of gradients not asked for are not used
-    if (!encode_bf16_map(&logits.x, H, M, d, rows) || !encode_bf16_map(&logits.y, W, V, d, rows) ||
+    if (!encode_bf16_map(&logits.x, H, M, d, h_rows) || !encode_bf16_map(&logits.y, W, V, d, rows) ||
         !encode_bf16_map(&operands.z, copy ? copy : H, copy ? p.g_rows : M, d, rows) ||
         !encode_bf16_map(&operands.dw, dW ? dW : W, V, d, 32) ||
         !encode_bf16_map(&operands.dh, dH ? dH : H, M, d, 32))

@@ -82,15 +82,16 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint3
 }
 
 // This CTA's 128 rows (columns of the output, for B) of an operand from `mn`, reduction indexes
-// from `k`.  MN: the map's x is the operand's row and y the reduction index, and `boxes` = 1 loads
-// the first 64 rows only; else the other way round.
+// from `k`, `boxes` (0 to 2) of its boxes.  MN: the map's x is the operand's row and y the
+// reduction index; else the other way round.  What is not loaded keeps whatever shared memory
+// held: those rows of the operand meet only rows (columns) of the output that nothing stores.
 template <bool MN, int ATOMS>
 __device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *tm, uint32_t bar,
                                              int mn, int k, uint64_t pol, int boxes) {
     using R = Ring<ATOMS>;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        if (MN && b == 1 && boxes == 1) break;
+        if (b >= boxes) break;
         uint8_t *to = dst + b * R::kBoxBytes;
         if (MN)
             tma_load_2d_pair(to, tm, bar, mn + 64 * b, k, pol);
@@ -99,6 +100,12 @@ __device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *tm
         else
             tma_load_2d_pair(to, tm, bar, k, mn + 64 * b, pol);
     }
+}
+// The boxes of a K-major operand's rows from mn that hold any of `rows` rows.
+template <int ATOMS>
+__device__ __forceinline__ int boxes_of(int rows, int mn) {
+    if (ATOMS == 2) return rows > mn ? 2 : 0;  // both 64-wide slices of the same 128 rows
+    return min(max((rows - mn + 63) >> 6, 0), 2);
 }
 constexpr uint32_t kIdescAMajorMN = 1u << 15, kIdescBMajorMN = 1u << 16;
 
@@ -218,19 +225,6 @@ struct Walk {
 };
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ bool epi_any(bool pred) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 256, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}\n"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(pred))
-        : "memory");
-    return r != 0;
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -280,23 +274,28 @@ struct Out {
     int q, h, lane;
 };
 
-// f(column in the tile, values): what becomes of 64 columns of the thread's row.
+// This warp is done with the accumulator.
+__device__ __forceinline__ void release(const Out &o) {
+    tc_fence_before();
+    __syncwarp();
+    if (o.lane == 0) {
+        if (o.tempty_remote)
+            mbar_arrive_remote(o.tempty_remote);
+        else
+            mbar_arrive(o.tempty);
+    }
+}
+
+// f(column in the tile, values): what becomes of 64 columns of the thread's row; `parts` of them
+// (of two) hold anything to store.
 template <typename F>
-__device__ __forceinline__ void for_parts(uint32_t taddr, Out &o, F f) {
+__device__ __forceinline__ void for_parts(uint32_t taddr, int parts, const Out &o, F f) {
+    if (parts <= 0) return release(o);
 #pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
+    for (int part = 0; part < parts; ++part) {
         uint32_t raw[64];
         tmem_ld32x32b_x64(taddr + 128 * o.h + 64 * part, raw);
-        if (part == 1) {  // the accumulator is read
-            tc_fence_before();
-            __syncwarp();
-            if (o.lane == 0) {
-                if (o.tempty_remote)
-                    mbar_arrive_remote(o.tempty_remote);
-                else
-                    mbar_arrive(o.tempty);
-            }
-        }
+        if (part + 1 == parts) release(o);
         float v[64];
 #pragma unroll
         for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(raw[j]);
@@ -349,8 +348,8 @@ __device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const C
         }
     }
     const bool dead = a == 0.f && b == 0.f;  // an ignored row, whatever its logits are
-    for_parts(taddr, o, [&](int c, float (&v)[64]) {
-        if (row0 >= p.M || u.col0 + c >= p.cols) return;
+    const int parts = row0 < p.M ? min(div_up(p.cols - u.col0 - 128 * o.h, 64), 2) : 0;
+    for_parts(taddr, parts, o, [&](int c, float (&v)[64]) {
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
             const float e = a * ex2_approx(fmaf(v[j], kLog2e, -l2));
@@ -377,10 +376,10 @@ __device__ __forceinline__ void epilogue_operands(const LossGradParams &p, const
     const bool through = !u.dw && (sums || !(p.first && p.last));
     const bool out = u.dw || (!sums && p.last);
     float *part = p.part + (static_cast<size_t>(u.split) * p.g_rows + row) * p.d;
-    for_parts(taddr, o, [&](int c, float (&v)[64]) {
+    const int parts = row0 < rows ? min(div_up(p.d - u.col0 - 128 * o.h, 64), 2) : 0;
+    for_parts(taddr, parts, o, [&](int c, float (&v)[64]) {
         const int col = u.col0 + c;
         const int n = min(64, p.d - col);
-        if (row0 >= rows || n <= 0) return;
         if (u.kblocks == 0) {
 #pragma unroll
             for (int j = 0; j < 64; ++j) v[j] = 0.f;
@@ -487,9 +486,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             // pipe's cycles).
             auto tile = [&](const Unit &u, auto a_mn, auto b_mn, const CUtensorMap *ta,
                             const CUtensorMap *tb, int b_row, int b_k, uint64_t pol_b) {
-                // 64 or 128 of the B operand's rows per CTA
+                // 64 or 128 of the B operand's rows per CTA, and those of A that there are
                 const int boxes = decltype(b_mn)::value && u.n <= 128 ? 1 : 2;
-                const uint32_t bytes = 2 * (R::kOperand + boxes * R::kBoxBytes);
+                int a_boxes = 2, a_all = 4;
+                if (!decltype(a_mn)::value) {
+                    const int rows = LOGITS ? p.M : p.g_rows, r0 = u.row0 - rank * kTileA;
+                    a_boxes = boxes_of<ATOMS>(rows, u.row0);
+                    a_all = boxes_of<ATOMS>(rows, r0) + boxes_of<ATOMS>(rows, r0 + kTileA);
+                }
+                const uint32_t bytes = a_all * (LOGITS ? p.h_box_bytes : R::kBoxBytes) +
+                                       2 * boxes * R::kBoxBytes;
                 for (int kb = 0; kb < u.kblocks; ++kb) {
                     if (!bwait_cluster(&empty[st], ph ^ 1u, wc)) return false;
                     if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
@@ -497,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the leader's barrier at its cluster address, for both CTAs
                     const uint32_t bar = mapa_rank(&full[st], 0);
                     const int k = u.k0 + kb * KB;  // past the end: zeros
-                    load_operand<decltype(a_mn)::value, ATOMS>(sa, ta, bar, u.row0, k, pol, 2);
+                    load_operand<decltype(a_mn)::value, ATOMS>(sa, ta, bar, u.row0, k, pol,
+                                                               a_boxes);
                     load_operand<decltype(b_mn)::value, ATOMS>(sa + R::kOperand, tb, bar, b_row,
                                                                b_k + k, pol_b, boxes);
                     ++issued;
@@ -630,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int b = i & 1;
             const uint32_t tph = (i >> 1) & 1;
             const bool ok = p.debug_stall ? bwait(stall, 0, wc) : bwait_cluster(&tfull[b], tph, wc);
-            if (epi_any(!ok)) break;
+            if (__any_sync(0xFFFFFFFFu, !ok)) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * o.q) << 16) +
                                    static_cast<uint32_t>(b * kTile);

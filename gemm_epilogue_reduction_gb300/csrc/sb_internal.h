@@ -103,6 +103,7 @@ struct LossGradParams {
     int g_rows;            // of G and of the copy of H: M, or 2 * lo
     int first, last;       // of the pieces
     int row_tiles, col_tiles, d_tiles;  // 256-wide tiles of M, cols and d
+    uint32_t h_box_bytes;  // of a box of H in the logits kernel
     uint32_t row_tiles_inv, d_tiles_inv;  // min(floor(2^32 / tiles), 2^32 - 1)
     int splits;            // of the reduction over the piece's columns in dH
     int dh_units, dw_units, fill;       // operands_kernel's tiles and how they are dealt out
