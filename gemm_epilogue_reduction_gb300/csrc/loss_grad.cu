@@ -661,16 +661,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// dH = scale * (split 0 + split 1 + ...), of both parts of G, four values per thread: n4 of them,
-// stride4 from split to split, the second part's rows lo4 after the first's (0: one part).
-__global__ void __launch_bounds__(256) sum_kernel(const float4 *part, uint2 *dH, size_t n4,
-                                                  size_t stride4, size_t lo4, int splits,
-                                                  const float *scale) {
+// dH = scale * (split 0 + split 1 + ...), of both parts of G: n4 groups of four values, stride4
+// from split to split, the second part's rows lo4 after the first's (0: one part).  A block sums
+// 32 groups: eight warps take an eighth of the splits each, in ascending order, and their sums
+// add up in ascending order.
+constexpr int kSumSlices = 8;
+__global__ void __launch_bounds__(32 * kSumSlices) sum_kernel(const float4 *part, uint2 *dH,
+                                                              size_t n4, size_t stride4,
+                                                              size_t lo4, int splits,
+                                                              const float *scale) {
+    __shared__ float4 sh[kSumSlices][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i >= n4) return;
-    const float f = *scale;
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const size_t i = static_cast<size_t>(blockIdx.x) * 32 + lane;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](const float4 x) {
         a.x += x.x;
@@ -678,11 +682,20 @@ __global__ void __launch_bounds__(256) sum_kernel(const float4 *part, uint2 *dH,
         a.z += x.z;
         a.w += x.w;
     };
+    if (i < n4) {
+        const int s1 = splits * (slice + 1) / kSumSlices;
 #pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-        add(part[s * stride4 + i]);
-        if (lo4) add(part[s * stride4 + lo4 + i]);
+        for (int s = splits * slice / kSumSlices; s < s1; ++s) {
+            add(part[s * stride4 + i]);
+            if (lo4) add(part[s * stride4 + lo4 + i]);
+        }
     }
+    sh[slice][lane] = a;
+    __syncthreads();
+    if (slice != 0 || i >= n4) return;
+    const float f = *scale;
+#pragma unroll
+    for (int s = 1; s < kSumSlices; ++s) add(sh[s][lane]);
     dH[i] = make_uint2(pack_bf16(f * a.x, f * a.y), pack_bf16(f * a.z, f * a.w));
 }
 
@@ -754,8 +767,8 @@ cudaError_t launch_loss_operands(const LossGradMaps &m, const LossGradParams &p,
 cudaError_t launch_loss_sum(const LossGradParams &p, cudaStream_t stream) {
     const size_t n4 = static_cast<size_t>(p.M) * p.d / 4;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((n4 + 255) / 256));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(static_cast<unsigned>((n4 + 31) / 32));
+    cfg.blockDim = dim3(32 * kSumSlices);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
