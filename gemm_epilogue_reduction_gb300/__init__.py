@@ -770,9 +770,11 @@ class AdamW:
         self.lr, self.betas, self.eps = lr, tuple(betas), eps
         self.state_bits, self.step_count = state_bits, step
         self.masters = [None] * n if masters is None else list(masters)
-        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        decay = (list(weight_decay) if isinstance(weight_decay, (list, tuple))
+                 else [weight_decay] * n)
         self.states = [None] * n if states is None else [tuple(s) for s in states]
-        for name, x in (("masters", self.masters), ("weight_decay", decay), ("states", self.states)):
+        for name, x in (("masters", self.masters), ("weight_decay", decay),
+                        ("states", self.states)):
             if len(x) != n:
                 raise ValueError(f"{where}: {len(x)} {name} for {n} parameters")
         self._device = torch.cuda.current_device()

@@ -6,12 +6,16 @@
 //   loss_r = lse_r - z_r,target + z_loss·lse_r²,  0 where the target is the ignored index,
 // one block per row.  The tensor cores truncate as they accumulate, which leaves a logit of d =
 // 5120 products some 1e-5 short; the target's logit stands alone in the loss (every other one is
-// averaged in lse), so its block forms it again in fp32 FMAs and lse follows by the target's share
-// p of the sum:  lse += log(1 + p·(exp(z - z_tc) - 1)).  The last block to finish adds the rows' losses up (SUM, MEAN) in a
-// fixed order, so the bits do not depend on which block that is.  The rows kernel reads
-// 8 bytes for each 128 columns of a row: next to the GEMM's time it is small (M = 4096,
-// V = 200,064: 51 MB).  Backward is loss_grad.cu; its host side here cuts the vocabulary into
-// pieces and chooses the split of the dH reduction.
+// averaged in lse), so its block forms it again in fp32 FMAs, and lse follows by the target's
+// share p of the sum:  lse += log(1 + p·(exp(z - z_tc) - 1)).  The last block to finish adds the
+// rows' losses up (SUM, MEAN) in a fixed order, so the bits do not depend on which block that is.
+//
+// The rows kernel reads 8 bytes for each 128 columns of a row, H's row and the target's row of W:
+// next to the GEMM it is small (M = 4096, d = 6144, V = 200,064: 150 MB, 35 us against 5.1 ms),
+// and for few rows its chain of dependent loads costs some 4 us.  The GEMM is bound by reading W
+// up to some 256 rows (16 x 5120 x 151,936: 232 us in all, 99 % of the measured memory rate) and
+// by the tensor cores beyond.  Backward is loss_grad.cu; its host side here cuts the vocabulary
+// into pieces and chooses the split of the dH reduction.
 #include <cmath>
 
 #include "sb.h"

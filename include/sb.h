@@ -459,8 +459,8 @@ size_t sb_cross_entropy_backward_workspace_bytes(int64_t M, int64_t d, int64_t V
 /*
  * The gradients, in pieces of the vocabulary: for each piece the logits are formed again and
  * G = dL/dz of the piece is written in bf16 (up to 32 rows: in two bf16 parts) to the
- * workspace, then dH += G·W and dW = Gᵀ·H in one launch.  Accumulation is fp32; dH and dW are rounded to bf16 once.  Every sum has a
- * fixed order, so equal calls give equal bits.
+ * workspace, then dH += G·W and dW = Gᵀ·H in one launch.  Accumulation is fp32; dH and dW are
+ * rounded to bf16 once.  Every sum has a fixed order, so equal calls give equal bits.
  *   H, W, targets, M, d, V, ignore_index, reduction, z_loss   as in the forward call.
  *   lse         device float [M], from the forward call.
  *   grad        device float: the incoming gradient, [M] for SB_REDUCE_NONE, else [1]; NULL
@@ -548,8 +548,9 @@ int32_t sb_residual_norm_backward(const void *dx, const void *dh, const void *h,
  * receives its rounding to bf16), else param.  The moments are held
  *   state_bits = 32: in fp32;
  *   state_bits = 8: as E4M3 codes (the 8-bit floating-point type with 4 exponent and 3 mantissa
- *     bits, largest value 448) in blocks of 256 consecutive values with one fp32 scale each (the
- *     largest magnitude top / 448, codes of value * (448 * (1 / top)); a block whose largest is below 2^-100 is stored as zeros).
+ *     bits, largest value 448) in blocks of 256 consecutive values with one fp32 scale each (top /
+ *     448 with the largest magnitude top; the codes are those of value * (1 / top * 448); a block
+ *     whose top is below 2^-100 is stored as zeros).
  *     exp_avg_sq then holds sqrt(v), whose range of exponents is half of v's, and a root that is
  *     not zero is never stored as zero, so that no small v turns into a division by eps alone.
  *     The step itself uses m and v before they are stored.
