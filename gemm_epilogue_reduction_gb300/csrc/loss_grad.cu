@@ -282,15 +282,18 @@ struct Out {
     int q, h, lane;
 };
 
-// This warp is done with the accumulator.
+// This warp is done with the accumulator: its loads from TMEM have completed (each one waits), so
+// the arrival has no memory writes to publish, and is a relaxed one.  With release semantics it
+// waited some 1000 cycles for the stores of the part before, which nothing behind the barrier
+// reads: a third of the time of a dW tile of few rows.
 __device__ __forceinline__ void release(const Out &o) {
     tc_fence_before();
     __syncwarp();
     if (o.lane == 0) {
         if (o.tempty_remote)
-            mbar_arrive_remote(o.tempty_remote);
+            mbar_arrive_remote_relaxed(o.tempty_remote);
         else
-            mbar_arrive(o.tempty);
+            mbar_arrive_relaxed(o.tempty);
     }
 }
 
@@ -338,39 +341,48 @@ __device__ __forceinline__ void store_box(const CUtensorMap *tm, Out &o, const f
     }
 }
 
+// What G's row needs of its loss: G_rj = a·exp(z_rj - lse_r) - (j = target ? b : 0).
+struct RowTerms {
+    int row0 = -1;       // of the warp's rows; the thread's is row0 + lane
+    int target = -1;     // inside the vocabulary, else -1
+    float a = 0.f, b = 0.f, l2 = 0.f;  // l2: lse·log2(e)
+};
+__device__ __forceinline__ RowTerms row_terms(const LossGradParams &p, int row0, int lane,
+                                              float scale) {
+    RowTerms r;
+    r.row0 = row0;
+    const int row = row0 + lane;
+    if (row >= p.M) return r;
+    const int t = __ldg(p.targets + row);
+    if (t == p.ignore_index) return r;
+    const float lse = __ldg(p.lse + row);
+    // NONE: the row's own weight relative to the shared scale
+    r.b = (p.reduction == 0 && p.grad) ? (scale > 0.f ? __ldg(p.grad + row) / scale : 0.f) : 1.f;
+    r.a = r.b * (1.f + 2.f * p.z_loss * lse);
+    r.l2 = lse * kLog2e;
+    if (t >= 0 && t < p.V) r.target = t;
+    return r;
+}
+
 template <int ATOMS>
 __device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const CUtensorMap *tmG,
                                                 const Unit &u, uint32_t taddr, Out &o,
-                                                float scale, uint64_t pol) {
-    const int row0 = u.row0 + 32 * o.q, row = row0 + o.lane;
-    float a = 0.f, b = 0.f, l2 = 0.f;
-    int tgt = -1;
-    if (row < p.M) {
-        const int t = __ldg(p.targets + row);
-        if (t != p.ignore_index) {
-            const float lse = __ldg(p.lse + row);
-            // NONE: the row's own weight relative to the shared scale
-            b = (p.reduction == 0 && p.grad) ? (scale > 0.f ? __ldg(p.grad + row) / scale : 0.f)
-                                             : 1.f;
-            a = b * (1.f + 2.f * p.z_loss * lse);
-            l2 = lse * kLog2e;
-            // the target's column in this tile (a target outside the vocabulary has none)
-            if (t >= 0 && t < p.V) tgt = t - p.c0 - u.col0;
-        }
-    }
-    const bool dead = a == 0.f && b == 0.f;  // an ignored row, whatever its logits are
-    const int parts = row0 < p.M ? min(div_up(p.cols - u.col0 - 128 * o.h, 64), 2) : 0;
+                                                const RowTerms &r, uint64_t pol) {
+    // the target's column in this tile
+    const int tgt = r.target >= 0 ? r.target - p.c0 - u.col0 : -1;
+    const bool dead = r.a == 0.f && r.b == 0.f;  // an ignored row, whatever its logits are
+    const int parts = r.row0 < p.M ? min(div_up(p.cols - u.col0 - 128 * o.h, 64), 2) : 0;
     for_parts(taddr, parts, o, [&](int c, float (&v)[64]) {
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
-            const float e = a * ex2_approx(fmaf(v[j], kLog2e, -l2));
-            v[j] = dead ? 0.f : (c + j == tgt ? e - b : e);
+            const float e = r.a * ex2_approx(fmaf(v[j], kLog2e, -r.l2));
+            v[j] = dead ? 0.f : (c + j == tgt ? e - r.b : e);
         }
-        store_box<ATOMS>(tmG, o, v, u.col0 + c, row0, pol);
+        store_box<ATOMS>(tmG, o, v, u.col0 + c, r.row0, pol);
         if (p.lo) {  // (rows past M, up to the next 32, are zero in both)
 #pragma unroll
             for (int j = 0; j < 64; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
-            store_box<ATOMS>(tmG, o, v, u.col0 + c, p.lo + row0, pol);
+            store_box<ATOMS>(tmG, o, v, u.col0 + c, p.lo + r.row0, pol);
         }
     });
 }
@@ -645,19 +657,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
             scale = *p.scale;
         }
+        // the leader's release barriers
+        const uint32_t remote0 = rank == 1 ? mapa_rank(&tempty[0], 0) : 0u;
+        const uint32_t remote1 = rank == 1 ? mapa_rank(&tempty[1], 0) : 0u;
+        RowTerms terms;
         for (int i = 0; i < walk.n; ++i) {
             const Unit u = walk.at(i);
             const int b = i & 1;
             const uint32_t tph = (i >> 1) & 1;
+            // the rows' terms while the tile is formed (few rows: once)
+            const int row0 = u.row0 + 32 * o.q;
+            if (LOGITS && row0 != terms.row0) terms = row_terms(p, row0, lane, scale);
             const bool ok = p.debug_stall ? bwait(stall, 0, wc) : bwait_cluster(&tfull[b], tph, wc);
             if (__any_sync(0xFFFFFFFFu, !ok)) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * o.q) << 16) +
                                    static_cast<uint32_t>(b * kTile);
             o.tempty = &tempty[b];
-            o.tempty_remote = rank == 1 ? mapa_rank(&tempty[b], 0) : 0u;
+            o.tempty_remote = b ? remote1 : remote0;
             if (LOGITS)
-                epilogue_logits<ATOMS>(p, &m.g, u, taddr, o, scale, pol);
+                epilogue_logits<ATOMS>(p, &m.g, u, taddr, o, terms, pol);
             else
                 epilogue_operands<ATOMS>(p, &m.dw, &m.dh, u, taddr, o, scale, pol);
         }
