@@ -168,8 +168,9 @@ int32_t check_loss(const void *H, const void *W, const int32_t *targets, int64_t
 
 // Rows of G: up to kTwoPartRows rows are held in two bf16 parts (loss_grad.cu), the second ones
 // from row `lo` on, which is the next multiple of an output box's 32 rows.  Up to 32 rows they
-// cost nothing (both parts are one 64-wide reduction block of dW); at 64 rows they would cost 7 %
-// (4096 x 151,936: 993 against 932 us a step), and the roundings of that many targets average out.
+// cost nothing (both parts are one 64-wide reduction block of dW); at 64 rows they cost 7 % (4096 x
+// 151,936, a step: 993 against 932 us when that was measured), and the roundings of that many
+// targets average out.
 constexpr int64_t kTwoPartRows = 32;
 int64_t lo_row(int64_t M) { return M <= kTwoPartRows ? (M + 31) / 32 * 32 : 0; }
 int64_t g_rows(int64_t M) { return M <= kTwoPartRows ? 2 * lo_row(M) : M; }
@@ -207,8 +208,8 @@ Work work_of(int64_t M, int64_t d, int64_t cols, bool with_dH, bool with_dW) {
 // blocks for 76 pairs); every split adds its fp32 partial sums' traffic.  Of several row tiles
 // the pairs without a dH unit can make it up with dW tiles, as both are bound by the tensor
 // cores; of one row tile dH is bound by reading W, which wants all SMs, so its rounds count in
-// full (64 rows, d = 4096, V = 151,936: two splits on 32 pairs took 541 us, 19 on all of them
-// take 505 us).
+// full (64 rows, d = 4096, V = 151,936, both products: two splits on 32 pairs took 541 us when 19
+// on all of them took 505).
 int choose_splits(int64_t M, int64_t d, int64_t piece, bool with_dH, bool with_dW, int pairs) {
     if (!with_dH) return 1;
     const Work w = work_of(M, d, piece, with_dH, with_dW);

@@ -26,12 +26,14 @@
 // further rows of G, which fill the row tile and the 64-wide reduction block that few rows leave
 // empty.  Accumulation is fp32 in TMEM and, over the pieces, fp32 in memory.
 //
-// Bounds.  From some 500 rows on the tensor cores (and under a long load the power limit): 4096 x
-// 6144 x 200,064 takes 23.6 ms forward and backward, 1.71 PFLOP/s over its four products of
+// Bounds.  From some 2000 rows on the tensor cores (and under a long load the power limit): 4096 x
+// 6144 x 200,064 takes 23.7 ms forward and backward, 1.70 PFLOP/s over its four products of
 // 2·M·d·V (the logits are formed twice), the rate of a library product under the same load; the
-// kernels have 90 to 92 % of the tensor pipe's cycles there.  For few rows the memory: W is read
-// three times (forward, logits, dH) and dW written once, and writes alone reach 4.0 TB/s on this
-// part: 64 x 4096 x 151,936 takes 892 us (forward 189, logits 195, dH and dW 490).
+// kernels have 90 to 92 % of the tensor pipe's cycles there.  Around 500 rows what L2 delivers to
+// an SM (some 54 bytes a cycle; a 256 x 256 tile wants 64 per CTA for the full tensor rate, and a
+// dW tile of so few rows stores 64 KB besides).  For few rows the memory: W is read three times
+// (forward, logits, dH) and dW written once: 64 x 4096 x 151,936 takes 797 us (forward 189, logits
+// 195, dH 204, dW 209).
 //
 // Both kernels: persistent CTA pairs, one cta_group::2 MMA of 256 x 256 per 16-wide K step
 // (tcgen05, bf16 x bf16 -> fp32), joint TMA stages, two TMEM accumulators, eight epilogue
@@ -145,9 +147,9 @@ __device__ __forceinline__ void div_mod(int t, int d, uint32_t inv, int &q, int 
 // out in turn; the short dW tiles then even out the pairs: those that are one dH unit behind
 // the others take `fill` dW tiles each before the rest is dealt out in turn.
 //
-// (With few rows dH reads W and dW writes its gradient, both at the memory's pace.  Half of the
-// pairs going through their units from the end, so that reads and writes overlap, was slower: 545
-// against 505 us at 64 x 4096 x 151,936.)
+// (With few rows dH reads W and dW writes its gradient.  Letting half of the pairs start with dW,
+// so that reads and writes overlap, was slower: 747 against 681 us for the backward call at 64 x
+// 4096 x 151,936.)
 template <bool LOGITS, int ATOMS>
 struct Walk {
     static constexpr int KB = ATOMS * kBlockK;
@@ -272,8 +274,9 @@ __device__ __forceinline__ float shared_scale(const LossGradParams &p, int e, fl
 // ------------------------------------------------------------------ epilogues
 // Warp (quadrant q, half h) owns 32 rows of the tile (thread: one row) and 128 of its 256
 // columns, in two parts of 64.  bf16 output leaves through shared memory: the warp's 32 x 64 box
-// in the 128-byte swizzle, then one TMA store (32 rows of whole 128-byte lines; stored row by
-// row from the threads, the short dW tiles of few tokens were bound by the stores).
+// in the 128-byte swizzle, then one TMA store (32 rows of whole 128-byte lines; from the threads,
+// row by row, the dW tiles of few rows took 40 % longer, and read back from shared memory in
+// whole lines 4 %).
 struct Out {
     uint8_t *box;        // this warp's boxes, 1024-byte aligned
     int next;            // the box that is written next
