@@ -352,3 +352,23 @@ def test_c_refusals():
                {"master": P + 2}, {"exp_avg": P + 2}, {"exp_avg_sq": P + 1},
                {"bits": 8, "scale": P + 2}, {"gs": P + 2}):
         assert call(**kw) == off, kw
+
+
+def test_the_descriptor_has_the_c_layout(tmp_path):
+    """sb_adamw_tensor as a C compiler lays it out is what the binding passes."""
+    import ctypes
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    names = [n for n, _ in sb.sb_adamw_tensor._fields_]
+    lines = "".join(f'printf("%zu ", offsetof(sb_adamw_tensor, {n}));' for n in names)
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include "sb.h"\nint main(void) {' + lines +
+                   'printf("%zu", sizeof(sb_adamw_tensor)); return 0; }\n')
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-I", os.path.join(root, "include"),
+                    str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    want = [getattr(sb.sb_adamw_tensor, n).offset for n in names]
+    assert got == want + [ctypes.sizeof(sb.sb_adamw_tensor)]
