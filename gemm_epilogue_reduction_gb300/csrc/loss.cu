@@ -19,7 +19,6 @@
 #include <cmath>
 
 #include "sb.h"
-#include "sb_combine_math.cuh"
 #include "sb_internal.h"
 #include "sb_ptx.cuh"
 
