@@ -539,21 +539,19 @@ def _current(device):
     return torch._C._cuda_getCurrentRawStream(device)
 
 
-class _on_stream:
-    """Makes `stream` (a torch stream or a raw handle) torch's current one, so that what a call
-    allocates belongs to the stream its kernels run on."""
-
-    def __init__(self, stream):
-        import torch
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        self._ctx = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        self._ctx.__enter__()
-
-    def __exit__(self, *exc):
-        self._ctx.__exit__(*exc)
+def _on_stream(stream, call, *tensors):
+    """call() with `stream` (a torch stream or a raw handle) as torch's current one, so that what
+    it allocates belongs to the stream its kernels run on; torch's allocator learns that the
+    given tensors (None are skipped) are read there, and keeps their memory until then."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        out = call()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return out
 
 
 def _reduction(reduction, where):
@@ -599,9 +597,9 @@ def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.
     Asynchronous on ``stream``; raises SbError on a bad status. A target outside [0, V) that is
     not ``ignore_index`` gives a NaN loss, and ``device_status`` of the workspace reports it."""
     if stream is not None:
-        with _on_stream(stream):
-            return cross_entropy(H, W, targets, ignore_index=ignore_index, z_loss=z_loss,
-                                 reduction=reduction, workspace=workspace)
+        return _on_stream(stream, lambda: cross_entropy(
+            H, W, targets, ignore_index=ignore_index, z_loss=z_loss, reduction=reduction,
+            workspace=workspace), H, W, targets, workspace)
     import torch
     red = _reduction(reduction, "cross_entropy")
     M, d, V, dev = _loss_problem(H, W, targets, "cross_entropy")
@@ -627,11 +625,10 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
     for ones). The vocabulary is worked off in pieces of ``piece`` columns (0: the library's
     choice). Returns a dict: dH, dW (None where not needed) and workspace."""
     if stream is not None:
-        with _on_stream(stream):
-            return cross_entropy_backward(H, W, targets, lse, grad=grad,
-                                          ignore_index=ignore_index, z_loss=z_loss,
-                                          reduction=reduction, need_dH=need_dH, need_dW=need_dW,
-                                          piece=piece, workspace=workspace)
+        return _on_stream(stream, lambda: cross_entropy_backward(
+            H, W, targets, lse, grad=grad, ignore_index=ignore_index, z_loss=z_loss,
+            reduction=reduction, need_dH=need_dH, need_dW=need_dW, piece=piece,
+            workspace=workspace), H, W, targets, lse, grad, workspace)
     import torch
     where = "cross_entropy_backward"
     red = _reduction(reduction, where)
@@ -699,8 +696,8 @@ def residual_norm(h, y, pre, *, post=None, gate=None, scale: float = 1.0, eps: f
     [M, d] bf16, or None. Returns a dict: h (h', of h's type) and x (bf16: what the next block,
     or ``project`` and ``cross_entropy``, read). Asynchronous on ``stream``."""
     if stream is not None:
-        with _on_stream(stream):
-            return residual_norm(h, y, pre, post=post, gate=gate, scale=scale, eps=eps)
+        return _on_stream(stream, lambda: residual_norm(
+            h, y, pre, post=post, gate=gate, scale=scale, eps=eps), h, y, pre, post, gate)
     import torch
     M, d, kind, ht, wt, dev = _norm_problem(h, y, pre, post, gate, "residual_norm")
     h_out, x = torch.empty_like(h), torch.empty_like(y)
@@ -719,9 +716,9 @@ def residual_norm_backward(dx, dh, h, y, pre, *, post=None, gate=None, scale: fl
     Returns a dict: dh (the gradient of the incoming stream), dy, dpre, dpost, dgate (None where
     there is no such input) and workspace. The weights' gradients have the weights' type."""
     if stream is not None:
-        with _on_stream(stream):
-            return residual_norm_backward(dx, dh, h, y, pre, post=post, gate=gate, scale=scale,
-                                          eps=eps, workspace=workspace)
+        return _on_stream(stream, lambda: residual_norm_backward(
+            dx, dh, h, y, pre, post=post, gate=gate, scale=scale, eps=eps, workspace=workspace),
+            dx, dh, h, y, pre, post, gate, workspace)
     import torch
     where = "residual_norm_backward"
     M, d, kind, ht, wt, dev = _norm_problem(h, y, pre, post, gate, where)
@@ -806,6 +803,7 @@ class AdamW:
                 t.scale, t.scale_sq = s[2].data_ptr(), s[3].data_ptr()
             t.n, t.weight_decay = k, decay[i]
             t.param_type = SB_F32 if p.dtype is f32 else SB_BF16
+        self._streams = set()
         self.grads = None
         if grads is not None:
             self._bind(grads)
@@ -839,3 +837,9 @@ class AdamW:
         if st != SB_OK:
             raise SbError(st, "sb_adamw_step")
         self.step_count += 1
+        if stream is not None:  # any of these may be let go of while that stream uses them
+            own = ()
+            if _stream(stream) not in self._streams:  # once is enough for what stays bound
+                self._streams.add(_stream(stream))
+                own = (*self.params, *self.masters, *(x for s in self.states for x in s))
+            _on_stream(stream, lambda: None, grad_scale, *(self.grads or ()), *own)
