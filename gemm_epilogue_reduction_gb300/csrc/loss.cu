@@ -6,9 +6,12 @@
 //   loss_r = lse_r - z_r,target + z_loss·lse_r²,  0 where the target is the ignored index,
 // one block per row.  The tensor cores truncate as they accumulate, which leaves a logit of d =
 // 5120 products some 1e-5 short; the target's logit stands alone in the loss (every other one is
-// averaged in lse), so its block forms it again in fp32 FMAs, and lse follows by the target's
-// share p of the sum:  lse += log(1 + p·(exp(z - z_tc) - 1)).  The last block to finish adds the
-// rows' losses up (SUM, MEAN) in a fixed order, so the bits do not depend on which block that is.
+// averaged in lse), so its block forms it again in fp32 FMAs (loss_common.cuh):
+//   lse - z = log(1 + R·e^(z_tc - z)),   R = sum over the others of e^(z_j - z_tc),
+// where R is summed without the target's term if that leads its record (below), so that a small R
+// keeps its own precision.  lse is z plus that: backward, which gets lse, forms the same z and
+// p - 1 from the two.  The last block to finish adds the rows' losses up (SUM, MEAN) in a fixed
+// order, so the bits do not depend on which block that is.
 //
 // The rows kernel reads 8 bytes for each 128 columns of a row, H's row and the target's row of W:
 // next to the GEMM it is small (M = 4096, d = 6144, V = 200,064: 150 MB, 35 us against 5.1 ms),
@@ -18,6 +21,7 @@
 // into pieces and chooses the split of the dH reduction.
 #include <cmath>
 
+#include "loss_common.cuh"
 #include "sb.h"
 #include "sb_internal.h"
 #include "sb_ptx.cuh"
@@ -25,7 +29,7 @@
 namespace sb {
 namespace {
 
-constexpr int kRowThreads = 128;
+constexpr int kRowThreads = kDotParts;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct MaxSum {
@@ -50,24 +54,22 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LossParams p) {
     // the target's logit
     float dot = 0.f;
     if (inside) {
-        const uint4 *h = reinterpret_cast<const uint4 *>(p.H + static_cast<size_t>(row) * p.d);
-        const uint4 *w = reinterpret_cast<const uint4 *>(p.W + static_cast<size_t>(t) * p.d);
-        float d0 = 0.f, d1 = 0.f;
-#pragma unroll 2
-        for (int i = threadIdx.x; i < p.d / 8; i += kRowThreads) {
-            const uint4 x = h[i], y = w[i];
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                d0 = fmaf(__uint_as_float(xs[j] << 16), __uint_as_float(ys[j] << 16), d0);
-                d1 = fmaf(__uint_as_float(xs[j] & 0xFFFF0000u),
-                          __uint_as_float(ys[j] & 0xFFFF0000u), d1);
-            }
-        }
-        dot = d0 + d1;
+        float part[1];
+        dot_parts(p.H + static_cast<size_t>(row) * p.d, p.W + static_cast<size_t>(t) * p.d, p.d,
+                  threadIdx.x, part);
+        dot = part[0];
     }
     const float *rm = p.ws.m + static_cast<size_t>(row) * p.T;
     const float *rs = p.ws.s + static_cast<size_t>(row) * p.T;
+    // The target's record, where the target is its largest column: its exponential was then the one
+    // below, bit for bit, and no rounded sum of it and other terms >= 0 is smaller.
+    int lead = -1;
+    float tz = 0.f, own = 0.f;
+    if (inside) {
+        tz = p.ws.tz[row];
+        if (rm[t / kTileA] == tz && tz > -INFINITY) lead = t / kTileA;
+        own = ex2_approx(fmaf(tz, kLog2e, -(tz * kLog2e)));
+    }
     MaxSum a{-INFINITY, 0.f};
     for (int k = threadIdx.x; k < p.T; k += 4 * kRowThreads) {
         MaxSum x[4];  // four records in flight
@@ -75,6 +77,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LossParams p) {
         for (int u = 0; u < 4; ++u) {
             const int i = k + u * kRowThreads;
             x[u] = i < p.T ? MaxSum{rm[i], rs[i]} : MaxSum{-INFINITY, 0.f};
+            if (i == lead) x[u].s -= own;
         }
         a = join(a, join(join(x[0], x[1]), join(x[2], x[3])));
     }
@@ -99,9 +102,15 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LossParams p) {
         float lse = a.m + logf(a.s);
         float loss = 0.f;
         if (inside) {
-            const float tz = p.ws.tz[row];
-            lse += log1pf(__expf(tz - lse) * expm1f(dot - tz));
-            loss = (lse - dot) + p.z_loss * lse * lse;
+            const float more = tz - dot;  // what the tensor cores' number has in excess
+            float n = (a.m - tz) + logf(a.s);
+            // from n = 16 on the target's share of the sum is below fp32's half unit
+            if (n >= 16.f || n != n)
+                n += more;
+            else
+                n = log1pf(lead >= 0 ? expf(n + more) : expm1f(n) * expf(more));
+            lse = dot + n;
+            loss = n + p.z_loss * lse * lse;
         } else if (t != p.ignore_index) {
             // a target outside the vocabulary has no logit: the status word reports it
             loss = __uint_as_float(0x7FC00000u);
@@ -374,6 +383,7 @@ int32_t sb_cross_entropy_backward(const void *H, const void *W, const int32_t *t
     p.grad = grad;
     p.G = reinterpret_cast<uint16_t *>(ws + pl.g_off);
     p.H = static_cast<const uint16_t *>(H);
+    p.W = static_cast<const uint16_t *>(W);
     p.part = reinterpret_cast<float *>(ws + pl.part_off);
     p.scale = reinterpret_cast<float *>(ws + 16);
     p.dH = static_cast<uint16_t *>(dH);

@@ -44,6 +44,7 @@
 #include <cuda_bf16.h>
 #include <type_traits>
 
+#include "loss_common.cuh"
 #include "sb_internal.h"
 #include "sb_pipe.cuh"
 #include "sb_ptx.cuh"
@@ -344,11 +345,13 @@ __device__ __forceinline__ void store_box(const CUtensorMap *tm, Out &o, const f
     }
 }
 
-// What G's row needs of its loss: G_rj = a·exp(z_rj - lse_r) - (j = target ? b : 0).
+// What G's row needs of its loss: G_rj = a·exp(z_rj - lse_r), and `at` in the target's column.
 struct RowTerms {
     int row0 = -1;       // of the warp's rows; the thread's is row0 + lane
     int target = -1;     // inside the vocabulary, else -1
-    float a = 0.f, b = 0.f, l2 = 0.f;  // l2: lse·log2(e)
+    float a = 0.f, b = 0.f, lse = 0.f;  // b: the weight, a: times 1 + 2·z_loss·lse
+    float at = 0.f;
+    __device__ __forceinline__ bool dead() const { return a == 0.f && b == 0.f; }
 };
 __device__ __forceinline__ RowTerms row_terms(const LossGradParams &p, int row0, int lane,
                                               float scale) {
@@ -358,13 +361,36 @@ __device__ __forceinline__ RowTerms row_terms(const LossGradParams &p, int row0,
     if (row >= p.M) return r;
     const int t = __ldg(p.targets + row);
     if (t == p.ignore_index) return r;
-    const float lse = __ldg(p.lse + row);
+    r.lse = __ldg(p.lse + row);
     // NONE: the row's own weight relative to the shared scale
     r.b = (p.reduction == 0 && p.grad) ? (scale > 0.f ? __ldg(p.grad + row) / scale : 0.f) : 1.f;
-    r.a = r.b * (1.f + 2.f * p.z_loss * lse);
-    r.l2 = lse * kLog2e;
+    r.a = r.b * (1.f + 2.f * p.z_loss * r.lse);
     if (t >= 0 && t < p.V) r.target = t;
     return r;
+}
+
+// The entries of those of the warp's rows whose target is among this warp's 128 columns of the
+// tile: b·(p - 1 + 2·z_loss·lse·p).  lse holds the target's fp32 logit, which the accumulator misses by
+// what the tensor cores truncate: with that one p - 1 would be wrong by as much, and where p is near
+// 1 by more than its size (z = 25, 1 - p = 1e-3, d = 5120: 15 %).  So the warp forms the fp32 logit
+// again, row by row (a row has one target: M sums of d products in all, each while its tile is still
+// being formed), and p - 1 = expm1(z - lse) comes without a difference of two numbers near 1.
+__device__ __forceinline__ void target_terms(const LossGradParams &p, int col0, int lane,
+                                             RowTerms &r) {
+    const int col = r.target - p.c0 - col0;
+    unsigned rows = __ballot_sync(0xFFFFFFFFu,
+                                  r.target >= 0 && col >= 0 && col < 128 && !r.dead());
+    while (rows) {
+        const int l = __ffs(rows) - 1;
+        rows &= rows - 1;
+        const int t = __shfl_sync(0xFFFFFFFFu, r.target, l);
+        const float z = warp_dot(p.H + static_cast<size_t>(r.row0 + l) * p.d,
+                                 p.W + static_cast<size_t>(t) * p.d, p.d, lane);
+        if (lane == l) {
+            const float less = expm1f(z - r.lse);
+            r.at = r.b * (less + 2.f * p.z_loss * r.lse * (1.f + less));
+        }
+    }
 }
 
 template <int ATOMS>
@@ -373,13 +399,14 @@ __device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const C
                                                 const RowTerms &r, uint64_t pol) {
     // the target's column in this tile
     const int tgt = r.target >= 0 ? r.target - p.c0 - u.col0 : -1;
-    const bool dead = r.a == 0.f && r.b == 0.f;  // an ignored row, whatever its logits are
+    const bool dead = r.dead();  // an ignored row, whatever its logits are
+    const float l2 = r.lse * kLog2e;
     const int parts = r.row0 < p.M ? min(div_up(p.cols - u.col0 - 128 * o.h, 64), 2) : 0;
     for_parts(taddr, parts, o, [&](int c, float (&v)[64]) {
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
-            const float e = r.a * ex2_approx(fmaf(v[j], kLog2e, -r.l2));
-            v[j] = dead ? 0.f : (c + j == tgt ? e - r.b : e);
+            const float e = r.a * ex2_approx(fmaf(v[j], kLog2e, -l2));
+            v[j] = dead ? 0.f : (c + j == tgt ? r.at : e);
         }
         store_box<ATOMS>(tmG, o, v, u.col0 + c, r.row0, pol);
         if (p.lo) {  // (rows past M, up to the next 32, are zero in both)
@@ -670,7 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tph = (i >> 1) & 1;
             // the rows' terms while the tile is formed (few rows: once)
             const int row0 = u.row0 + 32 * o.q;
-            if (LOGITS && row0 != terms.row0) terms = row_terms(p, row0, lane, scale);
+            if (LOGITS) {
+                if (row0 != terms.row0) terms = row_terms(p, row0, lane, scale);
+                target_terms(p, u.col0 + 128 * o.h, lane, terms);
+            }
             const bool ok = p.debug_stall ? bwait(stall, 0, wc) : bwait_cluster(&tfull[b], tph, wc);
             if (__any_sync(0xFFFFFFFFu, !ok)) break;
             tc_fence_after();

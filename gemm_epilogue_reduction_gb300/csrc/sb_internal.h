@@ -114,7 +114,7 @@ struct LossGradParams {
     const float *lse;
     const float *grad;     // [M] (NONE) or [1]; null: 1
     uint16_t *G;           // [g_rows][ldg] bf16
-    const uint16_t *H;
+    const uint16_t *H, *W;
     uint16_t *Hc;          // [g_rows][d]: H with its ignored rows zero; null: not to be written
     float *scale;          // written by the logits kernel, read by the others
     float *part;           // [splits][g_rows][d] fp32 partial sums of dH
