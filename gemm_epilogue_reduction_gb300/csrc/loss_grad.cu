@@ -241,18 +241,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// The incoming gradient where it is one number (SUM, MEAN), else 1.
+__device__ __forceinline__ float incoming(const LossGradParams &p) {
+    return (p.reduction != 0 && p.grad) ? __ldg(p.grad) : 1.f;
+}
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+
 // The scale that all rows share, by all 256 epilogue threads (e = 0..255); red: 16 words of
 // shared memory.  SUM: the incoming gradient; MEAN: that over the count of rows that are not
-// ignored (at least 1); NONE: the largest |g_r| of those rows.
+// ignored (at least 1); NONE: the largest |g_r| of those rows.  It multiplies every row, so it is
+// always finite and (NONE) above zero: infinities and NaN stay with the rows' own weights.
 __device__ __forceinline__ float shared_scale(const LossGradParams &p, int e, float *red) {
-    const float up = (p.reduction != 0 && p.grad) ? __ldg(p.grad) : 1.f;
+    const float all = incoming(p), up = finite(all) ? all : 1.f;
     if (p.reduction == 1 || (p.reduction == 0 && !p.grad)) return up;
     float best = 0.f;
     int count = 0;
     for (int r = e; r < p.M; r += 256)
         if (__ldg(p.targets + r) != p.ignore_index) {
             ++count;
-            if (p.reduction == 0) best = fmaxf(best, fabsf(__ldg(p.grad + r)));
+            if (p.reduction == 0) {
+                const float g = fabsf(__ldg(p.grad + r));
+                if (finite(g)) best = fmaxf(best, g);
+            }
         }
     count = __reduce_add_sync(0xFFFFFFFFu, count);
     // |g| >= 0: its bits order like the values
@@ -269,7 +279,8 @@ __device__ __forceinline__ float shared_scale(const LossGradParams &p, int e, fl
         best = fmaxf(best, red[w]);
         count += reinterpret_cast<int *>(red)[8 + w];
     }
-    return p.reduction == 2 ? up / static_cast<float>(count > 0 ? count : 1) : best;
+    if (p.reduction == 2) return up / static_cast<float>(count > 0 ? count : 1);
+    return best > 0.f ? best : 1.f;
 }
 
 // ------------------------------------------------------------------ epilogues
@@ -362,8 +373,9 @@ __device__ __forceinline__ RowTerms row_terms(const LossGradParams &p, int row0,
     const int t = __ldg(p.targets + row);
     if (t == p.ignore_index) return r;
     r.lse = __ldg(p.lse + row);
-    // NONE: the row's own weight relative to the shared scale
-    r.b = (p.reduction == 0 && p.grad) ? (scale > 0.f ? __ldg(p.grad + row) / scale : 0.f) : 1.f;
+    // the row's own weight relative to the shared scale
+    const float up = incoming(p);
+    r.b = (p.reduction == 0 && p.grad) ? __ldg(p.grad + row) / scale : (finite(up) ? 1.f : up);
     r.a = r.b * (1.f + 2.f * p.z_loss * r.lse);
     if (t >= 0 && t < p.V) r.target = t;
     return r;
@@ -411,7 +423,10 @@ __device__ __forceinline__ void epilogue_logits(const LossGradParams &p, const C
         store_box<ATOMS>(tmG, o, v, u.col0 + c, r.row0, pol);
         if (p.lo) {  // (rows past M, up to the next 32, are zero in both)
 #pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+            for (int j = 0; j < 64; ++j) {
+                const float hi = __bfloat162float(__float2bfloat16_rn(v[j]));
+                v[j] = finite(hi) ? v[j] - hi : 0.f;
+            }
             store_box<ATOMS>(tmG, o, v, u.col0 + c, p.lo + r.row0, pol);
         }
     });

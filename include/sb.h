@@ -464,7 +464,8 @@ size_t sb_cross_entropy_backward_workspace_bytes(int64_t M, int64_t d, int64_t V
  *   H, W, targets, M, d, V, ignore_index, reduction, z_loss   as in the forward call.
  *   lse         device float [M], from the forward call.
  *   grad        device float: the incoming gradient, [M] for SB_REDUCE_NONE, else [1]; NULL
- *               stands for ones.  Read on the device when the kernels run.
+ *               stands for ones.  Read on the device when the kernels run.  One that is not
+ *               finite shows in dW and in its rows of dH; ignored rows stay 0.
  *   piece       vocabulary columns per piece, rounded up to a multiple of 256; 0 leaves the
  *               choice to the library (at most 256 MB for the piece of G).
  *   dH, dW      device bf16 [M, d] and [V, d], 16-byte aligned, overwritten; either may be NULL
