@@ -104,12 +104,16 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const LossParams p) {
         if (inside) {
             const float more = tz - dot;  // what the tensor cores' number has in excess
             float n = (a.m - tz) + logf(a.s);
-            // from n = 16 on the target's share of the sum is below fp32's half unit
-            if (n >= 16.f || n != n)
-                n += more;
-            else
-                n = log1pf(lead >= 0 ? expf(n + more) : expm1f(n) * expf(more));
-            lse = dot + n;
+            if (dot == -INFINITY) {
+                n = INFINITY;  // no share of the sum, which is the others' lse
+            } else {
+                // from n = 16 on the target's share is below fp32's half unit
+                if (n >= 16.f || n != n)
+                    n += more;
+                else
+                    n = log1pf(lead >= 0 ? expf(n + more) : expm1f(n) * expf(more));
+                lse = dot + n;
+            }
             loss = n + p.z_loss * lse * lse;
         } else if (t != p.ignore_index) {
             // a target outside the vocabulary has no logit: the status word reports it
