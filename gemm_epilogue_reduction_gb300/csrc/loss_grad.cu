@@ -241,9 +241,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Everything that the kernel before may have written is read with __ldcg: that kernel can still be
+// running when this one starts, which the read-only path of __ldg does not allow for.
 // The incoming gradient where it is one number (SUM, MEAN), else 1.
 __device__ __forceinline__ float incoming(const LossGradParams &p) {
-    return (p.reduction != 0 && p.grad) ? __ldg(p.grad) : 1.f;
+    return (p.reduction != 0 && p.grad) ? __ldcg(p.grad) : 1.f;
 }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
@@ -257,10 +259,10 @@ __device__ __forceinline__ float shared_scale(const LossGradParams &p, int e, fl
     float best = 0.f;
     int count = 0;
     for (int r = e; r < p.M; r += 256)
-        if (__ldg(p.targets + r) != p.ignore_index) {
+        if (__ldcg(p.targets + r) != p.ignore_index) {
             ++count;
             if (p.reduction == 0) {
-                const float g = fabsf(__ldg(p.grad + r));
+                const float g = fabsf(__ldcg(p.grad + r));
                 if (finite(g)) best = fmaxf(best, g);
             }
         }
@@ -370,12 +372,12 @@ __device__ __forceinline__ RowTerms row_terms(const LossGradParams &p, int row0,
     r.row0 = row0;
     const int row = row0 + lane;
     if (row >= p.M) return r;
-    const int t = __ldg(p.targets + row);
+    const int t = __ldcg(p.targets + row);
     if (t == p.ignore_index) return r;
-    r.lse = __ldg(p.lse + row);
+    r.lse = __ldcg(p.lse + row);
     // the row's own weight relative to the shared scale
     const float up = incoming(p);
-    r.b = (p.reduction == 0 && p.grad) ? __ldg(p.grad + row) / scale : (finite(up) ? 1.f : up);
+    r.b = (p.reduction == 0 && p.grad) ? __ldcg(p.grad + row) / scale : (finite(up) ? 1.f : up);
     r.a = r.b * (1.f + 2.f * p.z_loss * r.lse);
     if (t >= 0 && t < p.V) r.target = t;
     return r;
@@ -675,14 +677,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n16 = p.d / 8;
             for (int r = blockIdx.x; r < p.g_rows; r += gridDim.x) {
                 const int from = p.lo && r >= p.lo ? r - p.lo : r;  // once for each part of G
-                const bool keep = from < p.M && __ldg(p.targets + from) != p.ignore_index;
+                const bool keep = from < p.M && __ldcg(p.targets + from) != p.ignore_index;
                 const uint4 *src =
                     reinterpret_cast<const uint4 *>(p.H + static_cast<size_t>(keep ? from : 0) *
                                                               p.d);
                 uint4 *dst = reinterpret_cast<uint4 *>(p.Hc + static_cast<size_t>(r) * p.d);
 #pragma unroll 4
                 for (int i = lane; i < n16; i += 32)
-                    dst[i] = keep ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    dst[i] = keep ? __ldcg(src + i) : make_uint4(0, 0, 0, 0);
             }
         }
     } else {
