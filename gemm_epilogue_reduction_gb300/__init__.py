@@ -813,9 +813,11 @@ class AdamW:
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"AdamW: {len(grads)} gradients for {len(self.params)} parameters")
-        for i, (g, p, t) in enumerate(zip(grads, self.params, self._list)):
+        # every check before the first address: a refused list leaves the bound one as it was
+        for i, (g, p) in enumerate(zip(grads, self.params)):
             _tensor(f"grads[{i}]", g, p.shape, (torch.bfloat16, torch.float32), self._device,
                     "AdamW")
+        for g, t in zip(grads, self._list):
             t.grad = g.data_ptr()
             t.grad_type = SB_F32 if g.dtype == torch.float32 else SB_BF16
         self.grads = grads
@@ -823,19 +825,19 @@ class AdamW:
     def step(self, grads=None, *, grad_scale=None, lr=None, stream=None) -> None:
         """One step, asynchronous on ``stream``: ``grads`` replaces the gradients bound so far,
         ``grad_scale`` (float32 [1] on the device) multiplies them, ``lr`` replaces the rate."""
+        if grad_scale is not None:
+            import torch
+            _tensor("grad_scale", grad_scale, (1,), (torch.float32,), self._device, "AdamW")
         if grads is not None:
             self._bind(grads)
         if self.grads is None and self.params:
             raise ValueError("AdamW: no gradients have been given")
-        if grad_scale is not None:
-            import torch
-            _tensor("grad_scale", grad_scale, (1,), (torch.float32,), self._device, "AdamW")
-        if lr is not None:
-            self.lr = lr
-        st = sb_adamw_step(self._list, len(self.params), self.lr, self.betas[0], self.betas[1],
+        rate = self.lr if lr is None else lr
+        st = sb_adamw_step(self._list, len(self.params), rate, self.betas[0], self.betas[1],
                            self.eps, self.step_count + 1, self.state_bits, grad_scale, stream)
         if st != SB_OK:
             raise SbError(st, "sb_adamw_step")
+        self.lr = rate
         self.step_count += 1
         if stream is not None:  # any of these may be let go of while that stream uses them
             own = ()
