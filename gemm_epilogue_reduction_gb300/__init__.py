@@ -825,8 +825,13 @@ class AdamW:
     def step(self, grads=None, *, grad_scale=None, lr=None, stream=None) -> None:
         """One step, asynchronous on ``stream``: ``grads`` replaces the gradients bound so far,
         ``grad_scale`` (float32 [1] on the device) multiplies them, ``lr`` replaces the rate."""
+        import torch
+        # the launch goes to the current device, the addresses are those of the handle's
+        for device in (torch.cuda.current_device(), getattr(stream, "device_index", self._device)):
+            if device != self._device:
+                raise ValueError(f"AdamW: the tensors are on cuda:{self._device}, the step would "
+                                 f"run on device {device}")
         if grad_scale is not None:
-            import torch
             _tensor("grad_scale", grad_scale, (1,), (torch.float32,), self._device, "AdamW")
         if grads is not None:
             self._bind(grads)
