@@ -581,6 +581,15 @@ def _loss_problem(H, W, targets, where):
     return M, d, V, dev
 
 
+def _workspace(workspace, device, where):
+    """Refuses a workspace that the kernels cannot write to; returns its size in bytes."""
+    if workspace.get_device() != device:
+        raise ValueError(f"{where}: workspace is on {workspace.device}, not cuda:{device}")
+    if not workspace.is_contiguous():
+        raise ValueError(f"{where}: workspace is not contiguous")
+    return workspace.nbytes
+
+
 def _nonzero(nbytes, where):
     if nbytes == 0:
         raise SbError(SB_ERR_INVALID_ARG, where)
@@ -605,13 +614,15 @@ def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.
     M, d, V, dev = _loss_problem(H, W, targets, "cross_entropy")
     L = lib()
     if workspace is None:
-        n = _nonzero(L.sb_cross_entropy_workspace_bytes(M, d, V), "cross_entropy")
-        workspace = torch.empty(n, dtype=torch.uint8, device=H.device)
+        size = _nonzero(L.sb_cross_entropy_workspace_bytes(M, d, V), "cross_entropy")
+        workspace = torch.empty(size, dtype=torch.uint8, device=H.device)
+    else:
+        size = _workspace(workspace, dev, "cross_entropy")
     loss = torch.empty(M if red == SB_REDUCE_NONE else 1, dtype=torch.float32, device=H.device)
     lse = torch.empty(M, dtype=torch.float32, device=H.device)
     st = L.sb_cross_entropy_forward(H.data_ptr(), W.data_ptr(), targets.data_ptr(), M, d, V,
                                     ignore_index, red, z_loss, loss.data_ptr(), lse.data_ptr(),
-                                    workspace.data_ptr(), workspace.numel(), _current(dev))
+                                    workspace.data_ptr(), size, _current(dev))
     if st != SB_OK:
         raise SbError(st, "sb_cross_entropy_forward")
     return {"loss": loss, "lse": lse, "workspace": workspace}
@@ -638,15 +649,17 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
         _tensor("grad", grad, (M if red == SB_REDUCE_NONE else 1,), (torch.float32,), dev, where)
     L = lib()
     if workspace is None:
-        n = _nonzero(L.sb_cross_entropy_backward_workspace_bytes(M, d, V, piece, need_dH, need_dW),
-                     where)
-        workspace = torch.empty(n, dtype=torch.uint8, device=H.device)
+        size = _nonzero(
+            L.sb_cross_entropy_backward_workspace_bytes(M, d, V, piece, need_dH, need_dW), where)
+        workspace = torch.empty(size, dtype=torch.uint8, device=H.device)
+    else:
+        size = _workspace(workspace, dev, where)
     dH = torch.empty_like(H) if need_dH else None
     dW = torch.empty_like(W) if need_dW else None
     st = L.sb_cross_entropy_backward(H.data_ptr(), W.data_ptr(), targets.data_ptr(),
                                      lse.data_ptr(), _ptr(grad), M, d, V, ignore_index, red,
                                      z_loss, piece, _ptr(dH), _ptr(dW), workspace.data_ptr(),
-                                     workspace.numel(), _current(dev))
+                                     size, _current(dev))
     if st != SB_OK:
         raise SbError(st, "sb_cross_entropy_backward")
     return {"dH": dH, "dW": dW, "workspace": workspace}
@@ -655,7 +668,7 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
 def device_status(workspace) -> int:
     """``sb_last_device_status`` of a workspace tensor (synchronises)."""
     return sb_last_device_status(sb_outputs(workspace=_ptr(workspace),
-                                            workspace_bytes=workspace.numel()))
+                                            workspace_bytes=workspace.nbytes))
 
 
 def _norm_problem(h, y, pre, post, gate, where):
@@ -727,8 +740,10 @@ def residual_norm_backward(dx, dh, h, y, pre, *, post=None, gate=None, scale: fl
         _tensor("dh", dh, (M, d), (h.dtype,), dev, where)
     L = lib()
     if workspace is None:
-        n = _nonzero(L.sb_residual_norm_workspace_bytes(M, d), where)
-        workspace = torch.empty(n, dtype=torch.uint8, device=h.device)
+        size = _nonzero(L.sb_residual_norm_workspace_bytes(M, d), where)
+        workspace = torch.empty(size, dtype=torch.uint8, device=h.device)
+    else:
+        size = _workspace(workspace, dev, where)
     dh_out, dy, dpre = torch.empty_like(h), torch.empty_like(y), torch.empty_like(pre)
     dpost = None if post is None else torch.empty_like(post)
     dgate = None if gate is None else torch.empty_like(gate)
@@ -736,7 +751,7 @@ def residual_norm_backward(dx, dh, h, y, pre, *, post=None, gate=None, scale: fl
                                      pre.data_ptr(), _ptr(post), _ptr(gate), kind, M, d, ht, wt,
                                      scale, eps, dh_out.data_ptr(), dy.data_ptr(),
                                      dpre.data_ptr(), _ptr(dpost), _ptr(dgate),
-                                     workspace.data_ptr(), workspace.numel(), _current(dev))
+                                     workspace.data_ptr(), size, _current(dev))
     if st != SB_OK:
         raise SbError(st, "sb_residual_norm_backward")
     return {"dh": dh_out, "dy": dy, "dpre": dpre, "dpost": dpost, "dgate": dgate,
