@@ -121,6 +121,8 @@ def lib():
         L.sb_partial_completion.argtypes = [P, P, i64, i64, i64, i32, P, i32, P,
                                             ctypes.c_size_t, P]
         L.sb_partial_completion.restype = i32
+        L.sb_debug_map_encodes.argtypes = []
+        L.sb_debug_map_encodes.restype = ctypes.c_uint64
         L.sb_cross_entropy_workspace_bytes.argtypes = [i64] * 3
         L.sb_cross_entropy_workspace_bytes.restype = ctypes.c_size_t
         L.sb_cross_entropy_forward.argtypes = [P, P, P, i64, i64, i64, i32, i32, ctypes.c_float,
@@ -432,6 +434,10 @@ def sb_debug_combine_math(op: int, x, y, count: int, stream=None) -> int:
 
 def sb_debug_configure(stall_epilogue: bool, wait_limit_ns: int) -> int:
     return int(lib().sb_debug_configure(1 if stall_epilogue else 0, int(wait_limit_ns)))
+
+
+def sb_debug_map_encodes() -> int:
+    return int(lib().sb_debug_map_encodes())
 
 
 # ------------------------------------------------------------------ convenience wrapper

@@ -436,7 +436,7 @@ int32_t sb_partial_completion(const void *X, const void *W, int64_t M, int64_t N
     p.timeout_ns = wait_limit_ns();
 
     CUtensorMap tmW, tmX;
-    if (!encode_bf16_map(&tmW, W, N, K, kTileA) || !encode_bf16_map(&tmX, X, M, K, p.nb))
+    if (!cached_bf16_map(&tmW, W, N, K, kTileA) || !cached_bf16_map(&tmX, X, M, K, p.nb))
         return SB_ERR_CUDA;
     const size_t smem = p_smem_bytes(p.nb, p.stages_w, p.stages_x);
     static std::atomic<uint64_t> opted_in{0};

@@ -118,6 +118,7 @@ struct MapCacheEntry {
 };
 constexpr int kMapCache = 16;
 std::mutex g_map_mu;
+std::atomic<uint64_t> g_map_encodes{0};
 MapCacheEntry g_map_cache[kMapCache];
 int g_map_next = 0;
 
@@ -127,6 +128,7 @@ bool encode_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t d, int6
                 int box_rows) {
     auto enc = encoder();
     if (!enc) return false;
+    g_map_encodes.fetch_add(1);
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(kBlockK), static_cast<cuuint32_t>(box_rows)};
@@ -282,6 +284,10 @@ CombineParams combine_params(const sb_outputs *out, const Workspace &w, int64_t 
 }  // namespace
 
 namespace sb {
+bool cached_bf16_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t cols,
+                     int box_rows) {
+    return make_map(tm, base, rows, cols, box_rows);
+}
 bool encode_bf16_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t cols,
                      int box_rows, int64_t ld) {
     return encode_map(tm, base, rows, cols, ld ? ld : cols, box_rows);
@@ -751,5 +757,7 @@ int32_t sb_debug_configure(int32_t stall_epilogue, uint64_t wait_limit_ns) {
     g_timeout_ns.store(wait_limit_ns);
     return SB_OK;
 }
+
+uint64_t sb_debug_map_encodes(void) { return g_map_encodes.load(); }
 
 }  // extern "C"

@@ -193,7 +193,11 @@ size_t lmhead_smem_bytes(int nb, int stages_a, int stages_b, bool vocab_mode, in
                          int topk, int atoms);
 
 // Host helpers shared by the entry points (sb_api.cu).
-// (ld: elements from row to row, 0: cols)
+// The map of a contiguous matrix that later calls are likely to read again, kept for them: a driver
+// call less each time.
+bool cached_bf16_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t cols, int box_rows);
+// One that is not kept (gradients and workspaces, whose addresses change, would push the others
+// out).  ld: elements from row to row, 0: cols.
 bool encode_bf16_map(CUtensorMap *tm, const void *base, int64_t rows, int64_t cols,
                      int box_rows, int64_t ld = 0);
 // The records of sb_lmhead_records (SB_TOKEN, k = 1) and the targets' logits; a target equal to

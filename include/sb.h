@@ -605,6 +605,10 @@ int32_t sb_device_info(int32_t *num_sms, int32_t *cc);
  * Returns SB_ERR_INVALID_ARG for wait_limit_ns == 0. */
 int32_t sb_debug_configure(int32_t stall_epilogue, uint64_t wait_limit_ns);
 
+/* Test hook: how many tensor maps of row-major matrices this process has encoded (calls with the
+ * operands of an earlier one find theirs and encode none). */
+uint64_t sb_debug_map_encodes(void);
+
 #ifdef __cplusplus
 }
 #endif
