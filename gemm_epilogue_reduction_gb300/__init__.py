@@ -774,7 +774,12 @@ class AdamW:
     has none, or None for none at all). state_bits: 32, or 8 for E4M3 codes in blocks of 256
     values. states: existing moments, a tuple for each parameter, ``(m, v)`` float32 or
     ``(m, root, m_scale, root_scale)`` with float8_e4m3fn codes; None starts from zeros.
-    weight_decay: one number, or one for each parameter. step: steps already taken."""
+    weight_decay: one number, or one for each parameter. step: steps already taken.
+
+    The handle keeps the tensors' addresses (and their memory): a parameter, copy or state that is
+    given other memory later (``x.data = ...``) needs a new handle. In a CUDA graph a step is
+    captured with its rate and step number, so that every replay repeats that step's bias
+    correction: capture the forward and backward calls and step outside, or capture per step."""
 
     def __init__(self, params, grads=None, *, lr: float = 1e-3, betas=(0.9, 0.999),
                  eps: float = 1e-8, weight_decay=0.01, state_bits: int = 32, masters=None,
@@ -824,6 +829,9 @@ class AdamW:
                 t.scale, t.scale_sq = s[2].data_ptr(), s[3].data_ptr()
             t.n, t.weight_decay = k, decay[i]
             t.param_type = SB_F32 if p.dtype is f32 else SB_BF16
+        # the descriptors hold addresses: these keep the memory there, whatever becomes of the tensors
+        self._memory = [x.untyped_storage() for q in (self.params, self.masters, *self.states)
+                        for x in q if x is not None]
         self._streams = set()
         self.grads = None
         if grads is not None:
@@ -835,23 +843,29 @@ class AdamW:
         if len(grads) != len(self.params):
             raise ValueError(f"AdamW: {len(grads)} gradients for {len(self.params)} parameters")
         # every check before the first address: a refused list leaves the bound one as it was
+        dev, types = self._device, (torch.bfloat16, torch.float32)
         for i, (g, p) in enumerate(zip(grads, self.params)):
-            _tensor(f"grads[{i}]", g, p.shape, (torch.bfloat16, torch.float32), self._device,
-                    "AdamW")
+            if not (g.shape == p.shape and g.dtype in types and g.get_device() == dev and
+                    g.is_contiguous()):
+                _tensor(f"grads[{i}]", g, p.shape, types, dev, "AdamW")
         for g, t in zip(grads, self._list):
             t.grad = g.data_ptr()
             t.grad_type = SB_F32 if g.dtype == torch.float32 else SB_BF16
         self.grads = grads
+        self._grad_memory = [g.untyped_storage() for g in grads]
 
     def step(self, grads=None, *, grad_scale=None, lr=None, stream=None) -> None:
         """One step, asynchronous on ``stream``: ``grads`` replaces the gradients bound so far,
         ``grad_scale`` (float32 [1] on the device) multiplies them, ``lr`` replaces the rate."""
         import torch
         # the launch goes to the current device, the addresses are those of the handle's
-        for device in (torch.cuda.current_device(), getattr(stream, "device_index", self._device)):
-            if device != self._device:
-                raise ValueError(f"AdamW: the tensors are on cuda:{self._device}, the step would "
-                                 f"run on device {device}")
+        device = torch.cuda.current_device()
+        if stream is not None and device == self._device:
+            device = getattr(stream, "device_index", device)
+        if device != self._device:
+            raise ValueError(f"AdamW: the tensors are on cuda:{self._device}, the step would run "
+                             f"on device {device}")
+        on = _current(device) if stream is None else stream
         if grad_scale is not None:
             _tensor("grad_scale", grad_scale, (1,), (torch.float32,), self._device, "AdamW")
         if grads is not None:
@@ -860,7 +874,7 @@ class AdamW:
             raise ValueError("AdamW: no gradients have been given")
         rate = self.lr if lr is None else lr
         st = sb_adamw_step(self._list, len(self.params), rate, self.betas[0], self.betas[1],
-                           self.eps, self.step_count + 1, self.state_bits, grad_scale, stream)
+                           self.eps, self.step_count + 1, self.state_bits, grad_scale, on)
         if st != SB_OK:
             raise SbError(st, "sb_adamw_step")
         self.lr = rate
