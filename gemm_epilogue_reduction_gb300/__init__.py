@@ -804,6 +804,7 @@ class AdamW:
         dev, bf16, f32 = self._device, torch.bfloat16, torch.float32
         code = torch.float8_e4m3fn if state_bits == 8 else f32
         self._list = (sb_adamw_tensor * n)()
+        written = []  # (first byte, byte past the end) of every array that a step writes
         for i, (p, w, t) in enumerate(zip(self.params, self.masters, self._list)):
             _tensor(f"params[{i}]", p, p.shape, (bf16, f32), dev, where)
             k = p.numel()
@@ -827,8 +828,13 @@ class AdamW:
             t.param, t.exp_avg, t.exp_avg_sq = p.data_ptr(), s[0].data_ptr(), s[1].data_ptr()
             if state_bits == 8:
                 t.scale, t.scale_sq = s[2].data_ptr(), s[3].data_ptr()
+            written += [(x.data_ptr(), x.data_ptr() + x.nbytes)
+                        for x in (p, w, *s) if x is not None and k]
             t.n, t.weight_decay = k, decay[i]
             t.param_type = SB_F32 if p.dtype is f32 else SB_BF16
+        written.sort()
+        if any(a[1] > b[0] for a, b in zip(written, written[1:])):
+            raise ValueError(f"{where}: tensors overlap (two blocks of a launch would write them)")
         # the descriptors hold addresses: these keep the memory there, whatever becomes of the tensors
         self._memory = [x.untyped_storage() for q in (self.params, self.masters, *self.states)
                         for x in q if x is not None]
