@@ -577,8 +577,9 @@ typedef struct sb_adamw_tensor {
  *   step        t, >= 1.
  *   grad_scale  device float [1] (an inverse loss scale, a clipping factor), read when the
  *               kernels run; NULL: 1.
- * One kernel per 384 tensors on `stream`; no workspace.  The kernel does not let its successor
- * start early, so a projection that follows may load the new weight at once.
+ * One kernel per 384 tensors on `stream`; no workspace.  The kernels signal no dependents early,
+ * which is what sb_lmhead_project asks of a kernel that writes its W.  Step number and rate are
+ * host values: a captured call repeats its step's bias correction at every replay.
  */
 int32_t sb_adamw_step(const sb_adamw_tensor *tensors, int64_t count, double lr, double beta1,
                       double beta2, double eps, int64_t step, int32_t state_bits,
