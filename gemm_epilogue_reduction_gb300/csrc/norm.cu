@@ -97,7 +97,7 @@ int32_t check_norm(const void *h, const void *y, const void *pre, const void *po
         return SB_ERR_INVALID_ARG;
     const uintptr_t ha = stream_type == SB_F32 ? 4 : 2, wa = weight_type == SB_F32 ? 4 : 2;
     if (!on(h, ha) || !on(y, 2) || !on(pre, wa) || !on(post, wa) ||
-        !on(gate, gate_kind == SB_GATE_TOKEN ? 2 : wa))
+        (gate_kind != SB_GATE_NONE && !on(gate, gate_kind == SB_GATE_TOKEN ? 2 : wa)))
         return SB_ERR_ALIGNMENT;
     return SB_OK;
 }
@@ -219,7 +219,9 @@ int32_t sb_residual_norm_backward(const void *dx, const void *dh, const void *h,
         return SB_ERR_INVALID_ARG;
     const uintptr_t ha = stream_type == SB_F32 ? 4 : 2, wa = weight_type == SB_F32 ? 4 : 2;
     if (!on(dx, 2) || !on(dh, ha) || !on(dh_out, ha) || !on(dy, 2) || !on(dpre, wa) ||
-        !on(dpost, wa) || !on(dgate, gate_kind == SB_GATE_TOKEN ? 2 : wa) || !on(workspace, 16))
+        (post && !on(dpost, wa)) ||
+        (gate_kind != SB_GATE_NONE && !on(dgate, gate_kind == SB_GATE_TOKEN ? 2 : wa)) ||
+        !on(workspace, 16))
         return SB_ERR_ALIGNMENT;
     int sms = 0;
     if (int32_t e = device_sms_cc(&sms, nullptr)) return e;
