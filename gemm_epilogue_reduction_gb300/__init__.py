@@ -568,9 +568,11 @@ def _reduction(reduction, where):
                          f"not {reduction!r}") from None
 
 
-def _loss_problem(H, W, targets, where):
+def _loss_problem(H, W, targets, ignore_index, where):
     """Checks the arguments both directions share; returns (M, d, V, device index)."""
     import torch
+    if not -2 ** 31 <= ignore_index < 2 ** 31:  # the C call would take its lowest 32 bits
+        raise ValueError(f"{where}: ignore_index {ignore_index} is not a 32-bit integer")
     dev = torch.cuda.current_device()
     if H.dim() != 2 or W.dim() != 2:
         raise ValueError(f"{where}: H is [M, d] and W [V, d]")
@@ -617,7 +619,7 @@ def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.
             workspace=workspace), H, W, targets, workspace)
     import torch
     red = _reduction(reduction, "cross_entropy")
-    M, d, V, dev = _loss_problem(H, W, targets, "cross_entropy")
+    M, d, V, dev = _loss_problem(H, W, targets, ignore_index, "cross_entropy")
     L = lib()
     if workspace is None:
         size = _nonzero(L.sb_cross_entropy_workspace_bytes(M, d, V), "cross_entropy")
@@ -649,7 +651,7 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
     import torch
     where = "cross_entropy_backward"
     red = _reduction(reduction, where)
-    M, d, V, dev = _loss_problem(H, W, targets, where)
+    M, d, V, dev = _loss_problem(H, W, targets, ignore_index, where)
     _tensor("lse", lse, (M,), (torch.float32,), dev, where)
     if grad is not None:
         _tensor("grad", grad, (M if red == SB_REDUCE_NONE else 1,), (torch.float32,), dev, where)
