@@ -19,21 +19,35 @@ __device__ __forceinline__ void dot_parts(const uint16_t *h, const uint16_t *w, 
     float even[N], odd[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) even[n] = odd[n] = 0.f;
-#pragma unroll 2
-    for (int k = first; k < d / 8; k += kDotParts) {
+    // a single warp has the loads of kAtOnce rounds in flight before the first sum (with two rounds a
+    // row took 1.9 us of its tile's time, and one target for all of 64 rows 65 us)
+    constexpr int kAtOnce = N == 1 ? 1 : 4;
+#pragma unroll(N == 1 ? 2 : 1)
+    for (int k = first; k < d / 8; k += kAtOnce * kDotParts) {
+        uint4 x[kAtOnce][N], y[kAtOnce][N];
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int i = k + 32 * n;
-            if (n > 0 && i >= d / 8) break;
-            const uint4 x = h8[i], y = w8[i];
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        for (int u = 0; u < kAtOnce; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                even[n] = fmaf(__uint_as_float(xs[j] << 16), __uint_as_float(ys[j] << 16), even[n]);
-                odd[n] = fmaf(__uint_as_float(xs[j] & 0xFFFF0000u),
-                              __uint_as_float(ys[j] & 0xFFFF0000u), odd[n]);
+            for (int n = 0; n < N; ++n) {
+                const int i = k + u * kDotParts + 32 * n;
+                const bool in = (u == 0 && n == 0) || i < d / 8;  // else products that are zero
+                x[u][n] = in ? h8[i] : make_uint4(0, 0, 0, 0);
+                y[u][n] = in ? w8[i] : make_uint4(0, 0, 0, 0);
             }
-        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const uint32_t xs[4] = {x[u][n].x, x[u][n].y, x[u][n].z, x[u][n].w};
+                const uint32_t ys[4] = {y[u][n].x, y[u][n].y, y[u][n].z, y[u][n].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    even[n] = fmaf(__uint_as_float(xs[j] << 16), __uint_as_float(ys[j] << 16),
+                                   even[n]);
+                    odd[n] = fmaf(__uint_as_float(xs[j] & 0xFFFF0000u),
+                                  __uint_as_float(ys[j] & 0xFFFF0000u), odd[n]);
+                }
+            }
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) part[n] = even[n] + odd[n];
