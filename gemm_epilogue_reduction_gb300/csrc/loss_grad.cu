@@ -7,9 +7,8 @@
 //   dH = G·W,   dW = Gᵀ·H,
 // three products of 2·M·d·V operations (the logits are formed again from H and W).  Rows whose
 // target is the ignored index have G = 0.  For each piece of `cols` vocabulary columns:
-//   logits_kernel    z tile by tile as in the forward pass, and G in bf16 straight out of TMEM
-//                    into the piece buffer [M][cols];
-//                    the piece buffer [M][cols]; with the first piece also a copy of H whose
+//   logits_kernel    z tile by tile as in the forward pass, and G in bf16 through shared memory
+//                    into the piece buffer [M][cols]; with the first piece also a copy of H whose
 //                    ignored rows are zero, so that what those rows hold (an infinity, a NaN)
 //                    does not meet the zeros of G in dW;
 //   operands_kernel  one launch for both products that read G: the dH tiles (reduction over
@@ -389,6 +388,9 @@ __device__ __forceinline__ RowTerms row_terms(const LossGradParams &p, int row0,
 // 1 by more than its size (z = 25, 1 - p = 1e-3, d = 5120: 15 %).  So the warp forms the fp32 logit
 // again, row by row (a row has one target: M sums of d products in all, each while its tile is still
 // being formed), and p - 1 = expm1(z - lse) comes without a difference of two numbers near 1.
+// Random targets cost nothing measurable (64 x 4096 x 151,936: 597 and 600 us without and with;
+// 2048 x 4096 x 2000: 94 and 89), one target for all rows 15 us at most.  (A kernel of its own for
+// the M sums took 1 to 7 us of every call.)
 __device__ __forceinline__ void target_terms(const LossGradParams &p, int col0, int lane,
                                              RowTerms &r) {
     const int col = r.target - p.c0 - col0;
@@ -682,9 +684,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     reinterpret_cast<const uint4 *>(p.H + static_cast<size_t>(keep ? from : 0) *
                                                               p.d);
                 uint4 *dst = reinterpret_cast<uint4 *>(p.Hc + static_cast<size_t>(r) * p.d);
-#pragma unroll 4
-                for (int i = lane; i < n16; i += 32)
-                    dst[i] = keep ? __ldcg(src + i) : make_uint4(0, 0, 0, 0);
+                constexpr int kAtOnce = 8;  // loads before the first store
+                for (int i = lane; i < n16; i += 32 * kAtOnce) {
+                    uint4 x[kAtOnce];
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+                        x[u] = keep && i + 32 * u < n16 ? __ldcg(src + i + 32 * u)
+                                                        : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+                        if (i + 32 * u < n16) dst[i + 32 * u] = x[u];
+                }
             }
         }
     } else {
