@@ -612,7 +612,9 @@ def cross_entropy(H, W, targets, *, ignore_index: int = -100, z_loss: float = 0.
     H [M, d] and W [V, d] bf16, targets [M] int32, contiguous CUDA tensors. Returns a dict:
     loss (float32, [M] for reduction "none", [1] for "sum" and "mean"), lse [M] and workspace.
     Asynchronous on ``stream``; raises SbError on a bad status. A target outside [0, V) that is
-    not ``ignore_index`` gives a NaN loss, and ``device_status`` of the workspace reports it."""
+    not ``ignore_index`` gives a NaN loss, and ``device_status`` of the workspace reports it. No
+    autograd graph is built, whatever the inputs ask for: ``cross_entropy_backward`` gives the
+    gradients (int64 labels are converted by ``targets.int()``)."""
     if stream is not None:
         return _on_stream(stream, lambda: cross_entropy(
             H, W, targets, ignore_index=ignore_index, z_loss=z_loss, reduction=reduction,
@@ -715,7 +717,8 @@ def residual_norm(h, y, pre, *, post=None, gate=None, scale: float = 1.0, eps: f
     h [M, d] bf16 or float32 (the residual stream), y [M, d] bf16 (the block's output), pre and
     post [d] of one type, bf16 or float32 (post None: no norm of y), gate [d] of that type,
     [M, d] bf16, or None. Returns a dict: h (h', of h's type) and x (bf16: what the next block,
-    or ``project`` and ``cross_entropy``, read). Asynchronous on ``stream``."""
+    or ``project`` and ``cross_entropy``, read). Asynchronous on ``stream``. No autograd graph is
+    built: ``residual_norm_backward`` gives the gradients."""
     if stream is not None:
         return _on_stream(stream, lambda: residual_norm(
             h, y, pre, post=post, gate=gate, scale=scale, eps=eps), h, y, pre, post, gate)

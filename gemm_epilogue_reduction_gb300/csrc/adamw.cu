@@ -3,9 +3,9 @@
 // Per value (formulas and formats in sb.h): read gradient, weight and moments, write weight and
 // moments; nothing is read twice, so memory bounds it (28 bytes a value for a bf16 parameter with
 // its 32-bit copy and 32-bit moments, 16 with 8-bit moments).  Measured: 622 M values with 32-bit
-// moments 2.46 ms (7.1 TB/s), 778 M with 8-bit moments 1.95 ms (6.4 TB/s; the IEEE roots keep the
-// SMs busy for half of the time); 128 small tensors 4.7 us, of which the search and the 28 KB of
-// kernel parameters are most.
+// moments 2.46 to 2.47 ms (7.1 TB/s), 778 M with 8-bit moments 1.96 to 1.98 ms (6.3 TB/s; the IEEE
+// roots keep the SMs busy for half of the time); 128 small tensors 3.1 us back to back in a graph
+// (4.4 in 8 bits), of which the search and the 28 KB of kernel parameters are most.
 //
 // The tensors' descriptors travel in the kernel's parameters, so a call allocates and copies
 // nothing; a block finds its tensor by a binary search over the running count of chunks.  A chunk

@@ -16,7 +16,7 @@
 // The rows kernel reads 8 bytes for each 128 columns of a row, H's row and the target's row of W:
 // next to the GEMM it is small (M = 4096, d = 6144, V = 200,064: 150 MB, 35 us against 5.1 ms),
 // and for few rows its chain of dependent loads costs some 4 us.  The GEMM is bound by reading W
-// up to some 256 rows (16 x 5120 x 151,936: 232 us in all, 99 % of the measured memory rate) and
+// up to some 256 rows (16 x 5120 x 151,936: 233 to 239 us in all, 96 to 98 % of the measured memory rate) and
 // by the tensor cores beyond.  Backward is loss_grad.cu; its host side here cuts the vocabulary
 // into pieces and chooses the split of the dH reduction.
 #include <cmath>

@@ -26,13 +26,13 @@
 // empty.  Accumulation is fp32 in TMEM and, over the pieces, fp32 in memory.
 //
 // Bounds.  From some 2000 rows on the tensor cores (and under a long load the power limit): 4096 x
-// 6144 x 200,064 takes 23.7 ms forward and backward, 1.70 PFLOP/s over its four products of
-// 2·M·d·V (the logits are formed twice), the rate of a library product under the same load; the
-// kernels have 90 to 92 % of the tensor pipe's cycles there.  Around 500 rows what L2 delivers to
+// 6144 x 200,064 takes 23.4 to 24.3 ms forward and backward, 1.66 to 1.72 PFLOP/s over its four
+// products of 2·M·d·V (the logits are formed twice), 97 to 100 % of a library product's rate under
+// the same load; the kernels have 90 to 92 % of the tensor pipe's cycles there.  Around 500 rows what L2 delivers to
 // an SM (some 54 bytes a cycle; a 256 x 256 tile wants 64 per CTA for the full tensor rate, and a
 // dW tile of so few rows stores 64 KB besides).  For few rows the memory: W is read three times
-// (forward, logits, dH) and dW written once: 64 x 4096 x 151,936 takes 797 us (forward 189, logits
-// 195, dH 204, dW 209).
+// (forward, logits, dH) and dW written once: 64 x 4096 x 151,936 takes 787 to 817 us (at 797:
+// forward 189, logits 195, dH 204, dW 209).
 //
 // Both kernels: persistent CTA pairs, one cta_group::2 MMA of 256 x 256 per 16-wide K step
 // (tcgen05, bf16 x bf16 -> fp32), joint TMA stages, two TMEM accumulators, eight epilogue
@@ -149,7 +149,7 @@ __device__ __forceinline__ void div_mod(int t, int d, uint32_t inv, int &q, int 
 //
 // (With few rows dH reads W and dW writes its gradient.  Letting half of the pairs start with dW,
 // so that reads and writes overlap, was slower: 747 against 681 us for the backward call at 64 x
-// 4096 x 151,936.)
+// 4096 x 151,936, when that was measured.)
 template <bool LOGITS, int ATOMS>
 struct Walk {
     static constexpr int KB = ATOMS * kBlockK;

@@ -461,6 +461,8 @@ size_t sb_cross_entropy_backward_workspace_bytes(int64_t M, int64_t d, int64_t V
  * G = dL/dz of the piece is written in bf16 (up to 32 rows: in two bf16 parts) to the
  * workspace, then dH += G·W and dW = Gᵀ·H in one launch.  Accumulation is fp32; dH and dW are
  * rounded to bf16 once.  Every sum has a fixed order, so equal calls give equal bits.
+ * A target's entry, p - 1, is formed from lse and an fp32 logit: it is off by the roundings of
+ * lse (2^-23 of it), however near 1 p is.
  *   H, W, targets, M, d, V, ignore_index, reduction, z_loss   as in the forward call.
  *   lse         device float [M], from the forward call.
  *   grad        device float: the incoming gradient, [M] for SB_REDUCE_NONE, else [1]; NULL
