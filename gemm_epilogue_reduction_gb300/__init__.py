@@ -143,6 +143,29 @@ def lib():
         L.sb_residual_norm_backward.restype = i32
         L.sb_adamw_step.argtypes = [P, i64, f64, f64, f64, f64, i64, i32, P, P]
         L.sb_adamw_step.restype = i32
+        L.sb_embedding_forward.argtypes = [P, P, i64, i64, i64, i32, f32, i32, i32, P, P]
+        L.sb_embedding_forward.restype = i32
+        L.sb_embedding_backward_workspace_bytes.argtypes = [i64] * 2
+        L.sb_embedding_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.sb_embedding_backward.argtypes = [P, P, i64, i64, i64, i32, f32, i32, i32, i32, P, P,
+                                            ctypes.c_size_t, P]
+        L.sb_embedding_backward.restype = i32
+        L.sb_dropout.argtypes = [P, P, i64, i32, i32, f32, u64, P, P, P]
+        L.sb_dropout.restype = i32
+        L.sb_layer_norm_forward.argtypes = [P] * 4 + [i64, i64, i32, i32, f32, u64, P, f32, P, P, P]
+        L.sb_layer_norm_forward.restype = i32
+        L.sb_layer_norm_workspace_bytes.argtypes = [i64] * 2
+        L.sb_layer_norm_workspace_bytes.restype = ctypes.c_size_t
+        L.sb_layer_norm_backward.argtypes = ([P] * 4 + [i64, i64, i32, i32, f32, u64, P, f32] +
+                                             [P] * 5 + [ctypes.c_size_t, P])
+        L.sb_layer_norm_backward.restype = i32
+        L.sb_verify_workspace_bytes.argtypes = [i64] * 3
+        L.sb_verify_workspace_bytes.restype = ctypes.c_size_t
+        L.sb_verify_drafts.argtypes = ([P] * 7 + [i64] * 4 + [i32, f32, u64] + [P] * 4 +
+                                       [ctypes.c_size_t, P])
+        L.sb_verify_drafts.restype = i32
+        L.sb_verify_greedy.argtypes = [P] * 3 + [i64] * 2 + [P] * 3
+        L.sb_verify_greedy.restype = i32
         L.sb_select_source_projection.argtypes = [ctypes.c_double] * 8 + [
             ctypes.POINTER(ctypes.c_double)]
         L.sb_select_source_projection.restype = i32
@@ -394,6 +417,68 @@ def sb_adamw_step(tensors, count, lr, beta1, beta2, eps, step, state_bits, grad_
     """tensors: a ctypes array of sb_adamw_tensor (or None for count 0)."""
     return int(lib().sb_adamw_step(tensors, count, lr, beta1, beta2, eps, step, state_bits,
                                    _ptr(grad_scale), _stream(stream)))
+
+
+def sb_embedding_forward(ids, W, M, d, V, ignore_index, scale, weight_type, out_type, out,
+                         stream=None) -> int:
+    return int(lib().sb_embedding_forward(_ptr(ids), _ptr(W), M, d, V, ignore_index, float(scale),
+                                          weight_type, out_type, _ptr(out), _stream(stream)))
+
+
+def sb_embedding_backward_workspace_bytes(M: int, d: int) -> int:
+    return int(lib().sb_embedding_backward_workspace_bytes(M, d))
+
+
+def sb_embedding_backward(ids, dout, M, d, V, ignore_index, scale, grad_type, weight_type, add, dW,
+                          workspace, workspace_bytes, stream=None) -> int:
+    return int(lib().sb_embedding_backward(_ptr(ids), _ptr(dout), M, d, V, ignore_index,
+                                           float(scale), grad_type, weight_type, int(add), _ptr(dW),
+                                           _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def sb_dropout(x, residual, n, x_type, out_type, p, seed, seed_offset, out, stream=None) -> int:
+    return int(lib().sb_dropout(_ptr(x), _ptr(residual), n, x_type, out_type, float(p),
+                                seed & (2**64 - 1), _ptr(seed_offset), _ptr(out), _stream(stream)))
+
+
+def sb_layer_norm_forward(h, y, weight, bias, M, d, stream_type, weight_type, p, seed, seed_offset,
+                          eps, h_out, x, stream=None) -> int:
+    return int(lib().sb_layer_norm_forward(_ptr(h), _ptr(y), _ptr(weight), _ptr(bias), M, d,
+                                           stream_type, weight_type, float(p), seed & (2**64 - 1),
+                                           _ptr(seed_offset), float(eps), _ptr(h_out), _ptr(x),
+                                           _stream(stream)))
+
+
+def sb_layer_norm_workspace_bytes(M: int, d: int) -> int:
+    return int(lib().sb_layer_norm_workspace_bytes(M, d))
+
+
+def sb_layer_norm_backward(dx, dh, h, weight, M, d, stream_type, weight_type, p, seed, seed_offset,
+                           eps, dh_out, dy, dweight, dbias, workspace, workspace_bytes,
+                           stream=None) -> int:
+    return int(lib().sb_layer_norm_backward(
+        _ptr(dx), _ptr(dh), _ptr(h), _ptr(weight), M, d, stream_type, weight_type, float(p),
+        seed & (2**64 - 1), _ptr(seed_offset), float(eps), _ptr(dh_out), _ptr(dy), _ptr(dweight),
+        _ptr(dbias), _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def sb_verify_workspace_bytes(R: int, draft_rows: int, V: int) -> int:
+    return int(lib().sb_verify_workspace_bytes(R, draft_rows, V))
+
+
+def sb_verify_drafts(logits, draft_logits, drafts, starts, uniforms, lse, draft_lse, R, draft_rows,
+                     B, V, logits_type, temperature, seed, token, accepted, token_logprob,
+                     workspace, workspace_bytes, stream=None) -> int:
+    return int(lib().sb_verify_drafts(
+        _ptr(logits), _ptr(draft_logits), _ptr(drafts), _ptr(starts), _ptr(uniforms), _ptr(lse),
+        _ptr(draft_lse), R, draft_rows, B, V, logits_type, float(temperature), seed & (2**64 - 1),
+        _ptr(token), _ptr(accepted), _ptr(token_logprob), _ptr(workspace), int(workspace_bytes),
+        _stream(stream)))
+
+
+def sb_verify_greedy(target, drafts, starts, R, B, token, accepted, stream=None) -> int:
+    return int(lib().sb_verify_greedy(_ptr(target), _ptr(drafts), _ptr(starts), R, B, _ptr(token),
+                                      _ptr(accepted), _stream(stream)))
 
 
 def sb_select_source_projection(bytes_ref, bytes_proj, frames_ref, frames_proj,
@@ -673,6 +758,332 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
     if st != SB_OK:
         raise SbError(st, "sb_cross_entropy_backward")
     return {"dH": dH, "dW": dW, "workspace": workspace}
+
+
+# ------------------------------------------------------------------ the two ends of the model
+def _type(dtype, where):
+    import torch
+    if dtype is torch.bfloat16:
+        return SB_BF16
+    if dtype is torch.float32:
+        return SB_F32
+    raise TypeError(f"{where}: dtype is bfloat16 or float32, not {dtype}")
+
+
+def _index32(ignore_index, where):
+    if not -2 ** 31 <= ignore_index < 2 ** 31:  # the C call would take its lowest 32 bits
+        raise ValueError(f"{where}: ignore_index {ignore_index} is not a 32-bit integer")
+
+
+def _seeded(seed, seed_offset, device, where):
+    """Checks a seed (an int of 64 bits, signed or not) and its offset on the device."""
+    import torch
+    if not -2 ** 63 <= seed < 2 ** 64:
+        raise ValueError(f"{where}: seed {seed} is not a 64-bit integer")
+    if seed_offset is not None:
+        _tensor("seed_offset", seed_offset, (1,), (torch.int64, torch.uint64), device, where)
+    return seed & 0xFFFFFFFFFFFFFFFF
+
+
+def embedding(ids, W, *, scale: float = 1.0, ignore_index: int = -100, dtype=None, stream=None):
+    """The tokens' rows of the vocabulary matrix: scale W[ids], [M, d], of ``dtype`` (bf16 or
+    float32; None: W's).
+
+    ids [M] int32 and W [V, d] bf16 or float32, contiguous CUDA tensors (W may be the output head's).
+    Rows of ``ignore_index`` (padding) are 0, those of other ids outside [0, V) NaN. Asynchronous on
+    ``stream``; raises SbError on a bad status. No autograd graph is built:
+    ``embedding_backward`` gives the gradient."""
+    if stream is not None:
+        return _on_stream(stream, lambda: embedding(
+            ids, W, scale=scale, ignore_index=ignore_index, dtype=dtype), ids, W)
+    import torch
+    where = "embedding"
+    dev = torch.cuda.current_device()
+    _index32(ignore_index, where)
+    if ids.dim() != 1 or W.dim() != 2:
+        raise ValueError(f"{where}: ids is [M] and W [V, d]")
+    M, (V, d) = ids.shape[0], W.shape
+    if not (ids.dtype is torch.int32 and ids.get_device() == dev and W.get_device() == dev and
+            ids.is_contiguous() and W.is_contiguous()):
+        _tensor("ids", ids, (M,), (torch.int32,), dev, where)
+        _tensor("W", W, (V, d), (torch.bfloat16, torch.float32), dev, where)
+    wt = _type(W.dtype, where)
+    ot = wt if dtype is None else _type(dtype, where)
+    out = torch.empty(M, d, dtype=W.dtype if dtype is None else dtype, device=W.device)
+    st = lib().sb_embedding_forward(ids.data_ptr(), W.data_ptr(), M, d, V, ignore_index, scale, wt,
+                                    ot, out.data_ptr(), _current(dev))
+    if st != SB_OK:
+        raise SbError(st, "sb_embedding_forward")
+    return out
+
+
+def embedding_backward(ids, dout, *, vocab=None, dW=None, scale: float = 1.0,
+                       ignore_index: int = -100, dtype=None, stream=None, workspace=None):
+    """The gradient of ``embedding`` in W: for each row of W scale times the sum of its tokens'
+    rows of dout [M, d] (bf16 or float32), summed in float32 in a fixed order.
+
+    Either ``vocab`` (the rows of W) is given, and the whole gradient of type ``dtype`` (None:
+    dout's) is returned, or ``dW`` [V, d], bf16 or float32, and the sums are added to it in place
+    (a tied embedding's: give the dW of ``cross_entropy_backward``). Returns a dict: dW and
+    workspace."""
+    if stream is not None:
+        return _on_stream(stream, lambda: embedding_backward(
+            ids, dout, vocab=vocab, dW=dW, scale=scale, ignore_index=ignore_index, dtype=dtype,
+            workspace=workspace), ids, dout, dW, workspace)
+    import torch
+    where = "embedding_backward"
+    dev = torch.cuda.current_device()
+    _index32(ignore_index, where)
+    if ids.dim() != 1 or dout.dim() != 2:
+        raise ValueError(f"{where}: ids is [M] and dout [M, d]")
+    if (vocab is None) == (dW is None):
+        raise ValueError(f"{where}: either vocab or dW is given")
+    M, d = ids.shape[0], dout.shape[1]
+    _tensor("ids", ids, (M,), (torch.int32,), dev, where)
+    _tensor("dout", dout, (M, d), (torch.bfloat16, torch.float32), dev, where)
+    L = lib()
+    if workspace is None:
+        size = _nonzero(L.sb_embedding_backward_workspace_bytes(M, d), where)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dout.device)
+    else:
+        size = _workspace(workspace, dev, where)
+    add = dW is not None
+    if add:
+        if dtype is not None and dtype is not dW.dtype:
+            raise ValueError(f"{where}: dtype is {dtype}, dW {dW.dtype}")
+        if dW.dim() != 2:
+            raise ValueError(f"{where}: dW is [V, d]")
+        _tensor("dW", dW, (dW.shape[0], d), (torch.bfloat16, torch.float32), dev, where)
+    else:
+        dtype = dout.dtype if dtype is None else dtype
+        _type(dtype, where)
+        if vocab < 1:
+            raise ValueError(f"{where}: vocab is {vocab}")
+        dW = torch.empty(vocab, d, dtype=dtype, device=dout.device)
+    st = L.sb_embedding_backward(ids.data_ptr(), dout.data_ptr(), M, d, dW.shape[0], ignore_index,
+                                 scale, _type(dout.dtype, where), _type(dW.dtype, where), add,
+                                 dW.data_ptr(), workspace.data_ptr(), size, _current(dev))
+    if st != SB_OK:
+        raise SbError(st, "sb_embedding_backward")
+    return {"dW": dW, "workspace": workspace}
+
+
+def dropout(x, p: float, *, seed: int, seed_offset=None, residual=None, dtype=None, stream=None):
+    """residual + dropout(x): each element of x is dropped with probability round(65536 p) / 65536,
+    as the counter-based stream of ``seed`` says, and divided by the probability of the others.
+
+    x bf16 or float32, of any shape, contiguous on CUDA; residual of its shape (None: 0). The result
+    has the type of residual, or ``dtype`` (None: x's). seed_offset: int64 [1] on the device, added
+    to the seed when the kernel runs (a step counter for captured calls). Asynchronous on
+    ``stream``. The gradient of x is the same call on the gradient of the result, without
+    residual."""
+    if stream is not None:
+        return _on_stream(stream, lambda: dropout(
+            x, p, seed=seed, seed_offset=seed_offset, residual=residual, dtype=dtype),
+            x, residual, seed_offset)
+    import torch
+    where = "dropout"
+    dev = torch.cuda.current_device()
+    types = (torch.bfloat16, torch.float32)
+    _tensor("x", x, x.shape, types, dev, where)
+    if residual is not None:
+        if dtype is not None and dtype is not residual.dtype:
+            raise ValueError(f"{where}: dtype is {dtype}, residual {residual.dtype}")
+        _tensor("residual", residual, x.shape, types, dev, where)
+        dtype = residual.dtype
+    elif dtype is None:
+        dtype = x.dtype
+    seed = _seeded(seed, seed_offset, dev, where)
+    ot = _type(dtype, where)
+    out = torch.empty(x.shape, dtype=dtype, device=x.device)
+    st = lib().sb_dropout(x.data_ptr(), _ptr(residual), x.numel(), _type(x.dtype, where), ot, p, seed,
+                          _ptr(seed_offset), out.data_ptr(), _current(dev))
+    if st != SB_OK:
+        raise SbError(st, "sb_dropout")
+    return out
+
+
+def _layer_norm_problem(h, weight, where):
+    """Checks the arguments both directions share; returns (M, d, the types of the stream and of
+    the weights, device index)."""
+    import torch
+    dev = torch.cuda.current_device()
+    if h.dim() != 2:
+        raise ValueError(f"{where}: h is [M, d]")
+    M, d = h.shape
+    f32, bf16 = torch.float32, torch.bfloat16
+    ht, wt = h.dtype, weight.dtype
+    if not ((ht is bf16 or ht is f32) and (wt is bf16 or wt is f32) and weight.shape == (d,) and
+            h.get_device() == dev and weight.get_device() == dev and h.is_contiguous() and
+            weight.is_contiguous()):
+        _tensor("h", h, (M, d), (bf16, f32), dev, where)
+        _tensor("weight", weight, (d,), (bf16, f32), dev, where)
+    return M, d, SB_F32 if ht is f32 else SB_BF16, SB_F32 if wt is f32 else SB_BF16, dev
+
+
+def layer_norm(h, weight, bias=None, *, y=None, p: float = 0.0, seed: int = 0, seed_offset=None,
+               eps: float = 1e-5, stream=None):
+    """The end of a block with dropout and a layer norm: h' = h + dropout(y) and
+    x = (h' - mean) / sqrt(variance + eps) weight + bias over the last axis.
+
+    h [M, d] bf16 or float32 (the residual stream), weight and bias [d] of one type, bf16 or float32
+    (bias None: 0), y [M, d] bf16 (None: h' is h). p, seed and seed_offset as for ``dropout``.
+    Returns a dict: h (h', of h's type; h itself without y) and x (bf16: what the next block, or
+    ``project`` and ``cross_entropy``, read). Asynchronous on ``stream``. No autograd graph is
+    built: ``layer_norm_backward`` gives the gradients."""
+    if stream is not None:
+        return _on_stream(stream, lambda: layer_norm(
+            h, weight, bias, y=y, p=p, seed=seed, seed_offset=seed_offset, eps=eps),
+            h, weight, bias, y, seed_offset)
+    import torch
+    where = "layer_norm"
+    M, d, ht, wt, dev = _layer_norm_problem(h, weight, where)
+    if bias is not None:
+        _tensor("bias", bias, (d,), (weight.dtype,), dev, where)
+    x = torch.empty(M, d, dtype=torch.bfloat16, device=h.device)
+    h_out = h
+    if y is not None:
+        _tensor("y", y, (M, d), (torch.bfloat16,), dev, where)
+        h_out = torch.empty_like(h)
+    seed = _seeded(seed, seed_offset, dev, where)
+    st = lib().sb_layer_norm_forward(h.data_ptr(), _ptr(y), weight.data_ptr(), _ptr(bias), M, d, ht,
+                                     wt, p, seed, _ptr(seed_offset), eps, h_out.data_ptr(),
+                                     x.data_ptr(), _current(dev))
+    if st != SB_OK:
+        raise SbError(st, "sb_layer_norm_forward")
+    return {"h": h_out, "x": x}
+
+
+def layer_norm_backward(dx, dh, h, weight, *, need_dbias: bool = True, need_dy: bool = False,
+                        p: float = 0.0, seed: int = 0, seed_offset=None, eps: float = 1e-5,
+                        stream=None, workspace=None):
+    """The gradients of ``layer_norm``: dx [M, d] bf16 is the gradient of its x, dh that of its h'
+    (None: nothing else reads h'), ``h`` the h' that it returned; p, seed, seed_offset (with the
+    value that it had then) and eps as there. need_dbias, need_dy: whether there was a bias, a y.
+    Returns a dict: dh (the gradient of the incoming stream), dy, dweight, dbias (None where not
+    needed) and workspace. The weights' gradients have the weights' type."""
+    if stream is not None:
+        return _on_stream(stream, lambda: layer_norm_backward(
+            dx, dh, h, weight, need_dbias=need_dbias, need_dy=need_dy, p=p, seed=seed,
+            seed_offset=seed_offset, eps=eps, workspace=workspace),
+            dx, dh, h, weight, seed_offset, workspace)
+    import torch
+    where = "layer_norm_backward"
+    M, d, ht, wt, dev = _layer_norm_problem(h, weight, where)
+    _tensor("dx", dx, (M, d), (torch.bfloat16,), dev, where)
+    if dh is not None:
+        _tensor("dh", dh, (M, d), (h.dtype,), dev, where)
+    seed = _seeded(seed, seed_offset, dev, where)
+    L = lib()
+    if workspace is None:
+        size = _nonzero(L.sb_layer_norm_workspace_bytes(M, d), where)
+        workspace = torch.empty(size, dtype=torch.uint8, device=h.device)
+    else:
+        size = _workspace(workspace, dev, where)
+    dh_out, dweight = torch.empty_like(h), torch.empty_like(weight)
+    dy = torch.empty_like(dx) if need_dy else None
+    dbias = torch.empty_like(weight) if need_dbias else None
+    st = L.sb_layer_norm_backward(dx.data_ptr(), _ptr(dh), h.data_ptr(), weight.data_ptr(), M, d, ht,
+                                  wt, p, seed, _ptr(seed_offset), eps, dh_out.data_ptr(), _ptr(dy),
+                                  dweight.data_ptr(), _ptr(dbias), workspace.data_ptr(), size,
+                                  _current(dev))
+    if st != SB_OK:
+        raise SbError(st, "sb_layer_norm_backward")
+    return {"dh": dh_out, "dy": dy, "dweight": dweight, "dbias": dbias, "workspace": workspace}
+
+
+def verify_drafts(logits, drafts, starts, uniforms, *, draft_logits=None, temperature: float = 1.0,
+                  seed: int = 0, lse=None, draft_lse=None, logprob: bool = True, stream=None,
+                  workspace=None):
+    """Which of the drafted tokens the head's distribution keeps, and the token that follows them
+    (speculative sampling; ``sb_verify_drafts`` describes it).
+
+    logits [R, V] bf16 or float32 (``project``'s with SB_FULL_LOGITS): request b's rows are
+    starts[b] .. starts[b + 1] - 1, one more than its drafts. drafts [R] int32 and uniforms [R]
+    float32 in [0, 1), a request's last one not read; starts [B + 1] int32. draft_logits
+    [drafts, V] of logits' type, one row for each draft in their order (None: drafts without a
+    distribution, as from a lookup). lse [R] and draft_lse float32: the logsumexp of logits /
+    temperature where it is known (``project`` returns it for temperature 1). seed: of the samples'
+    stream.
+
+    Returns a dict: token [R] int32 (from starts[b] on the drafts that stay and the sample behind
+    them, -1 in all other rows), accepted [B] int32 (how many stay), token_logprob [R] (if
+    ``logprob``) and workspace, whose ``device_status`` reports starts and drafts out of range.
+    Asynchronous on ``stream``; raises SbError on a bad status."""
+    if stream is not None:
+        return _on_stream(stream, lambda: verify_drafts(
+            logits, drafts, starts, uniforms, draft_logits=draft_logits, temperature=temperature,
+            seed=seed, lse=lse, draft_lse=draft_lse, logprob=logprob, workspace=workspace),
+            logits, drafts, starts, uniforms, draft_logits, lse, draft_lse, workspace)
+    import torch
+    where = "verify_drafts"
+    dev = torch.cuda.current_device()
+    if logits.dim() != 2 or starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError(f"{where}: logits is [R, V] and starts [B + 1]")
+    (R, V), B = logits.shape, starts.shape[0] - 1
+    i32, f32 = torch.int32, torch.float32
+    _tensor("logits", logits, (R, V), (torch.bfloat16, f32), dev, where)
+    _tensor("drafts", drafts, (R,), (i32,), dev, where)
+    _tensor("starts", starts, (B + 1,), (i32,), dev, where)
+    _tensor("uniforms", uniforms, (R,), (f32,), dev, where)
+    D = -1
+    if draft_logits is not None:
+        if draft_logits.dim() != 2:
+            raise ValueError(f"{where}: draft_logits is [drafts, V]")
+        D = draft_logits.shape[0]
+        _tensor("draft_logits", draft_logits, (D, V), (logits.dtype,), dev, where)
+    if lse is not None:
+        _tensor("lse", lse, (R,), (f32,), dev, where)
+    if draft_lse is not None:
+        if draft_logits is None:
+            raise ValueError(f"{where}: draft_lse without draft_logits")
+        _tensor("draft_lse", draft_lse, (D,), (f32,), dev, where)
+    seed = _seeded(seed, None, dev, where)
+    L = lib()
+    if workspace is None:
+        size = _nonzero(L.sb_verify_workspace_bytes(R, D, V), where)
+        workspace = torch.empty(size, dtype=torch.uint8, device=logits.device)
+    else:
+        size = _workspace(workspace, dev, where)
+    token = torch.empty(R, dtype=i32, device=logits.device)
+    accepted = torch.empty(B, dtype=i32, device=logits.device)
+    lp = torch.empty(R, dtype=f32, device=logits.device) if logprob else None
+    st = L.sb_verify_drafts(logits.data_ptr(), _ptr(draft_logits), drafts.data_ptr(),
+                            starts.data_ptr(), uniforms.data_ptr(), _ptr(lse), _ptr(draft_lse), R, D,
+                            B, V, SB_F32 if logits.dtype is f32 else SB_BF16, temperature, seed,
+                            token.data_ptr(), accepted.data_ptr(), _ptr(lp), workspace.data_ptr(),
+                            size, _current(dev))
+    if st != SB_OK:
+        raise SbError(st, "sb_verify_drafts")
+    out = {"token": token, "accepted": accepted, "workspace": workspace}
+    if logprob:
+        out["token_logprob"] = lp
+    return out
+
+
+def verify_greedy(target, drafts, starts, *, stream=None):
+    """``verify_drafts`` for greedy decoding: target [R] int32 holds each row's own choice
+    (``project``'s token), a draft stays while it is that choice. Returns a dict: token [R] and
+    accepted [B], as there."""
+    if stream is not None:
+        return _on_stream(stream, lambda: verify_greedy(target, drafts, starts), target, drafts,
+                          starts)
+    import torch
+    where = "verify_greedy"
+    dev = torch.cuda.current_device()
+    if target.dim() != 1 or starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError(f"{where}: target is [R] and starts [B + 1]")
+    R, B, i32 = target.shape[0], starts.shape[0] - 1, (torch.int32,)
+    _tensor("target", target, (R,), i32, dev, where)
+    _tensor("drafts", drafts, (R,), i32, dev, where)
+    _tensor("starts", starts, (B + 1,), i32, dev, where)
+    token = torch.empty_like(target)
+    accepted = torch.empty(B, dtype=torch.int32, device=target.device)
+    st = lib().sb_verify_greedy(target.data_ptr(), drafts.data_ptr(), starts.data_ptr(), R, B,
+                                token.data_ptr(), accepted.data_ptr(), _current(dev))
+    if st != SB_OK:
+        raise SbError(st, "sb_verify_greedy")
+    return {"token": token, "accepted": accepted}
 
 
 def device_status(workspace) -> int:

@@ -43,6 +43,7 @@
 #include <climits>
 #include <cuda_bf16.h>
 
+#include "sb_counter.cuh"
 #include "sb_gumbel.cuh"
 #include "sb_internal.h"
 #include "sb_pipe.cuh"
@@ -143,22 +144,6 @@ __device__ __forceinline__ bool epi_vote_any(bool pred) {
         : "r"(static_cast<uint32_t>(pred))
         : "memory");
     return r != 0;
-}
-
-// Counter-based uniform: SplitMix64 (Steele, Lea and Flood, OOPSLA 2014) at stream index n
-// of the stream seeded with `seed`: the state is seed + (n + 1) * golden-ratio increment,
-// then the finaliser; the top 24 bits b give u = b * 2^-24 in [0, 1).
-constexpr unsigned long long kGolden = 0x9E3779B97F4A7C15ull;
-__device__ __forceinline__ unsigned long long splitmix_state(unsigned long long seed,
-                                                             unsigned long long n) {
-    return seed + (n + 1ull) * kGolden;
-}
-// The finaliser ends with x ^= x >> 31; its top 24 bits are those of x itself (x >> 31
-// contributes nothing above bit 32), so that last step is left out.
-__device__ __forceinline__ uint32_t bits24_from_state(unsigned long long x) {
-    x = (x ^ (x >> 30)) * 0xBF58476D1CE4E5B9ull;
-    x = (x ^ (x >> 27)) * 0x94D049BB133111EBull;
-    return static_cast<uint32_t>(x >> 40);
 }
 
 __device__ __forceinline__ uint32_t select_u32(bool pred, uint32_t a, uint32_t b) {

@@ -26,7 +26,8 @@
 // so all six sums are known at once, with the rounding of t's own terms.  Its column sums stay
 // in registers over all rows of a group; the groups of a block add up in shared memory, every
 // block leaves one partial vector each, and columns_kernel adds the partials in ascending
-// order: equal calls give equal bits.
+// order: equal calls give equal bits.  Its vector 1, the sum of t·(gate of the row)·y·ry, serves
+// dpost and the gate vector's gradient.
 #include <cmath>
 
 #include "norm_common.cuh"
@@ -35,15 +36,6 @@
 namespace sb {
 namespace {
 
-// Column sums of the blocks' partial vectors, in ascending order: 32 columns x 8 slices of the
-// partials per block.  Vector 0 is dpre; vector 1, v = sum of t·(gate of the row)·y·ry, gives
-// dpost = gate·v and, where the gate is one vector, dgate = post·v.
-struct ColumnParams {
-    const float *part;
-    int blocks, sums, d, f32;
-    const void *post, *gate;
-    void *dpre, *dpost, *dgate;
-};
 constexpr int kSlices = 8;
 __device__ __forceinline__ float weight_at(const void *w, int f32, int i) {
     if (!w) return 1.f;
@@ -83,9 +75,6 @@ __global__ void __launch_bounds__(32 * kSlices) columns_kernel(const ColumnParam
     }
 }
 
-bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 int32_t check_norm(const void *h, const void *y, const void *pre, const void *post,
                    const void *gate, int32_t gate_kind, int64_t M, int64_t d, int32_t stream_type,
                    int32_t weight_type, float scale, float eps) {
@@ -102,54 +91,13 @@ int32_t check_norm(const void *h, const void *y, const void *pre, const void *po
     return SB_OK;
 }
 
-// The widest vector that d and every address allow: 8, 4 or 1 values.
-template <typename... Ptr>
-int vector_width(int64_t d, Ptr... ptrs) {
-    uintptr_t bits = 0;
-    ((bits |= reinterpret_cast<uintptr_t>(ptrs)), ...);
-    if ((bits & 15u) == 0) {
-        if (d % 8 == 0) return 8;
-        if (d % 4 == 0) return 4;
-    }
-    return 1;
-}
-
-int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
-
-// Sixteen values a thread: 384 threads hold a row of up to 6144 with 168 registers each, which
-// backward's weights, column sums and row take.  (Eight values on 768 threads: 73 and 192 us at
-// 8192 x 6144 against 71 and 119; a warp's fixed work per row then counts twice.)
-NormShape shape_of(int64_t d, int vec) {
-    return NormShape{vec, 16, d <= 16 * 384 ? 384 : (d <= 16 * 512 && vec == 8 ? 512 : 1024)};
-}
-
-// One block per SM, filled with groups; no more groups than a block has rows.
-struct NormLayout {
-    NormShape shape;
-    int row_threads, groups, blocks, depth;
-    size_t smem;
-};
-// row_bytes: of a row in the ring; sum_bytes: what the groups' column sums take.
-NormLayout layout_of(int64_t M, int64_t d, int vec, int value_bytes, size_t sum_bytes, int sms) {
-    NormLayout l{};
-    l.shape = shape_of(d, vec);
-    l.row_threads = round32((d + l.shape.ept - 1) / l.shape.ept);
-    const int64_t rows = (M + sms - 1) / sms;
-    l.groups = l.shape.max_threads / l.row_threads;
-    if (l.groups > kMaxGroups) l.groups = kMaxGroups;
-    if (l.groups > rows) l.groups = static_cast<int>(rows);
-    const int64_t blocks = (M + l.groups - 1) / l.groups;
-    l.blocks = static_cast<int>(blocks < sms ? blocks : sms);
-    const size_t row_bytes = static_cast<size_t>(l.row_threads) * l.shape.ept * value_bytes;
-    // a ring of two rows at least: one is on its way while another one is worked on
-    const size_t fit = vec == 1 ? 0 : kNormRingBytes / l.groups / row_bytes;
-    l.depth = fit < 2 ? 0 : (fit > kMaxDepth ? kMaxDepth : static_cast<int>(fit));
-    l.smem = static_cast<size_t>(l.depth) * l.groups * row_bytes;
-    if (l.groups > 1 && l.smem < sum_bytes) l.smem = sum_bytes;
-    return l;
-}
-
 }  // namespace
+
+cudaError_t launch_norm_columns(const ColumnParams &p, cudaStream_t st) {
+    return launch_dependent(columns_kernel, dim3(static_cast<unsigned>((p.d + 31) / 32), p.sums),
+                            32 * kSlices, 0, p, st);
+}
+
 }  // namespace sb
 
 using namespace sb;
@@ -274,8 +222,7 @@ int32_t sb_residual_norm_backward(const void *dx, const void *dh, const void *h,
     c.post = p.post;
     c.gate = p.gate;
     if (launch_norm_backward(p, l.shape, h32, l.blocks, l.smem, st) != cudaSuccess ||
-        launch_dependent(columns_kernel, dim3(static_cast<unsigned>((d + 31) / 32), c.sums),
-                         32 * kSlices, 0, c, st) != cudaSuccess)
+        launch_norm_columns(c, st) != cudaSuccess)
         return SB_ERR_CUDA;
     return SB_OK;
 }

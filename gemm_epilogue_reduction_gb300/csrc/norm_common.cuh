@@ -1,6 +1,6 @@
-// norm_common.cuh -- what both directions of the residual norm (norm.cu) share: the layout of a row
-// over threads, loads and stores of bf16 and fp32 in fp32 pairs, the ring of rows on their way,
-// and the sums over a row.
+// norm_common.cuh -- what both directions of the residual norm (norm.cu) and of the layer norm
+// (layer_norm.cu) share: the layout of a row over threads, loads and stores of bf16 and fp32 in
+// fp32 pairs, the ring of rows on their way, and the sums over a row.
 #pragma once
 #include <atomic>
 #include <type_traits>
@@ -274,7 +274,69 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int group, int threads, f
     for (int n = 0; n < N; ++n) v[n] = __shfl_sync(0xFFFFFFFFu, a, 4 * n);
 }
 
-// ------------------------------------------------------------------ launch
+// Column sums of the blocks' partial vectors, in ascending order (columns_kernel in norm.cu): 32
+// columns x 8 slices of the partials per block.  Vector 0 is dpre; vector 1, v, gives dpost = gate·v
+// and dgate = post·v, each where it is asked for (factors of 1 where there is no gate or post).
+struct ColumnParams {
+    const float *part;
+    int blocks, sums, d, f32;
+    const void *post, *gate;
+    void *dpre, *dpost, *dgate;
+};
+cudaError_t launch_norm_columns(const ColumnParams &p, cudaStream_t st);
+
+// ------------------------------------------------------------------ layout and launch
+inline bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// The widest vector that d and every address allow: 8, 4 or 1 values.
+template <typename... Ptr>
+int vector_width(int64_t d, Ptr... ptrs) {
+    uintptr_t bits = 0;
+    ((bits |= reinterpret_cast<uintptr_t>(ptrs)), ...);
+    if ((bits & 15u) == 0) {
+        if (d % 8 == 0) return 8;
+        if (d % 4 == 0) return 4;
+    }
+    return 1;
+}
+
+inline int round32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
+
+// Sixteen values a thread: 384 threads hold a row of up to 6144 with 168 registers each, which
+// backward's weights, column sums and row take.  (Eight values on 768 threads: 73 and 192 us at
+// 8192 x 6144 against 71 and 119; a warp's fixed work per row then counts twice.)
+inline NormShape shape_of(int64_t d, int vec) {
+    return NormShape{vec, 16, d <= 16 * 384 ? 384 : (d <= 16 * 512 && vec == 8 ? 512 : 1024)};
+}
+
+// One block per SM, filled with groups; no more groups than a block has rows.
+struct NormLayout {
+    NormShape shape;
+    int row_threads, groups, blocks, depth;
+    size_t smem;
+};
+// row_bytes: of a row in the ring; sum_bytes: what the groups' column sums take.
+inline NormLayout layout_of(int64_t M, int64_t d, int vec, int value_bytes, size_t sum_bytes,
+                            int sms) {
+    NormLayout l{};
+    l.shape = shape_of(d, vec);
+    l.row_threads = round32((d + l.shape.ept - 1) / l.shape.ept);
+    const int64_t rows = (M + sms - 1) / sms;
+    l.groups = l.shape.max_threads / l.row_threads;
+    if (l.groups > kMaxGroups) l.groups = kMaxGroups;
+    if (l.groups > rows) l.groups = static_cast<int>(rows);
+    const int64_t blocks = (M + l.groups - 1) / l.groups;
+    l.blocks = static_cast<int>(blocks < sms ? blocks : sms);
+    const size_t row_bytes = static_cast<size_t>(l.row_threads) * l.shape.ept * value_bytes;
+    // a ring of two rows at least: one is on its way while another one is worked on
+    const size_t fit = vec == 1 ? 0 : kNormRingBytes / l.groups / row_bytes;
+    l.depth = fit < 2 ? 0 : (fit > kMaxDepth ? kMaxDepth : static_cast<int>(fit));
+    l.smem = static_cast<size_t>(l.depth) * l.groups * row_bytes;
+    if (l.groups > 1 && l.smem < sum_bytes) l.smem = sum_bytes;
+    return l;
+}
+
 template <typename P, typename K>
 cudaError_t launch_dependent(K kern, dim3 grid, int threads, size_t smem, const P &p,
                              cudaStream_t stream) {
@@ -292,9 +354,9 @@ cudaError_t launch_dependent(K kern, dim3 grid, int threads, size_t smem, const 
 }
 
 // `kern` with the shared-memory opt-in, which is per device (remembered in `opted_in`).
-inline cudaError_t launch_norm_kernel(void (*kern)(const NormParams), std::atomic<uint64_t> &opted_in,
-                                      const NormParams &p, int blocks, size_t smem,
-                                      cudaStream_t st) {
+template <typename Params>
+cudaError_t launch_norm_kernel(void (*kern)(const Params), std::atomic<uint64_t> &opted_in,
+                               const Params &p, int blocks, size_t smem, cudaStream_t st) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -308,7 +370,8 @@ inline cudaError_t launch_norm_kernel(void (*kern)(const NormParams), std::atomi
     return launch_dependent(kern, dim3(blocks), p.groups * p.row_threads, smem, p, st);
 }
 
-// Calls f.template operator()<T, VEC, EPT, MAXT, ROWS>() for the call's types and shape.
+// Calls f.template operator()<T, VEC, EPT, MAXT, ROWS>() for the call's types and shape (ROWS: one
+// more array of rows).
 template <typename F>
 cudaError_t for_norm_shape(NormShape s, bool h32, bool rows, F f) {
     auto typed = [&](auto h) {

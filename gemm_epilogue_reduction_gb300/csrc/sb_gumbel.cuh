@@ -27,9 +27,8 @@ __device__ __forceinline__ float lg2_approx(float x) {
 
 constexpr float kGumbelC0 = 0.36651292058166435f;  // -ln(ln 2)
 
-// y + g - c0 for the 24-bit uniform b: the key less the constant c0.
-__device__ __forceinline__ float gumbel_key_less_c0(float y, uint32_t b) {
-    constexpr float kLn2 = 0.6931471805599453f;
+// -t2 = log2 u for the 24-bit uniform b.
+__device__ __forceinline__ float log2_uniform(uint32_t b) {
     constexpr float kL2e = 1.4426950408889634f;
     const float uf = static_cast<float>(b);                  // exact (b < 2^24)
     const float L = lg2_approx(uf * 5.9604644775390625e-8f);  // log2 u, u = b 2^-24 exact
@@ -42,7 +41,13 @@ __device__ __forceinline__ float gumbel_key_less_c0(float y, uint32_t b) {
     q = fmaf(q, x, -kL2e / 3.0f);
     q = fmaf(q, x, -kL2e / 2.0f);
     q = fmaf(q, x, -kL2e);
-    const float t2n = b > 14680064u ? x * q : L;  // -t2 <= 0; 14680064 = 7/8 * 2^24
+    return b > 14680064u ? x * q : L;  // -t2 <= 0; 14680064 = 7/8 * 2^24
+}
+
+// y + g - c0 for the 24-bit uniform b: the key less the constant c0.
+__device__ __forceinline__ float gumbel_key_less_c0(float y, uint32_t b) {
+    constexpr float kLn2 = 0.6931471805599453f;
+    const float t2n = log2_uniform(b);
     // b = 0: log2(0) = -inf, so t2 = +inf and the key is -inf with no special case
     return fmaf(-kLn2, lg2_approx(fabsf(t2n)), y);
 }

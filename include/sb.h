@@ -587,6 +587,162 @@ int32_t sb_adamw_step(const sb_adamw_tensor *tensors, int64_t count, double lr, 
                       double beta2, double eps, int64_t step, int32_t state_bits,
                       const float *grad_scale, void *stream);
 
+/*
+ * The other end of the model (no paper counterpart): the tokens' rows of the vocabulary matrix,
+ *   out[t] = scale * W[ids[t]],
+ * and the gradient of that lookup.  W may be the output head's (a tied embedding).
+ *   ids         device int32 [M]: in [0, V), or ignore_index (any value, also one inside the
+ *               vocabulary): padding, whose row of out is 0 and which adds nothing to dW.  Another
+ *               value gives a row of NaN, and adds nothing to dW; nothing outside W is read.
+ *   W           device [V, d] of weight_type (an sb_type), row-major.
+ *   M, d, V     M >= 0 tokens (M <= 2^31 - 65536); 1 <= d <= 2^22; 1 <= V < 2^31 - 1.  16-byte
+ *               aligned arrays with d a multiple of 8 (or 4) are read in wide loads, others value by
+ *               value.
+ *   scale       finite.
+ *   out         device [M, d] of out_type, rounded once.
+ * One kernel on `stream`; no workspace.
+ */
+int32_t sb_embedding_forward(const int32_t *ids, const void *W, int64_t M, int64_t d, int64_t V,
+                             int32_t ignore_index, float scale, int32_t weight_type,
+                             int32_t out_type, void *out, void *stream);
+
+/* Bytes of workspace of the backward call; 0 if the arguments are invalid. */
+size_t sb_embedding_backward_workspace_bytes(int64_t M, int64_t d);
+
+/*
+ * Its gradient: with S[v] = scale * (sum of dout[t] over the t with ids[t] = v), in fp32 and in a
+ * fixed order (equal calls give equal bits),
+ *   add = 0:  dW = S, all of it written (zeros for the rows that no token has);
+ *   add = 1:  dW = dW + S in the rows that a token has, rounded once; the others are not touched.
+ *             That is how a tied embedding's gradient joins the head's (sb_cross_entropy_backward).
+ *   dout        device [M, d] of grad_type (an sb_type).
+ *   dW          device [V, d] of weight_type.
+ *   workspace   device, 256-byte aligned, >= sb_embedding_backward_workspace_bytes(M, d); no
+ *               initialisation.
+ * Up to four kernels on `stream`.
+ */
+int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, int64_t d, int64_t V,
+                              int32_t ignore_index, float scale, int32_t grad_type,
+                              int32_t weight_type, int32_t add, void *dW, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * Dropout whose mask is a function of a seed (no paper counterpart):
+ *   out[i] = residual[i] + (element i is kept ? x[i] * 65536 / (65536 - t) : 0),   t = round(65536 p).
+ * Element i is kept where 16-bit field i mod 4 (0: the lowest bits) of draw i / 4 of the SplitMix64
+ * stream of the seed is >= t; draw n is the finaliser of seed + (n + 1) * 0x9E3779B97F4A7C15, as
+ * for sb_lmhead_project.  No mask is stored: the gradient of x is the same call, without residual,
+ * on the gradient of out.  Different layers and steps need different seeds.
+ *   x           device [n] of x_type (an sb_type).
+ *   residual    device [n] of out_type, or NULL: 0.
+ *   n           >= 0.  16-byte aligned arrays are read in wide loads, others value by value.
+ *   p           0 <= p <= 1; p = 1 drops everything.
+ *   seed_offset device uint64 [1], added to seed when the kernel runs (a step counter, so that the
+ *               replays of a captured call differ), or NULL: 0.
+ *   out         device [n] of out_type; may be x (of the same type) or residual.
+ * One kernel on `stream`.
+ */
+int32_t sb_dropout(const void *x, const void *residual, int64_t n, int32_t x_type, int32_t out_type,
+                   float p, uint64_t seed, const uint64_t *seed_offset, void *out, void *stream);
+
+/*
+ * The end of a block with dropout and a layer norm (no paper counterpart): over each row,
+ *   h_out = h + dropout(y),
+ *   x = (h_out - mean) / sqrt(variance + eps) * weight + bias,
+ * with mean and variance of h_out (variance: of the centred values, over d).  Element (r, c) of y
+ * is dropped as element r * d + c of sb_dropout is.
+ *   h           device [M, d] of stream_type (an sb_type): the residual stream.
+ *   y           device bf16 [M, d]: the block's output, or NULL: h_out is h and is not written.
+ *   weight, bias  device [d] of weight_type (an sb_type); bias may be NULL.
+ *   M, d, eps, alignment   as for sb_residual_norm_forward (with one value to a row, x is bias).
+ *   p, seed, seed_offset   as for sb_dropout; without y not used.
+ *   h_out       device [M, d] of stream_type; may be h itself.
+ *   x           device bf16 [M, d]; may be y itself.  Formed from h_out before its rounding.
+ * One kernel on `stream`; no workspace.
+ */
+int32_t sb_layer_norm_forward(const void *h, const void *y, const void *weight, const void *bias,
+                              int64_t M, int64_t d, int32_t stream_type, int32_t weight_type,
+                              float p, uint64_t seed, const uint64_t *seed_offset, float eps,
+                              void *h_out, void *x, void *stream);
+
+/* Bytes of workspace of the backward call, which depend on the SM count of the current device;
+ * 0 for invalid arguments or without a device. */
+size_t sb_layer_norm_workspace_bytes(int64_t M, int64_t d);
+
+/*
+ * Its gradients.  h is here the forward call's h_out as it was stored; weight, the types, p, seed,
+ * seed_offset (with the value that it had then) and eps as there.
+ *   dx          device bf16 [M, d]: the gradient of x.
+ *   dh          device [M, d] of stream_type: the gradient of h_out from its other readers, or
+ *               NULL where there is none.
+ *   dh_out      device [M, d] of stream_type: the gradient of the forward call's h; may be dh.
+ *   dy          device bf16 [M, d], the gradient of y, or NULL (there was none); may be dx.
+ *   dweight, dbias  device [d] of weight_type (dbias or NULL), summed over the rows in fp32 in a
+ *               fixed order: equal calls give equal bits.
+ *   workspace   device, 16-byte aligned, >= sb_layer_norm_workspace_bytes(M, d); no initialisation.
+ * Two kernels on `stream`.  M = 0 writes zeros to dweight and dbias.
+ */
+int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, const void *weight,
+                               int64_t M, int64_t d, int32_t stream_type, int32_t weight_type,
+                               float p, uint64_t seed, const uint64_t *seed_offset, float eps,
+                               void *dh_out, void *dy, void *dweight, void *dbias, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * Verification of drafted tokens against the head's distribution (no paper counterpart): what
+ * follows SB_FULL_LOGITS when a small model has proposed the next tokens of each request.
+ *
+ * Request b has the rows starts[b] .. starts[b+1] - 1 of the logits, one more than drafts: the
+ * target's logits behind each draft's predecessor, and behind the last draft.  With p the softmax
+ * of a row's logits / T and q that of the draft's (1 at the drafted token and 0 elsewhere where the
+ * drafts have no logits), the draft x of row r stays if
+ *   uniforms[r] < p(x) / q(x)
+ * and all drafts before it stay.  The first one that does not is replaced by a sample of
+ * max(p - q, 0) (of p, where that is nowhere positive); where all stay the last row adds a sample
+ * of its p.  The tokens are then distributed as samples of the target's own.  The sample of row r
+ * is the column with the largest w_j / -log u_rj (the lowest of equal ones) with the 24-bit uniform
+ * u of sb_lmhead_project at index r*V + j of the seed's stream: where all stay, SB_GUMBEL_TOKEN's.
+ *   logits      device [R, V] of logits_type (an sb_type).  -inf is a column without probability.
+ *   draft_logits  device [draft_rows, V] of that type: a row for every draft, one request's behind
+ *               the other's, without gaps; draft_rows = -1 and NULL: the drafts have none.
+ *   drafts      device int32 [R]: in row r the token drafted for it; a request's last one is not
+ *               read.  One outside [0, V) does not stay, its sample is of p, and
+ *               sb_last_device_status reports SB_ERR_INVALID_ARG.
+ *   starts      device int32 [B + 1], ascending, starts[B] <= R.  A request may have no rows.  One
+ *               whose rows are not inside R (or its drafts' not inside draft_rows) gets accepted -1
+ *               and nothing else, and the status reports SB_ERR_INVALID_ARG.
+ *   uniforms    device float [R], each in [0, 1); a request's last one is not read.
+ *   lse, draft_lse  device float [R] and [draft_rows]: the rows' logsumexp of logits / T where the
+ *               caller has it (T = 1: that of sb_lmhead_project), each or NULL: formed here.
+ *   R, B, V     R, draft_rows < 2^24; B <= 2^24; 1 <= V < 2^31 - 65536.
+ *   temperature finite, > 0; 1 / T is rounded to fp32 and has to be finite.
+ *   token       device int32 [R]: from starts[b] on the drafts that stay and the sample behind them,
+ *               and -1 in all other rows, those behind the last request among them.
+ *   accepted    device int32 [B]: how many drafts of the request stay.
+ *   token_logprob  device float [R], or NULL: log p(token); 0 where there is no token.
+ *   workspace   device, 256-byte aligned, >= sb_verify_workspace_bytes(R, draft_rows, V); no
+ *               initialisation.  Its header is read by sb_last_device_status.
+ * A sampled row without any finite logit answers -1 with log-prob NaN.  Up to two kernels on
+ * `stream`.  Equal calls give equal bits.
+ */
+size_t sb_verify_workspace_bytes(int64_t R, int64_t draft_rows, int64_t V);
+int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int32_t *drafts,
+                         const int32_t *starts, const float *uniforms, const float *lse,
+                         const float *draft_lse, int64_t R, int64_t draft_rows, int64_t B,
+                         int64_t V, int32_t logits_type, float temperature, uint64_t seed,
+                         int32_t *token, int32_t *accepted, float *token_logprob, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * The same for greedy decoding, where SB_TOKEN has given each row's own choice: a draft stays while
+ * it is that choice, and the choice of the row behind the last one that stays follows.
+ *   target      device int32 [R]: the rows' tokens; drafts, starts, token and accepted as above
+ *               (starts that are out of range give accepted -1; there is no status word).
+ * One kernel on `stream`; no workspace.
+ */
+int32_t sb_verify_greedy(const int32_t *target, const int32_t *drafts, const int32_t *starts,
+                         int64_t R, int64_t B, int32_t *token, int32_t *accepted, void *stream);
+
 /* Device status of the last call that used out->workspace: SB_OK, SB_ERR_DEVICE_TIMEOUT
  * (a bounded wait gave up) or SB_ERR_INVALID_ARG (a scoring target outside [0, V); when
  * both happen the timeout is reported).  Synchronous: copies the header to the host (call
