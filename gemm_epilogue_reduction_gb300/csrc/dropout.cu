@@ -61,12 +61,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutPara
                 f = dropout_fields(seed, static_cast<unsigned long long>(i) / 4 + h);
                 below = p.drop.below;
             }
-            float2 *a = v[s] + 2 * h, *b = r[s] + 2 * h;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                a[k].x = dropout_add(RES ? b[k].x : 0.f, a[k].x, f.field(2 * k), below, p.drop.scale);
-                a[k].y = dropout_add(RES ? b[k].y : 0.f, a[k].y, f.field(2 * k + 1), below, p.drop.scale);
-            }
+            if (!RES) r[s][2 * h] = r[s][2 * h + 1] = both(0.f);
+            dropout_add4(r[s] + 2 * h, v[s] + 2 * h, f, below, p.drop.scale);
         }
         if (VEC == 8 && i + VEC <= p.n) {
             store_pairs<VEC>(out + i, v[s]);

@@ -8,16 +8,16 @@
 // short, up to four vectors (64 bytes) of loads in flight each.
 //
 // Backward sums rows in a fixed order, so that equal calls give equal bits; atomics on fp32 values
-// would not.  Three kernels:
-//   sort_kernel    every token's rank among the tokens by (id, position): the count of smaller
-//                  keys, and of equal ones at earlier positions.  All pairs are compared, 32 tokens
-//                  to a block, a lane each, the keys broadcast from shared memory: M²/32·2.25 warp
-//                  instructions, 5 us of this GPU for 8192 tokens, in one launch without a pass
-//                  that waits for another.  Beyond kChunk tokens each chunk is sorted by itself and
-//                  merge_kernel adds the ranks in the other chunks, by binary search.
-//                  When the whole gradient is asked for, further blocks of the same launch write its
-//                  zeros meanwhile (that is most of its bytes: V rows against at most M that are
-//                  not zero).
+// would not.  Its kernels:
+//   sort_kernel    tokens by (id, position), in runs of 256: a token's place is the count of smaller
+//                  keys, and of equal ones at earlier positions; all pairs are compared, the keys
+//                  broadcast from shared memory.  When the whole gradient is asked for, further
+//                  blocks of the same launch write its zeros meanwhile (that is most of its bytes: V
+//                  rows against at most M that are not zero).
+//   merge_runs_kernel, merge_chunks_kernel   runs to chunks of 8192 and chunks to one order: the
+//                  counts of smaller keys in the other runs by binary search, four threads to a
+//                  token.  No pass of either waits for another block.  (All pairs over 8192 tokens
+//                  in one launch took 17 us.)
 //   reduce_kernel  a block takes a piece of consecutive sorted tokens and a slice of columns, and
 //                  adds the rows of each run of equal ids in registers; a run inside the piece is
 //                  scaled, added and rounded here.  What a piece holds of a run that crosses its
@@ -105,114 +105,181 @@ cudaError_t launch_lookup(LookupParams p, int vec, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ backward: order
-constexpr int kChunk = 8192;       // tokens sorted by all pairs
-constexpr int kSortThreads = 256;  // of a block, which ranks 32 tokens
-constexpr int kZeroBlocks = 152 * 4;
+constexpr int kRun = 256;            // tokens sorted by all pairs, a thread each
+constexpr int kFetchBlocks = 152;
+// What is fetched while the tokens are sorted: about what the memory delivers in that time (24, 48 and
+// 100 MB at 8192 tokens x 6144: 50.7, 51.0 and 52.6 us in all; nothing: 53.1).
+constexpr int64_t kFetchBytes = int64_t(24) << 20;
+constexpr int kChunk = 8192;         // tokens whose keys a block holds in shared memory
 
 struct SortParams {
     const int32_t *ids;
     int M, V, ignore;
     int sort_blocks;
-    int2 *sorted;      // (key, position), sorted within each chunk
+    uint32_t *key;     // sorted within each run
+    int *at;           // their positions
     uint8_t *zero;     // bytes to clear (null: none)
     size_t zero_bytes;
+    const uint8_t *dout;  // rows to fetch into L2
+    size_t dout_row;      // bytes
+    int fetch;            // how many of them
 };
 
-__device__ void clear_bytes(uint8_t *p, size_t n, size_t thread, size_t threads) {
-    // values are 2 or 4 bytes wide: so are what lies before and behind the 32-byte units
+// A block's share of the zeros; values are 2 or 4 bytes wide, and so is what lies before and behind
+// the 32-byte units.  A store to a thread and 8 KB to a block: 1.24 GB in 162 us, against 192 where
+// blocks of a grid that just fills the GPU (or bulk stores) go over the matrix in turn.
+__device__ __forceinline__ void clear_share(uint8_t *p, size_t n, size_t block) {
     size_t head = (32 - (reinterpret_cast<uintptr_t>(p) & 31)) & 31;
     if (head > n) head = n;
-    const size_t units = (n - head) / 32, tail = head + units * 32;
-    for (size_t i = thread; i < units; i += threads)
-        st_global_v8(p + head + i * 32, 0, 0, 0, 0, 0, 0, 0, 0);
-    if (thread < head / 2) *reinterpret_cast<uint16_t *>(p + thread * 2) = 0;
-    if (thread < (n - tail) / 2) *reinterpret_cast<uint16_t *>(p + tail + thread * 2) = 0;
+    const size_t o = head + (block * kRun + threadIdx.x) * 32;
+    if (o + 32 <= n) {
+        st_global_v8(p + o, 0, 0, 0, 0, 0, 0, 0, 0);
+    } else {
+        for (size_t i = o; i < n; i += 2) *reinterpret_cast<uint16_t *>(p + i) = 0;
+    }
+    if (block == 0 && threadIdx.x < head / 2) reinterpret_cast<uint16_t *>(p)[threadIdx.x] = 0;
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) {
-    extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ int counts[kSortThreads / 32][32];
+// A block's share of the rows that reduce_kernel will read.
+__device__ __forceinline__ void fetch_share(const SortParams &p, int block, int blocks) {
+    for (int t = block + static_cast<int>(threadIdx.x) * blocks; t < p.fetch; t += kRun * blocks) {
+        const int id = p.ids[t];
+        if (id >= 0 && id < p.V && id != p.ignore)
+            prefetch_l2(p.dout + t * p.dout_row, static_cast<uint32_t>(p.dout_row));
+    }
+}
+
+__global__ void __launch_bounds__(kRun) sort_kernel(const SortParams p) {
+    __shared__ __align__(16) uint4 room[kRun / 4];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (static_cast<int>(blockIdx.x) >= p.sort_blocks) {
-        const size_t blocks = gridDim.x - p.sort_blocks, block = blockIdx.x - p.sort_blocks;
-        clear_bytes(p.zero, p.zero_bytes, block * kSortThreads + threadIdx.x, blocks * kSortThreads);
+        const int block = blockIdx.x - p.sort_blocks;
+        if (p.zero)
+            clear_share(p.zero, p.zero_bytes, block);
+        else
+            fetch_share(p, block, gridDim.x - p.sort_blocks);
         return;
     }
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int chunk = blockIdx.x / (kChunk / 32), base = chunk * kChunk;
-    const int n = min(kChunk, p.M - base), groups = (n + 31) / 32;
-    const int mine = static_cast<int>(blockIdx.x) - chunk * (kChunk / 32);  // my group of 32
-    for (int j = threadIdx.x; j < groups * 32; j += kSortThreads) {
-        uint32_t key = 0xFFFFFFFFu;  // behind the last token: never counted
-        if (j < n) {
-            const int id = p.ids[base + j];
-            key = id >= 0 && id < p.V && id != p.ignore ? id : kNoToken;
-        }
-        keys[j] = key;
+    const int base = blockIdx.x * kRun, i = threadIdx.x;
+    const int n = min(kRun, p.M - base), groups = (n + 31) / 32;
+    uint32_t *keys = reinterpret_cast<uint32_t *>(room);
+    uint32_t key = 0xFFFFFFFFu;  // behind the last token: never counted
+    if (i < n) {
+        const int id = p.ids[base + i];
+        key = id >= 0 && id < p.V && id != p.ignore ? id : kNoToken;
     }
+    keys[i] = key;
     __syncthreads();
-    const uint32_t key = keys[mine * 32 + lane];
-    int count = 0;
-    for (int g = warp; g < groups; g += kSortThreads / 32) {
-        const uint4 *k4 = reinterpret_cast<const uint4 *>(keys + g * 32);
+    const int mine = i / 32, lane = i % 32;
+    if (mine >= groups) return;
+    int rank = 0;
+    for (int g = 0; g < groups; ++g) {
+        const uint4 *k4 = room + g * 8;
         if (g != mine) {
             const uint32_t limit = key + (g < mine);  // equal keys count where they come before
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint4 k = k4[j];
-                count += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+                rank += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint4 k = k4[j];
-                count += (k.x < key + (4 * j < lane)) + (k.y < key + (4 * j + 1 < lane)) +
-                         (k.z < key + (4 * j + 2 < lane)) + (k.w < key + (4 * j + 3 < lane));
+                rank += (k.x < key + (4 * j < lane)) + (k.y < key + (4 * j + 1 < lane)) +
+                        (k.z < key + (4 * j + 2 < lane)) + (k.w < key + (4 * j + 3 < lane));
             }
         }
     }
-    counts[warp][lane] = count;
-    __syncthreads();
-    if (warp == 0 && mine * 32 + lane < n) {
-        int rank = 0;
-#pragma unroll
-        for (int w = 0; w < kSortThreads / 32; ++w) rank += counts[w][lane];
-        p.sorted[base + rank] = make_int2(static_cast<int>(key), base + mine * 32 + lane);
+    if (i < n) {
+        p.key[base + rank] = key;
+        p.at[base + rank] = base + i;
     }
 }
 
-// The chunks' orders become one: a token's place is its rank in its own chunk and the counts of
-// smaller keys (of keys not larger, in earlier chunks) in the others.
+// Sorted runs become sorted chunks, and sorted chunks one order: a token's place is its place in its
+// own run and the counts of smaller keys (of keys not larger, in earlier runs) in the others.
 struct MergeParams {
-    const int2 *from;
-    int2 *to;
+    const uint32_t *key;
+    const int *at;
+    uint32_t *to_key;
+    int *to_at;
     int M;
 };
-__global__ void __launch_bounds__(256) merge_kernel(const MergeParams p) {
+constexpr int kMergeThreads = 256;
+constexpr int kMergeLanes = 4;  // threads of a token, which share the runs
+
+__global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(const MergeParams p) {
+    __shared__ __align__(16) uint32_t keys[kChunk];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    constexpr int kTokens = kMergeThreads / kMergeLanes;
+    const int base = blockIdx.x / (kChunk / kTokens) * kChunk;
+    const int n = min(kChunk, p.M - base), runs = (n + kRun - 1) / kRun;
+    const uint4 none = make_uint4(~0u, ~0u, ~0u, ~0u);  // behind the last token: never counted
+#pragma unroll 8
+    for (int j = threadIdx.x; j < runs * (kRun / 4); j += kMergeThreads) {
+        uint4 k = none;
+        if (4 * j + 3 < n) {
+            k = reinterpret_cast<const uint4 *>(p.key + base)[j];
+        } else {
+            if (4 * j < n) k.x = p.key[base + 4 * j];
+            if (4 * j + 1 < n) k.y = p.key[base + 4 * j + 1];
+            if (4 * j + 2 < n) k.z = p.key[base + 4 * j + 2];
+        }
+        reinterpret_cast<uint4 *>(keys)[j] = k;
+    }
+    const int i = blockIdx.x * kTokens - base + static_cast<int>(threadIdx.x) / kMergeLanes;
+    const int lane = threadIdx.x % kMergeLanes;
+    const int at = i < n && lane == 0 ? p.at[base + i] : 0;
+    __syncthreads();
+    const uint32_t key = i < n ? keys[i] : 0u;
+    const int own = i / kRun;
+    int place = 0;
+#pragma unroll 4
+    for (int r = lane; r < runs; r += kMergeLanes) {
+        const uint32_t limit = r == own ? 0u : key + (r < own);
+        const uint32_t *k = keys + r * kRun;
+        int c = 0;
+#pragma unroll
+        for (int step = kRun / 2; step > 0; step /= 2)
+            if (k[c + step - 1] < limit) c += step;
+        place += c + (k[c] < limit);
+    }
+    place += __shfl_xor_sync(0xFFFFFFFFu, place, 1);
+    place += __shfl_xor_sync(0xFFFFFFFFu, place, 2);
+    if (i < n && lane == 0) {
+        place += base + i % kRun;
+        p.to_key[place] = key;
+        p.to_at[place] = at;
+    }
+}
+
+__global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const MergeParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long i = static_cast<long long>(blockIdx.x) * kMergeThreads + threadIdx.x;
     if (i >= p.M) return;
-    const int2 token = p.from[i];
+    const uint32_t key = p.key[i];
     const int chunks = (p.M + kChunk - 1) / kChunk, own = static_cast<int>(i / kChunk);
     int place = static_cast<int>(i - static_cast<long long>(own) * kChunk);
 #pragma unroll 4
     for (int c = 0; c < chunks; ++c) {
-        const int2 *k = p.from + static_cast<size_t>(c) * kChunk;
-        const uint32_t limit = static_cast<uint32_t>(token.x) + (c < own);
-        int lo = 0, hi = min(kChunk, p.M - c * kChunk);
-        if (c == own) hi = 0;
+        const uint32_t *k = p.key + static_cast<size_t>(c) * kChunk;
+        const uint32_t limit = key + (c < own);
+        int lo = 0, hi = c == own ? 0 : min(kChunk, p.M - c * kChunk);
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
-            if (static_cast<uint32_t>(k[mid].x) < limit)
+            if (k[mid] < limit)
                 lo = mid + 1;
             else
                 hi = mid;
         }
         place += lo;
     }
-    p.to[place] = token;
+    p.to_key[place] = key;
+    p.to_at[place] = p.at[i];
 }
 
 // ------------------------------------------------------------------ backward: sums
@@ -221,7 +288,8 @@ constexpr int kReduceThreads = 128;
 constexpr int kAhead = 8;            // rows in flight
 
 struct ReduceParams {
-    const int2 *sorted;
+    const uint32_t *key;
+    const int *at;
     const void *dout;
     void *dW;
     float *part;  // [pieces][2][d]: of the run that comes in from the piece before, and of the one
@@ -232,16 +300,39 @@ struct ReduceParams {
     int add;
 };
 
-template <typename G, typename W, int VEC>
+// VEC values as they lie in memory: what is on its way takes no more registers than bytes.
+template <typename T, int VEC>
+using Raw = std::conditional_t<VEC == 1, T, std::conditional_t<VEC * sizeof(T) == 16, uint4, uint2>>;
+template <int VEC, typename T>
+__device__ __forceinline__ void widen(const Raw<T, VEC> &x, float2 (&v)[(VEC + 1) / 2], T) {
+    if constexpr (VEC == 1)
+        v[0] = make_float2(one(&x), 0.f);
+    else if constexpr (sizeof(T) == 4)
+        v[0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y)),
+        v[1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
+    else if constexpr (VEC == 8)
+        v[0] = unpack2(x.x), v[1] = unpack2(x.y), v[2] = unpack2(x.z), v[3] = unpack2(x.w);
+    else
+        v[0] = unpack2(x.x), v[1] = unpack2(x.y);
+}
+
+template <typename G, typename W, int VEC, bool ADD>
 __global__ void __launch_bounds__(kReduceThreads) reduce_kernel(const ReduceParams p) {
     constexpr int N = (VEC + 1) / 2;
-    __shared__ int2 token[kPiece + 2];
+    using RG = Raw<G, VEC>;
+    using RW = Raw<W, VEC>;
+    __shared__ int2 token[kPiece + 2];  // (key, position); key -1: none
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // no early launch_dependents: nothing that follows may read dW ahead of this kernel's end
     const int first = blockIdx.x * kPiece;
     if (threadIdx.x < kPiece + 2) {
         const int i = first + static_cast<int>(threadIdx.x) - 1;
-        token[threadIdx.x] = i >= 0 && i < p.M ? p.sorted[i] : make_int2(-1, 0);
+        int2 t = make_int2(-1, 0);
+        if (i >= 0 && i < p.M) {
+            t = make_int2(static_cast<int>(p.key[i]), p.at[i]);
+            if (t.x == kNoToken) t.x = -1;
+        }
+        token[threadIdx.x] = t;
     }
     __syncthreads();
     const long long e = (static_cast<long long>(blockIdx.y) * kReduceThreads + threadIdx.x) * VEC;
@@ -253,42 +344,35 @@ __global__ void __launch_bounds__(kReduceThreads) reduce_kernel(const ReducePara
     for (int j = 0; j < N; ++j) acc[j] = both(0.f);
     bool came = token[0].x == token[1].x;  // the run is one of the piece before
     for (int k0 = 1; k0 <= kPiece; k0 += kAhead) {
-        const int key0 = token[k0].x;
-        if (key0 < 0 || key0 == kNoToken) break;
-        float2 v[kAhead][N], old[kAhead][N];
+        if (token[k0].x < 0) break;
+        RG v[kAhead];
+        RW old[ADD ? kAhead : 1];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int2 t = token[k0 + u];
-            const bool there = t.x >= 0 && t.x != kNoToken;
-            const bool ends = there && t.x != token[k0 + u + 1].x;
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[u][j] = old[u][j] = both(0.f);
-            if (there) {
-                const G *from = dout + static_cast<size_t>(t.y) * p.d;
-                if constexpr (VEC == 1)
-                    v[u][0].x = one(from);
-                else
-                    load_pairs<VEC>(from, v[u]);
-            }
-            if (p.add && ends) {
-                const W *from = dW + static_cast<size_t>(t.x) * p.d;
-                if constexpr (VEC == 1)
-                    old[u][0].x = one(from);
-                else
-                    load_pairs<VEC>(from, old[u]);
-            }
+            if (t.x >= 0) v[u] = *reinterpret_cast<const RG *>(dout + static_cast<size_t>(t.y) * p.d);
+            if constexpr (ADD)
+                if (t.x >= 0 && t.x != token[k0 + u + 1].x)
+                    old[u] = *reinterpret_cast<const RW *>(dW + static_cast<size_t>(t.x) * p.d);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int2 t = token[k0 + u];
-            if (t.x < 0 || t.x == kNoToken) break;
+            if (t.x < 0) break;
             const bool ends = t.x != token[k0 + u + 1].x;
+            float2 x[N];
+            widen<VEC>(v[u], x, G{});
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] = __fadd2_rn(acc[j], v[u][j]);
+            for (int j = 0; j < N; ++j) acc[j] = __fadd2_rn(acc[j], x[j]);
             if (!ends && k0 + u < kPiece) continue;
             if (ends && !came) {
+                if constexpr (ADD)
+                    widen<VEC>(old[u], x, W{});
+                else
 #pragma unroll
-                for (int j = 0; j < N; ++j) acc[j] = __ffma2_rn(acc[j], both(p.scale), old[u][j]);
+                    for (int j = 0; j < N; ++j) x[j] = both(0.f);
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] = __ffma2_rn(acc[j], both(p.scale), x[j]);
                 W *to = dW + static_cast<size_t>(t.x) * p.d;
                 if constexpr (VEC == 1)
                     put_one(to, acc[0].x);
@@ -308,39 +392,46 @@ __global__ void __launch_bounds__(kReduceThreads) reduce_kernel(const ReducePara
     }
 }
 
-// The run that starts in a piece and ends in a later one: its parts in ascending order, eight
-// slices of them side by side, and then the slices.
+// The run that starts in a piece and ends in a later one: its parts in ascending order, or, where
+// they are many, eight slices of them side by side and then the slices.
 constexpr int kJoinSlices = 8;
 template <typename W, int VEC>
 __global__ void __launch_bounds__(32 * kJoinSlices) join_kernel(const ReduceParams p) {
     constexpr int N = (VEC + 1) / 2;
     __shared__ float2 sums[kJoinSlices][32][N];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int piece = blockIdx.x;
-    const long long behind = static_cast<long long>(piece + 1) * kPiece;
-    if (behind >= p.M) return;
-    const int key = p.sorted[behind - 1].x;
-    if (key == kNoToken || key != p.sorted[behind].x) return;
-    if (piece > 0 && p.sorted[behind - kPiece - 1].x == key) return;  // it started in an earlier one
-    // the last piece with a part of it
-    long long lo = behind, hi = p.M;
-    while (lo < hi) {
-        const long long mid = (lo + hi) / 2;
-        if (p.sorted[mid].x <= key)
-            lo = mid + 1;
-        else
-            hi = mid;
+    const int piece = blockIdx.x, lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const int behind = (piece + 1) * kPiece;  // (of a piece that is not the last one)
+    const uint32_t key = p.key[behind - 1];
+    const uint32_t before = piece > 0 ? p.key[behind - kPiece - 1] : kNoToken;
+    // the pieces behind that begin with the run's key: 32 at a time, the first of them beside the
+    // loads above
+    int parts = 1;
+    for (int q = piece + 1;; q += 32) {
+        const bool more = q + lane < p.pieces && p.key[(q + lane) * kPiece] == key;
+        const uint32_t with = __ballot_sync(0xFFFFFFFFu, more);
+        parts += __popc(with);
+        if (with != 0xFFFFFFFFu) break;
     }
-    const int parts = static_cast<int>((lo - 1) / kPiece) - piece + 1;
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int q0 = static_cast<int>(static_cast<long long>(parts) * slice / kJoinSlices);
-    const int q1 = static_cast<int>(static_cast<long long>(parts) * (slice + 1) / kJoinSlices);
-    for (long long e0 = static_cast<long long>(blockIdx.y) * 32 * VEC; e0 < p.d;
-         e0 += static_cast<long long>(gridDim.y) * 32 * VEC) {
-        const long long e = e0 + lane * VEC;
-        float2 acc[N];
+    if (key == kNoToken || parts == 1 || before == key) return;  // (before: it started earlier)
+    // few parts: every warp has columns of its own; many: the warps share the parts
+    const bool share = parts > 2 * kJoinSlices;
+    const int q0 = share ? static_cast<int>(static_cast<long long>(parts) * slice / kJoinSlices) : 0;
+    const int q1 = share ? static_cast<int>(static_cast<long long>(parts) * (slice + 1) / kJoinSlices) : parts;
+    const int width = (share ? 32 : 32 * kJoinSlices) * VEC;
+    for (long long e0 = static_cast<long long>(blockIdx.y) * width; e0 < p.d;
+         e0 += static_cast<long long>(gridDim.y) * width) {
+        const long long e = e0 + (share ? lane : static_cast<int>(threadIdx.x)) * VEC;
+        W *to = static_cast<W *>(p.dW) + static_cast<size_t>(key) * p.d + e;
+        float2 acc[N], old[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = both(0.f);
+        for (int j = 0; j < N; ++j) acc[j] = old[j] = both(0.f);
+        if (p.add && (!share || slice == 0) && e < p.d) {
+            if constexpr (VEC == 1)
+                old[0].x = one(to);
+            else
+                load_pairs<VEC>(to, old);
+        }
         if (e < p.d)
 #pragma unroll 4
             for (int q = q0; q < q1; ++q) {
@@ -353,24 +444,16 @@ __global__ void __launch_bounds__(32 * kJoinSlices) join_kernel(const ReducePara
 #pragma unroll
                 for (int j = 0; j < N; ++j) acc[j] = __fadd2_rn(acc[j], v[j]);
             }
+        if (share) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) sums[slice][lane][j] = acc[j];
-        __syncthreads();
-        if (slice == 0 && e < p.d) {
-            W *to = static_cast<W *>(p.dW) + static_cast<size_t>(key) * p.d + e;
-            float2 old[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) old[j] = both(0.f);
-            if (p.add) {
-                if constexpr (VEC == 1)
-                    old[0].x = one(to);
-                else
-                    load_pairs<VEC>(to, old);
-            }
+            for (int j = 0; j < N; ++j) sums[slice][lane][j] = acc[j];
+            __syncthreads();
 #pragma unroll
             for (int s = 1; s < kJoinSlices; ++s)
 #pragma unroll
                 for (int j = 0; j < N; ++j) acc[j] = __fadd2_rn(acc[j], sums[s][lane][j]);
+        }
+        if ((!share || slice == 0) && e < p.d) {
 #pragma unroll
             for (int j = 0; j < N; ++j) acc[j] = __ffma2_rn(acc[j], both(p.scale), old[j]);
             if constexpr (VEC == 1)
@@ -378,21 +461,21 @@ __global__ void __launch_bounds__(32 * kJoinSlices) join_kernel(const ReducePara
             else
                 store_pairs<VEC>(to, acc);
         }
-        __syncthreads();
+        if (share) __syncthreads();
     }
 }
 
 template <typename G, typename W, int VEC>
 cudaError_t launch_sums(const ReduceParams &p, cudaStream_t st) {
     const long long slices = (p.d + kReduceThreads * VEC - 1) / (kReduceThreads * VEC);
-    cudaError_t e = launch_dependent(reduce_kernel<G, W, VEC>,
-                                     dim3(p.pieces, static_cast<unsigned>(slices)), kReduceThreads,
-                                     0, p, st);
+    const dim3 grid(p.pieces, static_cast<unsigned>(slices));
+    cudaError_t e =
+        p.add ? launch_dependent(reduce_kernel<G, W, VEC, true>, grid, kReduceThreads, 0, p, st)
+              : launch_dependent(reduce_kernel<G, W, VEC, false>, grid, kReduceThreads, 0, p, st);
     if (e != cudaSuccess || p.pieces == 1) return e;
     constexpr int J = VEC == 1 ? 1 : 4;  // four values to a lane, of fp32 parts
-    long long cols = (p.d + 32 * J - 1) / (32 * J);
-    if (cols > 8) cols = 8;
-    return launch_dependent(join_kernel<W, J>, dim3(p.pieces, static_cast<unsigned>(cols)),
+    const long long cols = (p.d + 32 * kJoinSlices * J - 1) / (32 * kJoinSlices * J);
+    return launch_dependent(join_kernel<W, J>, dim3(p.pieces - 1, static_cast<unsigned>(cols)),
                             32 * kJoinSlices, 0, p, st);
 }
 template <typename G, typename W>
@@ -454,10 +537,10 @@ int32_t sb_embedding_forward(const int32_t *ids, const void *W, int64_t M, int64
     return e == cudaSuccess ? SB_OK : SB_ERR_CUDA;
 }
 
-// [chunk-sorted tokens (only beyond one chunk)] [sorted tokens] [parts]
+// [keys, positions, keys, positions (each step of the sort goes from one pair to the other)] [parts]
 size_t sb_embedding_backward_workspace_bytes(int64_t M, int64_t d) {
     if (M < 0 || M > kMaxTokens || d < 1 || d > kMaxWidth) return 0;
-    const size_t tokens = up256(static_cast<size_t>(M) * 8) * (M > kChunk ? 2 : 1);
+    const size_t tokens = up256(static_cast<size_t>(M) * 4) * 4;
     const size_t parts = M > kPiece ? up256(static_cast<size_t>(pieces_of(M)) * 2 * d * 4) : 0;
     return 256 + tokens + parts;
 }
@@ -476,37 +559,56 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
     if (M == 0 && add) return SB_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const size_t tokens = up256(static_cast<size_t>(M) * 8);
-    int2 *sorted = reinterpret_cast<int2 *>(ws), *merged = sorted;
-    ws += tokens;
-    if (M > kChunk) {
-        merged = reinterpret_cast<int2 *>(ws);
-        ws += tokens;
+    const size_t array = up256(static_cast<size_t>(M) * 4);
+    uint32_t *key[2];
+    int *at[2];
+    for (int k = 0; k < 2; ++k, ws += 2 * array) {
+        key[k] = reinterpret_cast<uint32_t *>(ws);
+        at[k] = reinterpret_cast<int *>(ws + array);
     }
+    int now = 0;  // where the tokens are
     SortParams s{};
     s.ids = ids;
     s.M = static_cast<int>(M);
     s.V = static_cast<int>(V);
     s.ignore = ignore_index;
-    s.sort_blocks = static_cast<int>((M + 31) / 32);
-    s.sorted = sorted;
+    s.sort_blocks = static_cast<int>((M + kRun - 1) / kRun);
+    s.key = key[0];
+    s.at = at[0];
     if (!add) {
         s.zero = static_cast<uint8_t *>(dW);
         s.zero_bytes = static_cast<size_t>(V) * d * (weight_type == SB_F32 ? 4 : 2);
     }
-    const size_t keys = static_cast<size_t>(M < kChunk ? (M + 31) / 32 * 32 : kChunk) * 4;
-    if (launch_dependent(sort_kernel, dim3(s.sort_blocks + (add ? 0 : kZeroBlocks)), kSortThreads,
-                         keys, s, st) != cudaSuccess)
+    // (rounded up, and one more for what an unaligned head shifts to the end)
+    if (add) {
+        s.dout_row = static_cast<size_t>(d) * (grad_type == SB_F32 ? 4 : 2);
+        if (on(dout, 16) && s.dout_row % 16 == 0 && M > kRun) {
+            s.dout = static_cast<const uint8_t *>(dout);
+            s.fetch = static_cast<int>(M < kFetchBytes / static_cast<int64_t>(s.dout_row)
+                                           ? M
+                                           : kFetchBytes / static_cast<int64_t>(s.dout_row));
+        }
+    }
+    const size_t fetch_blocks = s.fetch > 0 ? kFetchBlocks : 0;
+    const size_t zero_blocks = add ? fetch_blocks : s.zero_bytes / (kRun * 32) + 1;
+    if (zero_blocks > (size_t(1) << 30)) return SB_ERR_INVALID_ARG;
+    if (launch_dependent(sort_kernel, dim3(s.sort_blocks + static_cast<unsigned>(zero_blocks)), kRun, 0,
+                         s, st) != cudaSuccess)
         return SB_ERR_CUDA;
     if (M == 0) return SB_OK;
-    if (M > kChunk) {
-        const MergeParams m{sorted, merged, static_cast<int>(M)};
-        if (launch_dependent(merge_kernel, dim3(static_cast<unsigned>((M + 255) / 256)), 256, 0, m,
-                             st) != cudaSuccess)
-            return SB_ERR_CUDA;
-    }
+    for (const int run : {kRun, kChunk})
+        if (M > run) {
+            const MergeParams m{key[now], at[now], key[1 - now], at[1 - now], static_cast<int>(M)};
+            const int64_t threads = M * (run == kRun ? kMergeLanes : 1);
+            const dim3 grid(static_cast<unsigned>((threads + kMergeThreads - 1) / kMergeThreads));
+            if (launch_dependent(run == kRun ? merge_runs_kernel : merge_chunks_kernel, grid,
+                                 kMergeThreads, 0, m, st) != cudaSuccess)
+                return SB_ERR_CUDA;
+            now = 1 - now;
+        }
     ReduceParams r{};
-    r.sorted = merged;
+    r.key = key[now];
+    r.at = at[now];
     r.dout = dout;
     r.dW = dW;
     r.part = reinterpret_cast<float *>(ws);

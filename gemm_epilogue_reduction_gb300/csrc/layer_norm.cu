@@ -6,11 +6,24 @@
 //     t = dh + r·(a - mean(a) - c·r²·mean(a·c)),  gradient of h = t,  dy = dropout(t),
 //     dweight = sum over rows of dx·c·r,  dbias = sum over rows of dx.
 //
-// The layout is that of the residual norm (norm.cu): sixteen values to a thread, a row to a group
-// of threads, weights and column sums in registers, the next rows on their way in a cp.async ring.
-// The variance is summed over the centred values, in a second reduction over the registers: a
-// stream's level may be far from zero, and E(h²) - E(h)² would cancel.  Backward forms the same two
-// from the stored h' instead of reading them; its other two sums go with the variance's.
+// The variance is summed over the centred values, in a second reduction over registers: a stream's
+// level may be far from zero, and E(h²) - E(h)² would cancel.  Backward forms mean and deviation from
+// the stored h' instead of reading them; its other two sums go with the variance's.
+//
+// Both are bound by memory, and what keeps them from it is the time that a row's threads wait for
+// each other in the two reductions.  As in the residual norm (norm.cu) a row belongs to a group of
+// threads, sixteen values to a thread, and the next rows are on their way in a cp.async ring.
+//   Forward: 768 threads, two rows of 6144 at a time, so that one's work fills the other's waits.
+//   The weights are in shared memory in fp32 (in registers the second row would not fit); each row
+//   reads them there.  8192 x 6144 bf16 with branch and dropout: 70 us, 5.8 TB/s (one row at a time
+//   with 168 registers: 74).  Blocks that do one row each and end, with the weights from L1, took
+//   108 us: their fixed work and their loads of weights weigh more than the waits.
+//   Backward keeps weights and column sums in registers: 384 threads and two rows side by side in
+//   each thread, whose sums go through the same two reductions; dx and dh are read again from the
+//   ring.  85 us, 5.9 TB/s (one row: 110).
+// A row length that is no multiple of eight shifts each row against the vectors' boundaries
+// (layer_norm.cuh); backward gives a group rows a multiple of eight apart, so that their shift, and
+// with it a thread's columns, stay the same.
 #include <cmath>
 
 #include "layer_norm.cuh"
@@ -44,8 +57,62 @@ LayerNormParams params_of(const void *h, const void *weight, const void *bias, i
     q.h = h;
     q.weight = weight;
     q.bias = bias;
+    q.wide_weights = on(weight, 16) && on(bias, 16);
     q.drop = make_dropout(p, seed, seed_offset);
     return q;
+}
+
+template <typename... Ptr>
+LoadMode mode_of(int64_t d, Ptr... ptrs) {
+    uintptr_t bits = 0;
+    ((bits |= reinterpret_cast<uintptr_t>(ptrs)), ...);
+    if (bits & 15u) return kSingle;
+    return d % 8 == 0 ? kAligned : d > 8 ? kShifted : kSingle;
+}
+// A row's threads, the groups of a block and the steps of a group's ring.  row_bytes: of a thread for
+// a row of the ring; rows: of a step; weight_bytes: of a thread, for the weights kept beside the rings
+// (one copy, or one to a group where the groups' shifts differ).
+struct Layout {
+    LoadMode mode;
+    int row_threads, groups, steps, rows;
+    bool weights;  // kept in shared memory
+    int64_t blocks;
+    size_t smem;
+};
+Layout lay_out(int64_t M, int64_t d, LoadMode mode, int threads, size_t row_bytes, int rows,
+               size_t weight_bytes, int sms) {
+    Layout l{};
+    auto threads_of = [d](int shift) {
+        return round32(((d + shift + 7) / 8 + kNormVectors - 1) / kNormVectors);
+    };
+    if (mode == kShifted && threads_of(7) > 1024) mode = kSingle;
+    l.mode = mode;
+    l.row_threads = threads_of(mode == kShifted ? 7 : 0);
+    l.groups = threads / l.row_threads;
+    if (l.groups > kMaxGroups) l.groups = kMaxGroups;
+    const int64_t share = (M + sms - 1) / sms;  // rows of an SM
+    if (l.groups > share) l.groups = static_cast<int>(share);
+    // a ring of two steps at least: one is on its way while another one is worked on; fewer groups,
+    // then single rows, where they do not fit
+    const size_t step = l.row_threads * row_bytes;
+    l.rows = mode != kSingle && share >= 2 * rows * (l.groups < 1 ? 1 : l.groups) ? rows : 1;
+    if (l.groups < 1) l.groups = l.rows = 1;
+    // rows too long for weights and two steps: the weights are read from memory again for each row
+    if (weight_bytes && 2 * step + weight_bytes * l.row_threads > kNormRingBytes) weight_bytes = 0;
+    l.weights = weight_bytes > 0;
+    auto weights = [&] { return weight_bytes * l.row_threads * (mode == kShifted ? l.groups : 1); };
+    auto fit = [&] { return (kNormRingBytes - weights()) / (l.rows * l.groups * step); };
+    while (mode != kSingle && fit() < 2 && l.groups > 1) --l.groups;
+    if (mode != kSingle && fit() < 2) l.rows = 1;
+    // (a row of backward beyond 10240 in fp32 has the ring to itself: nothing is ahead)
+    l.steps = mode == kSingle ? 1 : static_cast<int>(fit());
+    if (l.steps < 1) l.mode = kSingle, l.steps = 1, l.smem = 0;  // (no row is that long)
+    if (l.steps > kMaxDepth) l.steps = kMaxDepth;
+    l.smem = weights() + (l.mode == kSingle ? 0 : l.steps * l.rows * l.groups * step);
+    l.blocks = (M + l.groups - 1) / l.groups;
+    // (a multiple of eight: the rows of a group then have the same shift)
+    if (l.blocks > sms) l.blocks = mode == kShifted && sms > 8 ? sms & ~7 : sms;
+    return l;
 }
 
 }  // namespace
@@ -74,12 +141,14 @@ int32_t sb_layer_norm_forward(const void *h, const void *y, const void *weight, 
     q.h_out = h_out;
     q.x = x;
     const bool h32 = stream_type == SB_F32;
-    const int vec = vector_width(d, h, y, weight, bias, y ? h_out : nullptr, x);
-    const NormLayout l = layout_of(M, d, vec, (h32 ? 4 : 2) + (y ? 2 : 0), 0, sms);
+    const Layout l = lay_out(M, d, mode_of(d, h, y, y ? h_out : nullptr, x), kForwardThreads,
+                             kNormVectors * 8 * ((h32 ? 4 : 2) + (y ? 2 : 0)), 1, kNormVectors * 64, sms);
     q.row_threads = l.row_threads;
     q.groups = l.groups;
-    q.depth = l.depth;
-    return launch_layer_norm_forward(q, l.shape, h32, l.blocks, l.smem,
+    q.steps = l.steps;
+    q.shared_weights = l.weights;
+    const LayerNormShape shape{l.mode, h32, l.groups * l.row_threads, 1};
+    return launch_layer_norm_forward(q, shape, static_cast<unsigned>(l.blocks), l.smem,
                                      static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? SB_OK
                : SB_ERR_CUDA;
@@ -125,21 +194,24 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
     q.part = static_cast<float *>(workspace);
     q.sums = dbias ? 2 : 1;
     const bool h32 = stream_type == SB_F32;
-    const int vec = vector_width(d, dx, dh, h, weight, dh_out, dy, workspace);
-    const NormLayout l = layout_of(M, d, vec, (h32 ? 8 : 4) + 2,
-                                   static_cast<size_t>(q.sums) * d * 4, sms);
+    const Layout l = lay_out(M, d, mode_of(d, dx, dh, h, dh_out, dy), kBackwardThreads,
+                             kNormVectors * 8 * ((h32 ? 8 : 4) + 2), 2, 0, sms);
     q.row_threads = l.row_threads;
     q.groups = l.groups;
-    q.depth = l.depth;
+    q.steps = l.steps;
+    const LayerNormShape shape{l.mode, h32, l.groups * l.row_threads, l.rows};
+    size_t smem = l.smem;
+    const size_t sum_bytes = static_cast<size_t>(q.sums) * d * 4;
+    if (q.groups > 1 && smem < sum_bytes) smem = sum_bytes;
     ColumnParams c{};
     c.part = q.part;
-    c.blocks = l.blocks;
+    c.blocks = static_cast<int>(l.blocks);
     c.sums = q.sums;
     c.d = static_cast<int>(d);
     c.f32 = weight_type == SB_F32;
     c.dpre = dweight;
     c.dpost = dbias;
-    if (launch_layer_norm_backward(q, l.shape, h32, l.blocks, l.smem, st) != cudaSuccess ||
+    if (launch_layer_norm_backward(q, shape, static_cast<unsigned>(l.blocks), smem, st) != cudaSuccess ||
         launch_norm_columns(c, st) != cudaSuccess)
         return SB_ERR_CUDA;
     return SB_OK;

@@ -4,108 +4,174 @@
 namespace sb {
 namespace {
 
-// BRANCH: the gradient of the branch in front of its dropout is written too.
-template <typename T, int VEC, int EPT, int MAXT, bool BRANCH>
+// BRANCH: the gradient of the branch in front of its dropout is written too.  The groups of all
+// blocks take ROWS rows in turn; in kShifted all rows of a group have the same shift (the host sees to
+// that), so that a thread's columns stay the same.
+template <typename T, int MODE, bool BRANCH, int MAXT, int ROWS>
 __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams p) {
-    constexpr int P = EPT / 2;
+    static_assert(MODE != kSingle || ROWS == 1, "a row behind the last is in the ring only");
+    constexpr int NV = kNormVectors;
     using B = __nv_bfloat16;
-    using RH = RingArray<VEC, EPT, T>;
-    using RB = RingArray<VEC, EPT, B>;
-    // a row of the ring: h, dh, dx
-    constexpr int kDh = RH::kPerThread, kDx = 2 * RH::kPerThread, kRow = kDx + RB::kPerThread;
+    using ST = Slots<T>;
+    using SB = Slots<B>;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) float red1_all[MAXT / 32 + 4 * kMaxGroups];
-    __shared__ float red2_all[MAXT / 32 * 8];
+    __shared__ float red1_all[MAXT / 32 * 8], red2_all[MAXT / 32 * 8];
     const int rt = p.row_threads, d = p.d;
     const int group = threadIdx.x / rt, t = threadIdx.x - group * rt;
-    float *red1 = red1_all + group * sum_words(rt / 32), *red2 = red2_all + group * (rt / 32) * 8;
-    uint8_t *ring = smem + group * p.depth * kRow * rt;
+    float *red1 = red1_all + group * (rt / 32) * 8, *red2 = red2_all + group * (rt / 32) * 8;
+    // a row of the ring: h, dh, dx
+    const uint32_t pitch = rt * 16, kDh = ST::kThread * rt, kDx = 2 * kDh, kRow = kDx + SB::kThread * rt;
+    const uint32_t kRing = p.steps * ROWS * kRow;
+    const uint32_t ring = smem_u32(smem) + group * kRing + t * 16;  // this thread's pieces of it
     const int first = blockIdx.x * p.groups + group, stride = gridDim.x * p.groups;
+    const long long base = static_cast<long long>(first) * d, advance = static_cast<long long>(stride) * d;
+    const int shift = MODE == kShifted ? static_cast<int>(base & 7) : 0;
+    const int e0 = t * 8 - shift, per = rt * 8;  // this thread's first vector, and from one to the next
+    const bool last_has = MODE != kAligned && (static_cast<long long>(p.M) * d & 7) != 0;
+
+    // the row whose copy comes next, and where this thread's first vector of it is
+    long long next = first, from = base + e0;
     const T *h = static_cast<const T *>(p.h), *dh = static_cast<const T *>(p.dh);
     const B *dx = static_cast<const B *>(p.dx);
-
-    auto copy = [&](int slot, long long row) {
-        if constexpr (VEC > 1) {
-            if (row < p.M) {
-                uint8_t *at = ring + slot * kRow * rt;
-                const size_t o = static_cast<size_t>(row) * d;
-                RH::copy(at, h + o, rt, t, d);
-                if (dh) RH::copy(at + kDh * rt, dh + o, rt, t, d);
-                RB::copy(at + kDx * rt, dx + o, rt, t, d);
-            }
+    auto copy = [&](uint32_t at) {
+        if constexpr (MODE != kSingle) {
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k, next += stride, from += advance, at += kRow)
+                if (next < p.M) {
+                    // the array's last row may end inside a vector
+                    const bool inner = !last_has || next + 1 < p.M;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int e = e0 + i * per;
+                        const bool whole = inner || e + 8 <= d;
+                        ST::template copy<MODE>(at, pitch, i, h + from + i * per, e, d, whole);
+                        if (dh) ST::template copy<MODE>(at + kDh, pitch, i, dh + from + i * per, e, d, whole);
+                        SB::template copy<MODE>(at + kDx, pitch, i, dx + from + i * per, e, d, whole);
+                    }
+                }
             ring_commit();  // also without a row, so that the count of groups stays in step
         }
     };
-    if (t < sum_words(rt / 32)) red1[t] = 0.f;
-    if constexpr (VEC > 1)
-        for (int s = 0; s < p.depth; ++s) {
-            uint8_t *at = ring + s * kRow * rt;
-            RH::clear(at, rt, t, d);
-            RH::clear(at + kDh * rt, rt, t, d);
-            RB::clear(at + kDx * rt, rt, t, d);
-        }
-    __syncthreads();
+    long long at_row = base;  // of the row in hand
+    auto get_dx = [&](uint32_t at, int i, float2 (&v)[4]) {
+        if constexpr (MODE == kSingle)
+            load_singles(dx + at_row, e0 + i * per, d, v);
+        else
+            SB::get(at + kDx, pitch, i, v);
+        mask8<MODE>(e0 + i * per, d, v);
+    };
+    if constexpr (MODE != kSingle)
+        for (int s = 0; s < p.steps * ROWS; ++s)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                ST::clear(ring + s * kRow, pitch, i, e0 + i * per, d);
+                SB::clear(ring + s * kRow + kDx, pitch, i, e0 + i * per, d);
+            }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int s = 0; s + 1 < p.depth; ++s) copy(s, first + static_cast<long long>(s) * stride);
-    const unsigned long long seed = BRANCH ? dropout_seed(p.drop) : 0ull;
-    float2 w[P], s_w[P], s_b[P], zero[P];
-    get_weight<VEC, EPT>(p.weight, p.w32, rt, t, d, w);
+    for (int s = 0; s + 1 < p.steps; ++s) copy(ring + s * ROWS * kRow);
+    float2 w[NV][4], s_w[NV][4], s_b[NV][4];
 #pragma unroll
-    for (int i = 0; i < P; ++i) s_w[i] = s_b[i] = zero[i] = both(0.f);
-    int slot = 0;
-    for (long long row = first; row < p.M; row += stride) {
-        const size_t base = static_cast<size_t>(row) * d;
-        float2 vh[P], vdh[P], vdx[P];
+    for (int i = 0; i < NV; ++i) {
+        load_weight8<MODE>(p.weight, p, e0 + i * per, w[i]);
 #pragma unroll
-        for (int i = 0; i < P; ++i) vdh[i] = both(0.f);
-        if (VEC > 1 && p.depth) {
-            int ahead = slot + p.depth - 1;
-            if (ahead >= p.depth) ahead -= p.depth;
-            copy(ahead, row + static_cast<long long>(p.depth - 1) * stride);
-            ring_wait(p.depth - 1);
-            const uint8_t *at = ring + slot * kRow * rt;
-            if constexpr (VEC > 1) {
-                RH::get(at, rt, t, vh);
-                if (dh) RH::get(at + kDh * rt, rt, t, vdh);
-                RB::get(at + kDx * rt, rt, t, vdx);
+        for (int j = 0; j < 4; ++j) s_w[i][j] = s_b[i][j] = both(0.f);
+    }
+    // the draws' state goes from row to row by an addition: stride·d is a multiple of four (or there
+    // is no second row)
+    unsigned long long seed = 0, state = 0, state_row = 0, state_vector = 0;
+    if (BRANCH) {
+        seed = dropout_seed(p.drop);
+        state = splitmix_state(seed, static_cast<unsigned long long>(base + e0) / 4);
+        state_row = static_cast<unsigned long long>(advance / 4) * kGolden;
+        state_vector = static_cast<unsigned long long>(rt * 2) * kGolden;
+    }
+    uint32_t slot = 0, ahead = (p.steps - 1) * ROWS * kRow;  // of the ring, in bytes
+    for (long long row0 = first; row0 < p.M; row0 += ROWS * stride) {
+        if constexpr (MODE != kSingle) {
+            copy(ring + ahead);
+            ahead = ahead + ROWS * kRow == kRing ? 0 : ahead + ROWS * kRow;
+            ring_wait(p.steps - 1);
+        }
+        const uint32_t at = ring + slot;
+        float2 c[ROWS][NV][4];
+        float sum1[ROWS], sum2[3 * ROWS];
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            float2 acc = both(0.f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = e0 + i * per;
+                if constexpr (MODE == kSingle)
+                    load_singles(h + at_row, e, d, c[k][i]);
+                else
+                    ST::get(at + k * kRow, pitch, i, c[k][i]);  // (a row behind the last: an old one)
+                mask8<MODE>(e, d, c[k][i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc = __fadd2_rn(acc, c[k][i][j]);
             }
-        } else {
-            get<VEC, EPT>(h + base, rt, t, d, vh);
-            if (dh) get<VEC, EPT>(dh + base, rt, t, d, vdh);
-            get<VEC, EPT>(dx + base, rt, t, d, vdx);
+            sum1[k] = acc.x + acc.y;
         }
-        float2 acc = both(0.f);
-#pragma unroll
-        for (int i = 0; i < P; ++i) acc = __fadd2_rn(acc, vh[i]);
-        const float mean = row_sum<MAXT>(acc.x + acc.y, group, rt, red1) * p.inv_d;
-        centre<VEC, EPT>(mean, rt, t, d, vh);
+        row_sum<MAXT>(sum1, group, rt, red1);
         // sums of c², a and a·c with c = h - mean
-        float2 s0 = both(0.f), s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float2 a = __fmul2_rn(vdx[i], w[i]);
-            s0 = __ffma2_rn(vh[i], vh[i], s0);
-            s1 = __fadd2_rn(s1, a);
-            s2 = __ffma2_rn(a, vh[i], s2);
-        }
-        float sum[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
-        row_sum<MAXT>(sum, group, rt, red2);
-        const float r = rsqrtf(sum[0] * p.inv_d + p.eps);
-        const float ma = -r * (sum[1] * p.inv_d), c2 = -r * r * r * (sum[2] * p.inv_d);
+        for (int k = 0; k < ROWS; ++k) {
+            const float mean = sum1[k] * p.inv_d;
+            float2 s0 = both(0.f), s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float2 xr = __fmul2_rn(vdx[i], both(r));
-            s_w[i] = __ffma2_rn(xr, vh[i], s_w[i]);
-            s_b[i] = __fadd2_rn(s_b[i], vdx[i]);
-            vdh[i] = __ffma2_rn(both(c2), vh[i], __ffma2_rn(xr, w[i], __fadd2_rn(vdh[i], both(ma))));
+            for (int i = 0; i < NV; ++i) {
+                float2 x[4];
+                get_dx(at + k * kRow, i, x);
+                centre8<MODE>(mean, e0 + i * per, d, c[k][i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 a = __fmul2_rn(x[j], w[i][j]);
+                    s0 = __ffma2_rn(c[k][i][j], c[k][i][j], s0);
+                    s1 = __fadd2_rn(s1, a);
+                    s2 = __ffma2_rn(a, c[k][i][j], s2);
+                }
+            }
+            sum2[3 * k] = s0.x + s0.y, sum2[3 * k + 1] = s1.x + s1.y, sum2[3 * k + 2] = s2.x + s2.y;
         }
-        put<VEC, EPT>(static_cast<T *>(p.dh_out) + base, rt, t, d, vdh);
-        if constexpr (BRANCH) {
-            add_dropped<VEC, EPT>(p.drop, seed, base, rt, t, d, zero, vdh);
-            put<VEC, EPT>(static_cast<B *>(p.dy) + base, rt, t, d, vdh);
+        row_sum<MAXT>(sum2, group, rt, red2);
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            if (k > 0 && row0 + k * stride >= p.M) break;
+            const float r = rsqrtf(sum2[3 * k] * p.inv_d + p.eps);
+            const float ma = -r * (sum2[3 * k + 1] * p.inv_d), c2 = -r * r * r * (sum2[3 * k + 2] * p.inv_d);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = e0 + i * per;
+                float2 x[4], v[4];
+                get_dx(at + k * kRow, i, x);
+                if (!dh) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = both(0.f);
+                } else if constexpr (MODE == kSingle) {
+                    load_singles(dh + at_row, e, d, v);
+                } else {
+                    ST::get(at + k * kRow + kDh, pitch, i, v);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 xr = __fmul2_rn(x[j], both(r));
+                    s_w[i][j] = __ffma2_rn(xr, c[k][i][j], s_w[i][j]);
+                    s_b[i][j] = __fadd2_rn(s_b[i][j], x[j]);
+                    v[j] = __ffma2_rn(both(c2), c[k][i][j],
+                                      __ffma2_rn(xr, w[i][j], __fadd2_rn(v[j], both(ma))));
+                }
+                store8<MODE>(static_cast<T *>(p.dh_out) + at_row + e, e, d, v);
+                if constexpr (BRANCH) {
+                    const float2 zero[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+                    add_dropped<MODE>(p.drop, seed, state + i * state_vector,
+                                      static_cast<unsigned long long>(at_row + e), zero, v);
+                    store8<MODE>(static_cast<B *>(p.dy) + at_row + e, e, d, v);
+                }
+            }
+            at_row += advance;
+            state += state_row;
         }
-        if (++slot >= p.depth) slot = 0;
+        slot = slot + ROWS * kRow == kRing ? 0 : slot + ROWS * kRow;
     }
     // the groups' column sums in ascending order, through shared memory (the ring's rows have
     // all been read), then this block's partial vectors
@@ -118,30 +184,50 @@ __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (k >= p.sums) break;
-            float2 v[P];
 #pragma unroll
-            for (int i = 0; i < P; ++i) v[i] = k == 0 ? s_w[i] : s_b[i];
-            if (g > 0) {
-                float2 x[P];
-                get<VEC, EPT>(all + k * d, rt, t, d, x);
+            for (int i = 0; i < NV; ++i) {
+                const int e = e0 + i * per;
+                float2 v[4];
 #pragma unroll
-                for (int i = 0; i < P; ++i) v[i] = __fadd2_rn(v[i], x[i]);
+                for (int j = 0; j < 4; ++j) v[j] = k == 0 ? s_w[i][j] : s_b[i][j];
+                if (g > 0) {
+                    float2 x[4];
+                    if (MODE == kAligned && e < d)
+                        load_pairs<8>(all + k * d + e, x);
+                    else
+                        load_singles(all + k * d, e, d, x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = __fadd2_rn(v[j], x[j]);
+                }
+                float *to = (g + 1 < p.groups ? all : part) + k * d;
+                if (MODE == kAligned && e < d)
+                    store_pairs<8>(to + e, v);
+                else
+                    store_singles(to, e, d, v);
             }
-            put<VEC, EPT>((g + 1 < p.groups ? all : part) + k * d, rt, t, d, v);
         }
     }
 }
 
 }  // namespace
 
-cudaError_t launch_layer_norm_backward(const LayerNormParams &p, NormShape s, bool h32, int blocks,
+cudaError_t launch_layer_norm_backward(const LayerNormParams &p, LayerNormShape s, unsigned blocks,
                                        size_t smem, cudaStream_t st) {
-    return for_norm_shape(s, h32, p.dy != nullptr,
-                          [&]<typename T, int VEC, int EPT, int MAXT, bool BRANCH>() {
-                              static std::atomic<uint64_t> opted_in{0};
-                              return launch_norm_kernel(backward_kernel<T, VEC, EPT, MAXT, BRANCH>,
-                                                        opted_in, p, blocks, smem, st);
-                          });
+    return for_layer_norm(s, p.dy != nullptr, [&]<typename T, int MODE, bool BRANCH>() {
+        static std::atomic<uint64_t> pairs{0}, small{0}, medium{0}, large{0};
+        const int n = static_cast<int>(blocks);
+        if (s.threads <= kBackwardThreads) {
+            if constexpr (MODE != kSingle)
+                if (s.rows == 2)
+                    return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kBackwardThreads, 2>, pairs, p,
+                                              n, smem, st);
+            return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kBackwardThreads, 1>, small, p, n,
+                                      smem, st);
+        }
+        if (s.threads <= 640)
+            return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, 640, 1>, medium, p, n, smem, st);
+        return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, 1024, 1>, large, p, n, smem, st);
+    });
 }
 
 }  // namespace sb

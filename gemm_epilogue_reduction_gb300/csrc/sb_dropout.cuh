@@ -49,15 +49,26 @@ struct DropoutFields {
         return k & 1 ? w : w << 16;  // what lies below the field cannot change the comparison
     }
 };
-__device__ __forceinline__ DropoutFields dropout_fields(unsigned long long seed,
-                                                        unsigned long long group) {
-    const unsigned long long x = bits64_from_state(splitmix_state(seed, group));
+__device__ __forceinline__ DropoutFields dropout_fields_at(unsigned long long state) {
+    const unsigned long long x = bits64_from_state(state);
     return DropoutFields{static_cast<uint32_t>(x), static_cast<uint32_t>(x >> 32)};
 }
-// base + dropout(x): a dropped x leaves no trace, not even as a NaN or an infinity.
-__device__ __forceinline__ float dropout_add(float base, float x, uint32_t field, uint32_t below,
-                                             float scale) {
-    return field > below ? fmaf(x, scale, base) : base;
+__device__ __forceinline__ DropoutFields dropout_fields(unsigned long long seed,
+                                                        unsigned long long group) {
+    return dropout_fields_at(splitmix_state(seed, group));
+}
+// x, or zero where it is dropped: no trace of it, not even of a NaN or an infinity.
+__device__ __forceinline__ float dropout_keep(float x, uint32_t field, uint32_t below) {
+    return field > below ? x : 0.f;
+}
+// v = base + dropout(v) for the four elements of a draw, in two pairs.
+__device__ __forceinline__ void dropout_add4(const float2 *base, float2 *v, const DropoutFields &f,
+                                             uint32_t below, float scale) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        v[k].x = f.field(2 * k) > below ? fmaf(v[k].x, scale, base[k].x) : base[k].x;
+        v[k].y = f.field(2 * k + 1) > below ? fmaf(v[k].y, scale, base[k].y) : base[k].y;
+    }
 }
 
 }  // namespace sb

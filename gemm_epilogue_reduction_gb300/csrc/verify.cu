@@ -14,9 +14,9 @@
 // reading the logits.  Skipped where the caller has the logsumexp (the head's projection returns
 // it).  verify_kernel: a cluster of blocks per request.  Every block joins the rows' pieces and
 // decides for itself, then scans its share of the one row that a sample is drawn from, with q's
-// beside it; the blocks exchange their best through distributed shared memory.  Most columns of
-// the scan cannot win and do not compute a logarithm: -ln u >= 1 - u, so w·ln 2 / (1 - u), which
-// takes one product each way, bounds the score from above.
+// beside it; the blocks exchange their best through distributed shared memory.  Few columns of the
+// scan can win: bounds of every score from both sides, without a logarithm, leave one or two columns
+// of a warp's vectors whose score is formed.
 #include <cmath>
 
 #include "norm_common.cuh"
@@ -32,8 +32,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLseThreads = 256;
 constexpr int kLseAhead = 4;         // 16-byte vectors in flight
 constexpr int kLsePiece = 4096;      // fewest columns of a piece
+constexpr int kLseBlocks = 152 * 16;  // that many pieces at least, where the rows are long enough
 constexpr int kVerifyThreads = 512;
-constexpr int kVerifyCluster = 8;
+constexpr int kVerifyCluster = 8;      // blocks of a request
+constexpr int kWideCluster = 16;       // the same for few requests, where the device allows it
+constexpr int kWideRequests = 9;       // 9 x 16 blocks: one to an SM
 
 struct VerifyParams {
     const void *z, *q;
@@ -69,13 +72,12 @@ __device__ __forceinline__ MaxSum warp_join(MaxSum a, float c) {
     return a;
 }
 
-__device__ __forceinline__ void unpack(uint4 x, float (&v)[8], __nv_bfloat16) {
-    const float2 a = unpack2(x.x), b = unpack2(x.y), c = unpack2(x.z), d = unpack2(x.w);
-    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
+__device__ __forceinline__ void unpack(uint4 x, float2 (&v)[4], __nv_bfloat16) {
+    v[0] = unpack2(x.x), v[1] = unpack2(x.y), v[2] = unpack2(x.z), v[3] = unpack2(x.w);
 }
-__device__ __forceinline__ void unpack(uint4 x, float (&v)[4], float) {
-    v[0] = __uint_as_float(x.x), v[1] = __uint_as_float(x.y);
-    v[2] = __uint_as_float(x.z), v[3] = __uint_as_float(x.w);
+__device__ __forceinline__ void unpack(uint4 x, float2 (&v)[2], float) {
+    v[0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+    v[1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
 }
 
 template <typename T>
@@ -104,29 +106,43 @@ __global__ void __launch_bounds__(kLseThreads) lse_kernel(const VerifyParams p) 
         if (i >= 32 && i - 32 < tail) a = MaxSum{one(from + head + nv * E + i - 32), 1.f};
         if (a.m == -INFINITY) a.s = 0.f;
     }
-    for (int i0 = v0 + static_cast<int>(threadIdx.x); i0 < v1; i0 += kLseThreads * kLseAhead) {
-        uint4 x[kLseAhead];
+    const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf: adds nothing
+    uint4 x[kLseAhead];
+    auto load = [&](int i0) {
 #pragma unroll
         for (int k = 0; k < kLseAhead; ++k) {
             const int i = i0 + k * kLseThreads;
-            x[k] = i < v1 ? vec[i] : make_uint4(0, 0, 0, 0);
+            x[k] = i < v1 ? vec[i] : make_uint4(none, none, none, none);
         }
+    };
+    int i0 = v0 + static_cast<int>(threadIdx.x);
+    load(i0);
+    while (i0 < v1) {
+        float2 v[kLseAhead][E / 2];
+        float top[kLseAhead];
 #pragma unroll
         for (int k = 0; k < kLseAhead; ++k) {
-            if (i0 + k * kLseThreads >= v1) break;
-            float v[E];
-            unpack(x[k], v, T{});
-            float m = a.m;
+            unpack(x[k], v[k], T{});
+            top[k] = fmaxf(v[k][0].x, v[k][0].y);
 #pragma unroll
-            for (int j = 0; j < E; ++j) m = fmaxf(m, v[j]);
-            if (m > a.m) {  // (not at all while every value is -inf)
-                a.s *= ex2_approx((a.m - m) * c);
-                a.m = m;
-            }
-            const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int j = 0; j < E; ++j) a.s += ex2_approx((v[j] - ref) * c);
+            for (int j = 1; j < E / 2; ++j) top[k] = fmaxf(top[k], fmaxf(v[k][j].x, v[k][j].y));
         }
+        i0 += kLseThreads * kLseAhead;
+        load(i0);  // the next ones are on their way meanwhile
+        float m = a.m;
+#pragma unroll
+        for (int k = 0; k < kLseAhead; ++k) m = fmaxf(m, top[k]);
+        const float ref = m == -INFINITY ? 0.f : m;
+        float2 sum[2] = {make_float2(a.s * ex2_approx((a.m - ref) * c), 0.f), both(0.f)};
+#pragma unroll
+        for (int k = 0; k < kLseAhead; ++k)
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j) {
+                const float2 y = __fmul2_rn(__fadd2_rn(v[k][j], both(-ref)), both(c));
+                sum[j & 1] = __fadd2_rn(sum[j & 1], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+            }
+        a.m = m;
+        a.s = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
     a = warp_join(a, c);
     if ((threadIdx.x & 31) == 0) {
@@ -151,7 +167,25 @@ __device__ double row_lse(const VerifyParams &p, bool draft, int at, int lane) {
     for (int s = lane; s < p.splits; s += 32) a = join(a, MaxSum{part[s].x, part[s].y}, c);
     a = warp_join(a, c);
     if (a.m == -INFINITY && a.s == 0.f) return -INFINITY;
-    return static_cast<double>(a.m) * p.inv_t + log(static_cast<double>(a.s));
+    // log s = e ln 2 + log f with s = f·2^e, f in [1, 2): in fp32 log s would be off by its own ulp
+    const uint32_t bits = __float_as_uint(a.s);
+    const int e = static_cast<int>((bits >> 23) & 255) - 127;  // s is 1 at least, but for roundings
+    const float f = __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
+    if (!(a.s > 0.f && a.s < INFINITY)) return static_cast<double>(a.m) * p.inv_t + a.s;  // not finite
+    return static_cast<double>(a.m) * p.inv_t + (e * 0.69314718055994531 + logf(f));
+}
+
+// Whether e^x > u, for x whose rounding to fp32 would count.
+__device__ __forceinline__ bool exp_above(double x, float u) {
+    const float hi = static_cast<float>(x), e = expf(hi);
+    if (!(e > 0.f && e < INFINITY)) return e > u;
+    return fmaf(e, static_cast<float>(x - hi), e) > u;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t cluster_blocks() {
@@ -170,41 +204,114 @@ __device__ __forceinline__ unsigned long long pack(float score, int column) {
 
 enum : int { kTarget = 0, kDifference = 1, kWithout = 2 };  // what a sample is drawn from
 
-// This thread's best of columns [c0, c1).
+// One row's scan: what a sample is drawn from, this thread's best so far, and what a column has to reach
+// (a lower bound of the best score that the warp has seen).
+template <typename T, int FROM>
+struct Scan {
+    const VerifyParams &p;
+    const T *z, *q;
+    float lse, qlse;
+    int x;
+    unsigned long long first;  // index of the row's first draw
+    float best, bar;
+    int column;
+
+    __device__ __forceinline__ float weight(float a, float b, int j) const {
+        float w = ex2_approx(fmaf(a, p.inv_t, -lse) * kLog2e);
+        if (FROM == kDifference) w -= ex2_approx(fmaf(b, p.inv_t, -qlse) * kLog2e);
+        if (FROM == kWithout && j == x) w = 0.f;
+        return w;
+    }
+    __device__ __forceinline__ void exact(int j) {
+        const uint32_t bits = bits24_from_state(splitmix_state(p.seed, first + j));
+        const float score =
+            bits ? weight(one(z + j), FROM == kDifference ? one(q + j) : 0.f, j) / -log2_uniform(bits) : 0.f;
+        // columns come in any order: of equal scores the lowest stays
+        if (score > best || (score == best && j < column)) best = score, column = j;
+    }
+    // N columns of each thread of the warp, with their logits: j, j + STEP, ...; `have` of them count.
+    template <int N, int STEP>
+    __device__ __forceinline__ void columns(const float (&a)[N], const float (&b)[N], int j, int have) {
+        float bound[N], low = 0.f;
+        const unsigned long long state = splitmix_state(p.seed, first + j);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float w = weight(a[k], b[k], j + k * STEP);
+            const uint32_t bits = bits24_from_state(state + static_cast<unsigned long long>(k * STEP) * kGolden);
+            // With l = 1 - u:  l <= -ln u <= l / (1 - l), so the score w / -log2 u lies between
+            // w·ln 2 / l and that times 1 - l.  The constants leave room for the roundings of both and
+            // of the score itself (2e-6 and 4e-6 against some 1e-6).
+            const float l = static_cast<float>(16777216u - bits) * 5.9604644775390625e-8f;
+            const float top = k < have ? w * 0.69314860f * rcp_approx(l) : 0.f;
+            bound[k] = top;
+            low = fmaxf(low, top * fmaf(l, -0.999994f, 0.999994f));
+        }
+        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(low));  // (low >= 0)
+        bar = fmaxf(bar, __uint_as_float(most));
+        uint32_t promising = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) promising |= static_cast<uint32_t>(bound[k] > bar) << k;
+        for (; promising; promising &= promising - 1) exact(j + (__ffs(promising) - 1) * STEP);
+    }
+};
+
+// This thread's best of the share of block `rank` of `blocks`.
 template <typename T, int FROM>
 __device__ __forceinline__ unsigned long long scan(const VerifyParams &p, const T *z, const T *q,
                                                    float lse, float qlse, int x,
-                                                   unsigned long long first, int c0, int c1) {
-    constexpr int U = 4;
-    float best = 0.f;
-    int column = 0;
-    for (int j0 = c0 + static_cast<int>(threadIdx.x); j0 < c1; j0 += U * kVerifyThreads) {
-        float a[U], b[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int j = j0 + k * kVerifyThreads;
-            a[k] = j < c1 ? one(z + j) : -INFINITY;
-            b[k] = FROM == kDifference && j < c1 ? one(q + j) : -INFINITY;
+                                                   unsigned long long first, int rank, int blocks) {
+    constexpr int E = 16 / sizeof(T);
+    const int tid = threadIdx.x;
+    Scan<T, FROM> s{p, z, q, lse, qlse, x, first, 0.f, 0.f, 0};
+    const uintptr_t off = reinterpret_cast<uintptr_t>(z) & 15;
+    if (FROM != kDifference || off == (reinterpret_cast<uintptr_t>(q) & 15)) {
+        const int head = min(p.V, static_cast<int>((16 - off) & 15) / static_cast<int>(sizeof(T)));
+        const int nv = (p.V - head) / E, tail = head + nv * E;
+        const int v0 = static_cast<int>(static_cast<long long>(nv) * rank / blocks);
+        const int v1 = static_cast<int>(static_cast<long long>(nv) * (rank + 1) / blocks);
+        const uint4 *za = reinterpret_cast<const uint4 *>(z + head);
+        const uint4 *qa = reinterpret_cast<const uint4 *>(q + head);
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (v0 + tid < v1) {
+            a = za[v0 + tid];
+            if (FROM == kDifference) b = qa[v0 + tid];
         }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int j = j0 + k * kVerifyThreads;
-            float w = ex2_approx(fmaf(a[k], p.inv_t, -lse) * kLog2e);
-            if (FROM == kDifference) w -= ex2_approx(fmaf(b[k], p.inv_t, -qlse) * kLog2e);
-            if (FROM == kWithout && j == x) w = 0.f;
-            const uint32_t bits = bits24_from_state(splitmix_state(p.seed, first + j));
-            // an upper bound of the score: -ln u >= 1 - u
-            const float left = static_cast<float>(16777216u - bits) * 5.9604644775390625e-8f;
-            if (w * 0.69314790f > best * left && j < c1 && bits != 0) {  // ln 2 and its rounding
-                const float score = w / -log2_uniform(bits);
-                if (score > best) {
-                    best = score;
-                    column = j;
-                }
+        for (int i0 = v0; i0 < v1; i0 += kVerifyThreads) {  // (the same turns for all threads)
+            const int i = i0 + tid, next = i + kVerifyThreads;
+            float2 pa[E / 2], pb[E / 2];
+            unpack(a, pa, T{});
+            unpack(b, pb, T{});
+            if (next < v1) {
+                a = za[next];
+                if (FROM == kDifference) b = qa[next];
             }
+            float va[E], vb[E];
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j)
+                va[2 * j] = pa[j].x, va[2 * j + 1] = pa[j].y, vb[2 * j] = pb[j].x, vb[2 * j + 1] = pb[j].y;
+            s.template columns<E, 1>(va, vb, head + i * E, i < v1 ? E : 0);
+        }
+        if (rank == 0 && tid < head) s.exact(tid);
+        if (rank == blocks - 1 && tid < p.V - tail) s.exact(tail + tid);
+    } else {
+        // rows of an odd vocabulary: z's and q's vectors never lie side by side
+        constexpr int W = 8;
+        const int c0 = static_cast<int>(static_cast<long long>(p.V) * rank / blocks);
+        const int c1 = static_cast<int>(static_cast<long long>(p.V) * (rank + 1) / blocks);
+        for (int j0 = c0; j0 < c1; j0 += W * kVerifyThreads) {
+            const int j = j0 + tid;
+            float a[W], b[W];
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const int i = min(j + k * kVerifyThreads, c1 - 1);
+                a[k] = one(z + i);
+                b[k] = one(q + i);
+            }
+            s.template columns<W, kVerifyThreads>(a, b, j,
+                                                  max(0, (c1 - j + kVerifyThreads - 1) / kVerifyThreads));
         }
     }
-    return pack(best, column);
+    return pack(s.best, s.column);
 }
 
 template <typename T>
@@ -260,7 +367,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
                 const double l = static_cast<double>(one(z + static_cast<size_t>(i) * p.V + x) * p.inv_t) - lse;
                 const double m = q ? static_cast<double>(one(q + static_cast<size_t>(i) * p.V + x) * p.inv_t) - qlse : 0.0;
                 lp = static_cast<float>(l);
-                stays = exp(l - m) > static_cast<double>(p.u[r]);
+                stays = exp_above(l - m, p.u[r]);
             } else if (rank == 0) {
                 record_status(p.status, p.epoch, 1u);
             }
@@ -282,8 +389,6 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     z += static_cast<size_t>(e) * p.V;
     const int x = e < n ? p.drafts[r] : -1;
     const bool known = x >= 0 && x < p.V;  // otherwise nothing is taken off p
-    const int c0 = static_cast<int>(static_cast<long long>(p.V) * rank / blocks);
-    const int c1 = static_cast<int>(static_cast<long long>(p.V) * (rank + 1) / blocks);
     const unsigned long long first = static_cast<unsigned long long>(r) * static_cast<unsigned>(p.V);
     const float lse = static_cast<float>(end_lse), qlse = static_cast<float>(end_qlse);
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -291,11 +396,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     for (int turn = 0; turn < 2 && !best; ++turn) {
         // a difference that is nowhere positive (p and q equal but for roundings): p itself
         if (turn == 0 && known && q)
-            best = scan<T, kDifference>(p, z, q + static_cast<size_t>(e) * p.V, lse, qlse, x, first, c0, c1);
+            best = scan<T, kDifference>(p, z, q + static_cast<size_t>(e) * p.V, lse, qlse, x, first, rank, blocks);
         else if (turn == 0 && known)
-            best = scan<T, kWithout>(p, z, nullptr, lse, 0.f, x, first, c0, c1);
+            best = scan<T, kWithout>(p, z, nullptr, lse, 0.f, x, first, rank, blocks);
         else
-            best = scan<T, kTarget>(p, z, nullptr, lse, 0.f, x, first, c0, c1);
+            best = scan<T, kTarget>(p, z, nullptr, lse, 0.f, x, first, rank, blocks);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const unsigned long long other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
@@ -370,18 +475,42 @@ cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
                                                kLseThreads, 0, p, st);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B > 0 ? p.B : 1) * kVerifyCluster);
-    cfg.blockDim = dim3(kVerifyThreads);
-    cfg.stream = st;
+    auto config = [&](int blocks, cudaLaunchAttribute (&attr)[2]) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(p.B > 0 ? p.B : 1) * blocks);
+        cfg.blockDim = dim3(kVerifyThreads);
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = blocks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cfg;
+    };
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kVerifyCluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    int blocks = kVerifyCluster;
+    if (p.B <= kWideRequests) {
+        // more than eight blocks to a cluster are no part of the portable model: asked once a device
+        static std::atomic<uint64_t> asked{0}, allowed{0};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+        if (bit && !(asked.load() & bit)) {
+            int clusters = 0;
+            cudaLaunchConfig_t cfg = config(kWideCluster, attr);
+            cfg.numAttrs = 1;
+            e = cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, verify_kernel<T>, &cfg);
+            if (e == cudaSuccess && clusters > 0) allowed.fetch_or(bit);
+            cudaGetLastError();  // a refusal is an answer here
+            asked.fetch_or(bit);
+        }
+        if (allowed.load() & bit) blocks = kWideCluster;
+    }
+    const cudaLaunchConfig_t cfg = config(blocks, attr);
     return cudaLaunchKernelEx(&cfg, verify_kernel<T>, p);
 }
 
@@ -389,7 +518,7 @@ cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
 // block has hardly begun with before it ends.
 int splits_of(int64_t rows, int64_t V) {
     if (rows < 1) return 1;
-    int64_t s = (152 * 8 + rows - 1) / rows;
+    int64_t s = (kLseBlocks + rows - 1) / rows;
     const int64_t most = (V + kLsePiece - 1) / kLsePiece;
     if (s > most) s = most;
     return static_cast<int>(s < 1 ? 1 : s);
@@ -412,7 +541,7 @@ size_t sb_verify_workspace_bytes(int64_t R, int64_t draft_rows, int64_t V) {
     // the number of pieces falls with the rows that are reduced: the largest product of the two
     const int64_t rows = R + (draft_rows > 0 ? draft_rows : 0), most = (V + kLsePiece - 1) / kLsePiece;
     int64_t parts = rows * most;
-    if (parts > rows + 152 * 8) parts = rows + 152 * 8;
+    if (parts > rows + kLseBlocks) parts = rows + kLseBlocks;
     return 256 + up256(static_cast<size_t>(parts) * 8);
 }
 
