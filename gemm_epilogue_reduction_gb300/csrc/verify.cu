@@ -10,13 +10,17 @@
 // choice of sb_lmhead_project's SB_GUMBEL_TOKEN with the logarithms taken away, which differences
 // of probabilities would not survive.
 //
-// lse_kernel: per (row, piece of the vocabulary) the maximum and the sum of exponentials; bound by
-// reading the logits.  Skipped where the caller has the logsumexp (the head's projection returns
-// it).  verify_kernel: a cluster of blocks per request.  Every block joins the rows' pieces and
-// decides for itself, then scans its share of the one row that a sample is drawn from, with q's
-// beside it; the blocks exchange their best through distributed shared memory.  Few columns of the
-// scan can win: bounds of every score from both sides, without a logarithm, leave one or two columns
-// of a warp's vectors whose score is formed.
+// lse_kernel: the maxima and sums of exponentials of the rows, where the caller has not got their
+// logsumexps (the head's projection returns them); bound by reading the logits.  All rows' vectors
+// are one sequence, cut into equal pieces for kLseBlocks blocks, whatever the number of rows and their
+// length (a block per row, or per part of one, took 36 us for 576 rows of 151,936 in waves that did
+// not fill the GPU).  verify_kernel: a cluster of blocks per request.  Every block joins the rows'
+// pieces and decides for itself which drafts stay, then scans its share of the one row that a sample
+// is drawn from, with q's beside it; the blocks exchange their best through distributed shared
+// memory.  Few columns of the scan can win: bounds of every score from both sides, without a
+// logarithm, leave one or two columns of a warp's vectors whose score is formed.  (One kernel for
+// both, each cluster with its own request's rows, took 108 us for 64 requests of 1 to 9 rows: the
+// long ones come last.)
 #include <cmath>
 
 #include "norm_common.cuh"
@@ -30,149 +34,220 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLseThreads = 256;
-constexpr int kLseAhead = 4;         // 16-byte vectors in flight
-constexpr int kLsePiece = 4096;      // fewest columns of a piece
-constexpr int kLseBlocks = 152 * 16;  // that many pieces at least, where the rows are long enough
-constexpr int kVerifyThreads = 512;
-constexpr int kVerifyCluster = 8;      // blocks of a request
-constexpr int kWideCluster = 16;       // the same for few requests, where the device allows it
-constexpr int kWideRequests = 9;       // 9 x 16 blocks: one to an SM
+constexpr int kLseBlocks = 152 * 4;    // as many as fit at a time
+constexpr int kAhead = 4;               // 16-byte vectors of a thread in flight
+constexpr int kBlocks = 8;              // of a request's cluster
+constexpr int kWideBlocks = 16;         // the same for few requests, where the device allows it
+constexpr int kWideRequests = 9;        // 9 x 16 blocks: one to an SM
+constexpr int kFewRequests = 38;        // 38 x 8 blocks of 512 threads: two to an SM; more: of 256
 
 struct VerifyParams {
     const void *z, *q;
     const int32_t *drafts, *starts;
     const float *u, *lse, *qlse;
     int R, B, V, Rd;
+    int zrows, qrows;   // of them, how many lse_kernel reduces (those behind the last request aside)
     int with_q;         // drafts have distributions of their own
-    int zrows, qrows;   // of them, how many lse_kernel reduces
-    int splits;
     float inv_t;
     unsigned long long seed;
     int32_t *token, *accepted;
     float *logprob;
-    float2 *part;       // [zrows + qrows][splits] (max, sum of exponentials relative to it)
+    float2 *part;       // MaxSum, see Pieces
     uint32_t *epoch_word;
     unsigned long long *status;
     uint32_t epoch;
 };
 
+// The largest logit m and the sum s of 2^((v - m)·c) with c = 1/T·log2(e), so that the largest one's term is
+// exactly 1.  m = -inf where nothing has been seen (s is then 0, or no number).
 struct MaxSum {
     float m, s;
 };
-// c: 1/T times log2(e).  -inf maxima (nothing seen) carry s = 0.
 __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
-    const float m = fmaxf(a.m, b.m);
-    if (m == -INFINITY) return MaxSum{m, a.s + b.s};
-    return MaxSum{m, a.s * ex2_approx((a.m - m) * c) + b.s * ex2_approx((b.m - m) * c)};
+    const float m = fmaxf(a.m, b.m), ref = m == -INFINITY ? 0.f : m;
+    return MaxSum{m, a.s * ex2_approx((a.m - ref) * c) + b.s * ex2_approx((b.m - ref) * c)};
 }
 __device__ __forceinline__ MaxSum warp_join(MaxSum a, float c) {
+    // (a maximum that is no number is none: its sum says so)
+    const float m = ordered_to_float(
+        __reduce_max_sync(0xFFFFFFFFu, float_to_ordered(a.m == a.m ? a.m : -INFINITY)));
+    a.s *= ex2_approx((a.m - (m == -INFINITY ? 0.f : m)) * c);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        a = join(a, MaxSum{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o)}, c);
-    return a;
+    for (int o = 16; o > 0; o >>= 1) a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, o);
+    return MaxSum{m, a.s};
 }
 
 __device__ __forceinline__ void unpack(uint4 x, float2 (&v)[4], __nv_bfloat16) {
     v[0] = unpack2(x.x), v[1] = unpack2(x.y), v[2] = unpack2(x.z), v[3] = unpack2(x.w);
+}
+__device__ __forceinline__ float largest(uint4 x) {
+    const auto pair = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(pair(x.x), pair(x.y)), __hmax2(pair(x.z), pair(x.w)));
+    return __bfloat162float(__hmax(m.x, m.y));
 }
 __device__ __forceinline__ void unpack(uint4 x, float2 (&v)[2], float) {
     v[0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
     v[1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
 }
 
+// Where a row's 16-byte vectors are, and a block's share of them; head and tail: the values before and
+// behind the vectors, which the first and the last block have.
 template <typename T>
-__global__ void __launch_bounds__(kLseThreads) lse_kernel(const VerifyParams p) {
-    constexpr int E = 16 / sizeof(T);
-    __shared__ float sm[kLseThreads / 32], ss[kLseThreads / 32];
+struct Share {
+    static constexpr int E = 16 / sizeof(T);
+    const uint4 *vec;
+    int head, tail, v0, v1;
+    __device__ __forceinline__ Share(const T *row, int V, int rank, int blocks) {
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+        head = min(V, ((16 - off) & 15) / static_cast<int>(sizeof(T)));
+        const int nv = (V - head) / E;
+        tail = head + nv * E;
+        vec = reinterpret_cast<const uint4 *>(row + head);
+        v0 = static_cast<int>(static_cast<long long>(nv) * rank / blocks);
+        v1 = static_cast<int>(static_cast<long long>(nv) * (rank + 1) / blocks);
+    }
+};
+
+// How the rows' vectors are dealt out to lse_kernel's blocks.  Row k of `rows` (the target's, then the
+// drafts') has the places k·nv .. (k + 1)·nv - 1 of one sequence; block i takes i·per .. (i + 1)·per - 1,
+// and leaves what it has of row k in part[i + k] (walking along the sequence, block or row goes up by
+// one at a time, so every pair that occurs has a number of its own).  Rows start anywhere, so a row
+// may have one vector less than nv = V / E: its last place is then empty.
+struct Pieces {
+    int zrows, rows, nv;
+    long long per;
+};
+template <typename T>
+__device__ __forceinline__ Pieces pieces_of(const VerifyParams &p) {
+    const int total = max(0, min(p.starts[p.B], p.R));
+    Pieces c;
+    c.zrows = min(p.zrows, total);
+    c.rows = c.zrows + min(p.qrows, total);
+    c.nv = max(1, p.V / Share<T>::E);
+    c.per = max(1LL, (static_cast<long long>(c.rows) * c.nv + kLseBlocks - 1) / kLseBlocks);
+    return c;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLseThreads, 4) lse_kernel(const VerifyParams p) {
+    constexpr int E = Share<T>::E, WARPS = kLseThreads / 32;
+    __shared__ float sm[2][WARPS], ss[2][WARPS];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int row = blockIdx.x / p.splits, split = blockIdx.x - row * p.splits;
-    const bool draft = row >= p.zrows;
-    const int at = draft ? row - p.zrows : row;
-    if (at >= p.starts[p.B]) return;  // behind the last request
-    const T *from = static_cast<const T *>(draft ? p.q : p.z) + static_cast<size_t>(at) * p.V;
+    const Pieces pieces = pieces_of<T>(p);
+    const int tid = threadIdx.x;
     const float c = p.inv_t * kLog2e;
-    // whole 16-byte vectors, and the values before and behind them
-    const int head = min(p.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(from) & 15)) & 15) /
-                                  static_cast<int>(sizeof(T)));
-    const int nv = (p.V - head) / E;
-    const int v0 = static_cast<int>(static_cast<long long>(nv) * split / p.splits);
-    const int v1 = static_cast<int>(static_cast<long long>(nv) * (split + 1) / p.splits);
-    const uint4 *vec = reinterpret_cast<const uint4 *>(from + head);
-    MaxSum a{-INFINITY, 0.f};
-    if (split == 0) {
-        const int tail = p.V - head - nv * E, i = threadIdx.x;
-        if (i < head) a = MaxSum{one(from + i), 1.f};
-        if (i >= 32 && i - 32 < tail) a = MaxSum{one(from + head + nv * E + i - 32), 1.f};
-        if (a.m == -INFINITY) a.s = 0.f;
-    }
     const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf: adds nothing
-    uint4 x[kLseAhead];
-    auto load = [&](int i0) {
-#pragma unroll
-        for (int k = 0; k < kLseAhead; ++k) {
-            const int i = i0 + k * kLseThreads;
-            x[k] = i < v1 ? vec[i] : make_uint4(none, none, none, none);
-        }
+    const long long all = static_cast<long long>(pieces.rows) * pieces.nv;
+    long long from = blockIdx.x * pieces.per;
+    const long long to = min(all, from + pieces.per);
+    if (from >= to) return;
+    int row = static_cast<int>(from / pieces.nv), turn = 0;
+    // the part of `row` that is this block's: vectors i .. end - 1 of it
+    const T *at;
+    const uint4 *vec;
+    int i, end, head, tail;
+    auto open = [&] {
+        const bool draft = row >= pieces.zrows;
+        at = static_cast<const T *>(draft ? p.q : p.z) +
+             static_cast<size_t>(draft ? row - pieces.zrows : row) * p.V;
+        const Share<T> s(at, p.V, 0, 1);
+        vec = s.vec, head = s.head, tail = s.tail;
+        const long long begin = static_cast<long long>(row) * pieces.nv;
+        i = static_cast<int>(from - begin);
+        end = static_cast<int>(min(to - begin, static_cast<long long>(pieces.nv)));
+        // the values in front of the vectors go with the first place, those behind with the last one
+        if (i > 0) head = 0;
+        if (end < pieces.nv) tail = p.V;
+        end = min(end, s.v1);
     };
-    int i0 = v0 + static_cast<int>(threadIdx.x);
-    load(i0);
-    while (i0 < v1) {
-        float2 v[kLseAhead][E / 2];
-        float top[kLseAhead];
+    uint4 x[kAhead];
+    auto load = [&] {
+        if (i + kLseThreads * kAhead <= end) {
 #pragma unroll
-        for (int k = 0; k < kLseAhead; ++k) {
-            unpack(x[k], v[k], T{});
-            top[k] = fmaxf(v[k][0].x, v[k][0].y);
+            for (int u = 0; u < kAhead; ++u) x[u] = vec[i + tid + u * kLseThreads];
+        } else {
 #pragma unroll
-            for (int j = 1; j < E / 2; ++j) top[k] = fmaxf(top[k], fmaxf(v[k][j].x, v[k][j].y));
+            for (int u = 0; u < kAhead; ++u) {
+                const int k = i + u * kLseThreads + tid;
+                x[u] = k < end ? vec[k] : make_uint4(none, none, none, none);
+            }
         }
-        i0 += kLseThreads * kLseAhead;
-        load(i0);  // the next ones are on their way meanwhile
-        float m = a.m;
+        i += kLseThreads * kAhead;
+    };
+    open();
+    load();
+    MaxSum a{-INFINITY, 0.f};
+    while (true) {
+        float2 v[kAhead][E / 2];
+        float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kLseAhead; ++k) m = fmaxf(m, top[k]);
-        const float ref = m == -INFINITY ? 0.f : m;
+        for (int u = 0; u < kAhead; ++u) {
+            unpack(x[u], v[u], T{});
+            if constexpr (sizeof(T) == 2)
+                top = fmaxf(top, largest(x[u]));
+            else
+                top = fmaxf(fmaxf(top, fmaxf(v[u][0].x, v[u][0].y)), fmaxf(v[u][1].x, v[u][1].y));
+        }
+        // the next vectors, of this row or the next one, are on their way meanwhile
+        const bool ends = i >= end;
+        const T *ended = at;
+        const int last_head = head, last_tail = tail, ended_row = row;
+        if (ends) {
+            from = static_cast<long long>(++row) * pieces.nv;
+            if (from < to) open();
+        }
+        if (from < to) load();
+        const float m = fmaxf(a.m, top), ref = m == -INFINITY ? 0.f : m;
         float2 sum[2] = {make_float2(a.s * ex2_approx((a.m - ref) * c), 0.f), both(0.f)};
 #pragma unroll
-        for (int k = 0; k < kLseAhead; ++k)
+        for (int u = 0; u < kAhead; ++u)
 #pragma unroll
             for (int j = 0; j < E / 2; ++j) {
-                const float2 y = __fmul2_rn(__fadd2_rn(v[k][j], both(-ref)), both(c));
+                const float2 y = __fmul2_rn(__fadd2_rn(v[u][j], both(-ref)), both(c));
                 sum[j & 1] = __fadd2_rn(sum[j & 1], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
             }
-        a.m = m;
-        a.s = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-    }
-    a = warp_join(a, c);
-    if ((threadIdx.x & 31) == 0) {
-        sm[threadIdx.x >> 5] = a.m;
-        ss[threadIdx.x >> 5] = a.s;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int w = 1; w < kLseThreads / 32; ++w) a = join(a, MaxSum{sm[w], ss[w]}, c);
-        p.part[blockIdx.x] = make_float2(a.m, a.s);
+        a = MaxSum{m, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)};
+        if (!ends) continue;
+        if (tid < last_head) a = join(a, MaxSum{one(ended + tid), 1.f}, c);
+        if (tid < p.V - last_tail) a = join(a, MaxSum{one(ended + last_tail + tid), 1.f}, c);
+        a = warp_join(a, c);
+        if ((tid & 31) == 0) sm[turn][tid / 32] = a.m, ss[turn][tid / 32] = a.s;
+        __syncthreads();  // (two turns' arrays: the next row's are written before these have been read)
+        if (tid < 32) {
+            a = warp_join(tid < WARPS ? MaxSum{sm[turn][tid], ss[turn][tid]} : MaxSum{-INFINITY, 0.f}, c);
+            if (tid == 0) p.part[blockIdx.x + ended_row] = make_float2(a.m, a.s);
+        }
+        a = MaxSum{-INFINITY, 0.f};
+        turn ^= 1;
+        if (from >= to) return;
     }
 }
 
-// The logsumexp of row `at` of the target (or the draft), by a warp.
-__device__ double row_lse(const VerifyParams &p, bool draft, int at, int lane) {
-    const float *given = draft ? p.qlse : p.lse;
-    if (given) return given[at];
-    const float c = p.inv_t * kLog2e;
-    const float2 *part = p.part + (static_cast<size_t>(draft ? p.zrows : 0) + at) * p.splits;
-    MaxSum a{-INFINITY, 0.f};
-    for (int s = lane; s < p.splits; s += 32) a = join(a, MaxSum{part[s].x, part[s].y}, c);
-    a = warp_join(a, c);
+// The logsumexp from a row's (max, sum).
+__device__ __forceinline__ double lse_of(MaxSum a, float inv_t) {
     if (a.m == -INFINITY && a.s == 0.f) return -INFINITY;
+    const double m = static_cast<double>(a.m) * inv_t;
+    if (!(a.s > 0.f && a.s < INFINITY)) return m + a.s;  // not finite
     // log s = e ln 2 + log f with s = f·2^e, f in [1, 2): in fp32 log s would be off by its own ulp
     const uint32_t bits = __float_as_uint(a.s);
-    const int e = static_cast<int>((bits >> 23) & 255) - 127;  // s is 1 at least, but for roundings
-    const float f = __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
-    if (!(a.s > 0.f && a.s < INFINITY)) return static_cast<double>(a.m) * p.inv_t + a.s;  // not finite
-    return static_cast<double>(a.m) * p.inv_t + (e * 0.69314718055994531 + logf(f));
+    const int e = static_cast<int>(bits >> 23) - 127;  // (s is no subnormal: its largest term is 1)
+    return m + (e * 0.69314718055994531 + logf(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u)));
+}
+
+// The logsumexp of row `at` of the target (or the draft), by a warp.
+template <typename T>
+__device__ __forceinline__ double row_lse(const VerifyParams &p, const Pieces &c, bool draft, int at,
+                                          int lane) {
+    const float *given = draft ? p.qlse : p.lse;
+    if (given) return given[at];
+    const int row = draft ? c.zrows + at : at;
+    const long long begin = static_cast<long long>(row) * c.nv;
+    const int first = static_cast<int>(begin / c.per), last = static_cast<int>((begin + c.nv - 1) / c.per);
+    MaxSum a{-INFINITY, 0.f};
+    for (int i = first + lane; i <= last; i += 32)
+        a = join(a, MaxSum{p.part[i + row].x, p.part[i + row].y}, p.inv_t * kLog2e);
+    return lse_of(warp_join(a, p.inv_t * kLog2e), p.inv_t);
 }
 
 // Whether e^x > u, for x whose rounding to fp32 would count.
@@ -210,22 +285,34 @@ template <typename T, int FROM>
 struct Scan {
     const VerifyParams &p;
     const T *z, *q;
-    float lse, qlse;
+    // log2 p = z·c - l2; q likewise, but for the factor k that takes back what the roundings of both l2
+    // have changed of p / q
+    float c, l2, ql2, k;
     int x;
     unsigned long long first;  // index of the row's first draw
     float best, bar;
     int column;
+    static constexpr float kUpper = 0.69314860f * 16777216.f;
 
-    __device__ __forceinline__ float weight(float a, float b, int j) const {
-        float w = ex2_approx(fmaf(a, p.inv_t, -lse) * kLog2e);
-        if (FROM == kDifference) w -= ex2_approx(fmaf(b, p.inv_t, -qlse) * kLog2e);
+    __device__ __forceinline__ Scan(const VerifyParams &p_, const T *z_, const T *q_, double lse, double qlse,
+                                    int x_, unsigned long long first_)
+        : p(p_), z(z_), q(q_), x(x_), first(first_), best(0.f), bar(0.f), column(0) {
+        constexpr double kLog2eWide = 1.4426950408889634;
+        c = p.inv_t * kLog2e;
+        l2 = static_cast<float>(lse * kLog2eWide);
+        ql2 = static_cast<float>(qlse * kLog2eWide);
+        k = ex2_approx(static_cast<float>((ql2 - qlse * kLog2eWide) - (l2 - lse * kLog2eWide)));
+    }
+    __device__ __forceinline__ float weight(float2 v, int j) const {  // v: logits of the target and the draft
+        float w = ex2_approx(fmaf(v.x, c, -l2));
+        if (FROM == kDifference) w = fmaf(-k, ex2_approx(fmaf(v.y, c, -ql2)), w);
         if (FROM == kWithout && j == x) w = 0.f;
         return w;
     }
     __device__ __forceinline__ void exact(int j) {
         const uint32_t bits = bits24_from_state(splitmix_state(p.seed, first + j));
-        const float score =
-            bits ? weight(one(z + j), FROM == kDifference ? one(q + j) : 0.f, j) / -log2_uniform(bits) : 0.f;
+        const float2 v = make_float2(one(z + j), FROM == kDifference ? one(q + j) : 0.f);
+        const float score = bits ? weight(v, j) / -log2_uniform(bits) : 0.f;
         // columns come in any order: of equal scores the lowest stays
         if (score > best || (score == best && j < column)) best = score, column = j;
     }
@@ -233,92 +320,87 @@ struct Scan {
     template <int N, int STEP>
     __device__ __forceinline__ void columns(const float (&a)[N], const float (&b)[N], int j, int have) {
         float bound[N], low = 0.f;
+        const float all = have >= N ? kUpper : 0.f;  // (`have` is N or 0 but where columns are STEP apart)
         const unsigned long long state = splitmix_state(p.seed, first + j);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const float w = weight(a[k], b[k], j + k * STEP);
-            const uint32_t bits = bits24_from_state(state + static_cast<unsigned long long>(k * STEP) * kGolden);
+        for (int i = 0; i < N; ++i) {
+            const float w = weight(make_float2(a[i], b[i]), j + i * STEP);
+            const uint32_t bits = bits24_from_state(state + static_cast<unsigned long long>(i * STEP) * kGolden);
             // With l = 1 - u:  l <= -ln u <= l / (1 - l), so the score w / -log2 u lies between
             // w·ln 2 / l and that times 1 - l.  The constants leave room for the roundings of both and
-            // of the score itself (2e-6 and 4e-6 against some 1e-6).
-            const float l = static_cast<float>(16777216u - bits) * 5.9604644775390625e-8f;
-            const float top = k < have ? w * 0.69314860f * rcp_approx(l) : 0.f;
-            bound[k] = top;
-            low = fmaxf(low, top * fmaf(l, -0.999994f, 0.999994f));
+            // of the score itself (2e-6 and 4e-6 against some 1e-6); l is counted in 2^-24.
+            const float l = static_cast<float>(16777216u - bits);
+            bound[i] = w * (STEP == 1 ? all : i < have ? kUpper : 0.f) * rcp_approx(l);
+            low = fmaxf(low, bound[i] * fmaf(l, -0.999994f * 5.9604644775390625e-8f, 0.999994f));
         }
         const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(low));  // (low >= 0)
         bar = fmaxf(bar, __uint_as_float(most));
         uint32_t promising = 0;
 #pragma unroll
-        for (int k = 0; k < N; ++k) promising |= static_cast<uint32_t>(bound[k] > bar) << k;
+        for (int i = 0; i < N; ++i) promising |= static_cast<uint32_t>(bound[i] > bar) << i;
         for (; promising; promising &= promising - 1) exact(j + (__ffs(promising) - 1) * STEP);
     }
 };
 
 // This thread's best of the share of block `rank` of `blocks`.
-template <typename T, int FROM>
+template <typename T, int FROM, int THREADS>
 __device__ __forceinline__ unsigned long long scan(const VerifyParams &p, const T *z, const T *q,
-                                                   float lse, float qlse, int x,
+                                                   double lse, double qlse, int x,
                                                    unsigned long long first, int rank, int blocks) {
-    constexpr int E = 16 / sizeof(T);
+    constexpr int E = Share<T>::E;
     const int tid = threadIdx.x;
-    Scan<T, FROM> s{p, z, q, lse, qlse, x, first, 0.f, 0.f, 0};
-    const uintptr_t off = reinterpret_cast<uintptr_t>(z) & 15;
-    if (FROM != kDifference || off == (reinterpret_cast<uintptr_t>(q) & 15)) {
-        const int head = min(p.V, static_cast<int>((16 - off) & 15) / static_cast<int>(sizeof(T)));
-        const int nv = (p.V - head) / E, tail = head + nv * E;
-        const int v0 = static_cast<int>(static_cast<long long>(nv) * rank / blocks);
-        const int v1 = static_cast<int>(static_cast<long long>(nv) * (rank + 1) / blocks);
-        const uint4 *za = reinterpret_cast<const uint4 *>(z + head);
-        const uint4 *qa = reinterpret_cast<const uint4 *>(q + head);
+    Scan<T, FROM> s(p, z, q, lse, qlse, x, first);
+    if (FROM != kDifference || ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0) {
+        const Share<T> za(z, p.V, rank, blocks);
+        const uint4 *qa = FROM == kDifference ? reinterpret_cast<const uint4 *>(q + za.head) : nullptr;
         uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (v0 + tid < v1) {
-            a = za[v0 + tid];
-            if (FROM == kDifference) b = qa[v0 + tid];
+        if (za.v0 + tid < za.v1) {
+            a = za.vec[za.v0 + tid];
+            if (FROM == kDifference) b = qa[za.v0 + tid];
         }
-        for (int i0 = v0; i0 < v1; i0 += kVerifyThreads) {  // (the same turns for all threads)
-            const int i = i0 + tid, next = i + kVerifyThreads;
+        for (int i0 = za.v0; i0 < za.v1; i0 += THREADS) {  // (the same turns for all threads)
+            const int i = i0 + tid, next = i + THREADS;
             float2 pa[E / 2], pb[E / 2];
             unpack(a, pa, T{});
             unpack(b, pb, T{});
-            if (next < v1) {
-                a = za[next];
+            if (next < za.v1) {
+                a = za.vec[next];
                 if (FROM == kDifference) b = qa[next];
             }
             float va[E], vb[E];
 #pragma unroll
             for (int j = 0; j < E / 2; ++j)
                 va[2 * j] = pa[j].x, va[2 * j + 1] = pa[j].y, vb[2 * j] = pb[j].x, vb[2 * j + 1] = pb[j].y;
-            s.template columns<E, 1>(va, vb, head + i * E, i < v1 ? E : 0);
+            s.template columns<E, 1>(va, vb, za.head + i * E, i < za.v1 ? E : 0);
         }
-        if (rank == 0 && tid < head) s.exact(tid);
-        if (rank == blocks - 1 && tid < p.V - tail) s.exact(tail + tid);
+        if (rank == 0 && tid < za.head) s.exact(tid);
+        if (rank == blocks - 1 && tid < p.V - za.tail) s.exact(za.tail + tid);
     } else {
         // rows of an odd vocabulary: z's and q's vectors never lie side by side
         constexpr int W = 8;
         const int c0 = static_cast<int>(static_cast<long long>(p.V) * rank / blocks);
         const int c1 = static_cast<int>(static_cast<long long>(p.V) * (rank + 1) / blocks);
-        for (int j0 = c0; j0 < c1; j0 += W * kVerifyThreads) {
+        for (int j0 = c0; j0 < c1; j0 += W * THREADS) {
             const int j = j0 + tid;
             float a[W], b[W];
 #pragma unroll
             for (int k = 0; k < W; ++k) {
-                const int i = min(j + k * kVerifyThreads, c1 - 1);
+                const int i = min(j + k * THREADS, c1 - 1);
                 a[k] = one(z + i);
                 b[k] = one(q + i);
             }
-            s.template columns<W, kVerifyThreads>(a, b, j,
-                                                  max(0, (c1 - j + kVerifyThreads - 1) / kVerifyThreads));
+            s.template columns<W, THREADS>(a, b, j, max(0, (c1 - j + THREADS - 1) / THREADS));
         }
     }
     return pack(s.best, s.column);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const VerifyParams p) {
+    constexpr int WARPS = THREADS / 32;
     __shared__ int end, busy;
-    __shared__ double end_lse, end_qlse;
-    __shared__ unsigned long long bests[2][16], warps[kVerifyThreads / 32];
+    __shared__ double lses[WARPS], qlses[WARPS];
+    __shared__ unsigned long long bests[2][kWideBlocks], warps[WARPS];
     const int blocks = static_cast<int>(cluster_blocks()), rank = static_cast<int>(cluster_ctarank());
     const int b = static_cast<int>(blockIdx.x) / blocks;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -327,80 +409,82 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int total = p.B ? p.starts[p.B] : 0;
+    const int s0 = p.B ? p.starts[b] : 0, s1 = p.B ? p.starts[b + 1] : 0;
     if (blockIdx.x == 0 && tid == 0) *p.epoch_word = p.epoch;
     if (b == (p.B ? p.B - 1 : 0) && total >= 0)  // the rows behind the last request
-        for (long long r = total + static_cast<long long>(rank) * kVerifyThreads + tid; r < p.R;
-             r += static_cast<long long>(blocks) * kVerifyThreads) {
+        for (long long r = total + static_cast<long long>(rank) * THREADS + tid; r < p.R;
+             r += static_cast<long long>(blocks) * THREADS) {
             p.token[r] = -1;
             if (p.logprob) p.logprob[r] = 0.f;
         }
-    const int s0 = p.B ? p.starts[b] : 0, s1 = p.B ? p.starts[b + 1] : 0;
     // draft rows are those of the requests before this one that have any rows
-    if (tid == 0) busy = 0;
+    const int n = static_cast<int>(static_cast<unsigned>(s1) - static_cast<unsigned>(s0) - 1u);
+    if (tid == 0) busy = 0, end = n;
     __syncthreads();
     int mine = 0;
-    for (int i = tid; i < b; i += kVerifyThreads) mine += p.starts[i + 1] > p.starts[i];
+    for (int i = tid; i < b; i += THREADS) mine += p.starts[i + 1] > p.starts[i];
     if (mine) atomicAdd(&busy, mine);
-    const int n = static_cast<int>(static_cast<unsigned>(s1) - static_cast<unsigned>(s0) - 1u);
-    if (tid == 0) end = n;
     __syncthreads();
     const int q0 = s0 - busy;  // the draft's row of row s0
     const bool sane = s0 >= 0 && s1 >= s0 && s1 <= total && total <= p.R &&
                       (!p.with_q || n <= 0 || (q0 >= 0 && q0 + n <= p.Rd));
-    if (!sane && tid == 0 && rank == 0) record_status(p.status, p.epoch, 1u);  // SB_ERR_INVALID_ARG
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (!sane || n < 0) {  // the same for all blocks of the cluster
+        if (!sane && tid == 0 && rank == 0) record_status(p.status, p.epoch, 1u);  // SB_ERR_INVALID_ARG
         if (p.B && tid == 0 && rank == 0) p.accepted[b] = sane ? 0 : -1;
-        __syncwarp();
-        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         return;
     }
     const T *z = static_cast<const T *>(p.z) + static_cast<size_t>(s0) * p.V;
     const T *q = p.with_q && n > 0 ? static_cast<const T *>(p.q) + static_cast<size_t>(q0) * p.V : nullptr;
-    // which drafts stay
-    for (int i = warp; i < n; i += kVerifyThreads / 32) {
-        const int r = s0 + i, x = p.drafts[r];
-        const double lse = row_lse(p, false, r, lane), qlse = q ? row_lse(p, true, q0 + i, lane) : 0.0;
-        if (lane == 0) {
-            bool stays = false;
-            float lp = 0.f;
-            if (x >= 0 && x < p.V) {
-                const double l = static_cast<double>(one(z + static_cast<size_t>(i) * p.V + x) * p.inv_t) - lse;
-                const double m = q ? static_cast<double>(one(q + static_cast<size_t>(i) * p.V + x) * p.inv_t) - qlse : 0.0;
-                lp = static_cast<float>(l);
-                stays = exp_above(l - m, p.u[r]);
-            } else if (rank == 0) {
-                record_status(p.status, p.epoch, 1u);
-            }
-            if (!stays) atomicMin(&end, i);
-            if (rank == 0) {  // (of a row behind the end it is taken back below)
-                p.token[r] = x;
-                if (p.logprob) p.logprob[r] = lp;
+    const Pieces pieces = pieces_of<T>(p);
+    // which drafts stay, one to a warp at a time; the last row has none, and ends the request
+    int g = 0;
+    for (;; g += WARPS) {
+        const int i = g + warp, r = s0 + i;
+        if (i <= n) {
+            const bool has = i < n;
+            const int x = has ? p.drafts[r] : -1;
+            const bool known = x >= 0 && x < p.V;
+            const size_t at = static_cast<size_t>(i) * p.V + (known ? x : 0);
+            const float zx = known ? one(z + at) : 0.f, qx = known && q ? one(q + at) : 0.f;
+            const float u = has ? p.u[r] : 0.f;
+            const double lse = row_lse<T>(p, pieces, false, r, lane);
+            const double qlse = has && q ? row_lse<T>(p, pieces, true, q0 + i, lane) : 0.0;
+            if (lane == 0) {
+                lses[warp] = lse;
+                qlses[warp] = qlse;
+                if (has) {
+                    const double l = static_cast<double>(zx * p.inv_t) - lse;
+                    const double m = q ? static_cast<double>(qx * p.inv_t) - qlse : 0.0;
+                    if (!known && rank == 0) record_status(p.status, p.epoch, 1u);
+                    if (!known || !exp_above(l - m, u)) atomicMin(&end, i);
+                    if (rank == 0) {  // (of a row behind the end it is taken back below)
+                        p.token[r] = x;
+                        if (p.logprob) p.logprob[r] = static_cast<float>(l);
+                    }
+                }
             }
         }
+        __syncthreads();
+        if (end < g + WARPS) break;  // (end is n at most, the last row's)
+        __syncthreads();             // before the next rows' are written
     }
-    __syncthreads();
     const int e = end, r = s0 + e;
-    if (warp == 0) {
-        const double l = row_lse(p, false, r, lane);
-        const double m = q && e < n ? row_lse(p, true, q0 + e, lane) : 0.0;
-        if (lane == 0) end_lse = l, end_qlse = m;
-    }
-    __syncthreads();
+    const double lse = lses[e - g], qlse = qlses[e - g];
     z += static_cast<size_t>(e) * p.V;
     const int x = e < n ? p.drafts[r] : -1;
     const bool known = x >= 0 && x < p.V;  // otherwise nothing is taken off p
     const unsigned long long first = static_cast<unsigned long long>(r) * static_cast<unsigned>(p.V);
-    const float lse = static_cast<float>(end_lse), qlse = static_cast<float>(end_qlse);
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     unsigned long long best = 0;
     for (int turn = 0; turn < 2 && !best; ++turn) {
         // a difference that is nowhere positive (p and q equal but for roundings): p itself
         if (turn == 0 && known && q)
-            best = scan<T, kDifference>(p, z, q + static_cast<size_t>(e) * p.V, lse, qlse, x, first, rank, blocks);
+            best = scan<T, kDifference, THREADS>(p, z, q + static_cast<size_t>(e) * p.V, lse, qlse, x, first,
+                                                 rank, blocks);
         else if (turn == 0 && known)
-            best = scan<T, kWithout>(p, z, nullptr, lse, 0.f, x, first, rank, blocks);
+            best = scan<T, kWithout, THREADS>(p, z, nullptr, lse, 0.0, x, first, rank, blocks);
         else
-            best = scan<T, kTarget>(p, z, nullptr, lse, 0.f, x, first, rank, blocks);
+            best = scan<T, kTarget, THREADS>(p, z, nullptr, lse, 0.0, x, first, rank, blocks);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const unsigned long long other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
@@ -409,7 +493,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         if (lane == 0) warps[warp] = best;
         __syncthreads();
         if (tid < blocks) {
-            for (int w = 0; w < kVerifyThreads / 32; ++w) best = warps[w] > best ? warps[w] : best;
+            for (int w = 0; w < WARPS; ++w) best = warps[w] > best ? warps[w] : best;
             asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_rank(&bests[turn][rank], tid)),
                          "l"(best)
                          : "memory");
@@ -420,14 +504,14 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         for (int k = 0; k < blocks; ++k) best = bests[turn][k] > best ? bests[turn][k] : best;
     }
     if (rank != 0) return;
-    for (int i = e + tid; i <= n; i += kVerifyThreads) {
+    for (int i = e + tid; i <= n; i += THREADS) {
         int token = -1;
         float lp = 0.f;
         if (i == e) {
             lp = __uint_as_float(0x7FC00000u);  // no column of the row has any probability
             if (best) {
                 token = ~static_cast<int>(static_cast<uint32_t>(best));
-                lp = static_cast<float>(static_cast<double>(one(z + token) * p.inv_t) - end_lse);
+                lp = static_cast<float>(static_cast<double>(one(z + token) * p.inv_t) - lse);
             }
         }
         p.token[s0 + i] = token;
@@ -467,18 +551,12 @@ __global__ void __launch_bounds__(128) greedy_kernel(const GreedyParams p) {
     if (lane == 0) p.accepted[b] = n ? e : 0;
 }
 
-template <typename T>
+template <typename T, int THREADS>
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
-    const long long rows = static_cast<long long>(p.zrows) + p.qrows;
-    if (rows > 0 && p.B > 0) {
-        const cudaError_t e = launch_dependent(lse_kernel<T>, dim3(static_cast<unsigned>(rows * p.splits)),
-                                               kLseThreads, 0, p, st);
-        if (e != cudaSuccess) return e;
-    }
     auto config = [&](int blocks, cudaLaunchAttribute (&attr)[2]) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(static_cast<unsigned>(p.B > 0 ? p.B : 1) * blocks);
-        cfg.blockDim = dim3(kVerifyThreads);
+        cfg.blockDim = dim3(THREADS);
         cfg.stream = st;
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = blocks;
@@ -490,7 +568,7 @@ cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
         return cfg;
     };
     cudaLaunchAttribute attr[2];
-    int blocks = kVerifyCluster;
+    int blocks = kBlocks;
     if (p.B <= kWideRequests) {
         // more than eight blocks to a cluster are no part of the portable model: asked once a device
         static std::atomic<uint64_t> asked{0}, allowed{0};
@@ -500,28 +578,26 @@ cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
         const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
         if (bit && !(asked.load() & bit)) {
             int clusters = 0;
-            cudaLaunchConfig_t cfg = config(kWideCluster, attr);
+            cudaLaunchConfig_t cfg = config(kWideBlocks, attr);
             cfg.numAttrs = 1;
-            e = cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, verify_kernel<T>, &cfg);
+            e = cudaFuncSetAttribute(verify_kernel<T, THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, verify_kernel<T, THREADS>, &cfg);
             if (e == cudaSuccess && clusters > 0) allowed.fetch_or(bit);
-            cudaGetLastError();  // a refusal is an answer here
+            if (e != cudaSuccess) cudaGetLastError();  // a refusal is an answer here
             asked.fetch_or(bit);
         }
-        if (allowed.load() & bit) blocks = kWideCluster;
+        if (allowed.load() & bit) blocks = kWideBlocks;
     }
     const cudaLaunchConfig_t cfg = config(blocks, attr);
-    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, p);
+    return cudaLaunchKernelEx(&cfg, verify_kernel<T, THREADS>, p);
 }
-
-// Pieces of a row: enough blocks for the GPU to be full several times over, but no piece that a
-// block has hardly begun with before it ends.
-int splits_of(int64_t rows, int64_t V) {
-    if (rows < 1) return 1;
-    int64_t s = (kLseBlocks + rows - 1) / rows;
-    const int64_t most = (V + kLsePiece - 1) / kLsePiece;
-    if (s > most) s = most;
-    return static_cast<int>(s < 1 ? 1 : s);
+template <typename T>
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
+    if (p.zrows + p.qrows > 0 && p.B > 0) {
+        const cudaError_t e = launch_dependent(lse_kernel<T>, dim3(kLseBlocks), kLseThreads, 0, p, st);
+        if (e != cudaSuccess) return e;
+    }
+    return p.B <= kFewRequests ? launch_verify<T, 512>(p, st) : launch_verify<T, 256>(p, st);
 }
 
 bool verify_sizes(int64_t R, int64_t draft_rows, int64_t V) {
@@ -538,11 +614,8 @@ extern "C" {
 
 size_t sb_verify_workspace_bytes(int64_t R, int64_t draft_rows, int64_t V) {
     if (!verify_sizes(R, draft_rows, V)) return 0;
-    // the number of pieces falls with the rows that are reduced: the largest product of the two
-    const int64_t rows = R + (draft_rows > 0 ? draft_rows : 0), most = (V + kLsePiece - 1) / kLsePiece;
-    int64_t parts = rows * most;
-    if (parts > rows + kLseBlocks) parts = rows + kLseBlocks;
-    return 256 + up256(static_cast<size_t>(parts) * 8);
+    // the header and lse_kernel's parts
+    return 256 + up256(static_cast<size_t>(R + (draft_rows > 0 ? draft_rows : 0) + kLseBlocks) * 8);
 }
 
 int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int32_t *drafts,
@@ -581,13 +654,12 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
     p.Rd = draft_rows > 0 ? static_cast<int>(draft_rows) : 0;
     p.zrows = lse ? 0 : p.R;
     p.qrows = draft_lse ? 0 : p.Rd;
-    p.splits = splits_of(static_cast<int64_t>(p.zrows) + p.qrows, V);
+    p.part = reinterpret_cast<float2 *>(ws + 256);
     p.inv_t = 1.0f / temperature;
     p.seed = seed;
     p.token = token;
     p.accepted = accepted;
     p.logprob = token_logprob;
-    p.part = reinterpret_cast<float2 *>(ws + 256);
     p.epoch_word = reinterpret_cast<uint32_t *>(ws);
     p.status = reinterpret_cast<unsigned long long *>(ws + 8);
     p.epoch = next_epoch();
