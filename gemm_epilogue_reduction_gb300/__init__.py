@@ -761,26 +761,31 @@ def cross_entropy_backward(H, W, targets, lse, *, grad=None, ignore_index: int =
 
 
 # ------------------------------------------------------------------ the two ends of the model
+_types = {}  # torch's types -> sb_type, filled by the first call
+
+
 def _type(dtype, where):
-    import torch
-    if dtype is torch.bfloat16:
-        return SB_BF16
-    if dtype is torch.float32:
-        return SB_F32
-    raise TypeError(f"{where}: dtype is bfloat16 or float32, not {dtype}")
+    t = _types.get(dtype)
+    if t is None:
+        import torch
+        _types.update({torch.bfloat16: SB_BF16, torch.float32: SB_F32})
+        t = _types.get(dtype)
+        if t is None:
+            raise TypeError(f"{where}: dtype is bfloat16 or float32, not {dtype}")
+    return t
 
 
 def _index32(ignore_index, where):
-    if not -2 ** 31 <= ignore_index < 2 ** 31:  # the C call would take its lowest 32 bits
+    if not -2147483648 <= ignore_index < 2147483648:  # the C call would take its lowest 32 bits
         raise ValueError(f"{where}: ignore_index {ignore_index} is not a 32-bit integer")
 
 
 def _seeded(seed, seed_offset, device, where):
     """Checks a seed (an int of 64 bits, signed or not) and its offset on the device."""
-    import torch
-    if not -2 ** 63 <= seed < 2 ** 64:
+    if not -0x8000000000000000 <= seed <= 0xFFFFFFFFFFFFFFFF:
         raise ValueError(f"{where}: seed {seed} is not a 64-bit integer")
     if seed_offset is not None:
+        import torch
         _tensor("seed_offset", seed_offset, (1,), (torch.int64, torch.uint64), device, where)
     return seed & 0xFFFFFFFFFFFFFFFF
 
@@ -798,18 +803,22 @@ def embedding(ids, W, *, scale: float = 1.0, ignore_index: int = -100, dtype=Non
             ids, W, scale=scale, ignore_index=ignore_index, dtype=dtype), ids, W)
     import torch
     where = "embedding"
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     _index32(ignore_index, where)
     if ids.dim() != 1 or W.dim() != 2:
         raise ValueError(f"{where}: ids is [M] and W [V, d]")
     M, (V, d) = ids.shape[0], W.shape
+    wt = _type(W.dtype, where)
     if not (ids.dtype is torch.int32 and ids.get_device() == dev and W.get_device() == dev and
             ids.is_contiguous() and W.is_contiguous()):
         _tensor("ids", ids, (M,), (torch.int32,), dev, where)
-        _tensor("W", W, (V, d), (torch.bfloat16, torch.float32), dev, where)
-    wt = _type(W.dtype, where)
-    ot = wt if dtype is None else _type(dtype, where)
-    out = torch.empty(M, d, dtype=W.dtype if dtype is None else dtype, device=W.device)
+        _tensor("W", W, (V, d), (W.dtype,), dev, where)
+    ot = wt
+    if dtype is None:
+        dtype = W.dtype
+    else:
+        ot = _type(dtype, where)
+    out = torch.empty(M, d, dtype=dtype, device=W.device)
     st = lib().sb_embedding_forward(ids.data_ptr(), W.data_ptr(), M, d, V, ignore_index, scale, wt,
                                     ot, out.data_ptr(), _current(dev))
     if st != SB_OK:
@@ -832,7 +841,7 @@ def embedding_backward(ids, dout, *, vocab=None, dW=None, scale: float = 1.0,
             workspace=workspace), ids, dout, dW, workspace)
     import torch
     where = "embedding_backward"
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     _index32(ignore_index, where)
     if ids.dim() != 1 or dout.dim() != 2:
         raise ValueError(f"{where}: ids is [M] and dout [M, d]")
@@ -840,11 +849,12 @@ def embedding_backward(ids, dout, *, vocab=None, dW=None, scale: float = 1.0,
         raise ValueError(f"{where}: either vocab or dW is given")
     M, d = ids.shape[0], dout.shape[1]
     _tensor("ids", ids, (M,), (torch.int32,), dev, where)
-    _tensor("dout", dout, (M, d), (torch.bfloat16, torch.float32), dev, where)
+    gt = _type(dout.dtype, where)
+    _tensor("dout", dout, (M, d), (dout.dtype,), dev, where)
     L = lib()
     if workspace is None:
         size = _nonzero(L.sb_embedding_backward_workspace_bytes(M, d), where)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dout.device)
+        workspace = torch.empty(size, dtype=torch.uint8, device=ids.device)
     else:
         size = _workspace(workspace, dev, where)
     add = dW is not None
@@ -853,16 +863,17 @@ def embedding_backward(ids, dout, *, vocab=None, dW=None, scale: float = 1.0,
             raise ValueError(f"{where}: dtype is {dtype}, dW {dW.dtype}")
         if dW.dim() != 2:
             raise ValueError(f"{where}: dW is [V, d]")
-        _tensor("dW", dW, (dW.shape[0], d), (torch.bfloat16, torch.float32), dev, where)
+        wt = _type(dW.dtype, where)
+        vocab = dW.shape[0]
+        _tensor("dW", dW, (vocab, d), (dW.dtype,), dev, where)
     else:
         dtype = dout.dtype if dtype is None else dtype
-        _type(dtype, where)
+        wt = _type(dtype, where)
         if vocab < 1:
             raise ValueError(f"{where}: vocab is {vocab}")
         dW = torch.empty(vocab, d, dtype=dtype, device=dout.device)
-    st = L.sb_embedding_backward(ids.data_ptr(), dout.data_ptr(), M, d, dW.shape[0], ignore_index,
-                                 scale, _type(dout.dtype, where), _type(dW.dtype, where), add,
-                                 dW.data_ptr(), workspace.data_ptr(), size, _current(dev))
+    st = L.sb_embedding_backward(ids.data_ptr(), dout.data_ptr(), M, d, vocab, ignore_index, scale,
+                                 gt, wt, add, dW.data_ptr(), workspace.data_ptr(), size, _current(dev))
     if st != SB_OK:
         raise SbError(st, "sb_embedding_backward")
     return {"dW": dW, "workspace": workspace}
@@ -883,20 +894,23 @@ def dropout(x, p: float, *, seed: int, seed_offset=None, residual=None, dtype=No
             x, residual, seed_offset)
     import torch
     where = "dropout"
-    dev = torch.cuda.current_device()
-    types = (torch.bfloat16, torch.float32)
-    _tensor("x", x, x.shape, types, dev, where)
+    dev = torch._C._cuda_getDevice()
+    xt = _type(x.dtype, where)
+    if not (x.get_device() == dev and x.is_contiguous()):
+        _tensor("x", x, x.shape, (x.dtype,), dev, where)
     if residual is not None:
         if dtype is not None and dtype is not residual.dtype:
             raise ValueError(f"{where}: dtype is {dtype}, residual {residual.dtype}")
-        _tensor("residual", residual, x.shape, types, dev, where)
         dtype = residual.dtype
+        ot = _type(dtype, where)
+        _tensor("residual", residual, x.shape, (dtype,), dev, where)
     elif dtype is None:
-        dtype = x.dtype
+        dtype, ot = x.dtype, xt
+    else:
+        ot = _type(dtype, where)
     seed = _seeded(seed, seed_offset, dev, where)
-    ot = _type(dtype, where)
-    out = torch.empty(x.shape, dtype=dtype, device=x.device)
-    st = lib().sb_dropout(x.data_ptr(), _ptr(residual), x.numel(), _type(x.dtype, where), ot, p, seed,
+    out = torch.empty_like(x, dtype=dtype)
+    st = lib().sb_dropout(x.data_ptr(), _ptr(residual), x.numel(), xt, ot, p, seed,
                           _ptr(seed_offset), out.data_ptr(), _current(dev))
     if st != SB_OK:
         raise SbError(st, "sb_dropout")
@@ -907,18 +921,16 @@ def _layer_norm_problem(h, weight, where):
     """Checks the arguments both directions share; returns (M, d, the types of the stream and of
     the weights, device index)."""
     import torch
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     if h.dim() != 2:
         raise ValueError(f"{where}: h is [M, d]")
     M, d = h.shape
-    f32, bf16 = torch.float32, torch.bfloat16
-    ht, wt = h.dtype, weight.dtype
-    if not ((ht is bf16 or ht is f32) and (wt is bf16 or wt is f32) and weight.shape == (d,) and
-            h.get_device() == dev and weight.get_device() == dev and h.is_contiguous() and
-            weight.is_contiguous()):
-        _tensor("h", h, (M, d), (bf16, f32), dev, where)
-        _tensor("weight", weight, (d,), (bf16, f32), dev, where)
-    return M, d, SB_F32 if ht is f32 else SB_BF16, SB_F32 if wt is f32 else SB_BF16, dev
+    ht, wt = _type(h.dtype, where), _type(weight.dtype, where)
+    if not (weight.shape == (d,) and h.get_device() == dev and weight.get_device() == dev and
+            h.is_contiguous() and weight.is_contiguous()):
+        _tensor("h", h, (M, d), (h.dtype,), dev, where)
+        _tensor("weight", weight, (d,), (weight.dtype,), dev, where)
+    return M, d, ht, wt, dev
 
 
 def layer_norm(h, weight, bias=None, *, y=None, p: float = 0.0, seed: int = 0, seed_offset=None,
@@ -940,7 +952,7 @@ def layer_norm(h, weight, bias=None, *, y=None, p: float = 0.0, seed: int = 0, s
     M, d, ht, wt, dev = _layer_norm_problem(h, weight, where)
     if bias is not None:
         _tensor("bias", bias, (d,), (weight.dtype,), dev, where)
-    x = torch.empty(M, d, dtype=torch.bfloat16, device=h.device)
+    x = torch.empty_like(h, dtype=torch.bfloat16)
     h_out = h
     if y is not None:
         _tensor("y", y, (M, d), (torch.bfloat16,), dev, where)
@@ -1017,40 +1029,47 @@ def verify_drafts(logits, drafts, starts, uniforms, *, draft_logits=None, temper
             logits, drafts, starts, uniforms, draft_logits, lse, draft_lse, workspace)
     import torch
     where = "verify_drafts"
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     if logits.dim() != 2 or starts.dim() != 1 or starts.shape[0] < 1:
         raise ValueError(f"{where}: logits is [R, V] and starts [B + 1]")
     (R, V), B = logits.shape, starts.shape[0] - 1
     i32, f32 = torch.int32, torch.float32
-    _tensor("logits", logits, (R, V), (torch.bfloat16, f32), dev, where)
-    _tensor("drafts", drafts, (R,), (i32,), dev, where)
-    _tensor("starts", starts, (B + 1,), (i32,), dev, where)
-    _tensor("uniforms", uniforms, (R,), (f32,), dev, where)
-    D = -1
+    zt = _type(logits.dtype, where)
+    if not (drafts.shape == (R,) and uniforms.shape == (R,) and drafts.dtype is i32 and
+            starts.dtype is i32 and uniforms.dtype is f32 and logits.get_device() == dev and
+            drafts.get_device() == dev and starts.get_device() == dev and
+            uniforms.get_device() == dev and logits.is_contiguous() and drafts.is_contiguous() and
+            starts.is_contiguous() and uniforms.is_contiguous()):
+        _tensor("logits", logits, (R, V), (logits.dtype,), dev, where)
+        _tensor("drafts", drafts, (R,), (i32,), dev, where)
+        _tensor("starts", starts, (B + 1,), (i32,), dev, where)
+        _tensor("uniforms", uniforms, (R,), (f32,), dev, where)
+    D, q, ql = -1, None, None
     if draft_logits is not None:
         if draft_logits.dim() != 2:
             raise ValueError(f"{where}: draft_logits is [drafts, V]")
         D = draft_logits.shape[0]
         _tensor("draft_logits", draft_logits, (D, V), (logits.dtype,), dev, where)
+        q = draft_logits.data_ptr()
     if lse is not None:
         _tensor("lse", lse, (R,), (f32,), dev, where)
     if draft_lse is not None:
         if draft_logits is None:
             raise ValueError(f"{where}: draft_lse without draft_logits")
         _tensor("draft_lse", draft_lse, (D,), (f32,), dev, where)
+        ql = draft_lse.data_ptr()
     seed = _seeded(seed, None, dev, where)
     L = lib()
     if workspace is None:
         size = _nonzero(L.sb_verify_workspace_bytes(R, D, V), where)
-        workspace = torch.empty(size, dtype=torch.uint8, device=logits.device)
+        workspace = torch.empty(size, dtype=torch.uint8, device=starts.device)
     else:
         size = _workspace(workspace, dev, where)
-    token = torch.empty(R, dtype=i32, device=logits.device)
-    accepted = torch.empty(B, dtype=i32, device=logits.device)
-    lp = torch.empty(R, dtype=f32, device=logits.device) if logprob else None
-    st = L.sb_verify_drafts(logits.data_ptr(), _ptr(draft_logits), drafts.data_ptr(),
-                            starts.data_ptr(), uniforms.data_ptr(), _ptr(lse), _ptr(draft_lse), R, D,
-                            B, V, SB_F32 if logits.dtype is f32 else SB_BF16, temperature, seed,
+    token = torch.empty_like(drafts)
+    accepted = torch.empty(B, dtype=i32, device=starts.device)
+    lp = torch.empty_like(uniforms) if logprob else None
+    st = L.sb_verify_drafts(logits.data_ptr(), q, drafts.data_ptr(), starts.data_ptr(),
+                            uniforms.data_ptr(), _ptr(lse), ql, R, D, B, V, zt, temperature, seed,
                             token.data_ptr(), accepted.data_ptr(), _ptr(lp), workspace.data_ptr(),
                             size, _current(dev))
     if st != SB_OK:

@@ -9,15 +9,16 @@
 //
 // Backward sums rows in a fixed order, so that equal calls give equal bits; atomics on fp32 values
 // would not.  Its kernels:
-//   sort_kernel    tokens by (id, position), in runs of 256: a token's place is the count of smaller
-//                  keys, and of equal ones at earlier positions; all pairs are compared, the keys
-//                  broadcast from shared memory.  When the whole gradient is asked for, further
-//                  blocks of the same launch write its zeros meanwhile (that is most of its bytes: V
-//                  rows against at most M that are not zero).
-//   merge_runs_kernel, merge_chunks_kernel   runs to chunks of 8192 and chunks to one order: the
-//                  counts of smaller keys in the other runs by binary search, four threads to a
-//                  token.  No pass of either waits for another block.  (All pairs over 8192 tokens
-//                  in one launch took 17 us.)
+//   sort_kernel    tokens by (id, position), in chunks of 8192: a token's place is the count of smaller
+//                  keys, and of equal ones at earlier positions.  All pairs are compared, two tokens
+//                  to a lane, the keys broadcast from shared memory, in one pass that waits for no
+//                  other block.  Ids below 2^24 are compared as fp32: the saturated difference of two
+//                  whole numbers is 1 or 0, an addition at full rate, where integer compares run at half
+//                  of it (8192 tokens: 8 us against 17; sorted runs merged by binary search in a second
+//                  kernel: 15 in the step).  When the whole gradient is asked for, further blocks of
+//                  the same launch write its zeros meanwhile (that is most of its bytes: V rows against
+//                  at most M that are not zero); else they fetch rows that reduce_kernel will read.
+//   merge_kernel   chunks to one order: the counts of smaller keys in the other chunks by binary search.
 //   reduce_kernel  a block takes a piece of consecutive sorted tokens and a slice of columns, and
 //                  adds the rows of each run of equal ids in registers; a run inside the piece is
 //                  scaled, added and rounded here.  What a piece holds of a run that crosses its
@@ -105,18 +106,19 @@ cudaError_t launch_lookup(LookupParams p, int vec, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ backward: order
-constexpr int kRun = 256;            // tokens sorted by all pairs, a thread each
+constexpr int kSortThreads = 512;
+constexpr int kSortTokens = 64;      // of a block, two to a lane
+constexpr int kChunk = 8192;         // tokens whose keys a block holds in shared memory
 constexpr int kFetchBlocks = 152;
 // What is fetched while the tokens are sorted: about what the memory delivers in that time (24, 48 and
 // 100 MB at 8192 tokens x 6144: 50.7, 51.0 and 52.6 us in all; nothing: 53.1).
 constexpr int64_t kFetchBytes = int64_t(24) << 20;
-constexpr int kChunk = 8192;         // tokens whose keys a block holds in shared memory
 
 struct SortParams {
     const int32_t *ids;
     int M, V, ignore;
     int sort_blocks;
-    uint32_t *key;     // sorted within each run
+    uint32_t *key;     // sorted within each chunk
     int *at;           // their positions
     uint8_t *zero;     // bytes to clear (null: none)
     size_t zero_bytes;
@@ -126,12 +128,12 @@ struct SortParams {
 };
 
 // A block's share of the zeros; values are 2 or 4 bytes wide, and so is what lies before and behind
-// the 32-byte units.  A store to a thread and 8 KB to a block: 1.24 GB in 162 us, against 192 where
+// the 32-byte units.  A store to a thread and 16 KB to a block: 1.24 GB in 163 us, against 192 where
 // blocks of a grid that just fills the GPU (or bulk stores) go over the matrix in turn.
 __device__ __forceinline__ void clear_share(uint8_t *p, size_t n, size_t block) {
     size_t head = (32 - (reinterpret_cast<uintptr_t>(p) & 31)) & 31;
     if (head > n) head = n;
-    const size_t o = head + (block * kRun + threadIdx.x) * 32;
+    const size_t o = head + (block * kSortThreads + threadIdx.x) * 32;
     if (o + 32 <= n) {
         st_global_v8(p + o, 0, 0, 0, 0, 0, 0, 0, 0);
     } else {
@@ -142,15 +144,37 @@ __device__ __forceinline__ void clear_share(uint8_t *p, size_t n, size_t block) 
 
 // A block's share of the rows that reduce_kernel will read.
 __device__ __forceinline__ void fetch_share(const SortParams &p, int block, int blocks) {
-    for (int t = block + static_cast<int>(threadIdx.x) * blocks; t < p.fetch; t += kRun * blocks) {
+    for (int t = block + static_cast<int>(threadIdx.x) * blocks; t < p.fetch; t += kSortThreads * blocks) {
         const int id = p.ids[t];
         if (id >= 0 && id < p.V && id != p.ignore)
             prefetch_l2(p.dout + t * p.dout_row, static_cast<uint32_t>(p.dout_row));
     }
 }
 
-__global__ void __launch_bounds__(kRun) sort_kernel(const SortParams p) {
-    __shared__ __align__(16) uint4 room[kRun / 4];
+// How many of four keys are below each lane's limit.  AS_FLOAT: whole numbers up to 2^25 as fp32, in
+// pairs of counts.
+struct Count {
+    float2 f;
+    int i;
+};
+template <bool AS_FLOAT>
+__device__ __forceinline__ void count_below(Count &c, uint4 k, uint32_t limit) {
+    if constexpr (AS_FLOAT) {
+        const float l = __uint_as_float(limit);
+        c.f = __fadd2_rn(c.f, make_float2(__saturatef(l - __uint_as_float(k.x)),
+                                          __saturatef(l - __uint_as_float(k.y))));
+        c.f = __fadd2_rn(c.f, make_float2(__saturatef(l - __uint_as_float(k.z)),
+                                          __saturatef(l - __uint_as_float(k.w))));
+    } else {
+        c.i += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+    }
+}
+
+template <bool AS_FLOAT>
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) {
+    constexpr int WARPS = kSortThreads / 32;
+    __shared__ __align__(16) uint32_t keys[kChunk];
+    __shared__ int counts[WARPS][kSortTokens];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (static_cast<int>(blockIdx.x) >= p.sort_blocks) {
@@ -161,45 +185,71 @@ __global__ void __launch_bounds__(kRun) sort_kernel(const SortParams p) {
             fetch_share(p, block, gridDim.x - p.sort_blocks);
         return;
     }
-    const int base = blockIdx.x * kRun, i = threadIdx.x;
-    const int n = min(kRun, p.M - base), groups = (n + 31) / 32;
-    uint32_t *keys = reinterpret_cast<uint32_t *>(room);
-    uint32_t key = 0xFFFFFFFFu;  // behind the last token: never counted
-    if (i < n) {
-        const int id = p.ids[base + i];
-        key = id >= 0 && id < p.V && id != p.ignore ? id : kNoToken;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int base = blockIdx.x / (kChunk / kSortTokens) * kChunk;
+    const int n = min(kChunk, p.M - base), groups = (n + 31) / 32;
+    const int mine = blockIdx.x % (kChunk / kSortTokens) * (kSortTokens / 32);  // my first group of 32
+    // what is compared: the number, or its fp32; a limit is the next number
+    auto coded = [](uint32_t v) { return AS_FLOAT ? __float_as_uint(static_cast<float>(v)) : v; };
+    // (fp32 has every whole number up to 2^24, the limit of kNone's equals)
+    constexpr uint32_t kNone = AS_FLOAT ? (1u << 24) - 1 : kNoToken, kBehind = AS_FLOAT ? 1u << 25 : ~0u;
+    auto key_of = [&](int j) {
+        if (j >= n) return kBehind;  // behind the last token: never counted
+        const int id = p.ids[base + j];
+        return id >= 0 && id < p.V && id != p.ignore ? static_cast<uint32_t>(id) : kNone;
+    };
+#pragma unroll 8
+    for (int j = tid; j < groups * 32; j += kSortThreads) keys[j] = coded(key_of(j));
+    uint32_t key[2], below[2], up_to[2];
+    Count c[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        key[k] = key_of((mine + k) * 32 + lane);
+        below[k] = coded(key[k]);
+        up_to[k] = coded(key[k] + 1);  // equal keys count where they come before
+        c[k] = Count{both(0.f), 0};
     }
-    keys[i] = key;
     __syncthreads();
-    const int mine = i / 32, lane = i % 32;
-    if (mine >= groups) return;
-    int rank = 0;
-    for (int g = 0; g < groups; ++g) {
-        const uint4 *k4 = room + g * 8;
-        if (g != mine) {
-            const uint32_t limit = key + (g < mine);  // equal keys count where they come before
+    for (int g = warp; g < groups; g += WARPS) {
+        const uint4 *k4 = reinterpret_cast<const uint4 *>(keys) + g * 8;
+        if (g < mine || g > mine + 1) {
+            const uint32_t l0 = g < mine ? up_to[0] : below[0], l1 = g < mine ? up_to[1] : below[1];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint4 k = k4[j];
-                rank += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+                count_below<AS_FLOAT>(c[0], k, l0);
+                count_below<AS_FLOAT>(c[1], k, l1);
             }
         } else {
+            // a group of my own tokens: equal keys of it count below their lane
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j) {
+                const uint32_t k = keys[g * 32 + j];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint4 k = k4[j];
-                rank += (k.x < key + (4 * j < lane)) + (k.y < key + (4 * j + 1 < lane)) +
-                        (k.z < key + (4 * j + 2 < lane)) + (k.w < key + (4 * j + 3 < lane));
+                for (int t = 0; t < 2; ++t) {
+                    const bool before = g < mine + t || (g == mine + t && j < lane);
+                    const uint32_t l = before ? up_to[t] : below[t];
+                    c[t].i += AS_FLOAT ? __uint_as_float(k) < __uint_as_float(l) : k < l;
+                }
             }
         }
     }
-    if (i < n) {
-        p.key[base + rank] = key;
-        p.at[base + rank] = base + i;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)  // (counts up to 8192 are exact)
+        counts[warp][t * 32 + lane] = c[t].i + static_cast<int>(c[t].f.x + c[t].f.y);
+    __syncthreads();
+    if (warp < 2 && (mine + warp) * 32 + lane < n) {
+        int rank = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) rank += counts[w][warp * 32 + lane];
+        const uint32_t k = warp ? key[1] : key[0];
+        p.key[base + rank] = k == kNone ? kNoToken : k;
+        p.at[base + rank] = base + (mine + warp) * 32 + lane;
     }
 }
 
-// Sorted runs become sorted chunks, and sorted chunks one order: a token's place is its place in its
-// own run and the counts of smaller keys (of keys not larger, in earlier runs) in the others.
+// The chunks' orders become one: a token's place is its place in its own chunk and the counts of smaller
+// keys (of keys not larger, in earlier chunks) in the others.
 struct MergeParams {
     const uint32_t *key;
     const int *at;
@@ -208,55 +258,8 @@ struct MergeParams {
     int M;
 };
 constexpr int kMergeThreads = 256;
-constexpr int kMergeLanes = 4;  // threads of a token, which share the runs
 
-__global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(const MergeParams p) {
-    __shared__ __align__(16) uint32_t keys[kChunk];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kTokens = kMergeThreads / kMergeLanes;
-    const int base = blockIdx.x / (kChunk / kTokens) * kChunk;
-    const int n = min(kChunk, p.M - base), runs = (n + kRun - 1) / kRun;
-    const uint4 none = make_uint4(~0u, ~0u, ~0u, ~0u);  // behind the last token: never counted
-#pragma unroll 8
-    for (int j = threadIdx.x; j < runs * (kRun / 4); j += kMergeThreads) {
-        uint4 k = none;
-        if (4 * j + 3 < n) {
-            k = reinterpret_cast<const uint4 *>(p.key + base)[j];
-        } else {
-            if (4 * j < n) k.x = p.key[base + 4 * j];
-            if (4 * j + 1 < n) k.y = p.key[base + 4 * j + 1];
-            if (4 * j + 2 < n) k.z = p.key[base + 4 * j + 2];
-        }
-        reinterpret_cast<uint4 *>(keys)[j] = k;
-    }
-    const int i = blockIdx.x * kTokens - base + static_cast<int>(threadIdx.x) / kMergeLanes;
-    const int lane = threadIdx.x % kMergeLanes;
-    const int at = i < n && lane == 0 ? p.at[base + i] : 0;
-    __syncthreads();
-    const uint32_t key = i < n ? keys[i] : 0u;
-    const int own = i / kRun;
-    int place = 0;
-#pragma unroll 4
-    for (int r = lane; r < runs; r += kMergeLanes) {
-        const uint32_t limit = r == own ? 0u : key + (r < own);
-        const uint32_t *k = keys + r * kRun;
-        int c = 0;
-#pragma unroll
-        for (int step = kRun / 2; step > 0; step /= 2)
-            if (k[c + step - 1] < limit) c += step;
-        place += c + (k[c] < limit);
-    }
-    place += __shfl_xor_sync(0xFFFFFFFFu, place, 1);
-    place += __shfl_xor_sync(0xFFFFFFFFu, place, 2);
-    if (i < n && lane == 0) {
-        place += base + i % kRun;
-        p.to_key[place] = key;
-        p.to_at[place] = at;
-    }
-}
-
-__global__ void __launch_bounds__(kMergeThreads) merge_chunks_kernel(const MergeParams p) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long i = static_cast<long long>(blockIdx.x) * kMergeThreads + threadIdx.x;
@@ -323,7 +326,9 @@ __global__ void __launch_bounds__(kReduceThreads) reduce_kernel(const ReducePara
     using RW = Raw<W, VEC>;
     __shared__ int2 token[kPiece + 2];  // (key, position); key -1: none
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // no early launch_dependents: nothing that follows may read dW ahead of this kernel's end
+    // Where join_kernel follows it may get ready (it waits for this kernel's end); else no early
+    // launch_dependents: nothing that follows may read dW ahead of that.
+    if (p.pieces > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int first = blockIdx.x * kPiece;
     if (threadIdx.x < kPiece + 2) {
         const int i = first + static_cast<int>(threadIdx.x) - 1;
@@ -393,8 +398,8 @@ __global__ void __launch_bounds__(kReduceThreads) reduce_kernel(const ReducePara
 }
 
 // The run that starts in a piece and ends in a later one: its parts in ascending order, or, where
-// they are many, eight slices of them side by side and then the slices.
-constexpr int kJoinSlices = 8;
+// they are many, sixteen slices of them side by side and then the slices.
+constexpr int kJoinSlices = 16;
 template <typename W, int VEC>
 __global__ void __launch_bounds__(32 * kJoinSlices) join_kernel(const ReduceParams p) {
     constexpr int N = (VEC + 1) / 2;
@@ -537,10 +542,10 @@ int32_t sb_embedding_forward(const int32_t *ids, const void *W, int64_t M, int64
     return e == cudaSuccess ? SB_OK : SB_ERR_CUDA;
 }
 
-// [keys, positions, keys, positions (each step of the sort goes from one pair to the other)] [parts]
+// [keys, positions] [the same, of the chunks merged (beyond one chunk)] [parts]
 size_t sb_embedding_backward_workspace_bytes(int64_t M, int64_t d) {
     if (M < 0 || M > kMaxTokens || d < 1 || d > kMaxWidth) return 0;
-    const size_t tokens = up256(static_cast<size_t>(M) * 4) * 4;
+    const size_t tokens = up256(static_cast<size_t>(M) * 4) * (M > kChunk ? 4 : 2);
     const size_t parts = M > kPiece ? up256(static_cast<size_t>(pieces_of(M)) * 2 * d * 4) : 0;
     return 256 + tokens + parts;
 }
@@ -562,7 +567,7 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
     const size_t array = up256(static_cast<size_t>(M) * 4);
     uint32_t *key[2];
     int *at[2];
-    for (int k = 0; k < 2; ++k, ws += 2 * array) {
+    for (int k = 0; k < (M > kChunk ? 2 : 1); ++k, ws += 2 * array) {
         key[k] = reinterpret_cast<uint32_t *>(ws);
         at[k] = reinterpret_cast<int *>(ws + array);
     }
@@ -572,7 +577,7 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
     s.M = static_cast<int>(M);
     s.V = static_cast<int>(V);
     s.ignore = ignore_index;
-    s.sort_blocks = static_cast<int>((M + kRun - 1) / kRun);
+    s.sort_blocks = static_cast<int>((M + kSortTokens - 1) / kSortTokens);
     s.key = key[0];
     s.at = at[0];
     if (!add) {
@@ -582,7 +587,7 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
     // (rounded up, and one more for what an unaligned head shifts to the end)
     if (add) {
         s.dout_row = static_cast<size_t>(d) * (grad_type == SB_F32 ? 4 : 2);
-        if (on(dout, 16) && s.dout_row % 16 == 0 && M > kRun) {
+        if (on(dout, 16) && s.dout_row % 16 == 0 && M > 256) {
             s.dout = static_cast<const uint8_t *>(dout);
             s.fetch = static_cast<int>(M < kFetchBytes / static_cast<int64_t>(s.dout_row)
                                            ? M
@@ -590,22 +595,20 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
         }
     }
     const size_t fetch_blocks = s.fetch > 0 ? kFetchBlocks : 0;
-    const size_t zero_blocks = add ? fetch_blocks : s.zero_bytes / (kRun * 32) + 1;
+    const size_t zero_blocks = add ? fetch_blocks : s.zero_bytes / (kSortThreads * 32) + 1;
     if (zero_blocks > (size_t(1) << 30)) return SB_ERR_INVALID_ARG;
-    if (launch_dependent(sort_kernel, dim3(s.sort_blocks + static_cast<unsigned>(zero_blocks)), kRun, 0,
-                         s, st) != cudaSuccess)
+    const dim3 grid(s.sort_blocks + static_cast<unsigned>(zero_blocks));
+    if ((V < 1 << 24 ? launch_dependent(sort_kernel<true>, grid, kSortThreads, 0, s, st)
+                      : launch_dependent(sort_kernel<false>, grid, kSortThreads, 0, s, st)) != cudaSuccess)
         return SB_ERR_CUDA;
     if (M == 0) return SB_OK;
-    for (const int run : {kRun, kChunk})
-        if (M > run) {
-            const MergeParams m{key[now], at[now], key[1 - now], at[1 - now], static_cast<int>(M)};
-            const int64_t threads = M * (run == kRun ? kMergeLanes : 1);
-            const dim3 grid(static_cast<unsigned>((threads + kMergeThreads - 1) / kMergeThreads));
-            if (launch_dependent(run == kRun ? merge_runs_kernel : merge_chunks_kernel, grid,
-                                 kMergeThreads, 0, m, st) != cudaSuccess)
-                return SB_ERR_CUDA;
-            now = 1 - now;
-        }
+    if (M > kChunk) {
+        const MergeParams m{key[0], at[0], key[1], at[1], static_cast<int>(M)};
+        if (launch_dependent(merge_kernel, dim3(static_cast<unsigned>((M + kMergeThreads - 1) / kMergeThreads)),
+                             kMergeThreads, 0, m, st) != cudaSuccess)
+            return SB_ERR_CUDA;
+        now = 1;
+    }
     ReduceParams r{};
     r.key = key[now];
     r.at = at[now];

@@ -619,7 +619,7 @@ size_t sb_embedding_backward_workspace_bytes(int64_t M, int64_t d);
  *   dW          device [V, d] of weight_type.
  *   workspace   device, 256-byte aligned, >= sb_embedding_backward_workspace_bytes(M, d); no
  *               initialisation.
- * Up to five kernels on `stream`.
+ * Up to four kernels on `stream`.
  */
 int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, int64_t d, int64_t V,
                               int32_t ignore_index, float scale, int32_t grad_type,
