@@ -15,9 +15,9 @@
 //                  other block.  Ids below 2^24 are compared as fp32: the saturated difference of two
 //                  whole numbers is 1 or 0, an addition at full rate, where integer compares run at half
 //                  of it (8192 tokens: 8 us against 17; sorted runs merged by binary search in a second
-//                  kernel: 15 in the step).  When the whole gradient is asked for, further blocks of
+//                  kernel took 15).  When the whole gradient is asked for, further blocks of
 //                  the same launch write its zeros meanwhile (that is most of its bytes: V rows against
-//                  at most M that are not zero); else they fetch rows that reduce_kernel will read.
+//                  at most M that are not zero).  (Fetching rows into L2 meanwhile did not pay.)
 //   merge_kernel   chunks to one order: the counts of smaller keys in the other chunks by binary search.
 //   reduce_kernel  a block takes a piece of consecutive sorted tokens and a slice of columns, and
 //                  adds the rows of each run of equal ids in registers; a run inside the piece is
@@ -106,13 +106,9 @@ cudaError_t launch_lookup(LookupParams p, int vec, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ backward: order
-constexpr int kSortThreads = 512;
+constexpr int kSortThreads = 1024;
 constexpr int kSortTokens = 64;      // of a block, two to a lane
 constexpr int kChunk = 8192;         // tokens whose keys a block holds in shared memory
-constexpr int kFetchBlocks = 152;
-// What is fetched while the tokens are sorted: about what the memory delivers in that time (24, 48 and
-// 100 MB at 8192 tokens x 6144: 50.7, 51.0 and 52.6 us in all; nothing: 53.1).
-constexpr int64_t kFetchBytes = int64_t(24) << 20;
 
 struct SortParams {
     const int32_t *ids;
@@ -122,13 +118,10 @@ struct SortParams {
     int *at;           // their positions
     uint8_t *zero;     // bytes to clear (null: none)
     size_t zero_bytes;
-    const uint8_t *dout;  // rows to fetch into L2
-    size_t dout_row;      // bytes
-    int fetch;            // how many of them
 };
 
 // A block's share of the zeros; values are 2 or 4 bytes wide, and so is what lies before and behind
-// the 32-byte units.  A store to a thread and 16 KB to a block: 1.24 GB in 163 us, against 192 where
+// the 32-byte units.  A store to a thread and 32 KB to a block: 1.24 GB in 163 us, against 192 where
 // blocks of a grid that just fills the GPU (or bulk stores) go over the matrix in turn.
 __device__ __forceinline__ void clear_share(uint8_t *p, size_t n, size_t block) {
     size_t head = (32 - (reinterpret_cast<uintptr_t>(p) & 31)) & 31;
@@ -140,15 +133,6 @@ __device__ __forceinline__ void clear_share(uint8_t *p, size_t n, size_t block) 
         for (size_t i = o; i < n; i += 2) *reinterpret_cast<uint16_t *>(p + i) = 0;
     }
     if (block == 0 && threadIdx.x < head / 2) reinterpret_cast<uint16_t *>(p)[threadIdx.x] = 0;
-}
-
-// A block's share of the rows that reduce_kernel will read.
-__device__ __forceinline__ void fetch_share(const SortParams &p, int block, int blocks) {
-    for (int t = block + static_cast<int>(threadIdx.x) * blocks; t < p.fetch; t += kSortThreads * blocks) {
-        const int id = p.ids[t];
-        if (id >= 0 && id < p.V && id != p.ignore)
-            prefetch_l2(p.dout + t * p.dout_row, static_cast<uint32_t>(p.dout_row));
-    }
 }
 
 // How many of four keys are below each lane's limit.  AS_FLOAT: whole numbers up to 2^25 as fp32, in
@@ -178,11 +162,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (static_cast<int>(blockIdx.x) >= p.sort_blocks) {
-        const int block = blockIdx.x - p.sort_blocks;
-        if (p.zero)
-            clear_share(p.zero, p.zero_bytes, block);
-        else
-            fetch_share(p, block, gridDim.x - p.sort_blocks);
+        clear_share(p.zero, p.zero_bytes, blockIdx.x - p.sort_blocks);
         return;
     }
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -585,17 +565,7 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
         s.zero_bytes = static_cast<size_t>(V) * d * (weight_type == SB_F32 ? 4 : 2);
     }
     // (rounded up, and one more for what an unaligned head shifts to the end)
-    if (add) {
-        s.dout_row = static_cast<size_t>(d) * (grad_type == SB_F32 ? 4 : 2);
-        if (on(dout, 16) && s.dout_row % 16 == 0 && M > 256) {
-            s.dout = static_cast<const uint8_t *>(dout);
-            s.fetch = static_cast<int>(M < kFetchBytes / static_cast<int64_t>(s.dout_row)
-                                           ? M
-                                           : kFetchBytes / static_cast<int64_t>(s.dout_row));
-        }
-    }
-    const size_t fetch_blocks = s.fetch > 0 ? kFetchBlocks : 0;
-    const size_t zero_blocks = add ? fetch_blocks : s.zero_bytes / (kSortThreads * 32) + 1;
+    const size_t zero_blocks = add ? 0 : s.zero_bytes / (kSortThreads * 32) + 1;
     if (zero_blocks > (size_t(1) << 30)) return SB_ERR_INVALID_ARG;
     const dim3 grid(s.sort_blocks + static_cast<unsigned>(zero_blocks));
     if ((V < 1 << 24 ? launch_dependent(sort_kernel<true>, grid, kSortThreads, 0, s, st)

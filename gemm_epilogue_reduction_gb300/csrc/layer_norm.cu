@@ -13,14 +13,13 @@
 // Both are bound by memory, and what keeps them from it is the time that a row's threads wait for
 // each other in the two reductions.  As in the residual norm (norm.cu) a row belongs to a group of
 // threads, sixteen values to a thread, and the next rows are on their way in a cp.async ring.
-//   Forward: 768 threads, two rows of 6144 at a time, so that one's work fills the other's waits.
-//   The weights are in shared memory in fp32 (in registers the second row would not fit); each row
-//   reads them there.  8192 x 6144 bf16 with branch and dropout: 70 us, 5.8 TB/s (one row at a time
-//   with 168 registers: 74).  Blocks that do one row each and end, with the weights from L1, took
-//   108 us: their fixed work and their loads of weights weigh more than the waits.
-//   Backward keeps weights and column sums in registers: 384 threads and two rows side by side in
-//   each thread, whose sums go through the same two reductions; dx and dh are read again from the
-//   ring.  85 us, 5.9 TB/s (one row: 110).
+// A thread works on two rows side by side: their sums go through the same two reductions, and one's
+// arithmetic fills the other's waits (8192 x 6144 bf16 with branch and dropout: forward 64 us, 6.3 TB/s,
+// and 84, 6.0 TB/s, backward; one row: 74 and 94; four rows in forward, whose ring then has no third
+// step: 71; two groups of 384 threads with the weights in shared memory: 70; a block to a row, which
+// ends with it: 108, its fixed work and its loads of weights weigh more than the waits).  Weights and
+// column sums are in registers; backward reads dx and dh again from the ring.  A draw's state goes from
+// row to row by one addition.
 // A row length that is no multiple of eight shifts each row against the vectors' boundaries
 // (layer_norm.cuh); backward gives a group rows a multiple of eight apart, so that their shift, and
 // with it a thread's columns, stay the same.
@@ -69,9 +68,9 @@ LoadMode mode_of(int64_t d, Ptr... ptrs) {
     if (bits & 15u) return kSingle;
     return d % 8 == 0 ? kAligned : d > 8 ? kShifted : kSingle;
 }
-// A row's threads, the groups of a block and the steps of a group's ring.  row_bytes: of a thread for
-// a row of the ring; rows: of a step; weight_bytes: of a thread, for the weights kept beside the rings
-// (one copy, or one to a group where the groups' shifts differ).
+// A row's threads, the groups of a block, the rows that a group works on at a time and the steps of its
+// ring.  row_bytes: of a thread for a row of the ring; weight_bytes: of a thread, for the weights of rows
+// too long to keep them in registers.
 struct Layout {
     LoadMode mode;
     int row_threads, groups, steps, rows;
@@ -79,8 +78,7 @@ struct Layout {
     int64_t blocks;
     size_t smem;
 };
-Layout lay_out(int64_t M, int64_t d, LoadMode mode, int threads, size_t row_bytes, int rows,
-               size_t weight_bytes, int sms) {
+Layout lay_out(int64_t M, int64_t d, LoadMode mode, size_t row_bytes, size_t weight_bytes, int sms) {
     Layout l{};
     auto threads_of = [d](int shift) {
         return round32(((d + shift + 7) / 8 + kNormVectors - 1) / kNormVectors);
@@ -88,27 +86,28 @@ Layout lay_out(int64_t M, int64_t d, LoadMode mode, int threads, size_t row_byte
     if (mode == kShifted && threads_of(7) > 1024) mode = kSingle;
     l.mode = mode;
     l.row_threads = threads_of(mode == kShifted ? 7 : 0);
-    l.groups = threads / l.row_threads;
-    if (l.groups > kMaxGroups) l.groups = kMaxGroups;
     const int64_t share = (M + sms - 1) / sms;  // rows of an SM
+    l.groups = kNormThreads / l.row_threads;
+    l.rows = mode == kSingle || l.groups < 1 ? 1 : 2;
+    if (l.groups > kMaxGroups) l.groups = kMaxGroups;
     if (l.groups > share) l.groups = static_cast<int>(share);
-    // a ring of two steps at least: one is on its way while another one is worked on; fewer groups,
-    // then single rows, where they do not fit
     const size_t step = l.row_threads * row_bytes;
-    l.rows = mode != kSingle && share >= 2 * rows * (l.groups < 1 ? 1 : l.groups) ? rows : 1;
-    if (l.groups < 1) l.groups = l.rows = 1;
-    // rows too long for weights and two steps: the weights are read from memory again for each row
-    if (weight_bytes && 2 * step + weight_bytes * l.row_threads > kNormRingBytes) weight_bytes = 0;
+    // rows of up to 6144 have their weights in registers; rows too long for weights and two steps in
+    // shared memory read the weights from memory again for each row
+    if (l.groups >= 1 || 2 * step + weight_bytes * l.row_threads > kNormRingBytes) weight_bytes = 0;
+    if (l.groups < 1) l.groups = 1;
     l.weights = weight_bytes > 0;
-    auto weights = [&] { return weight_bytes * l.row_threads * (mode == kShifted ? l.groups : 1); };
-    auto fit = [&] { return (kNormRingBytes - weights()) / (l.rows * l.groups * step); };
+    const size_t weights = weight_bytes * l.row_threads;  // (one group then)
+    // a ring of two steps at least: one is on its way while another one is worked on; two rows at a
+    // time where the SM's share fills that twice, and one row, then fewer groups, where they do not fit
+    auto fit = [&] { return (kNormRingBytes - weights) / (l.rows * l.groups * step); };
+    if (share < 2 * l.rows * l.groups || fit() < 2) l.rows = 1;
     while (mode != kSingle && fit() < 2 && l.groups > 1) --l.groups;
-    if (mode != kSingle && fit() < 2) l.rows = 1;
     // (a row of backward beyond 10240 in fp32 has the ring to itself: nothing is ahead)
     l.steps = mode == kSingle ? 1 : static_cast<int>(fit());
-    if (l.steps < 1) l.mode = kSingle, l.steps = 1, l.smem = 0;  // (no row is that long)
+    if (l.steps < 1) l.mode = kSingle, l.steps = 1;  // (no row is that long)
     if (l.steps > kMaxDepth) l.steps = kMaxDepth;
-    l.smem = weights() + (l.mode == kSingle ? 0 : l.steps * l.rows * l.groups * step);
+    l.smem = weights + (l.mode == kSingle ? 0 : l.steps * l.rows * l.groups * step);
     l.blocks = (M + l.groups - 1) / l.groups;
     // (a multiple of eight: the rows of a group then have the same shift)
     if (l.blocks > sms) l.blocks = mode == kShifted && sms > 8 ? sms & ~7 : sms;
@@ -141,13 +140,13 @@ int32_t sb_layer_norm_forward(const void *h, const void *y, const void *weight, 
     q.h_out = h_out;
     q.x = x;
     const bool h32 = stream_type == SB_F32;
-    const Layout l = lay_out(M, d, mode_of(d, h, y, y ? h_out : nullptr, x), kForwardThreads,
-                             kNormVectors * 8 * ((h32 ? 4 : 2) + (y ? 2 : 0)), 1, kNormVectors * 64, sms);
+    const Layout l = lay_out(M, d, mode_of(d, h, y, y ? h_out : nullptr, x),
+                             kNormVectors * 8 * ((h32 ? 4 : 2) + (y ? 2 : 0)), kNormVectors * 64, sms);
     q.row_threads = l.row_threads;
     q.groups = l.groups;
     q.steps = l.steps;
     q.shared_weights = l.weights;
-    const LayerNormShape shape{l.mode, h32, l.groups * l.row_threads, 1};
+    const LayerNormShape shape{l.mode, h32, l.groups * l.row_threads, l.rows};
     return launch_layer_norm_forward(q, shape, static_cast<unsigned>(l.blocks), l.smem,
                                      static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? SB_OK
@@ -194,8 +193,8 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
     q.part = static_cast<float *>(workspace);
     q.sums = dbias ? 2 : 1;
     const bool h32 = stream_type == SB_F32;
-    const Layout l = lay_out(M, d, mode_of(d, dx, dh, h, dh_out, dy), kBackwardThreads,
-                             kNormVectors * 8 * ((h32 ? 8 : 4) + 2), 2, 0, sms);
+    const Layout l = lay_out(M, d, mode_of(d, dx, dh, h, dh_out, dy),
+                             kNormVectors * 8 * ((h32 ? 8 : 4) + 2), 0, sms);
     q.row_threads = l.row_threads;
     q.groups = l.groups;
     q.steps = l.steps;
@@ -212,7 +211,7 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
     c.dpre = dweight;
     c.dpost = dbias;
     if (launch_layer_norm_backward(q, shape, static_cast<unsigned>(l.blocks), smem, st) != cudaSuccess ||
-        launch_norm_columns(c, st) != cudaSuccess)
+        launch_norm_columns(c, true, st) != cudaSuccess)
         return SB_ERR_CUDA;
     return SB_OK;
 }

@@ -15,17 +15,16 @@ namespace sb {
 enum LoadMode : int { kAligned = 0, kShifted = 1, kSingle = 2 };
 
 constexpr int kNormVectors = 2;         // of a thread: sixteen values
-constexpr int kForwardThreads = 768;    // of a block, where a row does not need more
-constexpr int kBackwardThreads = 384;
+constexpr int kNormThreads = 384;       // of a block, where a row does not need more
 
 struct LayerNormParams {
     int M, d;
     int row_threads;  // threads of a row's group, a multiple of 32
     int groups;       // of a block
-    int steps;        // of a group's ring (of one row; backward: of `rows`)
+    int steps;        // of a group's ring
     int w32;          // weights in fp32 (otherwise bf16)
     int wide_weights; // weight and bias on 16 bytes
-    int shared_weights;  // forward: kept in shared memory
+    int shared_weights;  // forward, rows too long for the registers: kept in shared memory
     float eps, inv_d;
     const void *h, *y, *weight, *bias;
     void *h_out, *x;          // forward
@@ -40,7 +39,7 @@ struct LayerNormShape {
     LoadMode mode;
     bool h32;
     int threads;  // of a block
-    int rows;     // backward: that a group works on at a time
+    int rows;     // that a group works on at a time
 };
 
 cudaError_t launch_layer_norm_forward(const LayerNormParams &p, LayerNormShape s, unsigned blocks,

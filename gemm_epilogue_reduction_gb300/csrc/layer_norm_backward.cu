@@ -216,12 +216,12 @@ cudaError_t launch_layer_norm_backward(const LayerNormParams &p, LayerNormShape 
     return for_layer_norm(s, p.dy != nullptr, [&]<typename T, int MODE, bool BRANCH>() {
         static std::atomic<uint64_t> pairs{0}, small{0}, medium{0}, large{0};
         const int n = static_cast<int>(blocks);
-        if (s.threads <= kBackwardThreads) {
+        if (s.threads <= kNormThreads) {
             if constexpr (MODE != kSingle)
                 if (s.rows == 2)
-                    return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kBackwardThreads, 2>, pairs, p,
+                    return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kNormThreads, 2>, pairs, p,
                                               n, smem, st);
-            return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kBackwardThreads, 1>, small, p, n,
+            return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kNormThreads, 1>, small, p, n,
                                       smem, st);
         }
         if (s.threads <= 640)

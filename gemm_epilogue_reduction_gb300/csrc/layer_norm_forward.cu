@@ -4,21 +4,23 @@
 namespace sb {
 namespace {
 
-// BRANCH: h' = h + dropout(y).  The groups of all blocks take rows in turn; in kShifted all rows of a
-// group have the same shift (the host sees to that), so that a thread's columns stay the same.
-template <typename T, int MODE, bool BRANCH, int MAXT>
+// BRANCH: h' = h + dropout(y).  The groups of all blocks take ROWS rows in turn; in kShifted all rows of
+// a group have the same shift (the host sees to that), so that a thread's columns stay the same.  KEPT:
+// weight and bias stay in registers; else in shared memory, or are read again for each row.
+template <typename T, int MODE, bool BRANCH, int MAXT, int ROWS, bool KEPT>
 __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams p) {
+    static_assert(MODE != kSingle || ROWS == 1, "a row behind the last is in the ring only");
     constexpr int NV = kNormVectors;
     using B = __nv_bfloat16;
     using ST = Slots<T>;
     using SB = Slots<B>;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) float red[2][MAXT / 32 + 4 * kMaxGroups];
+    __shared__ __align__(16) float red[2][MAXT / 32 * 8];
     const int rt = p.row_threads, d = p.d;
     const int group = threadIdx.x / rt, t = threadIdx.x - group * rt;
-    float *red1 = red[0] + group * sum_words(rt / 32), *red2 = red[1] + group * sum_words(rt / 32);
+    float *red1 = red[0] + group * (rt / 32) * 8, *red2 = red[1] + group * (rt / 32) * 8;
     const uint32_t pitch = rt * 16, kY = ST::kThread * rt, kRow = kY + (BRANCH ? SB::kThread * rt : 0);
-    const uint32_t kRing = p.steps * kRow, kBias = 32 * NV * rt, kWeights = 2 * kBias;
+    const uint32_t kStep = ROWS * kRow, kRing = p.steps * kStep, kBias = 32 * NV * rt, kWeights = 2 * kBias;
     // weight and bias in fp32 (one copy, or one for each group's shift), then the groups' rings;
     // addresses of this thread's pieces
     const uint32_t copies = !p.shared_weights ? 0 : MODE == kShifted ? p.groups : 1;
@@ -36,26 +38,32 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
     const B *y_next = static_cast<const B *>(p.y) + base + e0;
     auto copy = [&](uint32_t at) {
         if constexpr (MODE != kSingle) {
-            if (next < p.M) {
-                // the array's last row may end inside a vector
-                const bool inner = !last_has || next + 1 < p.M;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int e = e0 + i * per;
-                    const bool whole = inner || e + 8 <= d;
-                    ST::template copy<MODE>(at, pitch, i, h_next + i * per, e, d, whole);
-                    if (BRANCH) SB::template copy<MODE>(at + kY, pitch, i, y_next + i * per, e, d, whole);
+            for (int k = 0; k < ROWS; ++k, next += stride, h_next += advance, y_next += advance, at += kRow)
+                if (next < p.M) {
+                    // the array's last row may end inside a vector
+                    const bool inner = !last_has || next + 1 < p.M;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int e = e0 + i * per;
+                        const bool whole = inner || e + 8 <= d;
+                        ST::template copy<MODE>(at, pitch, i, h_next + i * per, e, d, whole);
+                        if (BRANCH) SB::template copy<MODE>(at + kY, pitch, i, y_next + i * per, e, d, whole);
+                    }
                 }
-            }
-            next += stride;
-            h_next += advance;
-            if (BRANCH) y_next += advance;
             ring_commit();  // also without a row, so that the count of groups stays in step
         }
     };
-    if (t < sum_words(rt / 32)) red1[t] = red2[t] = 0.f;
+    // the sums of a row each over the group
+    auto sums = [&](float (&v)[ROWS], float *words) {
+        if constexpr (ROWS == 1)
+            v[0] = row_sum<MAXT>(v[0], group, rt, words);
+        else
+            row_sum<MAXT>(v, group, rt, words);
+    };
+    if (ROWS == 1 && t < sum_words(rt / 32)) red1[t] = red2[t] = 0.f;
     if constexpr (MODE != kSingle)
-        for (int s = 0; s < p.steps; ++s)
+        for (int s = 0; s < p.steps * ROWS; ++s)
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 ST::clear(ring + s * kRow, pitch, i, e0 + i * per, d);
@@ -63,7 +71,7 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
             }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int s = 0; s + 1 < p.steps; ++s) copy(ring + s * kRow);
+    for (int s = 0; s + 1 < p.steps; ++s) copy(ring + s * kStep);
     auto read_bias = [&](int e, float2 (&v)[4]) {
         if (p.bias) {
             load_weight8<MODE>(p.bias, p, e, v);
@@ -72,7 +80,14 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
             for (int j = 0; j < 4; ++j) v[j] = both(0.f);
         }
     };
-    if (p.shared_weights && (MODE == kShifted || group == 0)) {
+    float2 w_kept[KEPT ? NV : 1][4], b_kept[KEPT ? NV : 1][4];
+    if constexpr (KEPT) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            load_weight8<MODE>(p.weight, p, e0 + i * per, w_kept[i]);
+            read_bias(e0 + i * per, b_kept[i]);
+        }
+    } else if (p.shared_weights && (MODE == kShifted || group == 0)) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float2 v[4];
@@ -94,68 +109,86 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
     }
     T *h_out = static_cast<T *>(p.h_out) + base + e0;
     B *x_out = static_cast<B *>(p.x) + base + e0;
-    uint32_t slot = 0, ahead = (p.steps - 1) * kRow;  // of the ring, in bytes
-    long long at_row = base;  // (kSingle)
-    for (long long row = first; row < p.M; row += stride) {
+    uint32_t slot = 0, ahead = (p.steps - 1) * kStep;  // of the ring, in bytes
+    long long at_row = base;                           // (kSingle)
+    for (long long row0 = first; row0 < p.M; row0 += ROWS * stride) {
         if constexpr (MODE != kSingle) {
             copy(ring + ahead);
-            ahead = ahead + kRow == kRing ? 0 : ahead + kRow;
+            ahead = ahead + kStep == kRing ? 0 : ahead + kStep;
             ring_wait(p.steps - 1);
         }
         const uint32_t at = ring + slot;
-        float2 a[NV][4];
-        float2 acc = both(0.f);
+        float2 a[ROWS][NV][4];
+        float sum[ROWS];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = e0 + i * per;
-            if constexpr (MODE == kSingle)
-                load_singles(static_cast<const T *>(p.h) + at_row, e, d, a[i]);
-            else
-                ST::get(at, pitch, i, a[i]);
-            mask8<MODE>(e, d, a[i]);
-            if constexpr (BRANCH) {
-                float2 v[4];
+        for (int k = 0; k < ROWS; ++k) {
+            float2 acc = both(0.f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = e0 + i * per;
                 if constexpr (MODE == kSingle)
-                    load_singles(static_cast<const B *>(p.y) + at_row, e, d, v);
+                    load_singles(static_cast<const T *>(p.h) + at_row, e, d, a[k][i]);
                 else
-                    SB::get(at + kY, pitch, i, v);
-                mask8<MODE>(e, d, v);
-                add_dropped<MODE>(p.drop, seed, state + i * state_vector,
-                                  static_cast<unsigned long long>(at_row + e), a[i], v);
+                    ST::get(at + k * kRow, pitch, i, a[k][i]);  // (a row behind the last: an old one)
+                mask8<MODE>(e, d, a[k][i]);
+                if constexpr (BRANCH) {
+                    float2 v[4];
+                    if constexpr (MODE == kSingle)
+                        load_singles(static_cast<const B *>(p.y) + at_row, e, d, v);
+                    else
+                        SB::get(at + k * kRow + kY, pitch, i, v);
+                    mask8<MODE>(e, d, v);
+                    add_dropped<MODE>(p.drop, seed, state + i * state_vector,
+                                      static_cast<unsigned long long>(at_row + e), a[k][i], v);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) a[i][j] = v[j];
-                store8<MODE>(h_out + i * per, e, d, a[i]);
+                    for (int j = 0; j < 4; ++j) a[k][i][j] = v[j];
+                    if (k == 0 || row0 + k * stride < p.M) store8<MODE>(h_out + i * per, e, d, a[k][i]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc = __fadd2_rn(acc, a[k][i][j]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc = __fadd2_rn(acc, a[i][j]);
+            sum[k] = acc.x + acc.y;
+            if (BRANCH) h_out += advance, state += state_row;
         }
-        const float mean = row_sum<MAXT>(acc.x + acc.y, group, rt, red1) * p.inv_d;
-        acc = both(0.f);
+        sums(sum, red1);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            centre8<MODE>(mean, e0 + i * per, d, a[i]);
+        for (int k = 0; k < ROWS; ++k) {
+            const float mean = sum[k] * p.inv_d;
+            float2 acc = both(0.f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc = __ffma2_rn(a[i][j], a[i][j], acc);
-        }
-        const float r = rsqrtf(row_sum<MAXT>(acc.x + acc.y, group, rt, red2) * p.inv_d + p.eps);
+            for (int i = 0; i < NV; ++i) {
+                centre8<MODE>(mean, e0 + i * per, d, a[k][i]);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float2 w[4], b[4];
-            if (p.shared_weights) {
-                Slots<float>::get(weights, pitch, i, w);
-                Slots<float>::get(weights + kBias, pitch, i, b);
-            } else {
-                load_weight8<MODE>(p.weight, p, e0 + i * per, w);
-                read_bias(e0 + i * per, b);
+                for (int j = 0; j < 4; ++j) acc = __ffma2_rn(a[k][i][j], a[k][i][j], acc);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[i][j] = __ffma2_rn(__fmul2_rn(a[i][j], both(r)), w[j], b[j]);
-            store8<MODE>(x_out + i * per, e0 + i * per, d, a[i]);
+            sum[k] = acc.x + acc.y;
         }
-        if (BRANCH) h_out += advance, state += state_row;
-        x_out += advance;
+        sums(sum, red2);
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            const float r = rsqrtf(sum[k] * p.inv_d + p.eps);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float2 w[4], b[4];
+                if constexpr (KEPT) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = w_kept[i][j], b[j] = b_kept[i][j];
+                } else if (p.shared_weights) {
+                    Slots<float>::get(weights, pitch, i, w);
+                    Slots<float>::get(weights + kBias, pitch, i, b);
+                } else {
+                    load_weight8<MODE>(p.weight, p, e0 + i * per, w);
+                    read_bias(e0 + i * per, b);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    a[k][i][j] = __ffma2_rn(__fmul2_rn(a[k][i][j], both(r)), w[j], b[j]);
+                if (k == 0 || row0 + k * stride < p.M) store8<MODE>(x_out + i * per, e0 + i * per, d, a[k][i]);
+            }
+            x_out += advance;
+        }
         if (MODE == kSingle) at_row += advance;
-        slot = slot + kRow == kRing ? 0 : slot + kRow;
+        slot = slot + kStep == kRing ? 0 : slot + kStep;
     }
 }
 
@@ -164,12 +197,17 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
 cudaError_t launch_layer_norm_forward(const LayerNormParams &p, LayerNormShape s, unsigned blocks,
                                       size_t smem, cudaStream_t st) {
     return for_layer_norm(s, p.y != nullptr, [&]<typename T, int MODE, bool BRANCH>() {
-        static std::atomic<uint64_t> small{0}, large{0};
-        if (s.threads <= kForwardThreads)
-            return launch_norm_kernel(forward_kernel<T, MODE, BRANCH, kForwardThreads>, small, p,
-                                      static_cast<int>(blocks), smem, st);
-        return launch_norm_kernel(forward_kernel<T, MODE, BRANCH, 1024>, large, p,
-                                  static_cast<int>(blocks), smem, st);
+        static std::atomic<uint64_t> two{0}, small{0}, large{0};
+        const int n = static_cast<int>(blocks);
+        if (s.threads <= kNormThreads) {
+            if constexpr (MODE != kSingle)
+                if (s.rows == 2)
+                    return launch_norm_kernel(forward_kernel<T, MODE, BRANCH, kNormThreads, 2, true>, two, p,
+                                              n, smem, st);
+            return launch_norm_kernel(forward_kernel<T, MODE, BRANCH, kNormThreads, 1, true>, small, p, n,
+                                      smem, st);
+        }
+        return launch_norm_kernel(forward_kernel<T, MODE, BRANCH, 1024, 1, false>, large, p, n, smem, st);
     });
 }
 

@@ -36,7 +36,6 @@
 namespace sb {
 namespace {
 
-constexpr int kSlices = 8;
 __device__ __forceinline__ float weight_at(const void *w, int f32, int i) {
     if (!w) return 1.f;
     return f32 ? one(static_cast<const float *>(w) + i)
@@ -48,8 +47,9 @@ __device__ __forceinline__ void put_at(void *w, int f32, int i, float v) {
     else
         put_one(static_cast<__nv_bfloat16 *>(w) + i, v);
 }
-__global__ void __launch_bounds__(32 * kSlices) columns_kernel(const ColumnParams p) {
-    __shared__ float sh[kSlices][32];
+template <int SLICES>
+__global__ void __launch_bounds__(32 * SLICES) columns_kernel(const ColumnParams p) {
+    __shared__ float sh[SLICES][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(32 * kSlices) columns_kernel(const ColumnParam
     if (col < p.d) {
         const float *src = p.part + static_cast<size_t>(k) * p.d + col;
         const size_t step = static_cast<size_t>(p.sums) * p.d;
-        const int b0 = p.blocks * slice / kSlices, b1 = p.blocks * (slice + 1) / kSlices;
+        const int b0 = p.blocks * slice / SLICES, b1 = p.blocks * (slice + 1) / SLICES;
 #pragma unroll 8
         for (int b = b0; b < b1; ++b) a += src[b * step];
     }
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(32 * kSlices) columns_kernel(const ColumnParam
     __syncthreads();
     if (slice != 0 || col >= p.d) return;
 #pragma unroll
-    for (int s = 1; s < kSlices; ++s) a += sh[s][lane];
+    for (int s = 1; s < SLICES; ++s) a += sh[s][lane];
     if (k == 0) {
         put_at(p.dpre, p.f32, col, a);
     } else {
@@ -93,9 +93,10 @@ int32_t check_norm(const void *h, const void *y, const void *pre, const void *po
 
 }  // namespace
 
-cudaError_t launch_norm_columns(const ColumnParams &p, cudaStream_t st) {
-    return launch_dependent(columns_kernel, dim3(static_cast<unsigned>((p.d + 31) / 32), p.sums),
-                            32 * kSlices, 0, p, st);
+cudaError_t launch_norm_columns(const ColumnParams &p, bool many, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>((p.d + 31) / 32), p.sums);
+    return many ? launch_dependent(columns_kernel<16>, grid, 32 * 16, 0, p, st)
+                : launch_dependent(columns_kernel<8>, grid, 32 * 8, 0, p, st);
 }
 
 }  // namespace sb
@@ -222,7 +223,7 @@ int32_t sb_residual_norm_backward(const void *dx, const void *dh, const void *h,
     c.post = p.post;
     c.gate = p.gate;
     if (launch_norm_backward(p, l.shape, h32, l.blocks, l.smem, st) != cudaSuccess ||
-        launch_norm_columns(c, st) != cudaSuccess)
+        launch_norm_columns(c, false, st) != cudaSuccess)
         return SB_ERR_CUDA;
     return SB_OK;
 }

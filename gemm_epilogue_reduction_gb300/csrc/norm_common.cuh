@@ -275,7 +275,8 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int group, int threads, f
 }
 
 // Column sums of the blocks' partial vectors, in ascending order (columns_kernel in norm.cu): 32
-// columns x 8 slices of the partials per block.  Vector 0 is dpre; vector 1, v, gives dpost = gate·v
+// columns x 8 slices of the partials per block, or 16 slices (`many`: all loads of a thread in flight at
+// once; the order of the sum is another).  Vector 0 is dpre; vector 1, v, gives dpost = gate·v
 // and dgate = post·v, each where it is asked for (factors of 1 where there is no gate or post).
 struct ColumnParams {
     const float *part;
@@ -283,7 +284,7 @@ struct ColumnParams {
     const void *post, *gate;
     void *dpre, *dpost, *dgate;
 };
-cudaError_t launch_norm_columns(const ColumnParams &p, cudaStream_t st);
+cudaError_t launch_norm_columns(const ColumnParams &p, bool many, cudaStream_t st);
 
 // ------------------------------------------------------------------ layout and launch
 inline bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

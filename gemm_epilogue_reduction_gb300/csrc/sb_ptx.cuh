@@ -104,10 +104,6 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *tm, const void *
         "r"(smem_u32(src)), "r"(c0), "r"(c1), "l"(policy)
         : "memory");
 }
-// Starts to bring `bytes` (a multiple of 16, from a 16-byte boundary) into L2.
-__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void bulk_commit() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
