@@ -85,7 +85,7 @@ def _sums(ids, dout, V, scale, ignore=-100):
 
 
 SHAPES = [(1, 1, 1), (1, 5120, 300), (2, 3, 5), (31, 64, 40), (32, 72, 9), (33, 68, 9), (64, 1032, 3),
-          (100, 257, 1000), (500, 640, 100), (1021, 4100, 60), (4097, 96, 2000), (8192, 40, 333),
+          (100, 257, 1000), (500, 640, 100), (1021, 4100, 60), (65, 72, 4), (4097, 4104, 90), (4097, 96, 2000), (8192, 40, 333),
           (8193, 40, 333), (20000, 33, 4000), (30011, 8, 7)]
 
 
