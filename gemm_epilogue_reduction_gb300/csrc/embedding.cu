@@ -19,7 +19,7 @@
 //                  the same launch write its zeros meanwhile (that is most of its bytes: V rows against
 //                  at most M that are not zero).  (Fetching rows into L2 meanwhile did not pay.)
 //   merge_kernel   chunks to one order: the counts of smaller keys in the other chunks by binary search.
-//   reduce_kernel  a block takes a piece of consecutive sorted tokens and a slice of columns, and
+//   reduce_kernel  (up to 64 tokens: sorts them too) a block takes a piece of consecutive sorted tokens and a slice of columns, and
 //                  adds the rows of each run of equal ids in registers; a run inside the piece is
 //                  scaled, added and rounded here.  What a piece holds of a run that crosses its
 //                  ends goes to the workspace in fp32.  So a token that takes most of the batch costs
@@ -274,6 +274,8 @@ constexpr int kAhead = 8;            // rows in flight
 static_assert(kPiece % kAhead == 0 && kLongPiece % kAhead == 0 && kLongPiece + 2 <= kReduceThreads);
 
 struct ReduceParams {
+    const int32_t *ids;  // of one piece at most: every block sorts them itself (null: key and at are given)
+    int V, ignore;
     const uint32_t *key;
     const int *at;
     const void *dout;
@@ -312,15 +314,29 @@ __global__ void __launch_bounds__(kReduceThreads) reduce_kernel(const ReducePara
     // Where join_kernel follows it may get ready (it waits for this kernel's end); else no early
     // launch_dependents: nothing that follows may read dW ahead of that.
     if (p.pieces > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int first = blockIdx.x * p.piece;
-    if (static_cast<int>(threadIdx.x) < p.piece + 2) {
-        const int i = first + static_cast<int>(threadIdx.x) - 1;
+    const int first = blockIdx.x * p.piece, tid = threadIdx.x;
+    if (p.ids) {
+        __shared__ int keys[kLongPiece];
+        if (tid < kLongPiece + 2) token[tid] = make_int2(-1, 0);
+        if (tid < kLongPiece) {
+            const int id = tid < p.M ? p.ids[tid] : -1;
+            keys[tid] = id >= 0 && id < p.V && id != p.ignore ? id : kNoToken;
+        }
+        __syncthreads();
+        if (tid < kLongPiece && keys[tid] != kNoToken) {
+            int rank = 0;
+#pragma unroll 16
+            for (int j = 0; j < kLongPiece; ++j) rank += keys[j] < keys[tid] + (j < tid);
+            token[1 + rank] = make_int2(keys[tid], tid);
+        }
+    } else if (tid < p.piece + 2) {
+        const int i = first + tid - 1;
         int2 t = make_int2(-1, 0);
         if (i >= 0 && i < p.M) {
             t = make_int2(static_cast<int>(p.key[i]), p.at[i]);
             if (t.x == kNoToken) t.x = -1;
         }
-        token[threadIdx.x] = t;
+        token[tid] = t;
     }
     __syncthreads();
     const long long e = (static_cast<long long>(blockIdx.y) * kReduceThreads + threadIdx.x) * VEC;
@@ -567,7 +583,8 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
     s.M = static_cast<int>(M);
     s.V = static_cast<int>(V);
     s.ignore = ignore_index;
-    s.sort_blocks = static_cast<int>((M + kSortTokens - 1) / kSortTokens);
+    const bool few = M <= kLongPiece;  // reduce_kernel sorts them itself
+    s.sort_blocks = few ? 0 : static_cast<int>((M + kSortTokens - 1) / kSortTokens);
     s.key = key[0];
     s.at = at[0];
     if (!add) {
@@ -578,7 +595,8 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
     const size_t zero_blocks = add ? 0 : s.zero_bytes / (kSortThreads * 32) + 1;
     if (zero_blocks > (size_t(1) << 30)) return SB_ERR_INVALID_ARG;
     const dim3 grid(s.sort_blocks + static_cast<unsigned>(zero_blocks));
-    if ((V < 1 << 24 ? launch_dependent(sort_kernel<true>, grid, kSortThreads, 0, s, st)
+    if (grid.x > 0 &&
+        (V < 1 << 24 ? launch_dependent(sort_kernel<true>, grid, kSortThreads, 0, s, st)
                       : launch_dependent(sort_kernel<false>, grid, kSortThreads, 0, s, st)) != cudaSuccess)
         return SB_ERR_CUDA;
     if (M == 0) return SB_OK;
@@ -590,6 +608,9 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
         now = 1;
     }
     ReduceParams r{};
+    r.ids = few ? ids : nullptr;
+    r.V = static_cast<int>(V);
+    r.ignore = ignore_index;
     r.key = key[now];
     r.at = at[now];
     r.dout = dout;

@@ -36,10 +36,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLseThreads = 256;
 constexpr int kLseBlocks = 152 * 4;    // as many as fit at a time
 constexpr int kAhead = 4;               // 16-byte vectors of a thread in flight
-constexpr int kBlocks = 8;              // of a request's cluster
-constexpr int kWideBlocks = 16;         // the same for few requests, where the device allows it
-constexpr int kWideRequests = 9;        // 9 x 16 blocks: one to an SM
-constexpr int kFewRequests = 38;        // 38 x 8 blocks of 512 threads: two to an SM; more: of 256
+constexpr int kVerifyThreads = 512;
+// Blocks of a request's cluster: as many as leave all blocks on the GPU at a time, two to an SM (64
+// requests: 4 blocks 62 us, 8 in two turns 71, 8 of 256 threads 64); 16 where they have an SM each and
+// the device allows such clusters.
+constexpr int kWideBlocks = 16, kMostBlocks = 8, kLeastBlocks = 2;
 
 struct VerifyParams {
     const void *z, *q;
@@ -343,7 +344,7 @@ struct Scan {
 };
 
 // This thread's best of the share of block `rank` of `blocks`.
-template <typename T, int FROM, int THREADS>
+template <typename T, int FROM>
 __device__ __forceinline__ unsigned long long scan(const VerifyParams &p, const T *z, const T *q,
                                                    double lse, double qlse, int x,
                                                    unsigned long long first, int rank, int blocks) {
@@ -358,8 +359,8 @@ __device__ __forceinline__ unsigned long long scan(const VerifyParams &p, const 
             a = za.vec[za.v0 + tid];
             if (FROM == kDifference) b = qa[za.v0 + tid];
         }
-        for (int i0 = za.v0; i0 < za.v1; i0 += THREADS) {  // (the same turns for all threads)
-            const int i = i0 + tid, next = i + THREADS;
+        for (int i0 = za.v0; i0 < za.v1; i0 += kVerifyThreads) {  // (the same turns for all threads)
+            const int i = i0 + tid, next = i + kVerifyThreads;
             float2 pa[E / 2], pb[E / 2];
             unpack(a, pa, T{});
             unpack(b, pb, T{});
@@ -380,24 +381,24 @@ __device__ __forceinline__ unsigned long long scan(const VerifyParams &p, const 
         constexpr int W = 8;
         const int c0 = static_cast<int>(static_cast<long long>(p.V) * rank / blocks);
         const int c1 = static_cast<int>(static_cast<long long>(p.V) * (rank + 1) / blocks);
-        for (int j0 = c0; j0 < c1; j0 += W * THREADS) {
+        for (int j0 = c0; j0 < c1; j0 += W * kVerifyThreads) {
             const int j = j0 + tid;
             float a[W], b[W];
 #pragma unroll
             for (int k = 0; k < W; ++k) {
-                const int i = min(j + k * THREADS, c1 - 1);
+                const int i = min(j + k * kVerifyThreads, c1 - 1);
                 a[k] = one(z + i);
                 b[k] = one(q + i);
             }
-            s.template columns<W, THREADS>(a, b, j, max(0, (c1 - j + THREADS - 1) / THREADS));
+            s.template columns<W, kVerifyThreads>(a, b, j, max(0, (c1 - j + kVerifyThreads - 1) / kVerifyThreads));
         }
     }
     return pack(s.best, s.column);
 }
 
-template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const VerifyParams p) {
-    constexpr int WARPS = THREADS / 32;
+template <typename T>
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyParams p) {
+    constexpr int THREADS = kVerifyThreads, WARPS = THREADS / 32;
     __shared__ int end, busy;
     __shared__ double lses[WARPS], qlses[WARPS];
     __shared__ unsigned long long bests[2][kWideBlocks], warps[WARPS];
@@ -479,12 +480,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const V
     for (int turn = 0; turn < 2 && !best; ++turn) {
         // a difference that is nowhere positive (p and q equal but for roundings): p itself
         if (turn == 0 && known && q)
-            best = scan<T, kDifference, THREADS>(p, z, q + static_cast<size_t>(e) * p.V, lse, qlse, x, first,
+            best = scan<T, kDifference>(p, z, q + static_cast<size_t>(e) * p.V, lse, qlse, x, first,
                                                  rank, blocks);
         else if (turn == 0 && known)
-            best = scan<T, kWithout, THREADS>(p, z, nullptr, lse, 0.0, x, first, rank, blocks);
+            best = scan<T, kWithout>(p, z, nullptr, lse, 0.0, x, first, rank, blocks);
         else
-            best = scan<T, kTarget, THREADS>(p, z, nullptr, lse, 0.0, x, first, rank, blocks);
+            best = scan<T, kTarget>(p, z, nullptr, lse, 0.0, x, first, rank, blocks);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const unsigned long long other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
@@ -551,12 +552,16 @@ __global__ void __launch_bounds__(128) greedy_kernel(const GreedyParams p) {
     if (lane == 0) p.accepted[b] = n ? e : 0;
 }
 
-template <typename T, int THREADS>
-cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
+template <typename T>
+cudaError_t launch_verify(const VerifyParams &p, int sms, cudaStream_t st) {
+    if (p.zrows + p.qrows > 0 && p.B > 0) {
+        const cudaError_t e = launch_dependent(lse_kernel<T>, dim3(kLseBlocks), kLseThreads, 0, p, st);
+        if (e != cudaSuccess) return e;
+    }
     auto config = [&](int blocks, cudaLaunchAttribute (&attr)[2]) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(static_cast<unsigned>(p.B > 0 ? p.B : 1) * blocks);
-        cfg.blockDim = dim3(THREADS);
+        cfg.blockDim = dim3(kVerifyThreads);
         cfg.stream = st;
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = blocks;
@@ -568,8 +573,9 @@ cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
         return cfg;
     };
     cudaLaunchAttribute attr[2];
-    int blocks = kBlocks;
-    if (p.B <= kWideRequests) {
+    int blocks = kMostBlocks;
+    while (blocks > kLeastBlocks && static_cast<int64_t>(p.B) * blocks > 2 * sms) blocks /= 2;
+    if (p.B * kWideBlocks <= sms) {
         // more than eight blocks to a cluster are no part of the portable model: asked once a device
         static std::atomic<uint64_t> asked{0}, allowed{0};
         int dev = 0;
@@ -580,8 +586,8 @@ cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
             int clusters = 0;
             cudaLaunchConfig_t cfg = config(kWideBlocks, attr);
             cfg.numAttrs = 1;
-            e = cudaFuncSetAttribute(verify_kernel<T, THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, verify_kernel<T, THREADS>, &cfg);
+            e = cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, verify_kernel<T>, &cfg);
             if (e == cudaSuccess && clusters > 0) allowed.fetch_or(bit);
             if (e != cudaSuccess) cudaGetLastError();  // a refusal is an answer here
             asked.fetch_or(bit);
@@ -589,15 +595,7 @@ cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
         if (allowed.load() & bit) blocks = kWideBlocks;
     }
     const cudaLaunchConfig_t cfg = config(blocks, attr);
-    return cudaLaunchKernelEx(&cfg, verify_kernel<T, THREADS>, p);
-}
-template <typename T>
-cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
-    if (p.zrows + p.qrows > 0 && p.B > 0) {
-        const cudaError_t e = launch_dependent(lse_kernel<T>, dim3(kLseBlocks), kLseThreads, 0, p, st);
-        if (e != cudaSuccess) return e;
-    }
-    return p.B <= kFewRequests ? launch_verify<T, 512>(p, st) : launch_verify<T, 256>(p, st);
+    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, p);
 }
 
 bool verify_sizes(int64_t R, int64_t draft_rows, int64_t V) {
@@ -635,7 +633,8 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
         !on(uniforms, 4) || !on(lse, 4) || !on(draft_lse, 4) || !on(token, 4) || !on(accepted, 4) ||
         !on(token_logprob, 4) || !on(workspace, 256))
         return SB_ERR_ALIGNMENT;
-    if (int32_t e = device_sms_cc(nullptr, nullptr)) return e;
+    int sms = 0;
+    if (int32_t e = device_sms_cc(&sms, nullptr)) return e;
     if (workspace_bytes < sb_verify_workspace_bytes(R, draft_rows, V)) return SB_ERR_WORKSPACE_TOO_SMALL;
     if (R == 0 && B == 0) return SB_OK;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -664,7 +663,7 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
     p.status = reinterpret_cast<unsigned long long *>(ws + 8);
     p.epoch = next_epoch();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return (logits_type == SB_BF16 ? launch_verify<__nv_bfloat16>(p, st) : launch_verify<float>(p, st)) ==
+    return (logits_type == SB_BF16 ? launch_verify<__nv_bfloat16>(p, sms, st) : launch_verify<float>(p, sms, st)) ==
                    cudaSuccess
                ? SB_OK
                : SB_ERR_CUDA;

@@ -139,6 +139,15 @@ def test_against_the_definition(lengths, V, kind, draft):
 
 
 @gpu
+@pytest.mark.parametrize("B", [9, 10, 38, 39, 76, 77, 152, 153, 400])
+@pytest.mark.parametrize("draft", [True, False])
+def test_many_requests(B, draft):
+    """Each number of blocks to a request, and more requests than fit the GPU at a time."""
+    s = _make([(5 * b) % 4 for b in range(B)], 1003, draft=draft, seed=B)
+    _check(s, seed=B)
+
+
+@gpu
 @pytest.mark.parametrize("V", [50257, 151936, 200064])
 @pytest.mark.parametrize("kind", [BF, F32])
 @pytest.mark.parametrize("draft,T", [(True, 0.7), (False, 1.3), (True, 1.0)])
