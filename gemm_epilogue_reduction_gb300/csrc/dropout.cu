@@ -101,6 +101,10 @@ extern "C" int32_t sb_dropout(const void *x, const void *residual, int64_t n, in
     const uintptr_t xa = x_type == SB_F32 ? 4 : 2, oa = out_type == SB_F32 ? 4 : 2;
     if (!on(x, xa) || !on(residual, oa) || !on(out, oa) || !on(seed_offset, 8))
         return SB_ERR_ALIGNMENT;
+    const size_t ob = n * oa;
+    if ((x_type == out_type ? overlap_partly(out, ob, x, n * xa) : overlap(out, ob, x, n * xa)) ||
+        overlap_partly(out, ob, residual, ob) || overlap(out, ob, seed_offset, 8))
+        return SB_ERR_INVALID_ARG;
     if (int32_t e = device_sms_cc(nullptr, nullptr)) return e;
     if (n == 0) return SB_OK;
     DropoutParams d{};

@@ -18,7 +18,8 @@
 //                  kernel took 15).  When the whole gradient is asked for, further blocks of
 //                  the same launch write its zeros meanwhile (that is most of its bytes: V rows against
 //                  at most M that are not zero).  (Fetching rows into L2 meanwhile did not pay.)
-//   merge_kernel   chunks to one order: the counts of smaller keys in the other chunks by binary search.
+//   merge_kernel   eight chunks, or merged ones, to one: the counts of smaller keys in the others by binary
+//                  search.
 //   reduce_kernel  (up to 64 tokens: sorts them too) a block takes a piece of consecutive sorted tokens and a slice of columns, and
 //                  adds the rows of each run of equal ids in registers; a run inside the piece is
 //                  scaled, added and rounded here.  What a piece holds of a run that crosses its
@@ -115,6 +116,7 @@ struct SortParams {
     const int32_t *ids;
     int M, V, ignore;
     int sort_blocks;
+    int last;          // no kernel of this call follows
     uint32_t *key;     // sorted within each chunk
     int *at;           // their positions
     uint8_t *zero;     // bytes to clear (null: none)
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
     __shared__ __align__(16) uint32_t keys[kChunk];
     __shared__ int counts[WARPS][kSortTokens];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!p.last) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (static_cast<int>(blockIdx.x) >= p.sort_blocks) {
         clear_share(p.zero, p.zero_bytes, blockIdx.x - p.sort_blocks);
         return;
@@ -229,16 +231,18 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
     }
 }
 
-// The chunks' orders become one: a token's place is its place in its own chunk and the counts of smaller
-// keys (of keys not larger, in earlier chunks) in the others.
+// Sorted runs become runs of kFan times their length: a token's place is its place in its own run and the
+// counts of smaller keys (of keys not larger, in earlier runs) in the others.
 struct MergeParams {
     const uint32_t *key;
     const int *at;
     uint32_t *to_key;
     int *to_at;
     int M;
+    long long run;
 };
 constexpr int kMergeThreads = 256;
+constexpr int kFan = 8;
 
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -246,15 +250,17 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
     const long long i = static_cast<long long>(blockIdx.x) * kMergeThreads + threadIdx.x;
     if (i >= p.M) return;
     const uint32_t key = p.key[i];
-    const int chunks = (p.M + kChunk - 1) / kChunk, own = static_cast<int>(i / kChunk);
-    int place = static_cast<int>(i - static_cast<long long>(own) * kChunk);
-#pragma unroll 4
-    for (int c = 0; c < chunks; ++c) {
-        const uint32_t *k = p.key + static_cast<size_t>(c) * kChunk;
+    const long long base = i / (kFan * p.run) * (kFan * p.run);
+    const int own = static_cast<int>((i - base) / p.run);
+    long long place = i - own * p.run;
+#pragma unroll
+    for (int c = 0; c < kFan; ++c) {
+        const long long from = base + c * p.run;
+        const uint32_t *k = p.key + from;
         const uint32_t limit = key + (c < own);
-        int lo = 0, hi = c == own ? 0 : min(kChunk, p.M - c * kChunk);
+        long long lo = 0, hi = c == own ? 0 : max(0LL, min(p.run, p.M - from));
         while (lo < hi) {
-            const int mid = (lo + hi) / 2;
+            const long long mid = (lo + hi) / 2;
             if (k[mid] < limit)
                 lo = mid + 1;
             else
@@ -525,6 +531,9 @@ int32_t sb_embedding_forward(const int32_t *ids, const void *W, int64_t M, int64
     if (!W || (M > 0 && !out)) return SB_ERR_INVALID_ARG;
     if (!on(W, weight_type == SB_F32 ? 4 : 2) || !on(out, out_type == SB_F32 ? 4 : 2))
         return SB_ERR_ALIGNMENT;
+    const size_t ws = weight_type == SB_F32 ? 4 : 2, os = out_type == SB_F32 ? 4 : 2;
+    if (overlap(out, M * d * os, W, V * d * ws) || overlap(out, M * d * os, ids, M * 4))
+        return SB_ERR_INVALID_ARG;
     if (int32_t e = device_sms_cc(nullptr, nullptr)) return e;
     if (M == 0) return SB_OK;
     LookupParams p{};
@@ -565,6 +574,12 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
     if (!on(dout, grad_type == SB_F32 ? 4 : 2) || !on(dW, weight_type == SB_F32 ? 4 : 2) ||
         !on(workspace, 256))
         return SB_ERR_ALIGNMENT;
+    const size_t dw_bytes = V * d * (weight_type == SB_F32 ? 4 : 2);
+    const size_t dout_bytes = M * d * (grad_type == SB_F32 ? 4 : 2);
+    if (overlap(dW, dw_bytes, dout, dout_bytes) || overlap(dW, dw_bytes, ids, M * 4) ||
+        overlap(workspace, workspace_bytes, dW, dw_bytes) ||
+        overlap(workspace, workspace_bytes, dout, dout_bytes))
+        return SB_ERR_INVALID_ARG;
     if (int32_t e = device_sms_cc(nullptr, nullptr)) return e;
     if (workspace_bytes < sb_embedding_backward_workspace_bytes(M, d)) return SB_ERR_WORKSPACE_TOO_SMALL;
     if (M == 0 && add) return SB_OK;
@@ -585,6 +600,7 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
     s.ignore = ignore_index;
     const bool few = M <= kLongPiece;  // reduce_kernel sorts them itself
     s.sort_blocks = few ? 0 : static_cast<int>((M + kSortTokens - 1) / kSortTokens);
+    s.last = M == 0;
     s.key = key[0];
     s.at = at[0];
     if (!add) {
@@ -600,12 +616,11 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
                       : launch_dependent(sort_kernel<false>, grid, kSortThreads, 0, s, st)) != cudaSuccess)
         return SB_ERR_CUDA;
     if (M == 0) return SB_OK;
-    if (M > kChunk) {
-        const MergeParams m{key[0], at[0], key[1], at[1], static_cast<int>(M)};
+    for (int64_t run = kChunk; run < M; run *= kFan, now = 1 - now) {
+        const MergeParams m{key[now], at[now], key[1 - now], at[1 - now], static_cast<int>(M), run};
         if (launch_dependent(merge_kernel, dim3(static_cast<unsigned>((M + kMergeThreads - 1) / kMergeThreads)),
                              kMergeThreads, 0, m, st) != cudaSuccess)
             return SB_ERR_CUDA;
-        now = 1;
     }
     ReduceParams r{};
     r.ids = few ? ids : nullptr;

@@ -288,6 +288,15 @@ cudaError_t launch_norm_columns(const ColumnParams &p, bool many, cudaStream_t s
 
 // ------------------------------------------------------------------ layout and launch
 inline bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// Whether two arrays share memory (null: there is none).
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x && y && x < y + nb && y < x + na;
+}
+// The same, but that `a` may be `b` itself.
+inline bool overlap_partly(const void *a, size_t na, const void *b, size_t nb) {
+    return a != b && overlap(a, na, b, nb);
+}
 inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // The widest vector that d and every address allow: 8, 4 or 1 values.

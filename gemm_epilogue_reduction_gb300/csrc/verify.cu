@@ -50,6 +50,7 @@ struct VerifyParams {
     int zrows, qrows;   // of them, how many lse_kernel reduces (those behind the last request aside)
     int with_q;         // drafts have distributions of their own
     float inv_t;
+    double t;           // 1 / inv_t
     unsigned long long seed;
     int32_t *token, *accepted;
     float *logprob;
@@ -286,53 +287,61 @@ template <typename T, int FROM>
 struct Scan {
     const VerifyParams &p;
     const T *z, *q;
-    // log2 p = z·c - l2; q likewise, but for the factor k that takes back what the roundings of both l2
-    // have changed of p / q
-    float c, l2, ql2, k;
+    // log2 p = (z - lse·T)·c: what is subtracted is in two parts, so that columns near the largest keep
+    // their precision whatever T is (fp32 products would be off by 2^-24 of z / T)
+    float c, ref, rest, qref, qrest;
     int x;
     unsigned long long first;  // index of the row's first draw
     float best, bar;
     int column;
     static constexpr float kUpper = 0.69314860f * 16777216.f;
 
-    __device__ __forceinline__ Scan(const VerifyParams &p_, const T *z_, const T *q_, double lse, double qlse,
-                                    int x_, unsigned long long first_)
-        : p(p_), z(z_), q(q_), x(x_), first(first_), best(0.f), bar(0.f), column(0) {
-        constexpr double kLog2eWide = 1.4426950408889634;
-        c = p.inv_t * kLog2e;
-        l2 = static_cast<float>(lse * kLog2eWide);
-        ql2 = static_cast<float>(qlse * kLog2eWide);
-        k = ex2_approx(static_cast<float>((ql2 - qlse * kLog2eWide) - (l2 - lse * kLog2eWide)));
-    }
-    __device__ __forceinline__ float weight(float2 v, int j) const {  // v: logits of the target and the draft
-        float w = ex2_approx(fmaf(v.x, c, -l2));
-        if (FROM == kDifference) w = fmaf(-k, ex2_approx(fmaf(v.y, c, -ql2)), w);
-        if (FROM == kWithout && j == x) w = 0.f;
+    __device__ __forceinline__ Scan(const VerifyParams &p_, const T *z_, const T *q_, float4 refs, int x_,
+                                    unsigned long long first_)
+        : p(p_), z(z_), q(q_), c(p_.inv_t * kLog2e), ref(refs.x), rest(-refs.y * c), qref(refs.z),
+          qrest(-refs.w * c), x(x_), first(first_), best(0.f), bar(0.f), column(0) {}
+    // Of two columns, j and j + step; v, u: their logits, the target's and the draft's.
+    __device__ __forceinline__ float2 weights(float2 v, float2 u, int j, int step) const {
+        const float2 y = __ffma2_rn(__fadd2_rn(v, both(-ref)), both(c), both(rest));
+        float2 w = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+        if (FROM == kDifference) {
+            const float2 n = __ffma2_rn(__fadd2_rn(u, both(-qref)), both(c), both(qrest));
+            w = make_float2(w.x - ex2_approx(n.x), w.y - ex2_approx(n.y));
+        }
+        if (FROM == kWithout) {
+            if (j == x) w.x = 0.f;
+            if (j + step == x) w.y = 0.f;
+        }
         return w;
     }
     __device__ __forceinline__ void exact(int j) {
         const uint32_t bits = bits24_from_state(splitmix_state(p.seed, first + j));
-        const float2 v = make_float2(one(z + j), FROM == kDifference ? one(q + j) : 0.f);
-        const float score = bits ? weight(v, j) / -log2_uniform(bits) : 0.f;
+        const float2 w = weights(both(one(z + j)), both(FROM == kDifference ? one(q + j) : 0.f), j, 1);
+        const float score = bits ? w.x / -log2_uniform(bits) : 0.f;
         // columns come in any order: of equal scores the lowest stays
         if (score > best || (score == best && j < column)) best = score, column = j;
     }
     // N columns of each thread of the warp, with their logits: j, j + STEP, ...; `have` of them count.
     template <int N, int STEP>
-    __device__ __forceinline__ void columns(const float (&a)[N], const float (&b)[N], int j, int have) {
+    __device__ __forceinline__ void columns(const float2 (&a)[N / 2], const float2 (&b)[N / 2], int j,
+                                            int have) {
         float bound[N], low = 0.f;
         const float all = have >= N ? kUpper : 0.f;  // (`have` is N or 0 but where columns are STEP apart)
         const unsigned long long state = splitmix_state(p.seed, first + j);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float w = weight(make_float2(a[i], b[i]), j + i * STEP);
-            const uint32_t bits = bits24_from_state(state + static_cast<unsigned long long>(i * STEP) * kGolden);
-            // With l = 1 - u:  l <= -ln u <= l / (1 - l), so the score w / -log2 u lies between
-            // w·ln 2 / l and that times 1 - l.  The constants leave room for the roundings of both and
-            // of the score itself (2e-6 and 4e-6 against some 1e-6); l is counted in 2^-24.
-            const float l = static_cast<float>(16777216u - bits);
-            bound[i] = w * (STEP == 1 ? all : i < have ? kUpper : 0.f) * rcp_approx(l);
-            low = fmaxf(low, bound[i] * fmaf(l, -0.999994f * 5.9604644775390625e-8f, 0.999994f));
+        for (int i = 0; i < N; i += 2) {
+            const float2 pair = weights(a[i / 2], b[i / 2], j + i * STEP, STEP);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t bits =
+                    bits24_from_state(state + static_cast<unsigned long long>((i + h) * STEP) * kGolden);
+                // With l = 1 - u:  l <= -ln u <= l / (1 - l), so the score w / -log2 u lies between
+                // w·ln 2 / l and that times 1 - l.  The constants leave room for the roundings of both and
+                // of the score itself (2e-6 and 4e-6 against some 1e-6); l is counted in 2^-24.
+                const float l = static_cast<float>(16777216u - bits), w = h ? pair.y : pair.x;
+                bound[i + h] = w * (STEP == 1 ? all : i + h < have ? kUpper : 0.f) * rcp_approx(l);
+                low = fmaxf(low, bound[i + h] * fmaf(l, -0.999994f * 5.9604644775390625e-8f, 0.999994f));
+            }
         }
         const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(low));  // (low >= 0)
         bar = fmaxf(bar, __uint_as_float(most));
@@ -346,11 +355,11 @@ struct Scan {
 // This thread's best of the share of block `rank` of `blocks`.
 template <typename T, int FROM>
 __device__ __forceinline__ unsigned long long scan(const VerifyParams &p, const T *z, const T *q,
-                                                   double lse, double qlse, int x,
-                                                   unsigned long long first, int rank, int blocks) {
+                                                   float4 refs, int x, unsigned long long first,
+                                                   int rank, int blocks) {
     constexpr int E = Share<T>::E;
     const int tid = threadIdx.x;
-    Scan<T, FROM> s(p, z, q, lse, qlse, x, first);
+    Scan<T, FROM> s(p, z, q, refs, x, first);
     if (FROM != kDifference || ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0) {
         const Share<T> za(z, p.V, rank, blocks);
         const uint4 *qa = FROM == kDifference ? reinterpret_cast<const uint4 *>(q + za.head) : nullptr;
@@ -368,11 +377,7 @@ __device__ __forceinline__ unsigned long long scan(const VerifyParams &p, const 
                 a = za.vec[next];
                 if (FROM == kDifference) b = qa[next];
             }
-            float va[E], vb[E];
-#pragma unroll
-            for (int j = 0; j < E / 2; ++j)
-                va[2 * j] = pa[j].x, va[2 * j + 1] = pa[j].y, vb[2 * j] = pb[j].x, vb[2 * j + 1] = pb[j].y;
-            s.template columns<E, 1>(va, vb, za.head + i * E, i < za.v1 ? E : 0);
+            s.template columns<E, 1>(pa, pb, za.head + i * E, i < za.v1 ? E : 0);
         }
         if (rank == 0 && tid < za.head) s.exact(tid);
         if (rank == blocks - 1 && tid < p.V - za.tail) s.exact(za.tail + tid);
@@ -383,12 +388,12 @@ __device__ __forceinline__ unsigned long long scan(const VerifyParams &p, const 
         const int c1 = static_cast<int>(static_cast<long long>(p.V) * (rank + 1) / blocks);
         for (int j0 = c0; j0 < c1; j0 += W * kVerifyThreads) {
             const int j = j0 + tid;
-            float a[W], b[W];
+            float2 a[W / 2], b[W / 2];
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-                const int i = min(j + k * kVerifyThreads, c1 - 1);
-                a[k] = one(z + i);
-                b[k] = one(q + i);
+            for (int k = 0; k < W; k += 2) {
+                const int i = min(j + k * kVerifyThreads, c1 - 1), n = min(i + kVerifyThreads, c1 - 1);
+                a[k / 2] = make_float2(one(z + i), one(z + n));
+                b[k / 2] = make_float2(one(q + i), one(q + n));
             }
             s.template columns<W, kVerifyThreads>(a, b, j, max(0, (c1 - j + kVerifyThreads - 1) / kVerifyThreads));
         }
@@ -400,7 +405,8 @@ template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyParams p) {
     constexpr int THREADS = kVerifyThreads, WARPS = THREADS / 32;
     __shared__ int end, busy;
-    __shared__ double lses[WARPS], qlses[WARPS];
+    __shared__ double lses[WARPS];
+    __shared__ float4 refs[WARPS];  // lse·T and the draft's, in two parts each
     __shared__ unsigned long long bests[2][kWideBlocks], warps[WARPS];
     const int blocks = static_cast<int>(cluster_blocks()), rank = static_cast<int>(cluster_ctarank());
     const int b = static_cast<int>(blockIdx.x) / blocks;
@@ -452,11 +458,13 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
             const double lse = row_lse<T>(p, pieces, false, r, lane);
             const double qlse = has && q ? row_lse<T>(p, pieces, true, q0 + i, lane) : 0.0;
             if (lane == 0) {
+                const double t = lse * p.t, qt = qlse * p.t;
+                const float hi = static_cast<float>(t), qhi = static_cast<float>(qt);
                 lses[warp] = lse;
-                qlses[warp] = qlse;
+                refs[warp] = make_float4(hi, static_cast<float>(t - hi), qhi, static_cast<float>(qt - qhi));
                 if (has) {
-                    const double l = static_cast<double>(zx * p.inv_t) - lse;
-                    const double m = q ? static_cast<double>(qx * p.inv_t) - qlse : 0.0;
+                    const double l = static_cast<double>(zx) * p.inv_t - lse;
+                    const double m = q ? static_cast<double>(qx) * p.inv_t - qlse : 0.0;
                     if (!known && rank == 0) record_status(p.status, p.epoch, 1u);
                     if (!known || !exp_above(l - m, u)) atomicMin(&end, i);
                     if (rank == 0) {  // (of a row behind the end it is taken back below)
@@ -471,7 +479,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
         __syncthreads();             // before the next rows' are written
     }
     const int e = end, r = s0 + e;
-    const double lse = lses[e - g], qlse = qlses[e - g];
+    const double lse = lses[e - g];
+    const float4 ref = refs[e - g];
     z += static_cast<size_t>(e) * p.V;
     const int x = e < n ? p.drafts[r] : -1;
     const bool known = x >= 0 && x < p.V;  // otherwise nothing is taken off p
@@ -480,12 +489,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
     for (int turn = 0; turn < 2 && !best; ++turn) {
         // a difference that is nowhere positive (p and q equal but for roundings): p itself
         if (turn == 0 && known && q)
-            best = scan<T, kDifference>(p, z, q + static_cast<size_t>(e) * p.V, lse, qlse, x, first,
-                                                 rank, blocks);
+            best = scan<T, kDifference>(p, z, q + static_cast<size_t>(e) * p.V, ref, x, first, rank, blocks);
         else if (turn == 0 && known)
-            best = scan<T, kWithout>(p, z, nullptr, lse, 0.0, x, first, rank, blocks);
+            best = scan<T, kWithout>(p, z, nullptr, ref, x, first, rank, blocks);
         else
-            best = scan<T, kTarget>(p, z, nullptr, lse, 0.0, x, first, rank, blocks);
+            best = scan<T, kTarget>(p, z, nullptr, ref, x, first, rank, blocks);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const unsigned long long other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
@@ -512,7 +520,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
             lp = __uint_as_float(0x7FC00000u);  // no column of the row has any probability
             if (best) {
                 token = ~static_cast<int>(static_cast<uint32_t>(best));
-                lp = static_cast<float>(static_cast<double>(one(z + token) * p.inv_t) - lse);
+                lp = static_cast<float>(static_cast<double>(one(z + token)) * p.inv_t - lse);
             }
         }
         p.token[s0 + i] = token;
@@ -625,7 +633,7 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
     if (!verify_sizes(R, draft_rows, V) || B < 0 || B > (int64_t(1) << 24) ||
         logits_type < SB_BF16 || logits_type > SB_F32 ||
         !(std::isfinite(temperature) && temperature > 0.f) ||
-        !std::isfinite(1.f / temperature) || (R > 0 && (!logits || !drafts || !uniforms || !token)) ||
+        temperature < 1e-30f || (R > 0 && (!logits || !drafts || !uniforms || !token)) ||
         (B > 0 && (!starts || !accepted)) || (draft_rows > 0 && !draft_logits) || !workspace)
         return SB_ERR_INVALID_ARG;
     const uintptr_t za = logits_type == SB_F32 ? 4 : 2;
@@ -655,6 +663,7 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
     p.qrows = draft_lse ? 0 : p.Rd;
     p.part = reinterpret_cast<float2 *>(ws + 256);
     p.inv_t = 1.0f / temperature;
+    p.t = 1.0 / p.inv_t;
     p.seed = seed;
     p.token = token;
     p.accepted = accepted;

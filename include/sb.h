@@ -599,7 +599,7 @@ int32_t sb_adamw_step(const sb_adamw_tensor *tensors, int64_t count, double lr, 
  *               aligned arrays with d a multiple of 8 (or 4) are read in wide loads, others value by
  *               value.
  *   scale       finite.
- *   out         device [M, d] of out_type, rounded once.
+ *   out         device [M, d] of out_type, rounded once; not over W's or ids' memory.
  * One kernel on `stream`; no workspace.
  */
 int32_t sb_embedding_forward(const int32_t *ids, const void *W, int64_t M, int64_t d, int64_t V,
@@ -616,10 +616,10 @@ size_t sb_embedding_backward_workspace_bytes(int64_t M, int64_t d);
  *   add = 1:  dW = dW + S in the rows that a token has, rounded once; the others are not touched.
  *             That is how a tied embedding's gradient joins the head's (sb_cross_entropy_backward).
  *   dout        device [M, d] of grad_type (an sb_type).
- *   dW          device [V, d] of weight_type.
+ *   dW          device [V, d] of weight_type; not over dout's memory.
  *   workspace   device, 256-byte aligned, >= sb_embedding_backward_workspace_bytes(M, d); no
  *               initialisation.
- * Up to four kernels on `stream`.
+ * Up to four kernels on `stream` (one more for every factor of 8 that M is above 65,536).
  */
 int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, int64_t d, int64_t V,
                               int32_t ignore_index, float scale, int32_t grad_type,
@@ -639,7 +639,8 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
  *   p           0 <= p <= 1; p = 1 drops everything.
  *   seed_offset device uint64 [1], added to seed when the kernel runs (a step counter, so that the
  *               replays of a captured call differ), or NULL: 0.
- *   out         device [n] of out_type; may be x (of the same type) or residual.
+ *   out         device [n] of out_type; may be x (of the same type) or residual, but not lie over a part
+ *               of them.
  * One kernel on `stream`.
  */
 int32_t sb_dropout(const void *x, const void *residual, int64_t n, int32_t x_type, int32_t out_type,
@@ -654,11 +655,12 @@ int32_t sb_dropout(const void *x, const void *residual, int64_t n, int32_t x_typ
  *   h           device [M, d] of stream_type (an sb_type): the residual stream.
  *   y           device bf16 [M, d]: the block's output, or NULL: h_out is h and is not written.
  *   weight, bias  device [d] of weight_type (an sb_type); bias may be NULL.
- *   M, d, eps, alignment   as for sb_residual_norm_forward (with one value to a row, x is bias).
+ *   M, d, eps, alignment   as for sb_residual_norm_forward (with one value to a row x is bias; a row of
+ *               equal values with eps = 0 gives NaN).
  *   p, seed, seed_offset   as for sb_dropout; without y not used.
  *   h_out       device [M, d] of stream_type; may be h itself.
  *   x           device bf16 [M, d]; may be y itself.  Formed from h_out before its rounding.
- * One kernel on `stream`; no workspace.
+ * No other output may share memory with an input.  One kernel on `stream`; no workspace.
  */
 int32_t sb_layer_norm_forward(const void *h, const void *y, const void *weight, const void *bias,
                               int64_t M, int64_t d, int32_t stream_type, int32_t weight_type,
@@ -680,7 +682,8 @@ size_t sb_layer_norm_workspace_bytes(int64_t M, int64_t d);
  *   dweight, dbias  device [d] of weight_type (dbias or NULL), summed over the rows in fp32 in a
  *               fixed order: equal calls give equal bits.
  *   workspace   device, 16-byte aligned, >= sb_layer_norm_workspace_bytes(M, d); no initialisation.
- * Two kernels on `stream`.  M = 0 writes zeros to dweight and dbias.
+ * No other output may share memory with an input.  Two kernels on `stream`.  M = 0 writes zeros to
+ * dweight and dbias.
  */
 int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, const void *weight,
                                int64_t M, int64_t d, int32_t stream_type, int32_t weight_type,
@@ -715,7 +718,7 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
  *   lse, draft_lse  device float [R] and [draft_rows]: the rows' logsumexp of logits / T where the
  *               caller has it (T = 1: that of sb_lmhead_project), each or NULL: formed here.
  *   R, B, V     R, draft_rows < 2^24; B <= 2^24; 1 <= V < 2^31 - 65536.
- *   temperature finite, > 0; 1 / T is rounded to fp32 and has to be finite.
+ *   temperature finite, >= 1e-30; 1 / T is rounded to fp32.
  *   token       device int32 [R]: from starts[b] on the drafts that stay and the sample behind them,
  *               and -1 in all other rows, those behind the last request among them.
  *   accepted    device int32 [B]: how many drafts of the request stay.

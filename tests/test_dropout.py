@@ -178,3 +178,8 @@ def test_c_refusals():
         assert call(**kw) == sb.SB_ERR_INVALID_ARG, kw
     for kw in ({"x": P + 1}, {"x": P + 2, "xt": 1}, {"res": P + 1}, {"out": P + 2, "ot": 1}, {"off": P + 4}):
         assert call(**kw) == sb.SB_ERR_ALIGNMENT, kw
+    # out over a part of x (4 bf16 or fp32 values) or of the residual, or over x of another type
+    far = P + 4096
+    for kw in ({"out": P + 4, "res": far}, {"x": far, "out": P + 2}, {"ot": 1, "out": P, "res": far},
+               {"xt": 1, "out": P + 12, "res": far}):
+        assert call(**{"off": 2 * far, **kw}) == sb.SB_ERR_INVALID_ARG, kw

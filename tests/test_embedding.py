@@ -86,7 +86,8 @@ def _sums(ids, dout, V, scale, ignore=-100):
 
 SHAPES = [(1, 1, 1), (1, 5120, 300), (2, 3, 5), (31, 64, 40), (32, 72, 9), (33, 68, 9), (64, 1032, 3),
           (100, 257, 1000), (500, 640, 100), (1021, 4100, 60), (65, 72, 4), (4097, 4104, 90), (4097, 96, 2000), (8192, 40, 333),
-          (8193, 40, 333), (20000, 33, 4000), (30011, 8, 7)]
+          (8193, 40, 333), (20000, 33, 4000), (30011, 8, 7),
+          (70001, 8, 500)]
 
 
 @gpu
@@ -294,6 +295,12 @@ def test_c_refusals():
     for kw in ({"dout": P + 1}, {"dout": P + 2, "gt": 1}, {"dW": P + 1}, {"dW": P + 2, "wt": 1},
                {"ws": P + 128}):
         assert bwd(**kw) == off, kw
+    # outputs over the inputs' memory (arrays of bf16: W 12,800 bytes, out and dout 512)
+    far = P + (1 << 18)
+    assert fwd(ids=far, out=P + 12798) == bad and fwd(ids=P + 12800 + 508, out=P + 12800) == bad
+    assert bwd(ids=far, ws=2 * far, dout=P + 12798, dW=P) == bad and bwd(ids=far, ws=2 * far, dout=P, dW=P) == bad
+    assert bwd(ids=far, ws=far + 4096, dout=far - 4096, dW=P, n=64) in (sb.SB_ERR_WORKSPACE_TOO_SMALL,
+                                                                     sb.SB_ERR_UNSUPPORTED, sb.SB_ERR_CUDA)
     assert sb.sb_embedding_backward_workspace_bytes(-1, 64) == 0
     assert sb.sb_embedding_backward_workspace_bytes(4, 0) == 0
     assert sb.sb_embedding_backward_workspace_bytes(0, 64) > 0

@@ -331,4 +331,14 @@ def test_c_refusals():
     for kw in ({"dx": P + 1}, {"dh": P + 1}, {"dho": P + 1}, {"dy": P + 1}, {"dw": P + 2}, {"db": P + 2},
                {"ws": P + 8}):
         assert bwd(**kw) == off, kw
+    # outputs over a part of an input (rows of 512 bytes), or over another one than their own
+    A, B_, C, D, W_, Z = (P + k * 4096 for k in range(1, 7))
+    f = {"h": A, "y": B_, "weight": W_, "bias": Z, "off": P, "ho": C, "x": D}
+    for kw in ({"ho": A + 2}, {"x": B_ + 2}, {"x": A}, {"ho": B_}, {"ho": D}, {"x": W_}, {"ho": Z}):
+        assert fwd(**{**f, **kw}) == bad, kw
+    g = {"dx": A, "dh": B_, "h": C, "weight": W_, "off": P, "dho": D, "dy": Z, "dw": P + 99 * 4096,
+         "db": P + 100 * 4096, "ws": P + 101 * 4096}
+    for kw in ({"dho": C}, {"dho": A}, {"dho": B_ + 2}, {"dy": A + 2}, {"dy": C}, {"dy": B_}, {"dy": D},
+               {"dy": W_}):
+        assert bwd(**{**g, **kw}) == bad, kw
     assert sb.sb_layer_norm_workspace_bytes(4, 0) == 0 and sb.sb_layer_norm_workspace_bytes(-1, 64) == 0

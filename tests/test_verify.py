@@ -164,6 +164,29 @@ def test_temperatures(draft, T):
 
 
 @gpu
+def test_the_smallest_temperature():
+    """A row's largest logits share it all, each with 1 / their number (of equal bf16 values there may be
+    two): a draft stays if it is one of them and that is above u, and one of them replaces it."""
+    s = _make([3, 2, 0], 500, seed=18)
+    z, u = s["logits"].float(), s["uniforms"].tolist()
+    best = z == z.amax(1, keepdim=True)
+    p = (best.double() / best.sum(1, keepdim=True)).cpu()
+    top = z.argmax(1).int()
+    for drafts in (top, (top + 1) % 500):
+        f = sb.verify_drafts(s["logits"], drafts, s["starts"], s["uniforms"], temperature=1e-30)
+        for b, (a, end) in enumerate(zip(s["starts"].tolist(), s["starts"].tolist()[1:])):
+            x = drafts[a:end].tolist()
+            n = next((i for i in range(end - a - 1) if not p[a + i, x[i]] > u[a + i]), end - a - 1)
+            assert f["accepted"][b] == n and f["token"][a:a + n].tolist() == x[:n]
+            t = int(f["token"][a + n])
+            # (without the refused draft, where another one is left)
+            left = best[a + n].clone()
+            if n < end - a - 1 and int(left.sum()) > int(left[x[n]]):
+                left[x[n]] = False
+            assert left[t]
+
+
+@gpu
 def test_given_logsumexps_are_taken():
     s = _make([3, 5, 0], 2003, seed=5)
     lse = torch.logsumexp(s["logits"].double(), 1).float()
@@ -414,7 +437,7 @@ def test_refusals():
                 {"draft_logits": None, "draft_lse": torch.zeros(2, device="cuda")}):
         with pytest.raises(ValueError):
             sb.verify_drafts(**{**s, **bad})
-    for T in (0.0, -1.0, float("inf"), float("nan"), 1e-42):
+    for T in (0.0, -1.0, float("inf"), float("nan"), 1e-42, 9e-31):
         with pytest.raises(sb.SbError):
             sb.verify_drafts(**s, temperature=T)
     with pytest.raises(sb.SbError):
