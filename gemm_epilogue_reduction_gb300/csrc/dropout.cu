@@ -3,7 +3,8 @@
 // The call is its own gradient: the gradient of x is dropout of the gradient of out.
 //
 // Bound by memory: x (and the residual) in once, out once.  Eight values to a thread and step, four
-// steps of loads in flight.
+// steps of loads in flight; blocks end with their 8192 values (8192 x 6144 bf16 with residual: 43.5 us,
+// 6.9 TB/s).  Some ten instructions an element, half of them the draw, hide behind that.
 #include "norm_common.cuh"
 #include "sb.h"
 #include "sb_dropout.cuh"

@@ -14,15 +14,16 @@
 // each other in the two reductions.  As in the residual norm (norm.cu) a row belongs to a group of
 // threads, sixteen values to a thread, and the next rows are on their way in a cp.async ring.
 // A thread works on two rows side by side: their sums go through the same two reductions, and one's
-// arithmetic fills the other's waits (8192 x 6144 bf16 with branch and dropout: forward 64 us, 6.3 TB/s,
-// and 84, 6.0 TB/s, backward; one row: 74 and 94; four rows in forward, whose ring then has no third
-// step: 71; two groups of 384 threads with the weights in shared memory: 70; a block to a row, which
-// ends with it: 108, its fixed work and its loads of weights weigh more than the waits).  Weights and
-// column sums are in registers; backward reads dx and dh again from the ring.  A draw's state goes from
-// row to row by one addition.
+// arithmetic fills the other's waits.  8192 x 6144 bf16 with branch and dropout: forward 64 us, 6.3
+// TB/s, backward 83, 6.1 TB/s; one row at a time: 74 and 94; four rows in forward, whose ring then has
+// no third step: 71; two groups of 384 threads with the weights in shared memory: 70; a block to a
+// row, which ends with it: 108 (its fixed work and its loads of weights weigh more than the waits).
+// Weights and column sums are in registers; backward reads dx and dh again from the ring.  A draw's
+// state goes from row to row by one addition.
+//
 // A row length that is no multiple of eight shifts each row against the vectors' boundaries
-// (layer_norm.cuh); backward gives a group rows a multiple of eight apart, so that their shift, and
-// with it a thread's columns, stay the same.
+// (layer_norm.cuh); a group's rows are a multiple of eight apart, so that their shift, and with it a
+// thread's columns, stay the same.
 #include <cmath>
 
 #include "layer_norm.cuh"
