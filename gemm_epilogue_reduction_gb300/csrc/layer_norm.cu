@@ -88,11 +88,15 @@ Layout lay_out(int64_t M, int64_t d, LoadMode mode, size_t row_bytes, size_t wei
     l.mode = mode;
     l.row_threads = threads_of(mode == kShifted ? 7 : 0);
     const int64_t share = (M + sms - 1) / sms;  // rows of an SM
+    const size_t step = l.row_threads * row_bytes;
+    // longer rows have a block of 512 threads, and so have two groups that leave much of 384 idle, if
+    // their ring still has three steps of two rows
     l.groups = kNormThreads / l.row_threads;
+    if (l.groups == 0 || (l.groups == 1 && 2 * l.row_threads <= kWideThreads && 3 * 4 * step <= kNormRingBytes))
+        l.groups = kWideThreads / l.row_threads;
     l.rows = mode == kSingle || l.groups < 1 ? 1 : 2;
     if (l.groups > kMaxGroups) l.groups = kMaxGroups;
     if (l.groups > share) l.groups = static_cast<int>(share);
-    const size_t step = l.row_threads * row_bytes;
     // rows of up to 6144 have their weights in registers; rows too long for weights and two steps in
     // shared memory read the weights from memory again for each row
     if (l.groups >= 1 || 2 * step + weight_bytes * l.row_threads > kNormRingBytes) weight_bytes = 0;

@@ -15,7 +15,8 @@ namespace sb {
 enum LoadMode : int { kAligned = 0, kShifted = 1, kSingle = 2 };
 
 constexpr int kNormVectors = 2;         // of a thread: sixteen values
-constexpr int kNormThreads = 384;       // of a block, where a row does not need more
+constexpr int kNormThreads = 384;       // of a block, or, where a row's groups then fill it better,
+constexpr int kWideThreads = 512;       // this many, with fewer registers; longer rows have up to 1024
 
 struct LayerNormParams {
     int M, d;
@@ -47,27 +48,34 @@ cudaError_t launch_layer_norm_forward(const LayerNormParams &p, LayerNormShape s
 cudaError_t launch_layer_norm_backward(const LayerNormParams &p, LayerNormShape s, unsigned blocks,
                                        size_t smem, cudaStream_t st);
 
-__device__ __forceinline__ bool inside8(int e, int d) { return e >= 0 && e + 8 <= d; }
-// Zeros in the places of a vector at e that are not the row's (in kAligned no vector has both, and
-// the ones past the row's end are zeros already).
+// Which values of a vector at e are the row's, a bit for each.  They are the same for all rows of a
+// thread, and a test of a bit is all that the vectors at a row's ends cost more than the others.
 template <int MODE>
-__device__ __forceinline__ void mask8(int e, int d, float2 (&v)[4]) {
+__device__ __forceinline__ uint32_t inside8(int e, int d) {
+    if (MODE == kAligned) return e < d ? 0xFFu : 0u;
+    const uint32_t from = e < 0 ? 0xFFu << min(-e, 8) : 0xFFu, to = e + 8 > d ? 0xFFu >> min(e + 8 - d, 8) : 0xFFu;
+    return from & to & 0xFFu;
+}
+// Zeros in the places of a vector that are not the row's (in kAligned no vector has both, and the
+// ones past the row's end are zeros already).
+template <int MODE>
+__device__ __forceinline__ void mask8(uint32_t in, float2 (&v)[4]) {
     if constexpr (MODE != kAligned) {
-        if (inside8(e, d)) return;
+        if (in == 0xFFu) return;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (e + 2 * j < 0 || e + 2 * j >= d) v[j].x = 0.f;
-            if (e + 2 * j + 1 < 0 || e + 2 * j + 1 >= d) v[j].y = 0.f;
+            if (!(in >> (2 * j) & 1)) v[j].x = 0.f;
+            if (!(in >> (2 * j + 1) & 1)) v[j].y = 0.f;
         }
     }
 }
 // v less the row's mean; zeros stay past the row's ends, where they add nothing to the sums.
 template <int MODE>
-__device__ __forceinline__ void centre8(float mean, int e, int d, float2 (&v)[4]) {
-    const float m = MODE != kAligned || e < d ? -mean : 0.f;
+__device__ __forceinline__ void centre8(float mean, uint32_t in, float2 (&v)[4]) {
+    const float m = MODE != kAligned || in ? -mean : 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = __fadd2_rn(v[j], both(m));
-    mask8<MODE>(e, d, v);
+    mask8<MODE>(in, v);
 }
 
 template <typename T>
@@ -88,13 +96,18 @@ __device__ __forceinline__ void store_singles(T *row, int e, int d, const float2
         if (i + 1 >= 0 && i + 1 < d) put_one(row + i + 1, v[j].y);
     }
 }
-// The vector that is at `to` in memory and at e in its row.
+// The row's values of the vector that is at `to`.
 template <int MODE, typename T>
-__device__ __forceinline__ void store8(T *to, int e, int d, const float2 (&v)[4]) {
-    if (MODE == kAligned ? e < d : MODE == kShifted && inside8(e, d))
+__device__ __forceinline__ void store8(T *to, uint32_t in, const float2 (&v)[4]) {
+    if (MODE != kSingle && in == 0xFFu) {
         store_pairs<8>(to, v);
-    else if (MODE != kAligned)
-        store_singles(to - e, e, d, v);
+    } else if (MODE != kAligned) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (in >> (2 * j) & 1) put_one(to + 2 * j, v[j].x);
+            if (in >> (2 * j + 1) & 1) put_one(to + 2 * j + 1, v[j].y);
+        }
+    }
 }
 template <int MODE>
 __device__ __forceinline__ void load_weight8(const void *w, const LayerNormParams &p, int e,

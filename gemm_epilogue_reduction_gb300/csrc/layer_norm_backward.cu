@@ -27,6 +27,9 @@ __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams
     const long long base = static_cast<long long>(first) * d, advance = static_cast<long long>(stride) * d;
     const int shift = MODE == kShifted ? static_cast<int>(base & 7) : 0;
     const int e0 = t * 8 - shift, per = rt * 8;  // this thread's first vector, and from one to the next
+    uint32_t in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) in[i] = inside8<MODE>(e0 + i * per, d);
     const bool last_has = MODE != kAligned && (static_cast<long long>(p.M) * d & 7) != 0;
 
     // the row whose copy comes next, and where this thread's first vector of it is
@@ -58,7 +61,7 @@ __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams
             load_singles(dx + at_row, e0 + i * per, d, v);
         else
             SB::get(at + kDx, pitch, i, v);
-        mask8<MODE>(e0 + i * per, d, v);
+        mask8<MODE>(in[i], v);
     };
     if constexpr (MODE != kSingle)
         for (int s = 0; s < p.steps * ROWS; ++s)
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams
                     load_singles(h + at_row, e, d, c[k][i]);
                 else
                     ST::get(at + k * kRow, pitch, i, c[k][i]);  // (a row behind the last: an old one)
-                mask8<MODE>(e, d, c[k][i]);
+                mask8<MODE>(in[i], c[k][i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc = __fadd2_rn(acc, c[k][i][j]);
             }
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams
             for (int i = 0; i < NV; ++i) {
                 float2 x[4];
                 get_dx(at + k * kRow, i, x);
-                centre8<MODE>(mean, e0 + i * per, d, c[k][i]);
+                centre8<MODE>(mean, in[i], c[k][i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 a = __fmul2_rn(x[j], w[i][j]);
@@ -160,12 +163,12 @@ __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams
                     v[j] = __ffma2_rn(both(c2), c[k][i][j],
                                       __ffma2_rn(xr, w[i][j], __fadd2_rn(v[j], both(ma))));
                 }
-                store8<MODE>(static_cast<T *>(p.dh_out) + at_row + e, e, d, v);
+                store8<MODE>(static_cast<T *>(p.dh_out) + at_row + e, in[i], v);
                 if constexpr (BRANCH) {
                     const float2 zero[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
                     add_dropped<MODE>(p.drop, seed, state + i * state_vector,
                                       static_cast<unsigned long long>(at_row + e), zero, v);
-                    store8<MODE>(static_cast<B *>(p.dy) + at_row + e, e, d, v);
+                    store8<MODE>(static_cast<B *>(p.dy) + at_row + e, in[i], v);
                 }
             }
             at_row += advance;
@@ -214,7 +217,8 @@ __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams
 cudaError_t launch_layer_norm_backward(const LayerNormParams &p, LayerNormShape s, unsigned blocks,
                                        size_t smem, cudaStream_t st) {
     return for_layer_norm(s, p.dy != nullptr, [&]<typename T, int MODE, bool BRANCH>() {
-        static std::atomic<uint64_t> pairs{0}, small{0}, medium{0}, large{0};
+        static std::atomic<uint64_t> pairs{0}, small{0}, wide_pairs{0}, wide{0}, medium{0},
+            large{0};
         const int n = static_cast<int>(blocks);
         if (s.threads <= kNormThreads) {
             if constexpr (MODE != kSingle)
@@ -223,6 +227,14 @@ cudaError_t launch_layer_norm_backward(const LayerNormParams &p, LayerNormShape 
                                               n, smem, st);
             return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kNormThreads, 1>, small, p, n,
                                       smem, st);
+        }
+        if (s.threads <= kWideThreads) {
+            if constexpr (MODE != kSingle)
+                if (s.rows == 2)
+                    return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kWideThreads, 2>, wide_pairs,
+                                              p, n, smem, st);
+            return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kWideThreads, 1>, wide, p, n, smem,
+                                      st);
         }
         if (s.threads <= 640)
             return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, 640, 1>, medium, p, n, smem, st);

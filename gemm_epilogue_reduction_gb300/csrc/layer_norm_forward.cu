@@ -30,6 +30,9 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
     const long long base = static_cast<long long>(first) * d, advance = static_cast<long long>(stride) * d;
     const int shift = MODE == kShifted ? static_cast<int>(base & 7) : 0;
     const int e0 = t * 8 - shift, per = rt * 8;  // this thread's first vector, and from one to the next
+    uint32_t in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) in[i] = inside8<MODE>(e0 + i * per, d);
     const bool last_has = MODE != kAligned && (static_cast<long long>(p.M) * d & 7) != 0;
 
     // the row whose copy comes next, and where this thread's first vector of it is
@@ -130,19 +133,19 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
                     load_singles(static_cast<const T *>(p.h) + at_row, e, d, a[k][i]);
                 else
                     ST::get(at + k * kRow, pitch, i, a[k][i]);  // (a row behind the last: an old one)
-                mask8<MODE>(e, d, a[k][i]);
+                mask8<MODE>(in[i], a[k][i]);
                 if constexpr (BRANCH) {
                     float2 v[4];
                     if constexpr (MODE == kSingle)
                         load_singles(static_cast<const B *>(p.y) + at_row, e, d, v);
                     else
                         SB::get(at + k * kRow + kY, pitch, i, v);
-                    mask8<MODE>(e, d, v);
+                    mask8<MODE>(in[i], v);
                     add_dropped<MODE>(p.drop, seed, state + i * state_vector,
                                       static_cast<unsigned long long>(at_row + e), a[k][i], v);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) a[k][i][j] = v[j];
-                    if (k == 0 || row0 + k * stride < p.M) store8<MODE>(h_out + i * per, e, d, a[k][i]);
+                    if (k == 0 || row0 + k * stride < p.M) store8<MODE>(h_out + i * per, in[i], a[k][i]);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc = __fadd2_rn(acc, a[k][i][j]);
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
             float2 acc = both(0.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                centre8<MODE>(mean, e0 + i * per, d, a[k][i]);
+                centre8<MODE>(mean, in[i], a[k][i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc = __ffma2_rn(a[k][i][j], a[k][i][j], acc);
             }
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     a[k][i][j] = __ffma2_rn(__fmul2_rn(a[k][i][j], both(r)), w[j], b[j]);
-                if (k == 0 || row0 + k * stride < p.M) store8<MODE>(x_out + i * per, e0 + i * per, d, a[k][i]);
+                if (k == 0 || row0 + k * stride < p.M) store8<MODE>(x_out + i * per, in[i], a[k][i]);
             }
             x_out += advance;
         }
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
 cudaError_t launch_layer_norm_forward(const LayerNormParams &p, LayerNormShape s, unsigned blocks,
                                       size_t smem, cudaStream_t st) {
     return for_layer_norm(s, p.y != nullptr, [&]<typename T, int MODE, bool BRANCH>() {
-        static std::atomic<uint64_t> two{0}, small{0}, large{0};
+        static std::atomic<uint64_t> two{0}, small{0}, wide_two{0}, wide{0}, large{0};
         const int n = static_cast<int>(blocks);
         if (s.threads <= kNormThreads) {
             if constexpr (MODE != kSingle)
@@ -205,6 +208,14 @@ cudaError_t launch_layer_norm_forward(const LayerNormParams &p, LayerNormShape s
                     return launch_norm_kernel(forward_kernel<T, MODE, BRANCH, kNormThreads, 2, true>, two, p,
                                               n, smem, st);
             return launch_norm_kernel(forward_kernel<T, MODE, BRANCH, kNormThreads, 1, true>, small, p, n,
+                                      smem, st);
+        }
+        if (s.threads <= kWideThreads) {
+            if constexpr (MODE != kSingle)
+                if (s.rows == 2)
+                    return launch_norm_kernel(forward_kernel<T, MODE, BRANCH, kWideThreads, 2, true>,
+                                              wide_two, p, n, smem, st);
+            return launch_norm_kernel(forward_kernel<T, MODE, BRANCH, kWideThreads, 1, true>, wide, p, n,
                                       smem, st);
         }
         return launch_norm_kernel(forward_kernel<T, MODE, BRANCH, 1024, 1, false>, large, p, n, smem, st);
