@@ -71,7 +71,7 @@ LoadMode mode_of(int64_t d, Ptr... ptrs) {
 }
 // A row's threads, the groups of a block, the rows that a group works on at a time and the steps of its
 // ring.  row_bytes: of a thread for a row of the ring; weight_bytes: of a thread, for the weights of rows
-// too long to keep them in registers.
+// too long to keep them in registers; wide_rows: rows at a time in a block of more than 384 threads.
 struct Layout {
     LoadMode mode;
     int row_threads, groups, steps, rows;
@@ -79,7 +79,8 @@ struct Layout {
     int64_t blocks;
     size_t smem;
 };
-Layout lay_out(int64_t M, int64_t d, LoadMode mode, size_t row_bytes, size_t weight_bytes, int sms) {
+Layout lay_out(int64_t M, int64_t d, LoadMode mode, size_t row_bytes, size_t weight_bytes, int wide_rows,
+               int sms) {
     Layout l{};
     auto threads_of = [d](int shift) {
         return round32(((d + shift + 7) / 8 + kNormVectors - 1) / kNormVectors);
@@ -89,12 +90,12 @@ Layout lay_out(int64_t M, int64_t d, LoadMode mode, size_t row_bytes, size_t wei
     l.row_threads = threads_of(mode == kShifted ? 7 : 0);
     const int64_t share = (M + sms - 1) / sms;  // rows of an SM
     const size_t step = l.row_threads * row_bytes;
-    // longer rows have a block of 512 threads, and so have two groups that leave much of 384 idle, if
-    // their ring still has three steps of two rows
+    // longer rows have a block of 512 threads, and so have two groups where one leaves much of 384 idle,
+    // if their ring still has three steps
     l.groups = kNormThreads / l.row_threads;
-    if (l.groups == 0 || (l.groups == 1 && 2 * l.row_threads <= kWideThreads && 3 * 4 * step <= kNormRingBytes))
+    if (l.groups == 0 || (l.groups == 1 && 2 * l.row_threads <= kWideThreads && 3 * 2 * wide_rows * step <= kNormRingBytes))
         l.groups = kWideThreads / l.row_threads;
-    l.rows = mode == kSingle || l.groups < 1 ? 1 : 2;
+    l.rows = mode == kSingle || l.groups < 1 ? 1 : l.groups * l.row_threads > kNormThreads ? wide_rows : 2;
     if (l.groups > kMaxGroups) l.groups = kMaxGroups;
     if (l.groups > share) l.groups = static_cast<int>(share);
     // rows of up to 6144 have their weights in registers; rows too long for weights and two steps in
@@ -154,7 +155,7 @@ int32_t sb_layer_norm_forward(const void *h, const void *y, const void *weight, 
     q.x = x;
     const bool h32 = stream_type == SB_F32;
     const Layout l = lay_out(M, d, mode_of(d, h, y, y ? h_out : nullptr, x),
-                             kNormVectors * 8 * ((h32 ? 4 : 2) + (y ? 2 : 0)), kNormVectors * 64, sms);
+                             kNormVectors * 8 * ((h32 ? 4 : 2) + (y ? 2 : 0)), kNormVectors * 64, 2, sms);
     q.row_threads = l.row_threads;
     q.groups = l.groups;
     q.steps = l.steps;
@@ -212,7 +213,7 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
     q.sums = dbias ? 2 : 1;
     const bool h32 = stream_type == SB_F32;
     const Layout l = lay_out(M, d, mode_of(d, dx, dh, h, dh_out, dy),
-                             kNormVectors * 8 * ((h32 ? 8 : 4) + 2), 0, sms);
+                             kNormVectors * 8 * ((h32 ? 8 : 4) + 2), 0, 1, sms);
     q.row_threads = l.row_threads;
     q.groups = l.groups;
     q.steps = l.steps;

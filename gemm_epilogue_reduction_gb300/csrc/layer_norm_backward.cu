@@ -217,8 +217,7 @@ __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams
 cudaError_t launch_layer_norm_backward(const LayerNormParams &p, LayerNormShape s, unsigned blocks,
                                        size_t smem, cudaStream_t st) {
     return for_layer_norm(s, p.dy != nullptr, [&]<typename T, int MODE, bool BRANCH>() {
-        static std::atomic<uint64_t> pairs{0}, small{0}, wide_pairs{0}, wide{0}, medium{0},
-            large{0};
+        static std::atomic<uint64_t> pairs{0}, small{0}, wide{0}, medium{0}, large{0};
         const int n = static_cast<int>(blocks);
         if (s.threads <= kNormThreads) {
             if constexpr (MODE != kSingle)
@@ -228,14 +227,10 @@ cudaError_t launch_layer_norm_backward(const LayerNormParams &p, LayerNormShape 
             return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kNormThreads, 1>, small, p, n,
                                       smem, st);
         }
-        if (s.threads <= kWideThreads) {
-            if constexpr (MODE != kSingle)
-                if (s.rows == 2)
-                    return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kWideThreads, 2>, wide_pairs,
-                                              p, n, smem, st);
+        // (two rows at a time do not fit into 128 registers)
+        if (s.threads <= kWideThreads)
             return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, kWideThreads, 1>, wide, p, n, smem,
                                       st);
-        }
         if (s.threads <= 640)
             return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, 640, 1>, medium, p, n, smem, st);
         return launch_norm_kernel(backward_kernel<T, MODE, BRANCH, 1024, 1>, large, p, n, smem, st);
