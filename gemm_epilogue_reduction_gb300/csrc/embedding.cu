@@ -95,8 +95,111 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
     }
 }
 
+// Rows of an odd length: a row of W and its row of the output start at different places of a vector's
+// eight values.  A thread stores whole vectors of the output; what belongs into one lies in two vectors
+// of W, and a shift through their registers, by the same number of values along the row, brings it into
+// place.  (The second vector is the neighbour's first: it comes from L1.)
+//
+// Values from .. from + 8 of an array of n values, as 32-bit words; from: a multiple of eight.
+template <typename T>
+__device__ __forceinline__ void load_words(const T *base, long long from, long long n, uint32_t *w) {
+    constexpr int WORDS = 2 * static_cast<int>(sizeof(T));
+    if (from >= 0 && from + 8 <= n) {
+#pragma unroll
+        for (int c = 0; c < WORDS / 4; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(base + from + c * 4 * (4 / sizeof(T)));
+            w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
+        }
+        return;
+    }
+    // the array's end, or in front of it
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j) {
+        w[j] = 0;
+        if constexpr (sizeof(T) == 4) {
+            if (from + j >= 0 && from + j < n) w[j] = reinterpret_cast<const uint32_t *>(base)[from + j];
+        } else {
+            const uint16_t *b = reinterpret_cast<const uint16_t *>(base) + from + 2 * j;
+            if (from + 2 * j >= 0 && from + 2 * j < n) w[j] = b[0];
+            if (from + 2 * j + 1 >= 0 && from + 2 * j + 1 < n) w[j] |= static_cast<uint32_t>(b[1]) << 16;
+        }
+    }
+}
+// The eight values that begin r values behind the first of sixteen.
+template <typename T>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[4 * sizeof(T)], int r, float2 (&v)[4]) {
+    constexpr int WORDS = 4 * static_cast<int>(sizeof(T));
+    const int words = sizeof(T) == 4 ? r : r >> 1;
+#pragma unroll
+    for (int by = WORDS / 4; by > 0; by >>= 1)
+#pragma unroll
+        for (int j = 0; j + by < WORDS; ++j) w[j] = words & by ? w[j + by] : w[j];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = unpack2(__funnelshift_r(w[j], w[j + 1], r & 1 ? 16 : 0));
+    }
+}
+
+template <typename W, typename O>
+__global__ void __launch_bounds__(kLookupThreads) lookup_shifted_kernel(const LookupParams p) {
+    constexpr int U = 4 / sizeof(W);  // vectors in flight, two loads each and two of 16 bytes in fp32
+    const int tx = kLookupThreads / p.rows;
+    const int x = threadIdx.x % tx;
+    const long long row = static_cast<long long>(blockIdx.x) * p.rows + threadIdx.x / tx;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // no early launch_dependents: as above
+    if (row >= p.M) return;
+    const int id = p.ids[row];
+    const bool has = id >= 0 && id < p.V && id != p.ignore;
+    const float none = id == p.ignore ? 0.f : __uint_as_float(0x7FC00000u);
+    const W *all = static_cast<const W *>(p.W);
+    const long long n = p.V * p.d, at = has ? id * p.d : 0;
+    O *to = static_cast<O *>(p.out) + row * p.d;
+    const int shift = static_cast<int>(row * p.d & 7), r = static_cast<int>((at - shift) & 7);
+    for (long long e0 = x * 8 - shift; e0 < p.d; e0 += U * tx * 8) {
+        uint32_t w[U][4 * sizeof(W)];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long e = e0 + u * tx * 8;
+            if (has && e < p.d) {
+                load_words(all, at + e - r, n, w[u]);
+                load_words(all, at + e - r + 8, n, w[u] + 2 * sizeof(W));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long e = e0 + u * tx * 8;
+            if (e >= p.d) break;
+            float2 v[4] = {both(none), both(none), both(none), both(none)};
+            if (has) {
+                shift_words<W>(w[u], r, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(v[j], both(p.scale));
+            }
+            if (e >= 0 && e + 8 <= p.d) {
+                store_pairs<8>(to + e, v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (e + j >= 0 && e + j < p.d) put_one(to + e + j, j & 1 ? v[j / 2].y : v[j / 2].x);
+            }
+        }
+    }
+}
+
 template <typename W, typename O>
 cudaError_t launch_lookup(LookupParams p, int vec, cudaStream_t st) {
+    if (vec == 1 && p.d > 8 && on(p.W, 16) && on(p.out, 16)) {
+        int tx = 8;
+        while (tx < kLookupThreads && tx * (4 / static_cast<long long>(sizeof(W))) * 8 < p.d + 7) tx *= 2;
+        p.rows = kLookupThreads / tx;
+        return launch_dependent(lookup_shifted_kernel<W, O>,
+                                dim3(static_cast<unsigned>((p.M + p.rows - 1) / p.rows)), kLookupThreads, 0, p, st);
+    }
     const long long steps = (p.d + vec - 1) / vec;
     const int per = vec == 1 ? 8 : 4;
     int tx = 8;

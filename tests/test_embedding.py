@@ -63,6 +63,29 @@ def test_lookup(M, d, V, weights, out):
 
 
 @gpu
+@pytest.mark.parametrize("d", [9, 10, 15, 31, 257, 1021, 2046, 4099])
+@pytest.mark.parametrize("weights", [BF, F32])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_lookup_of_odd_rows(d, weights, out):
+    # every place of a row of W against every place of a row of the output; what lies around both stays
+    # unread and unwritten
+    V, M = 13, 13 * 8 + 5
+    W = torch.randn(V * d, generator=_gen(1), device="cuda").to(weights).view(V, d)
+    ids = (torch.arange(M, device="cuda") * 5 + torch.arange(M, device="cuda") // 13).remainder(V).int()
+    ids[7], ids[20], ids[-2] = -100, V, V - 1
+    room = torch.full((M * d + 64,), 7.0, dtype=out, device="cuda")
+    got = room[32:32 + M * d].view(M, d)
+    want = W[ids.clamp(0, V - 1).long()].float() * 1.7
+    want[7], want[20] = 0, float("nan")
+    kind = {BF: 0, F32: 1}
+    assert sb.sb_embedding_forward(ids.data_ptr(), W.data_ptr(), M, d, V, -100, 1.7, kind[weights], kind[out],
+                                   got.data_ptr(), torch.cuda.current_stream().cuda_stream) == sb.SB_OK
+    keep = torch.arange(M, device="cuda") != 20
+    assert _bits(got[keep], want[keep].to(out)) and got[20].isnan().all()
+    assert (room[:32] == 7).all() and (room[32 + M * d:] == 7).all()
+
+
+@gpu
 def test_lookup_of_ids_outside():
     W = torch.randn(10, 24, device="cuda").bfloat16()
     ids = torch.tensor([3, -1, 10, 2 ** 31 - 1, -2 ** 31, 9, 4], dtype=torch.int32, device="cuda")
