@@ -149,6 +149,34 @@ def test_gradient(M, d, V, kind, grad, weights):
 
 
 @gpu
+@pytest.mark.parametrize("d", [129, 247, 249, 255, 993, 1022, 1983, 4099])
+@pytest.mark.parametrize("M,V", [(50, 40), (333, 61), (2500, 17)])
+@pytest.mark.parametrize("grad,weights", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
+def test_gradient_of_odd_rows(M, d, V, grad, weights):
+    # whole numbers: no rounding in fp32 (sums below 2500·16 + 64), one to bf16 at the end; runs of one token,
+    # inside a piece and over several, rows at every place of a vector, what lies around dW unwritten
+    g = _gen(M + d)
+    ids = _ids(M, V, M, "padded")
+    dout = torch.randint(-8, 9, (M, d), generator=g, device="cuda").to(grad)
+    room = torch.full((V * d + 64,), 3.0, dtype=weights, device="cuda")
+    dW = room[32:32 + V * d].view(V, d)
+    for add in (False, True):
+        dW.copy_(torch.randint(-32, 33, (V, d), generator=g, device="cuda"))
+        old = dW.double() * add
+        sums, _, _ = _sums(ids, dout, V, 2.0)
+        if add:
+            sb.embedding_backward(ids, dout, dW=dW, scale=2.0)
+        else:
+            ws = torch.empty(sb.sb_embedding_backward_workspace_bytes(M, d), dtype=torch.uint8, device="cuda")
+            kind = {BF: 0, F32: 1}
+            assert sb.sb_embedding_backward(
+                ids.data_ptr(), dout.data_ptr(), M, d, V, -100, 2.0, kind[grad], kind[weights], 0, dW.data_ptr(),
+                ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == sb.SB_OK
+        assert torch.equal(dW, (sums + old).to(weights))
+        assert (room[:32] == 3).all() and (room[32 + V * d:] == 3).all()
+
+
+@gpu
 def test_gradient_ignores_what_has_no_row():
     V, d = 20, 40
     ids = torch.tensor([5, -7, 20, 2 ** 31 - 1, -2 ** 31, 3, 5, 3], dtype=torch.int32, device="cuda")
