@@ -53,7 +53,8 @@ cudaError_t launch_layer_norm_backward(const LayerNormParams &p, LayerNormShape 
 template <int MODE>
 __device__ __forceinline__ uint32_t inside8(int e, int d) {
     if (MODE == kAligned) return e < d ? 0xFFu : 0u;
-    const uint32_t from = e < 0 ? 0xFFu << min(-e, 8) : 0xFFu, to = e + 8 > d ? 0xFFu >> min(e + 8 - d, 8) : 0xFFu;
+    const uint32_t from = e < 0 ? 0xFFu << min(-e, 8) : 0xFFu;
+    const uint32_t to = e + 8 > d ? 0xFFu >> min(e + 8 - d, 8) : 0xFFu;
     return from & to & 0xFFu;
 }
 // Zeros in the places of a vector that are not the row's (in kAligned no vector has both, and the
