@@ -131,6 +131,15 @@ def test_values_and_gradients(M, d, stream, weights):
 
 
 @gpu
+@pytest.mark.parametrize("M,d", [(1250, 4096), (1251, 3737), (1249, 3585), (650, 8192), (700, 7001), (613, 6143),
+                                 (1111, 6137), (153, 7168)])
+@pytest.mark.parametrize("stream,branch", [(BF, True), (BF, False), (F32, True), (F32, False)])
+def test_blocks_that_fill_an_sm(M, d, stream, branch):
+    # two groups of long rows, rows of more than 6144 values; several turns, the last one with a row missing
+    _check(_make(M, d, stream=stream, branch=branch, seed=M + d), p=0.2 * branch, seed=5)
+
+
+@gpu
 @pytest.mark.parametrize("M,d", [(1, 5120), (50, 1032), (7, 333), (64, 100), (33, 12)])
 @pytest.mark.parametrize("bias", [True, False])
 @pytest.mark.parametrize("branch,p", [(False, 0.0), (True, 0.0), (True, 0.5), (True, 1.0)])
