@@ -226,30 +226,40 @@ __global__ void __launch_bounds__(kLseThreads, 4) lse_kernel(const VerifyParams 
     }
 }
 
-// The logsumexp from a row's (max, sum).
-__device__ __forceinline__ double lse_of(MaxSum a, float inv_t) {
-    if (a.m == -INFINITY && a.s == 0.f) return -INFINITY;
-    const double m = static_cast<double>(a.m) * inv_t;
-    if (!(a.s > 0.f && a.s < INFINITY)) return m + a.s;  // not finite
+// A row's distribution: log p = (z - m) / T - l.  Formed here m is the largest logit and l the logarithm of
+// the sum of exponentials, so that no number of the size of z / T is ever rounded (z - m is exact in 64
+// bits), whatever T is; given m is 0 and l the logsumexp.
+struct Norm {
+    double m, l;
+};
+__device__ __forceinline__ Norm norm_of(MaxSum a) {
+    if (!(a.s > 0.f && a.s < INFINITY)) return Norm{a.m, a.s == 0.f ? -INFINITY : a.s};  // no finite logit
     // log s = e ln 2 + log f with s = f·2^e, f in [1, 2): in fp32 log s would be off by its own ulp
     const uint32_t bits = __float_as_uint(a.s);
     const int e = static_cast<int>(bits >> 23) - 127;  // (s is no subnormal: its largest term is 1)
-    return m + (e * 0.69314718055994531 + logf(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u)));
+    return Norm{a.m, e * 0.69314718055994531 + logf(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u))};
+}
+// The same for the scan: log2 p = (z - ref)·c + rest.  ref is m, or where the logsumexp is given the logit whose
+// p is 1 (inside fp32's range), so that columns near the largest keep their precision.
+__device__ __forceinline__ float2 ref_of(Norm a, bool given, const VerifyParams &p) {
+    const double at = given ? a.l * p.t : a.m;
+    const float ref = isfinite(at) ? static_cast<float>(fmin(fmax(at, -3.4e38), 3.4e38)) : static_cast<float>(at);
+    return make_float2(ref, static_cast<float>(((ref - a.m) * p.inv_t - a.l) * 1.4426950408889634));
 }
 
-// The logsumexp of row `at` of the target (or the draft), by a warp.
+// The distribution of row `at` of the target (or the draft), by a warp.
 template <typename T>
-__device__ __forceinline__ double row_lse(const VerifyParams &p, const Pieces &c, bool draft, int at,
-                                          int lane) {
+__device__ __forceinline__ Norm row_norm(const VerifyParams &p, const Pieces &c, bool draft, int at,
+                                         int lane) {
     const float *given = draft ? p.qlse : p.lse;
-    if (given) return given[at];
+    if (given) return Norm{0.0, given[at]};
     const int row = draft ? c.zrows + at : at;
     const long long begin = static_cast<long long>(row) * c.nv;
     const int first = static_cast<int>(begin / c.per), last = static_cast<int>((begin + c.nv - 1) / c.per);
     MaxSum a{-INFINITY, 0.f};
     for (int i = first + lane; i <= last; i += 32)
         a = join(a, MaxSum{p.part[i + row].x, p.part[i + row].y}, p.inv_t * kLog2e);
-    return lse_of(warp_join(a, p.inv_t * kLog2e), p.inv_t);
+    return norm_of(warp_join(a, p.inv_t * kLog2e));
 }
 
 // Whether e^x > u, for x whose rounding to fp32 would count.
@@ -287,9 +297,7 @@ template <typename T, int FROM>
 struct Scan {
     const VerifyParams &p;
     const T *z, *q;
-    // log2 p = (z - lse·T)·c: what is subtracted is in two parts, so that columns near the largest keep
-    // their precision whatever T is (fp32 products would be off by 2^-24 of z / T)
-    float c, ref, rest, qref, qrest;
+    float c, ref, rest, qref, qrest;  // see ref_of
     int x;
     unsigned long long first;  // index of the row's first draw
     float best, bar;
@@ -298,8 +306,8 @@ struct Scan {
 
     __device__ __forceinline__ Scan(const VerifyParams &p_, const T *z_, const T *q_, float4 refs, int x_,
                                     unsigned long long first_)
-        : p(p_), z(z_), q(q_), c(p_.inv_t * kLog2e), ref(refs.x), rest(-refs.y * c), qref(refs.z),
-          qrest(-refs.w * c), x(x_), first(first_), best(0.f), bar(0.f), column(0) {}
+        : p(p_), z(z_), q(q_), c(p_.inv_t * kLog2e), ref(refs.x), rest(refs.y), qref(refs.z),
+          qrest(refs.w), x(x_), first(first_), best(0.f), bar(0.f), column(0) {}
     // Of two columns, j and j + step; v, u: their logits, the target's and the draft's.
     __device__ __forceinline__ float2 weights(float2 v, float2 u, int j, int step) const {
         const float2 y = __ffma2_rn(__fadd2_rn(v, both(-ref)), both(c), both(rest));
@@ -405,8 +413,8 @@ template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyParams p) {
     constexpr int THREADS = kVerifyThreads, WARPS = THREADS / 32;
     __shared__ int end, busy;
-    __shared__ double lses[WARPS];
-    __shared__ float4 refs[WARPS];  // lse·T and the draft's, in two parts each
+    __shared__ Norm norms[WARPS];
+    __shared__ float4 refs[WARPS];  // see ref_of: the target's and the draft's
     __shared__ unsigned long long bests[2][kWideBlocks], warps[WARPS];
     const int blocks = static_cast<int>(cluster_blocks()), rank = static_cast<int>(cluster_ctarank());
     const int b = static_cast<int>(blockIdx.x) / blocks;
@@ -455,21 +463,20 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
             const size_t at = static_cast<size_t>(i) * p.V + (known ? x : 0);
             const float zx = known ? one(z + at) : 0.f, qx = known && q ? one(q + at) : 0.f;
             const float u = has ? p.u[r] : 0.f;
-            const double lse = row_lse<T>(p, pieces, false, r, lane);
-            const double qlse = has && q ? row_lse<T>(p, pieces, true, q0 + i, lane) : 0.0;
+            const Norm norm = row_norm<T>(p, pieces, false, r, lane);
+            const Norm qnorm = has && q ? row_norm<T>(p, pieces, true, q0 + i, lane) : Norm{0.0, 0.0};
             if (lane == 0) {
-                const double t = lse * p.t, qt = qlse * p.t;
-                const float hi = static_cast<float>(t), qhi = static_cast<float>(qt);
-                lses[warp] = lse;
-                refs[warp] = make_float4(hi, static_cast<float>(t - hi), qhi, static_cast<float>(qt - qhi));
+                const float2 a = ref_of(norm, p.lse, p), b = ref_of(qnorm, p.qlse, p);
+                norms[warp] = norm;
+                refs[warp] = make_float4(a.x, a.y, b.x, b.y);
                 if (has) {
-                    const double l = static_cast<double>(zx) * p.inv_t - lse;
-                    const double m = q ? static_cast<double>(qx) * p.inv_t - qlse : 0.0;
+                    // the two logits' differences first: of the size of z / T they may cancel
+                    const double gap = zx - norm.m, qgap = q ? qx - qnorm.m : 0.0;
                     if (!known && rank == 0) record_status(p.status, p.epoch, 1u);
-                    if (!known || !exp_above(l - m, u)) atomicMin(&end, i);
+                    if (!known || !exp_above((gap - qgap) * p.inv_t - (norm.l - qnorm.l), u)) atomicMin(&end, i);
                     if (rank == 0) {  // (of a row behind the end it is taken back below)
                         p.token[r] = x;
-                        if (p.logprob) p.logprob[r] = static_cast<float>(l);
+                        if (p.logprob) p.logprob[r] = static_cast<float>(gap * p.inv_t - norm.l);
                     }
                 }
             }
@@ -479,7 +486,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
         __syncthreads();             // before the next rows' are written
     }
     const int e = end, r = s0 + e;
-    const double lse = lses[e - g];
+    const Norm norm = norms[e - g];
     const float4 ref = refs[e - g];
     z += static_cast<size_t>(e) * p.V;
     const int x = e < n ? p.drafts[r] : -1;
@@ -520,7 +527,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
             lp = __uint_as_float(0x7FC00000u);  // no column of the row has any probability
             if (best) {
                 token = ~static_cast<int>(static_cast<uint32_t>(best));
-                lp = static_cast<float>(static_cast<double>(one(z + token)) * p.inv_t - lse);
+                lp = static_cast<float>((one(z + token) - norm.m) * p.inv_t - norm.l);
             }
         }
         p.token[s0 + i] = token;

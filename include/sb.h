@@ -717,6 +717,8 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
  *   uniforms    device float [R], each in [0, 1); a request's last one is not read.
  *   lse, draft_lse  device float [R] and [draft_rows]: the rows' logsumexp of logits / T where the
  *               caller has it (T = 1: that of sb_lmhead_project), each or NULL: formed here.
+ *              Given ones are taken as they are: log p is off by what they are, of which fp32's
+ *              rounding alone is 2^-24 max|z| / T.  At temperatures where that counts leave them out.
  *   R, B, V     R, draft_rows < 2^24; B <= 2^24; 1 <= V < 2^31 - 65536.
  *   temperature finite, >= 1e-30; 1 / T is rounded to fp32.
  *   token       device int32 [R]: from starts[b] on the drafts that stay and the sample behind them,
