@@ -303,6 +303,7 @@ struct Scan {
     float best, bar;
     int column;
     static constexpr float kUpper = 0.69314860f * 16777216.f;
+    static constexpr float kLeastScore = 1.40129846e-45f;  // fp32's smallest number
 
     __device__ __forceinline__ Scan(const VerifyParams &p_, const T *z_, const T *q_, float4 refs, int x_,
                                     unsigned long long first_)
@@ -325,7 +326,9 @@ struct Scan {
     __device__ __forceinline__ void exact(int j) {
         const uint32_t bits = bits24_from_state(splitmix_state(p.seed, first + j));
         const float2 w = weights(both(one(z + j)), both(FROM == kDifference ? one(q + j) : 0.f), j, 1);
-        const float score = bits ? w.x / -log2_uniform(bits) : 0.f;
+        // A uniform of 0, or a weight too small for the quotient, scores less than any other column but more
+        // than none: a row with a weight has a sample.
+        const float score = w.x > 0.f ? fmaxf(w.x / -log2_uniform(bits), kLeastScore) : 0.f;
         // columns come in any order: of equal scores the lowest stays
         if (score > best || (score == best && j < column)) best = score, column = j;
     }

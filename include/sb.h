@@ -705,6 +705,7 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
  * of its p.  The tokens are then distributed as samples of the target's own.  The sample of row r
  * is the column with the largest w_j / -log u_rj (the lowest of equal ones) with the 24-bit uniform
  * u of sb_lmhead_project at index r*V + j of the seed's stream: where all stay, SB_GUMBEL_TOKEN's.
+ * u = 0 gives a score of 0, which wins only where no other column has a weight (in fp32).
  *   logits      device [R, V] of logits_type (an sb_type).  -inf is a column without probability.
  *   draft_logits  device [draft_rows, V] of that type: a row for every draft, one request's behind
  *               the other's, without gaps; draft_rows = -1 and NULL: the drafts have none.
