@@ -427,14 +427,18 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int total = p.B ? p.starts[p.B] : 0;
-    const int s0 = p.B ? p.starts[b] : 0, s1 = p.B ? p.starts[b + 1] : 0;
+    const int s0 = p.B ? p.starts[b] : 0, s1 = p.B ? p.starts[b + 1] : 0, front = p.B ? p.starts[0] : 0;
     if (blockIdx.x == 0 && tid == 0) *p.epoch_word = p.epoch;
-    if (b == (p.B ? p.B - 1 : 0) && total >= 0)  // the rows behind the last request
-        for (long long r = total + static_cast<long long>(rank) * THREADS + tid; r < p.R;
+    auto clear = [&](int from, int to) {
+        for (long long r = from + static_cast<long long>(rank) * THREADS + tid; r < to;
              r += static_cast<long long>(blocks) * THREADS) {
             p.token[r] = -1;
             if (p.logprob) p.logprob[r] = 0.f;
         }
+    };
+    // the rows in front of the first request and behind the last one, where no request has its own
+    if (b == 0) clear(0, min(front, p.R));
+    if (b == (p.B ? p.B - 1 : 0) && total >= 0) clear(total, p.R);
     // draft rows are those of the requests before this one that have any rows
     const int n = static_cast<int>(static_cast<unsigned>(s1) - static_cast<unsigned>(s0) - 1u);
     if (tid == 0) busy = 0, end = n;
@@ -443,8 +447,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
     for (int i = tid; i < b; i += THREADS) mine += p.starts[i + 1] > p.starts[i];
     if (mine) atomicAdd(&busy, mine);
     __syncthreads();
-    const int q0 = s0 - busy;  // the draft's row of row s0
-    const bool sane = s0 >= 0 && s1 >= s0 && s1 <= total && total <= p.R &&
+    const int q0 = s0 - max(front, 0) - busy;  // the draft's row of row s0
+    const bool sane = s0 >= 0 && s0 >= front && s1 >= s0 && s1 <= total && total <= p.R &&
                       (!p.with_q || n <= 0 || (q0 >= 0 && q0 + n <= p.Rd));
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (!sane || n < 0) {  // the same for all blocks of the cluster
@@ -549,12 +553,14 @@ __global__ void __launch_bounds__(128) greedy_kernel(const GreedyParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, b = blockIdx.x * 4 + threadIdx.x / 32;
-    const int total = p.B ? p.starts[p.B] : 0;
+    const int total = p.B ? p.starts[p.B] : 0, front = p.B ? p.starts[0] : 0;
+    if (b == 0)
+        for (int r = lane; r < min(front, p.R); r += 32) p.token[r] = -1;
     if (b == (p.B ? p.B - 1 : 0) && total >= 0)
         for (long long r = static_cast<long long>(total) + lane; r < p.R; r += 32) p.token[r] = -1;
     if (b >= p.B) return;
     const int s0 = p.starts[b], s1 = p.starts[b + 1];
-    if (s0 < 0 || s1 < s0 || s1 > total || total > p.R) {
+    if (s0 < 0 || s0 < front || s1 < s0 || s1 > total || total > p.R) {
         if (lane == 0) p.accepted[b] = -1;
         return;
     }

@@ -712,9 +712,11 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
  *   drafts      device int32 [R]: in row r the token drafted for it; a request's last one is not
  *               read.  One outside [0, V) does not stay, its sample is of p, and
  *               sb_last_device_status reports SB_ERR_INVALID_ARG.
- *   starts      device int32 [B + 1], ascending, starts[B] <= R.  A request may have no rows.  One
- *               whose rows are not inside R (or its drafts' not inside draft_rows) gets accepted -1
- *               and nothing else, and the status reports SB_ERR_INVALID_ARG.
+ *   starts      device int32 [B + 1], ascending, 0 <= starts[0], starts[B] <= R.  A request may have
+ *               no rows, and rows in front of starts[0] belong to none (nor do they have draft rows).
+ *               One whose rows are not between starts[0] and starts[B], or not inside R (or its
+ *               drafts' not inside draft_rows) gets accepted -1 and nothing else, not in its rows
+ *               either, and the status reports SB_ERR_INVALID_ARG.
  *   uniforms    device float [R], each in [0, 1); a request's last one is not read.
  *   lse, draft_lse  device float [R] and [draft_rows]: the rows' logsumexp of logits / T where the
  *               caller has it (T = 1: that of sb_lmhead_project), each or NULL: formed here.
@@ -723,7 +725,8 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
  *   R, B, V     R, draft_rows < 2^24; B <= 2^24; 1 <= V < 2^31 - 65536.
  *   temperature finite, >= 1e-30; 1 / T is rounded to fp32.
  *   token       device int32 [R]: from starts[b] on the drafts that stay and the sample behind them,
- *               and -1 in all other rows, those behind the last request among them.
+ *               and -1 in all other rows, those in front of the first request and behind the last
+ *               one among them.
  *   accepted    device int32 [B]: how many drafts of the request stay.
  *   token_logprob  device float [R], or NULL: log p(token); 0 where there is no token.
  *   workspace   device, 256-byte aligned, >= sb_verify_workspace_bytes(R, draft_rows, V); no
