@@ -288,14 +288,26 @@ cudaError_t launch_norm_columns(const ColumnParams &p, bool many, cudaStream_t s
 
 // ------------------------------------------------------------------ layout and launch
 inline bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-// Whether two arrays share memory (null: there is none).
+// Whether two arrays share memory (null, or no bytes: there is none).
 inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x && y && x < y + nb && y < x + na;
+    return x && y && na && nb && x < y + nb && y < x + na;
 }
 // The same, but that `a` may be `b` itself.
 inline bool overlap_partly(const void *a, size_t na, const void *b, size_t nb) {
     return a != b && overlap(a, na, b, nb);
+}
+// Whether one of the first `outputs` of these arrays shares memory with any other of them.
+struct Span {
+    const void *at;
+    size_t bytes;
+};
+template <size_t N>
+bool any_overlap(const Span (&a)[N], size_t outputs) {
+    for (size_t i = 0; i < outputs; ++i)
+        for (size_t j = i + 1; j < N; ++j)
+            if (overlap(a[i].at, a[i].bytes, a[j].at, a[j].bytes)) return true;
+    return false;
 }
 inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 

@@ -657,9 +657,18 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
         !on(uniforms, 4) || !on(lse, 4) || !on(draft_lse, 4) || !on(token, 4) || !on(accepted, 4) ||
         !on(token_logprob, 4) || !on(workspace, 256))
         return SB_ERR_ALIGNMENT;
+    // every block of a request reads its drafts, uniforms and sums for itself, while one of them writes
+    const size_t need = sb_verify_workspace_bytes(R, draft_rows, V), rows = R * 4;
+    const size_t q_rows = draft_rows > 0 ? draft_rows : 0;
+    const Span arrays[] = {{token, rows}, {accepted, static_cast<size_t>(B) * 4}, {token_logprob, rows},
+                           {workspace, need}, {logits, R * V * za}, {draft_logits, q_rows * V * za},
+                           // (a draft's place takes the draft itself until all blocks have read it)
+                           {token == drafts ? nullptr : drafts, rows}, {starts, B > 0 ? (B + 1) * size_t(4) : 0},
+                           {uniforms, rows}, {lse, rows}, {draft_lse, q_rows * 4}};
+    if (any_overlap(arrays, 4)) return SB_ERR_INVALID_ARG;
     int sms = 0;
     if (int32_t e = device_sms_cc(&sms, nullptr)) return e;
-    if (workspace_bytes < sb_verify_workspace_bytes(R, draft_rows, V)) return SB_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < need) return SB_ERR_WORKSPACE_TOO_SMALL;
     if (R == 0 && B == 0) return SB_OK;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     VerifyParams p{};
@@ -701,6 +710,12 @@ int32_t sb_verify_greedy(const int32_t *target, const int32_t *drafts, const int
         return SB_ERR_INVALID_ARG;
     if (!on(target, 4) || !on(drafts, 4) || !on(starts, 4) || !on(token, 4) || !on(accepted, 4))
         return SB_ERR_ALIGNMENT;
+    // (a request's warp has read its drafts when it writes, and a row's target in the same thread)
+    const size_t rows = R * 4;
+    const Span arrays[] = {{token, rows}, {accepted, static_cast<size_t>(B) * 4},
+                           {token == drafts ? nullptr : drafts, rows}, {token == target ? nullptr : target, rows},
+                           {starts, B > 0 ? (B + 1) * size_t(4) : 0}};
+    if (any_overlap(arrays, 2)) return SB_ERR_INVALID_ARG;
     if (int32_t e = device_sms_cc(nullptr, nullptr)) return e;
     if (R == 0 && B == 0) return SB_OK;
     const GreedyParams p{target, drafts, starts, static_cast<int>(R), static_cast<int>(B), token, accepted};

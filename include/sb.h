@@ -731,8 +731,9 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
  *   token_logprob  device float [R], or NULL: log p(token); 0 where there is no token.
  *   workspace   device, 256-byte aligned, >= sb_verify_workspace_bytes(R, draft_rows, V); no
  *               initialisation.  Its header is read by sb_last_device_status.
- * A sampled row without any finite logit answers -1 with log-prob NaN.  Up to two kernels on
- * `stream`.  Equal calls give equal bits.
+ * token may be drafts itself.  No other output (nor the workspace) may share memory with an input or
+ * another output.  A sampled row without any finite logit answers -1 with log-prob NaN.  Up to two
+ * kernels on `stream`.  Equal calls give equal bits.
  */
 size_t sb_verify_workspace_bytes(int64_t R, int64_t draft_rows, int64_t V);
 int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int32_t *drafts,
@@ -746,7 +747,8 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
  * The same for greedy decoding, where SB_TOKEN has given each row's own choice: a draft stays while
  * it is that choice, and the choice of the row behind the last one that stays follows.
  *   target      device int32 [R]: the rows' tokens; drafts, starts, token and accepted as above
- *               (starts that are out of range give accepted -1; there is no status word).
+ *               (starts that are out of range give accepted -1; there is no status word).  token may
+ *               also be target itself.
  * One kernel on `stream`; no workspace.
  */
 int32_t sb_verify_greedy(const int32_t *target, const int32_t *drafts, const int32_t *starts,
