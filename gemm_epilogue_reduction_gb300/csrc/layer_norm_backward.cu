@@ -141,7 +141,9 @@ __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams
         for (int k = 0; k < ROWS; ++k) {
             if (k > 0 && row0 + k * stride >= p.M) break;
             const float r = rsqrtf(sum2[3 * k] * p.inv_d + p.eps);
-            const float ma = -r * (sum2[3 * k + 1] * p.inv_d), c2 = -r * r * r * (sum2[3 * k + 2] * p.inv_d);
+            // t = dh + r·(a - mean(a) - r·(r·mean(a·c))·c): no r³, which leaves fp32's range for deviations
+            // whose squares are far from doing so
+            const float ma = -(sum2[3 * k + 1] * p.inv_d), mac = -r * (r * (sum2[3 * k + 2] * p.inv_d));
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int e = e0 + i * per;
@@ -157,11 +159,10 @@ __global__ void __launch_bounds__(MAXT, 1) backward_kernel(const LayerNormParams
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 xr = __fmul2_rn(x[j], both(r));
-                    s_w[i][j] = __ffma2_rn(xr, c[k][i][j], s_w[i][j]);
+                    s_w[i][j] = __ffma2_rn(__fmul2_rn(x[j], both(r)), c[k][i][j], s_w[i][j]);
                     s_b[i][j] = __fadd2_rn(s_b[i][j], x[j]);
-                    v[j] = __ffma2_rn(both(c2), c[k][i][j],
-                                      __ffma2_rn(xr, w[i][j], __fadd2_rn(v[j], both(ma))));
+                    const float2 a = __ffma2_rn(x[j], w[i][j], both(ma));
+                    v[j] = __ffma2_rn(both(r), __ffma2_rn(both(mac), c[k][i][j], a), v[j]);
                 }
                 store8<MODE>(static_cast<T *>(p.dh_out) + at_row + e, in[i], v);
                 if constexpr (BRANCH) {
