@@ -146,14 +146,13 @@ int32_t sb_layer_norm_forward(const void *h, const void *y, const void *weight, 
     if (M > 0 && (!x || (y && !h_out))) return SB_ERR_INVALID_ARG;
     if (!on(y, 2) || (y && !on(h_out, stream_type == SB_F32 ? 4 : 2)) || !on(x, 2))
         return SB_ERR_ALIGNMENT;
-    // outputs over an input's memory: only the ones that the same thread has read by then
+    // outputs over an input's memory: only the ones that the same thread has read by then (which then
+    // stand here once)
     const size_t hb = M * d * (stream_type == SB_F32 ? 4 : 2), bb = M * d * 2;
     const size_t wb = d * (weight_type == SB_F32 ? 4 : 2);
-    if (overlap_partly(x, bb, y, bb) || overlap(x, bb, h, hb) || overlap(x, bb, weight, wb) ||
-        overlap(x, bb, bias, wb) ||
-        (y && (overlap_partly(h_out, hb, h, hb) || overlap(h_out, hb, y, bb) || overlap(h_out, hb, x, bb) ||
-               overlap(h_out, hb, weight, wb) || overlap(h_out, hb, bias, wb))))
-        return SB_ERR_INVALID_ARG;
+    const Span arrays[] = {{x, bb}, {y ? h_out : nullptr, hb}, {x == y ? nullptr : y, bb},
+                           {y && h_out == h ? nullptr : h, hb}, {weight, wb}, {bias, wb}, {seed_offset, 8}};
+    if (any_overlap(arrays, 2)) return SB_ERR_INVALID_ARG;
     int sms = 0;
     if (int32_t e = device_sms_cc(&sms, nullptr)) return e;
     if (M == 0) return SB_OK;
@@ -198,13 +197,16 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
         !on(dbias, wa) || !on(workspace, 16))
         return SB_ERR_ALIGNMENT;
     const size_t hb = M * d * ha, bb = M * d * 2, wb = d * wa;
-    if (overlap_partly(dh_out, hb, dh, hb) || overlap(dh_out, hb, h, hb) || overlap(dh_out, hb, dx, bb) ||
-        overlap(dh_out, hb, dy, bb) || overlap_partly(dy, bb, dx, bb) || overlap(dy, bb, h, hb) ||
-        overlap(dy, bb, dh, hb) || overlap(dh_out, hb, weight, wb) || overlap(dy, bb, weight, wb))
-        return SB_ERR_INVALID_ARG;
+    Span arrays[] = {{workspace, 0}, {dweight, wb}, {dbias, wb}, {dh_out, hb}, {dy, bb},
+                     {dy == dx ? nullptr : dx, bb}, {dh_out == dh ? nullptr : dh, hb}, {h, hb}, {weight, wb},
+                     {seed_offset, 8}};
+    if (any_overlap(arrays, 5)) return SB_ERR_INVALID_ARG;
     int sms = 0;
     if (int32_t e = device_sms_cc(&sms, nullptr)) return e;
-    if (workspace_bytes < sb_layer_norm_workspace_bytes(M, d)) return SB_ERR_WORKSPACE_TOO_SMALL;
+    const size_t need = sb_layer_norm_workspace_bytes(M, d);
+    arrays[0].bytes = need;  // (which the device decides)
+    if (any_overlap(arrays, 1)) return SB_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return SB_ERR_WORKSPACE_TOO_SMALL;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (M == 0) {  // the empty sums
         for (void *v : {dweight, dbias})

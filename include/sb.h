@@ -660,7 +660,8 @@ int32_t sb_dropout(const void *x, const void *residual, int64_t n, int32_t x_typ
  *   p, seed, seed_offset   as for sb_dropout; without y not used.
  *   h_out       device [M, d] of stream_type; may be h itself.
  *   x           device bf16 [M, d]; may be y itself.  Formed from h_out before its rounding.
- * No other output may share memory with an input.  One kernel on `stream`; no workspace.
+ * No other output may share memory with an input or another output.  One kernel on `stream`; no
+ * workspace.
  */
 int32_t sb_layer_norm_forward(const void *h, const void *y, const void *weight, const void *bias,
                               int64_t M, int64_t d, int32_t stream_type, int32_t weight_type,
@@ -682,8 +683,8 @@ size_t sb_layer_norm_workspace_bytes(int64_t M, int64_t d);
  *   dweight, dbias  device [d] of weight_type (dbias or NULL), summed over the rows in fp32 in a
  *               fixed order: equal calls give equal bits.
  *   workspace   device, 16-byte aligned, >= sb_layer_norm_workspace_bytes(M, d); no initialisation.
- * No other output may share memory with an input.  Two kernels on `stream`.  M = 0 writes zeros to
- * dweight and dbias.
+ * No other output (nor the workspace) may share memory with an input or another output.  Two kernels
+ * on `stream`.  M = 0 writes zeros to dweight and dbias.
  */
 int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, const void *weight,
                                int64_t M, int64_t d, int32_t stream_type, int32_t weight_type,
