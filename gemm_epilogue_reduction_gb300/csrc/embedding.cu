@@ -681,12 +681,11 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
         return SB_ERR_ALIGNMENT;
     const size_t dw_bytes = V * d * (weight_type == SB_F32 ? 4 : 2);
     const size_t dout_bytes = M * d * (grad_type == SB_F32 ? 4 : 2);
-    if (overlap(dW, dw_bytes, dout, dout_bytes) || overlap(dW, dw_bytes, ids, M * 4) ||
-        overlap(workspace, workspace_bytes, dW, dw_bytes) ||
-        overlap(workspace, workspace_bytes, dout, dout_bytes))
-        return SB_ERR_INVALID_ARG;
+    const size_t need = sb_embedding_backward_workspace_bytes(M, d);
+    const Span arrays[] = {{workspace, need}, {dW, dw_bytes}, {dout, dout_bytes}, {ids, static_cast<size_t>(M) * 4}};
+    if (any_overlap(arrays, 2)) return SB_ERR_INVALID_ARG;
     if (int32_t e = device_sms_cc(nullptr, nullptr)) return e;
-    if (workspace_bytes < sb_embedding_backward_workspace_bytes(M, d)) return SB_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < need) return SB_ERR_WORKSPACE_TOO_SMALL;
     if (M == 0 && add) return SB_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);

@@ -616,9 +616,9 @@ size_t sb_embedding_backward_workspace_bytes(int64_t M, int64_t d);
  *   add = 1:  dW = dW + S in the rows that a token has, rounded once; the others are not touched.
  *             That is how a tied embedding's gradient joins the head's (sb_cross_entropy_backward).
  *   dout        device [M, d] of grad_type (an sb_type).
- *   dW          device [V, d] of weight_type; not over dout's memory.
+ *   dW          device [V, d] of weight_type; not over ids' or dout's memory.
  *   workspace   device, 256-byte aligned, >= sb_embedding_backward_workspace_bytes(M, d); no
- *               initialisation.
+ *               initialisation; not over the other arrays' memory.
  * Up to four kernels on `stream` (one more for every factor of 8 that M is above 65,536).
  */
 int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, int64_t d, int64_t V,
