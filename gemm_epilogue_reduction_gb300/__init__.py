@@ -164,6 +164,9 @@ def lib():
         L.sb_verify_drafts.argtypes = ([P] * 7 + [i64] * 4 + [i32, f32, u64] + [P] * 4 +
                                        [ctypes.c_size_t, P])
         L.sb_verify_drafts.restype = i32
+        L.sb_verify_drafts_at.argtypes = ([P] * 7 + [i64] * 4 + [i32, f32, u64] + [P] * 5 +
+                                          [ctypes.c_size_t, P])
+        L.sb_verify_drafts_at.restype = i32
         L.sb_verify_greedy.argtypes = [P] * 3 + [i64] * 2 + [P] * 3
         L.sb_verify_greedy.restype = i32
         L.sb_select_source_projection.argtypes = [ctypes.c_double] * 8 + [
@@ -468,7 +471,13 @@ def sb_verify_workspace_bytes(R: int, draft_rows: int, V: int) -> int:
 
 def sb_verify_drafts(logits, draft_logits, drafts, starts, uniforms, lse, draft_lse, R, draft_rows,
                      B, V, logits_type, temperature, seed, token, accepted, token_logprob,
-                     workspace, workspace_bytes, stream=None) -> int:
+                     workspace, workspace_bytes, stream=None, seed_offset=None) -> int:
+    if seed_offset is not None:
+        return int(lib().sb_verify_drafts_at(
+            _ptr(logits), _ptr(draft_logits), _ptr(drafts), _ptr(starts), _ptr(uniforms), _ptr(lse),
+            _ptr(draft_lse), R, draft_rows, B, V, logits_type, float(temperature),
+            seed & (2**64 - 1), _ptr(seed_offset), _ptr(token), _ptr(accepted), _ptr(token_logprob),
+            _ptr(workspace), int(workspace_bytes), _stream(stream)))
     return int(lib().sb_verify_drafts(
         _ptr(logits), _ptr(draft_logits), _ptr(drafts), _ptr(starts), _ptr(uniforms), _ptr(lse),
         _ptr(draft_lse), R, draft_rows, B, V, logits_type, float(temperature), seed & (2**64 - 1),
@@ -1005,8 +1014,8 @@ def layer_norm_backward(dx, dh, h, weight, *, need_dbias: bool = True, need_dy: 
 
 
 def verify_drafts(logits, drafts, starts, uniforms, *, draft_logits=None, temperature: float = 1.0,
-                  seed: int = 0, lse=None, draft_lse=None, logprob: bool = True, stream=None,
-                  workspace=None):
+                  seed: int = 0, seed_offset=None, lse=None, draft_lse=None, logprob: bool = True,
+                  stream=None, workspace=None):
     """Which of the drafted tokens the head's distribution keeps, and the token that follows them
     (speculative sampling; ``sb_verify_drafts`` describes it).
 
@@ -1016,7 +1025,8 @@ def verify_drafts(logits, drafts, starts, uniforms, *, draft_logits=None, temper
     [drafts, V] of logits' type, one row for each draft in their order (None: drafts without a
     distribution, as from a lookup). lse [R] and draft_lse float32: the logsumexp of logits /
     temperature where it is known (``project`` returns it for temperature 1). seed: of the samples'
-    stream.
+    stream; seed_offset: int64 [1] on the device, added to the seed when the kernels run (a step
+    counter: a captured call repeats its seed at every replay).
 
     Returns a dict: token [R] int32 (from starts[b] on the drafts that stay and the sample behind
     them, -1 in all other rows), accepted [B] int32 (how many stay), token_logprob [R] (if
@@ -1025,8 +1035,9 @@ def verify_drafts(logits, drafts, starts, uniforms, *, draft_logits=None, temper
     if stream is not None:
         return _on_stream(stream, lambda: verify_drafts(
             logits, drafts, starts, uniforms, draft_logits=draft_logits, temperature=temperature,
-            seed=seed, lse=lse, draft_lse=draft_lse, logprob=logprob, workspace=workspace),
-            logits, drafts, starts, uniforms, draft_logits, lse, draft_lse, workspace)
+            seed=seed, seed_offset=seed_offset, lse=lse, draft_lse=draft_lse, logprob=logprob,
+            workspace=workspace),
+            logits, drafts, starts, uniforms, draft_logits, lse, draft_lse, seed_offset, workspace)
     import torch
     where = "verify_drafts"
     dev = torch._C._cuda_getDevice()
@@ -1058,7 +1069,7 @@ def verify_drafts(logits, drafts, starts, uniforms, *, draft_logits=None, temper
             raise ValueError(f"{where}: draft_lse without draft_logits")
         _tensor("draft_lse", draft_lse, (D,), (f32,), dev, where)
         ql = draft_lse.data_ptr()
-    seed = _seeded(seed, None, dev, where)
+    seed = _seeded(seed, seed_offset, dev, where)
     L = lib()
     if workspace is None:
         size = _nonzero(L.sb_verify_workspace_bytes(R, D, V), where)
@@ -1068,10 +1079,10 @@ def verify_drafts(logits, drafts, starts, uniforms, *, draft_logits=None, temper
     token = torch.empty_like(drafts)
     accepted = torch.empty(B, dtype=i32, device=starts.device)
     lp = torch.empty_like(uniforms) if logprob else None
-    st = L.sb_verify_drafts(logits.data_ptr(), q, drafts.data_ptr(), starts.data_ptr(),
-                            uniforms.data_ptr(), _ptr(lse), ql, R, D, B, V, zt, temperature, seed,
-                            token.data_ptr(), accepted.data_ptr(), _ptr(lp), workspace.data_ptr(),
-                            size, _current(dev))
+    st = L.sb_verify_drafts_at(logits.data_ptr(), q, drafts.data_ptr(), starts.data_ptr(),
+                               uniforms.data_ptr(), _ptr(lse), ql, R, D, B, V, zt, temperature, seed,
+                               _ptr(seed_offset), token.data_ptr(), accepted.data_ptr(), _ptr(lp),
+                               workspace.data_ptr(), size, _current(dev))
     if st != SB_OK:
         raise SbError(st, "sb_verify_drafts")
     out = {"token": token, "accepted": accepted, "workspace": workspace}

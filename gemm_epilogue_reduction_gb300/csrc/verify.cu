@@ -52,6 +52,7 @@ struct VerifyParams {
     float inv_t;
     double t;           // 1 / inv_t
     unsigned long long seed;
+    const unsigned long long *seed_offset;  // added to it (null: 0), read when the kernel runs
     int32_t *token, *accepted;
     float *logprob;
     float2 *part;       // MaxSum, see Pieces
@@ -299,16 +300,16 @@ struct Scan {
     const T *z, *q;
     float c, ref, rest, qref, qrest;  // see ref_of
     int x;
-    unsigned long long first;  // index of the row's first draw
+    unsigned long long seed, first;  // of the stream; index of the row's first draw in it
     float best, bar;
     int column;
     static constexpr float kUpper = 0.69314860f * 16777216.f;
     static constexpr float kLeastScore = 1.40129846e-45f;  // fp32's smallest number
 
     __device__ __forceinline__ Scan(const VerifyParams &p_, const T *z_, const T *q_, float4 refs, int x_,
-                                    unsigned long long first_)
+                                    unsigned long long seed_, unsigned long long first_)
         : p(p_), z(z_), q(q_), c(p_.inv_t * kLog2e), ref(refs.x), rest(refs.y), qref(refs.z),
-          qrest(refs.w), x(x_), first(first_), best(0.f), bar(0.f), column(0) {}
+          qrest(refs.w), x(x_), seed(seed_), first(first_), best(0.f), bar(0.f), column(0) {}
     // Of two columns, j and j + step; v, u: their logits, the target's and the draft's.
     __device__ __forceinline__ float2 weights(float2 v, float2 u, int j, int step) const {
         const float2 y = __ffma2_rn(__fadd2_rn(v, both(-ref)), both(c), both(rest));
@@ -324,7 +325,7 @@ struct Scan {
         return w;
     }
     __device__ __forceinline__ void exact(int j) {
-        const uint32_t bits = bits24_from_state(splitmix_state(p.seed, first + j));
+        const uint32_t bits = bits24_from_state(splitmix_state(seed, first + j));
         const float2 w = weights(both(one(z + j)), both(FROM == kDifference ? one(q + j) : 0.f), j, 1);
         // A uniform of 0, or a weight too small for the quotient, scores less than any other column but more
         // than none: a row with a weight has a sample.
@@ -338,7 +339,7 @@ struct Scan {
                                             int have) {
         float bound[N], low = 0.f;
         const float all = have >= N ? kUpper : 0.f;  // (`have` is N or 0 but where columns are STEP apart)
-        const unsigned long long state = splitmix_state(p.seed, first + j);
+        const unsigned long long state = splitmix_state(seed, first + j);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
             const float2 pair = weights(a[i / 2], b[i / 2], j + i * STEP, STEP);
@@ -366,11 +367,11 @@ struct Scan {
 // This thread's best of the share of block `rank` of `blocks`.
 template <typename T, int FROM>
 __device__ __forceinline__ unsigned long long scan(const VerifyParams &p, const T *z, const T *q,
-                                                   float4 refs, int x, unsigned long long first,
-                                                   int rank, int blocks) {
+                                                   float4 refs, int x, unsigned long long seed,
+                                                   unsigned long long first, int rank, int blocks) {
     constexpr int E = Share<T>::E;
     const int tid = threadIdx.x;
-    Scan<T, FROM> s(p, z, q, refs, x, first);
+    Scan<T, FROM> s(p, z, q, refs, x, seed, first);
     if (FROM != kDifference || ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0) {
         const Share<T> za(z, p.V, rank, blocks);
         const uint4 *qa = FROM == kDifference ? reinterpret_cast<const uint4 *>(q + za.head) : nullptr;
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int total = p.B ? p.starts[p.B] : 0;
     const int s0 = p.B ? p.starts[b] : 0, s1 = p.B ? p.starts[b + 1] : 0, front = p.B ? p.starts[0] : 0;
+    const unsigned long long seed = p.seed + (p.seed_offset ? *p.seed_offset : 0ull);
     if (blockIdx.x == 0 && tid == 0) *p.epoch_word = p.epoch;
     auto clear = [&](int from, int to) {
         for (long long r = from + static_cast<long long>(rank) * THREADS + tid; r < to;
@@ -503,11 +505,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
     for (int turn = 0; turn < 2 && !best; ++turn) {
         // a difference that is nowhere positive (p and q equal but for roundings): p itself
         if (turn == 0 && known && q)
-            best = scan<T, kDifference>(p, z, q + static_cast<size_t>(e) * p.V, ref, x, first, rank, blocks);
+            best = scan<T, kDifference>(p, z, q + static_cast<size_t>(e) * p.V, ref, x, seed, first, rank, blocks);
         else if (turn == 0 && known)
-            best = scan<T, kWithout>(p, z, nullptr, ref, x, first, rank, blocks);
+            best = scan<T, kWithout>(p, z, nullptr, ref, x, seed, first, rank, blocks);
         else
-            best = scan<T, kTarget>(p, z, nullptr, ref, x, first, rank, blocks);
+            best = scan<T, kTarget>(p, z, nullptr, ref, x, seed, first, rank, blocks);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const unsigned long long other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
@@ -646,6 +648,18 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
                          int64_t V, int32_t logits_type, float temperature, uint64_t seed,
                          int32_t *token, int32_t *accepted, float *token_logprob, void *workspace,
                          size_t workspace_bytes, void *stream) {
+    return sb_verify_drafts_at(logits, draft_logits, drafts, starts, uniforms, lse, draft_lse, R,
+                               draft_rows, B, V, logits_type, temperature, seed, nullptr, token,
+                               accepted, token_logprob, workspace, workspace_bytes, stream);
+}
+
+int32_t sb_verify_drafts_at(const void *logits, const void *draft_logits, const int32_t *drafts,
+                            const int32_t *starts, const float *uniforms, const float *lse,
+                            const float *draft_lse, int64_t R, int64_t draft_rows, int64_t B,
+                            int64_t V, int32_t logits_type, float temperature, uint64_t seed,
+                            const uint64_t *seed_offset, int32_t *token, int32_t *accepted,
+                            float *token_logprob, void *workspace, size_t workspace_bytes,
+                            void *stream) {
     if (!verify_sizes(R, draft_rows, V) || B < 0 || B > (int64_t(1) << 24) ||
         logits_type < SB_BF16 || logits_type > SB_F32 ||
         !(std::isfinite(temperature) && temperature > 0.f) ||
@@ -655,7 +669,7 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
     const uintptr_t za = logits_type == SB_F32 ? 4 : 2;
     if (!on(logits, za) || !on(draft_logits, za) || !on(drafts, 4) || !on(starts, 4) ||
         !on(uniforms, 4) || !on(lse, 4) || !on(draft_lse, 4) || !on(token, 4) || !on(accepted, 4) ||
-        !on(token_logprob, 4) || !on(workspace, 256))
+        !on(token_logprob, 4) || !on(workspace, 256) || !on(seed_offset, 8))
         return SB_ERR_ALIGNMENT;
     // every block of a request reads its drafts, uniforms and sums for itself, while one of them writes
     const size_t need = sb_verify_workspace_bytes(R, draft_rows, V), rows = R * 4;
@@ -664,7 +678,7 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
                            {workspace, need}, {logits, R * V * za}, {draft_logits, q_rows * V * za},
                            // (a draft's place takes the draft itself until all blocks have read it)
                            {token == drafts ? nullptr : drafts, rows}, {starts, B > 0 ? (B + 1) * size_t(4) : 0},
-                           {uniforms, rows}, {lse, rows}, {draft_lse, q_rows * 4}};
+                           {uniforms, rows}, {lse, rows}, {draft_lse, q_rows * 4}, {seed_offset, 8}};
     if (any_overlap(arrays, 4)) return SB_ERR_INVALID_ARG;
     int sms = 0;
     if (int32_t e = device_sms_cc(&sms, nullptr)) return e;
@@ -690,6 +704,7 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
     p.inv_t = 1.0f / temperature;
     p.t = 1.0 / p.inv_t;
     p.seed = seed;
+    p.seed_offset = reinterpret_cast<const unsigned long long *>(seed_offset);
     p.token = token;
     p.accepted = accepted;
     p.logprob = token_logprob;

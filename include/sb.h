@@ -745,6 +745,19 @@ int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int
                          size_t workspace_bytes, void *stream);
 
 /*
+ * The same with a seed that moves on: seed_offset, device uint64 [1] (NULL: 0), is added to seed when
+ * the kernels run.  A captured call repeats its seed at every replay, and with it the draws of every
+ * row; a decoding loop that replays a step counts seed_offset up (and fills in new uniforms).
+ */
+int32_t sb_verify_drafts_at(const void *logits, const void *draft_logits, const int32_t *drafts,
+                            const int32_t *starts, const float *uniforms, const float *lse,
+                            const float *draft_lse, int64_t R, int64_t draft_rows, int64_t B,
+                            int64_t V, int32_t logits_type, float temperature, uint64_t seed,
+                            const uint64_t *seed_offset, int32_t *token, int32_t *accepted,
+                            float *token_logprob, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/*
  * The same for greedy decoding, where SB_TOKEN has given each row's own choice: a draft stays while
  * it is that choice, and the choice of the row behind the last one that stays follows.
  *   target      device int32 [R]: the rows' tokens; drafts, starts, token and accepted as above
