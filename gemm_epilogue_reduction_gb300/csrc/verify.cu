@@ -49,8 +49,7 @@ struct VerifyParams {
     int R, B, V, Rd;
     int zrows, qrows;   // of them, how many lse_kernel reduces (those behind the last request aside)
     int with_q;         // drafts have distributions of their own
-    float inv_t;
-    double t;           // 1 / inv_t
+    float t, inv_t;
     unsigned long long seed;
     const unsigned long long *seed_offset;  // added to it (null: 0), read when the kernel runs
     int32_t *token, *accepted;
@@ -227,25 +226,56 @@ __global__ void __launch_bounds__(kLseThreads, 4) lse_kernel(const VerifyParams 
     }
 }
 
-// A row's distribution: log p = (z - m) / T - l.  Formed here m is the largest logit and l the logarithm of
-// the sum of exponentials, so that no number of the size of z / T is ever rounded (z - m is exact in 64
-// bits), whatever T is; given m is 0 and l the logsumexp.
+// The rounded difference and what it is off by (Knuth's sum of two numbers).
+__device__ __forceinline__ float2 difference(float a, float b) {
+    const float d = a - b, t = d - a, off = (a - (d - t)) + (-b - t);
+    return make_float2(d, fabsf(d) < INFINITY ? off : 0.f);
+}
+
+// A row's distribution: log p = (z - m) / T - (l + rest).  Formed here m is the largest logit and l the
+// logarithm of the sum of exponentials, so that no number of the size of z / T is ever rounded, whatever T
+// is; given m is 0 and l the logsumexp.  Two fp32 parts where one is not enough: a row's chain in 64 bits took
+// 13.0 us instead of 10.4 (32 requests, logsumexps given), the fp64 pipe being as narrow as it is.
 struct Norm {
-    double m, l;
+    float m, l, rest;
 };
 __device__ __forceinline__ Norm norm_of(MaxSum a) {
-    if (!(a.s > 0.f && a.s < INFINITY)) return Norm{a.m, a.s == 0.f ? -INFINITY : a.s};  // no finite logit
-    // log s = e ln 2 + log f with s = f·2^e, f in [1, 2): in fp32 log s would be off by its own ulp
+    if (!(a.s > 0.f && a.s < INFINITY)) return Norm{a.m, a.s == 0.f ? -INFINITY : a.s, 0.f};  // no finite logit
+    // log s = e ln 2 + log f with s = f·2^e, f in [1, 2), and ln 2 as 2839/4096 and the rest
     const uint32_t bits = __float_as_uint(a.s);
-    const int e = static_cast<int>(bits >> 23) - 127;  // (s is no subnormal: its largest term is 1)
-    return Norm{a.m, e * 0.69314718055994531 + logf(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u))};
+    const float e = static_cast<float>(static_cast<int>(bits >> 23) - 127);  // (s is no subnormal: its largest term is 1)
+    const float2 l = difference(e * 0.693115234375f, -logf(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u)));
+    return Norm{a.m, l.x, fmaf(e, 3.194618494530942e-05f, l.y)};
 }
 // The same for the scan: log2 p = (z - ref)·c + rest.  ref is m, or where the logsumexp is given the logit whose
 // p is 1 (inside fp32's range), so that columns near the largest keep their precision.
 __device__ __forceinline__ float2 ref_of(Norm a, bool given, const VerifyParams &p) {
-    const double at = given ? a.l * p.t : a.m;
-    const float ref = isfinite(at) ? static_cast<float>(fmin(fmax(at, -3.4e38), 3.4e38)) : static_cast<float>(at);
-    return make_float2(ref, static_cast<float>(((ref - a.m) * p.inv_t - a.l) * 1.4426950408889634));
+    if (!given) return make_float2(a.m, fmaf(-a.l, kLog2e, -a.rest * kLog2e));
+    const float ref = fabsf(a.l) < INFINITY ? fminf(fmaxf(a.l * p.t, -3.4e38f), 3.4e38f) : a.l * 0.f;
+    return make_float2(ref, fmaf(ref, p.inv_t, -a.l) * kLog2e);
+}
+// log p of a column of logit z.
+__device__ __forceinline__ float log_p(float z, Norm a, float inv_t) {
+    const float2 gap = difference(z, a.m);
+    return fmaf(gap.x, inv_t, -a.l) + fmaf(gap.y, inv_t, -a.rest);
+}
+// Whether p / q > u, for p of logit z and q of logit x (1 where there is no q).  The two logits' differences
+// come first: of the size of z / T they may cancel.
+__device__ __forceinline__ bool stays(float z, Norm a, float x, Norm b, bool with_q, float inv_t, float u) {
+    float2 d = difference(z, a.m);
+    if (with_q) {
+        const float2 g = d, h = difference(x, b.m);
+        d = difference(g.x, h.x);
+        d.y += g.y - h.y;
+    }
+    float2 l = difference(a.l, b.l);
+    l.y += a.rest - b.rest;
+    const float y = d.x * inv_t;
+    if (!(fabsf(y) < INFINITY)) return y - l.x > 0.f;
+    const float2 sum = difference(y, l.x);
+    const float e = expf(sum.x);
+    if (!(e > 0.f && e < INFINITY)) return e > u;
+    return fmaf(e, sum.y + (fmaf(d.x, inv_t, -y) + fmaf(d.y, inv_t, -l.y)), e) > u;
 }
 
 // The distribution of row `at` of the target (or the draft), by a warp.
@@ -253,7 +283,7 @@ template <typename T>
 __device__ __forceinline__ Norm row_norm(const VerifyParams &p, const Pieces &c, bool draft, int at,
                                          int lane) {
     const float *given = draft ? p.qlse : p.lse;
-    if (given) return Norm{0.0, given[at]};
+    if (given) return Norm{0.f, given[at], 0.f};
     const int row = draft ? c.zrows + at : at;
     const long long begin = static_cast<long long>(row) * c.nv;
     const int first = static_cast<int>(begin / c.per), last = static_cast<int>((begin + c.nv - 1) / c.per);
@@ -261,13 +291,6 @@ __device__ __forceinline__ Norm row_norm(const VerifyParams &p, const Pieces &c,
     for (int i = first + lane; i <= last; i += 32)
         a = join(a, MaxSum{p.part[i + row].x, p.part[i + row].y}, p.inv_t * kLog2e);
     return norm_of(warp_join(a, p.inv_t * kLog2e));
-}
-
-// Whether e^x > u, for x whose rounding to fp32 would count.
-__device__ __forceinline__ bool exp_above(double x, float u) {
-    const float hi = static_cast<float>(x), e = expf(hi);
-    if (!(e > 0.f && e < INFINITY)) return e > u;
-    return fmaf(e, static_cast<float>(x - hi), e) > u;
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -473,19 +496,17 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
             const float zx = known ? one(z + at) : 0.f, qx = known && q ? one(q + at) : 0.f;
             const float u = has ? p.u[r] : 0.f;
             const Norm norm = row_norm<T>(p, pieces, false, r, lane);
-            const Norm qnorm = has && q ? row_norm<T>(p, pieces, true, q0 + i, lane) : Norm{0.0, 0.0};
+            const Norm qnorm = has && q ? row_norm<T>(p, pieces, true, q0 + i, lane) : Norm{};
             if (lane == 0) {
                 const float2 a = ref_of(norm, p.lse, p), b = ref_of(qnorm, p.qlse, p);
                 norms[warp] = norm;
                 refs[warp] = make_float4(a.x, a.y, b.x, b.y);
                 if (has) {
-                    // the two logits' differences first: of the size of z / T they may cancel
-                    const double gap = zx - norm.m, qgap = q ? qx - qnorm.m : 0.0;
                     if (!known && rank == 0) record_status(p.status, p.epoch, 1u);
-                    if (!known || !exp_above((gap - qgap) * p.inv_t - (norm.l - qnorm.l), u)) atomicMin(&end, i);
+                    if (!known || !stays(zx, norm, qx, qnorm, q, p.inv_t, u)) atomicMin(&end, i);
                     if (rank == 0) {  // (of a row behind the end it is taken back below)
                         p.token[r] = x;
-                        if (p.logprob) p.logprob[r] = static_cast<float>(gap * p.inv_t - norm.l);
+                        if (p.logprob) p.logprob[r] = log_p(zx, norm, p.inv_t);
                     }
                 }
             }
@@ -536,7 +557,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
             lp = __uint_as_float(0x7FC00000u);  // no column of the row has any probability
             if (best) {
                 token = ~static_cast<int>(static_cast<uint32_t>(best));
-                lp = static_cast<float>((one(z + token) - norm.m) * p.inv_t - norm.l);
+                lp = log_p(one(z + token), norm, p.inv_t);
             }
         }
         p.token[s0 + i] = token;
@@ -701,8 +722,8 @@ int32_t sb_verify_drafts_at(const void *logits, const void *draft_logits, const 
     p.zrows = lse ? 0 : p.R;
     p.qrows = draft_lse ? 0 : p.Rd;
     p.part = reinterpret_cast<float2 *>(ws + 256);
+    p.t = temperature;
     p.inv_t = 1.0f / temperature;
-    p.t = 1.0 / p.inv_t;
     p.seed = seed;
     p.seed_offset = reinterpret_cast<const unsigned long long *>(seed_offset);
     p.token = token;
