@@ -41,6 +41,12 @@ constexpr int kVerifyThreads = 512;
 // requests: 4 blocks 62 us, 8 in two turns 71, 8 of 256 threads 64); 16 where they have an SM each and
 // the device allows such clusters.
 constexpr int kWideBlocks = 16, kMostBlocks = 8, kLeastBlocks = 2;
+// Which draft row is a request's first depends on how many requests in front of it have rows.  A cluster
+// counts them itself; of more than this many it counts its own share's, and count_kernel has counted the
+// shares in front (4096 requests: 78 us either way; 8192: 131 -> 127; 16,384: 258 -> 217, shares of 8192 240;
+// 262,144: 18.4 ms -> 3).
+constexpr int kCountRequests = 2048, kCountThreads = 512;
+constexpr int64_t kMostRequests = int64_t(1) << 24;
 
 struct VerifyParams {
     const void *z, *q;
@@ -55,6 +61,7 @@ struct VerifyParams {
     int32_t *token, *accepted;
     float *logprob;
     float2 *part;       // MaxSum, see Pieces
+    int *counts;        // of kCountRequests requests each, how many have rows (null: not counted)
     uint32_t *epoch_word;
     unsigned long long *status;
     uint32_t epoch;
@@ -128,6 +135,21 @@ __device__ __forceinline__ Pieces pieces_of(const VerifyParams &p) {
     c.nv = max(1, p.V / Share<T>::E);
     c.per = max(1LL, (static_cast<long long>(c.rows) * c.nv + kLseBlocks - 1) / kLseBlocks);
     return c;
+}
+
+__global__ void __launch_bounds__(kCountThreads) count_kernel(const VerifyParams p) {
+    __shared__ int count;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    const int first = blockIdx.x * kCountRequests, end = min(p.B, first + kCountRequests);
+    int mine = 0;
+#pragma unroll 4
+    for (int i = first + threadIdx.x; i < end; i += kCountThreads) mine += p.starts[i + 1] > p.starts[i];
+    if (mine) atomicAdd(&count, mine);
+    __syncthreads();
+    if (threadIdx.x == 0) p.counts[blockIdx.x] = count;
 }
 
 template <typename T>
@@ -469,7 +491,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
     if (tid == 0) busy = 0, end = n;
     __syncthreads();
     int mine = 0;
-    for (int i = tid; i < b; i += THREADS) mine += p.starts[i + 1] > p.starts[i];
+    if (p.with_q) {
+        const int shares = p.counts ? b / kCountRequests : 0;
+        for (int i = tid; i < shares; i += THREADS) mine += p.counts[i];
+        for (int i = shares * kCountRequests + tid; i < b; i += THREADS) mine += p.starts[i + 1] > p.starts[i];
+    }
     if (mine) atomicAdd(&busy, mine);
     __syncthreads();
     const int q0 = s0 - max(front, 0) - busy;  // the draft's row of row s0
@@ -601,6 +627,11 @@ __global__ void __launch_bounds__(128) greedy_kernel(const GreedyParams p) {
 
 template <typename T>
 cudaError_t launch_verify(const VerifyParams &p, int sms, cudaStream_t st) {
+    if (p.counts) {
+        const unsigned shares = static_cast<unsigned>((p.B + kCountRequests - 1) / kCountRequests);
+        const cudaError_t e = launch_dependent(count_kernel, dim3(shares), kCountThreads, 0, p, st);
+        if (e != cudaSuccess) return e;
+    }
     if (p.zrows + p.qrows > 0 && p.B > 0) {
         const cudaError_t e = launch_dependent(lse_kernel<T>, dim3(kLseBlocks), kLseThreads, 0, p, st);
         if (e != cudaSuccess) return e;
@@ -650,6 +681,10 @@ bool verify_sizes(int64_t R, int64_t draft_rows, int64_t V) {
            V >= 1 && V < (int64_t(1) << 31) - 65536;
 }
 
+size_t verify_part_bytes(int64_t R, int64_t draft_rows) {
+    return up256(static_cast<size_t>(R + (draft_rows > 0 ? draft_rows : 0) + kLseBlocks) * 8);
+}
+
 }  // namespace
 }  // namespace sb
 
@@ -659,8 +694,8 @@ extern "C" {
 
 size_t sb_verify_workspace_bytes(int64_t R, int64_t draft_rows, int64_t V) {
     if (!verify_sizes(R, draft_rows, V)) return 0;
-    // the header and lse_kernel's parts
-    return 256 + up256(static_cast<size_t>(R + (draft_rows > 0 ? draft_rows : 0) + kLseBlocks) * 8);
+    // the header, lse_kernel's parts and count_kernel's counts
+    return 256 + verify_part_bytes(R, draft_rows) + (draft_rows > 0 ? kMostRequests / kCountRequests * 4 : 0);
 }
 
 int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int32_t *drafts,
@@ -681,7 +716,7 @@ int32_t sb_verify_drafts_at(const void *logits, const void *draft_logits, const 
                             const uint64_t *seed_offset, int32_t *token, int32_t *accepted,
                             float *token_logprob, void *workspace, size_t workspace_bytes,
                             void *stream) {
-    if (!verify_sizes(R, draft_rows, V) || B < 0 || B > (int64_t(1) << 24) ||
+    if (!verify_sizes(R, draft_rows, V) || B < 0 || B > kMostRequests ||
         logits_type < SB_BF16 || logits_type > SB_F32 ||
         !(std::isfinite(temperature) && temperature > 0.f) ||
         temperature < 1e-30f || (R > 0 && (!logits || !drafts || !uniforms || !token)) ||
@@ -710,6 +745,8 @@ int32_t sb_verify_drafts_at(const void *logits, const void *draft_logits, const 
     p.z = logits;
     p.q = draft_logits;
     p.with_q = draft_rows >= 0;
+    if (draft_rows > 0 && B > kCountRequests)
+        p.counts = reinterpret_cast<int *>(ws + 256 + verify_part_bytes(R, draft_rows));
     p.drafts = drafts;
     p.starts = starts;
     p.u = uniforms;
@@ -741,7 +778,7 @@ int32_t sb_verify_drafts_at(const void *logits, const void *draft_logits, const 
 
 int32_t sb_verify_greedy(const int32_t *target, const int32_t *drafts, const int32_t *starts,
                          int64_t R, int64_t B, int32_t *token, int32_t *accepted, void *stream) {
-    if (R < 0 || R >= (int64_t(1) << 31) - 65536 || B < 0 || B > (int64_t(1) << 24) ||
+    if (R < 0 || R >= (int64_t(1) << 31) - 65536 || B < 0 || B > kMostRequests ||
         (R > 0 && (!target || !drafts || !token)) || (B > 0 && (!starts || !accepted)))
         return SB_ERR_INVALID_ARG;
     if (!on(target, 4) || !on(drafts, 4) || !on(starts, 4) || !on(token, 4) || !on(accepted, 4))

@@ -734,7 +734,7 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
  *               initialisation.  Its header is read by sb_last_device_status.
  * token may be drafts itself.  No other output (nor the workspace) may share memory with an input or
  * another output.  A sampled row without any finite logit answers -1 with log-prob NaN.  Up to two
- * kernels on `stream`.  Equal calls give equal bits.
+ * kernels on `stream`, three for more than 2048 requests with draft_logits.  Equal calls give equal bits.
  */
 size_t sb_verify_workspace_bytes(int64_t R, int64_t draft_rows, int64_t V);
 int32_t sb_verify_drafts(const void *logits, const void *draft_logits, const int32_t *drafts,
