@@ -739,7 +739,7 @@ int32_t sb_verify_drafts_at(const void *logits, const void *draft_logits, const 
     int sms = 0;
     if (int32_t e = device_sms_cc(&sms, nullptr)) return e;
     if (workspace_bytes < need) return SB_ERR_WORKSPACE_TOO_SMALL;
-    if (R == 0 && B == 0) return SB_OK;
+    // (without rows or requests too: the header's status is this call's)
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     VerifyParams p{};
     p.z = logits;
