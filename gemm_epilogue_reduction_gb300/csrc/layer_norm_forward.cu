@@ -21,11 +21,10 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
     float *red1 = red[0] + group * (rt / 32) * 8, *red2 = red[1] + group * (rt / 32) * 8;
     const uint32_t pitch = rt * 16, kY = ST::kThread * rt, kRow = kY + (BRANCH ? SB::kThread * rt : 0);
     const uint32_t kStep = ROWS * kRow, kRing = p.steps * kStep, kBias = 32 * NV * rt, kWeights = 2 * kBias;
-    // weight and bias in fp32 (one copy, or one for each group's shift), then the groups' rings;
-    // addresses of this thread's pieces
-    const uint32_t copies = !p.shared_weights ? 0 : MODE == kShifted ? p.groups : 1;
-    const uint32_t weights = smem_u32(smem) + (MODE == kShifted ? group * kWeights : 0) + t * 16;
-    const uint32_t ring = smem_u32(smem) + copies * kWeights + group * kRing + t * 16;
+    // weight and bias in fp32 (the block is one group then), then the groups' rings; addresses of this
+    // thread's pieces
+    const uint32_t weights = smem_u32(smem) + t * 16;
+    const uint32_t ring = weights + (p.shared_weights ? kWeights : 0) + group * kRing;
     const int first = blockIdx.x * p.groups + group, stride = gridDim.x * p.groups;
     const long long base = static_cast<long long>(first) * d, advance = static_cast<long long>(stride) * d;
     const int shift = MODE == kShifted ? static_cast<int>(base & 7) : 0;
@@ -90,7 +89,7 @@ __global__ void __launch_bounds__(MAXT, 1) forward_kernel(const LayerNormParams 
             load_weight8<MODE>(p.weight, p, e0 + i * per, w_kept[i]);
             read_bias(e0 + i * per, b_kept[i]);
         }
-    } else if (p.shared_weights && (MODE == kShifted || group == 0)) {
+    } else if (p.shared_weights) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float2 v[4];
