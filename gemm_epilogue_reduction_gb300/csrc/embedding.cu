@@ -684,7 +684,8 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
     const size_t need = sb_embedding_backward_workspace_bytes(M, d);
     const Span arrays[] = {{workspace, need}, {dW, dw_bytes}, {dout, dout_bytes}, {ids, static_cast<size_t>(M) * 4}};
     if (any_overlap(arrays, 2)) return SB_ERR_INVALID_ARG;
-    if (int32_t e = device_sms_cc(nullptr, nullptr)) return e;
+    int sms = 0;
+    if (int32_t e = device_sms_cc(&sms, nullptr)) return e;
     if (workspace_bytes < need) return SB_ERR_WORKSPACE_TOO_SMALL;
     if (M == 0 && add) return SB_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -740,10 +741,12 @@ int32_t sb_embedding_backward(const int32_t *ids, const void *dout, int64_t M, i
     r.scale = scale;
     r.add = add;
     const int vec = vector_width(d, dout, dW);
-    // Long pieces where they fill the GPU four times over (8192 x 6144: 43.7 us against 45.4), and where
-    // one is all there is, so that there is nothing to join; else twice the blocks are worth more.
+    // Long pieces where they fill the GPU four times over, and where one is all there is, so that there
+    // is nothing to join; else twice the blocks are worth more.  Long against short, in us (bf16, 50,257
+    // rows): 8192 x 6144 41.0 and 43.0, 8192 x 5120 35.7 and 37.6, 65,536 x 768 121.7 and 124.6; below the
+    // limit 1000 x 4096 15.3 and 10.9, 4096 x 6144 23.2 and 19.3.
     const int64_t slices = (d + kReduceThreads * vec - 1) / (kReduceThreads * vec);
-    const bool long_pieces = M <= kLongPiece || pieces_of(M, kLongPiece) * slices >= 4 * 152;
+    const bool long_pieces = M <= kLongPiece || pieces_of(M, kLongPiece) * slices >= 4 * sms;
     r.piece = long_pieces ? kLongPiece : kPiece;
     r.pieces = static_cast<int>(pieces_of(M, r.piece));
     using B = __nv_bfloat16;
