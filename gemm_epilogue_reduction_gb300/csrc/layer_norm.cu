@@ -15,7 +15,7 @@
 // threads, sixteen values to a thread, and the next rows are on their way in a cp.async ring.
 // A thread works on two rows side by side: their sums go through the same two reductions, and one's
 // arithmetic fills the other's waits.  8192 x 6144 bf16 with branch and dropout: forward 64 us, 6.3
-// TB/s, backward 83, 6.1 TB/s; one row at a time: 74 and 94; four rows in forward, whose ring then has
+// TB/s, backward 82, 6.1 TB/s; one row at a time: 74 and 94; four rows in forward, whose ring then has
 // no third step: 71; two groups of 384 threads with the weights in shared memory: 70; a block to a
 // row, which ends with it: 108 (its fixed work and its loads of weights weigh more than the waits).
 // Weights and column sums are in registers; backward reads dx and dh again from the ring.  A draw's
@@ -25,13 +25,16 @@
 // values), and 512 with 128 registers for rows of up to 8192 and for two groups of 193 to 256 threads.
 // Two rows at a time still fit into those in forward, in backward they would spill: it takes one.
 // Measured with branch and dropout, bf16, against 384 threads for short rows and 640 to 1024 for long:
-// 8192 x 4096 forward 50 -> 45 us, backward 69 -> 61; 4096 x 8192 58 -> 46 and 118 -> 66 (91 with two rows
+// 8192 x 4096 forward 50 -> 46 us, backward 69 -> 61; 4096 x 8192 58 -> 45 and 118 -> 64 (91 with two rows
 // at a time).  Two groups need a ring of three steps: with two, 8192 x 4096 fp32 forward takes 83 us
-// against 76, backward 120 against 114.
+// against 73, backward 120 against 114.  Longer rows have up to 1024 threads of 64 registers, which
+// spill: 2048 x 16384 without branch forward 33 us, backward 130.
 //
 // A row length that is no multiple of eight shifts each row against the vectors' boundaries
 // (layer_norm.cuh); a group's rows are a multiple of eight apart, so that their shift, and with it a
-// thread's columns, stay the same.  8192 x 6135: forward 83 us, backward 118.
+// thread's columns, stay the same.  8192 x 6135: forward 82 us, backward 119; 8192
+// x 6143: 95 and 145 (with a shift of up to seven values such a row is one vector more than 384 threads
+// hold, and the wider block takes one row at a time in backward).
 #include <cmath>
 
 #include "layer_norm.cuh"

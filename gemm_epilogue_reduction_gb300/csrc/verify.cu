@@ -34,12 +34,12 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLseThreads = 256;
-constexpr int kLseBlocks = 152 * 4;    // as many as fit at a time
+constexpr int kLseBlocks = 152 * 4;    // as many as fit 152 SMs at a time (the workspace's size goes by it)
 constexpr int kAhead = 4;               // 16-byte vectors of a thread in flight
 constexpr int kVerifyThreads = 512;
 // Blocks of a request's cluster: as many as leave all blocks on the GPU at a time, two to an SM (64
-// requests: 4 blocks 62 us, 8 in two turns 71, 8 of 256 threads 64); 16 where they have an SM each and
-// the device allows such clusters.
+// requests, when that was measured: 4 blocks 62 us, 8 in two turns 71, 8 of 256 threads 64); 16 where
+// they have an SM each and the device allows such clusters.
 constexpr int kWideBlocks = 16, kMostBlocks = 8, kLeastBlocks = 2;
 // Which draft row is a request's first depends on how many requests in front of it have rows.  A cluster
 // counts them itself; of more than this many it counts its own share's, and count_kernel has counted the

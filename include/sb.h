@@ -596,8 +596,8 @@ int32_t sb_adamw_step(const sb_adamw_tensor *tensors, int64_t count, double lr, 
  *               value gives a row of NaN, and adds nothing to dW; nothing outside W is read.
  *   W           device [V, d] of weight_type (an sb_type), row-major.
  *   M, d, V     M >= 0 tokens (M <= 2^31 - 65536); 1 <= d <= 2^22; 1 <= V < 2^31 - 1.  16-byte
- *               aligned arrays with d a multiple of 8 (or 4) are read in wide loads, others value by
- *               value.
+ *               aligned arrays are read in wide loads, by the gradient where d is a multiple of 8 (or
+ *               4), others value by value.
  *   scale       finite.
  *   out         device [M, d] of out_type, rounded once; not over W's or ids' memory.
  * One kernel on `stream`; no workspace.
@@ -656,7 +656,7 @@ int32_t sb_dropout(const void *x, const void *residual, int64_t n, int32_t x_typ
  *   y           device bf16 [M, d]: the block's output, or NULL: h_out is h and is not written.
  *   weight, bias  device [d] of weight_type (an sb_type); bias may be NULL.
  *   M, d, eps, alignment   as for sb_residual_norm_forward (with one value to a row x is bias; a row of
- *               equal values with eps = 0 gives NaN).
+ *               equal values has no answer with eps = 0: NaN, or what the mean's rounding leaves).
  *   p, seed, seed_offset   as for sb_dropout; without y not used.
  *   h_out       device [M, d] of stream_type; may be h itself.
  *   x           device bf16 [M, d]; may be y itself.  Formed from h_out before its rounding.
@@ -705,8 +705,10 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
  * max(p - q, 0) (of p, where that is nowhere positive); where all stay the last row adds a sample
  * of its p.  The tokens are then distributed as samples of the target's own.  The sample of row r
  * is the column with the largest w_j / -log u_rj (the lowest of equal ones) with the 24-bit uniform
- * u of sb_lmhead_project at index r*V + j of the seed's stream: where all stay, SB_GUMBEL_TOKEN's.
- * u = 0 gives a score of 0, which wins only where no other column has a weight (in fp32).
+ * u of sb_lmhead_project at index r*V + j of the seed's stream.  u = 0 gives a score of 0, which wins
+ * only where no other column has a weight (in fp32).  Where all stay that is SB_GUMBEL_TOKEN's choice
+ * for the same logits; sb_lmhead_project races on its fp32 logits, SB_FULL_LOGITS has them rounded to
+ * bf16 (2^-8 of a logit, over T), so that keys nearer than that may change places.
  *   logits      device [R, V] of logits_type (an sb_type).  -inf is a column without probability.
  *   draft_logits  device [draft_rows, V] of that type: a row for every draft, one request's behind
  *               the other's, without gaps; draft_rows = -1 and NULL: the drafts have none.
@@ -723,6 +725,8 @@ int32_t sb_layer_norm_backward(const void *dx, const void *dh, const void *h, co
  *               caller has it (T = 1: that of sb_lmhead_project), each or NULL: formed here.
  *              Given ones are taken as they are: log p is off by what they are, of which fp32's
  *              rounding alone is 2^-24 max|z| / T.  At temperatures where that counts leave them out.
+ *              (sb_lmhead_project's is that of its fp32 logits: for bf16 ones the row's p then sum to 1
+ *              but for what their roundings leave, 2^-8 max|z| at most and far less on average.)
  *   R, B, V     R, draft_rows < 2^24; B <= 2^24; 1 <= V < 2^31 - 65536.
  *   temperature finite, >= 1e-30; 1 / T is rounded to fp32.
  *   token       device int32 [R]: from starts[b] on the drafts that stay and the sample behind them,
