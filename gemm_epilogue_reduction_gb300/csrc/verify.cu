@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
     if (tid == 0) busy = 0, end = n;
     __syncthreads();
     int mine = 0;
-    if (p.with_q) {
+    if (p.Rd > 0) {
         const int shares = p.counts ? b / kCountRequests : 0;
         for (int i = tid; i < shares; i += THREADS) mine += p.counts[i];
         for (int i = shares * kCountRequests + tid; i < b; i += THREADS) mine += p.starts[i + 1] > p.starts[i];

@@ -39,3 +39,20 @@ def test_requests_without_rows_in_between(B, front, draft):
     assert torch.equal(f["token"][front:], want["token"]) and torch.equal(f["accepted"][at], want["accepted"])
     assert (f["token_logprob"][front:] - want["token_logprob"]).abs().max() <= BOUND
     assert int(f["accepted"].abs().sum()) == int(want["accepted"].sum())
+
+
+@gpu
+def test_no_draft_rows_at_all():
+    """Draft logits without a row: requests of one row each, and one whose draft has no row."""
+    B, V = 1 << 23, 5
+    R = 1000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    z = torch.randn(R, V, generator=g, device="cuda")
+    starts = torch.full((B + 1,), R, dtype=torch.int32, device="cuda")
+    starts[:R - 1] = torch.arange(R - 1, device="cuda")
+    s = (z, torch.zeros(R, dtype=torch.int32, device="cuda"), starts, torch.zeros(R, device="cuda"))
+    f = sb.verify_drafts(*s, draft_logits=z[:0], seed=3)
+    assert sb.device_status(f["workspace"]) == sb.SB_ERR_INVALID_ARG  # rows 998 and 999: a draft
+    want = sb.verify_drafts(*s, seed=3)
+    assert torch.equal(f["token"][:R - 2], want["token"][:R - 2])
+    assert int(f["accepted"][R - 2]) == -1 and int(f["accepted"].abs().sum()) == 1
